@@ -37,6 +37,10 @@ Volumes (NCDHW, "Fully Fused Differentiable SSIM", 3D data):
   ssim3d_forward, ssim3d_backward, ssim3d_saved_maps_bytes, ssim3d_map_shape
   ssim3d_loss(vol1, vol2, padding="same", train=True) -> 1 - mean SSIM
   fused_ssim3d(vol1, vol2, padding="same", train=True) -> mean SSIM
+The rest of a training step (the ``train`` subpackage, with a C ABI of its own):
+  clip_grads_(grads, max_norm, out=None), grad_norm(grads)
+  AdamW(params, lr, ..., max_norm=None).step(grads)
+  block_norm(x, branch, gate, scale, post_weight, pre_weight) -> (residual, normed)
 """
 from __future__ import annotations
 
@@ -794,3 +798,8 @@ def fused_ssim3d(vol1, vol2, padding: str = "same", train: bool = True):
     """Mean SSIM of two volumes ("Fully Fused Differentiable SSIM", 3D data:
     fused_ssim3d on [BS, CH, D, H, W])."""
     return 1.0 - ssim3d_loss(vol1, vol2, padding, train)
+
+
+# --------------------------------------------------------------------------- the rest of a training step
+from . import train  # noqa: E402
+from .train import AdamW, TrainError, block_norm, clip_grads_, grad_norm  # noqa: E402,F401

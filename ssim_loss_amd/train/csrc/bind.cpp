@@ -1,0 +1,433 @@
+// bind.cpp -- the training operators on torch tensors: checks, outputs and
+// scratch from torch's caching allocator, and the calls of the C ABI
+// (ssim_train_amd.h) on torch's current stream of the tensors' device.
+//
+// A module of its own in C++ and not ctypes calls: a step over 160 tensors
+// looks at some 800 of them, and a small network's joint takes the GPU less
+// time than a Python autograd function takes to be recorded.
+
+#include <ATen/ATen.h>
+#include <c10/core/DeviceGuard.h>
+#include <c10/core/GradMode.h>
+#include <c10/hip/HIPStream.h>
+#include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/utils/pybind.h>
+
+#include <optional>
+#include <string>
+#include <vector>
+
+#include "ssim_train_amd.h"
+
+namespace py = pybind11;
+using at::Tensor;
+
+namespace {
+
+std::string text(int code) {
+  return std::string(ssim_train_strerror(code)) + " (code " + std::to_string(code) + ")";
+}
+
+// Python callers get the package's TrainError
+void raise(int code, const char* where) {
+  py::object type = py::module_::import("ssim_loss_amd.train").attr("TrainError");
+  py::object error = type(code, where);
+  PyErr_SetObject(type.ptr(), error.ptr());
+  throw py::error_already_set();
+}
+
+std::string at_index(const char* name, Py_ssize_t k) {
+  return k < 0 ? std::string(name) : std::string(name) + "[" + std::to_string(k) + "]";
+}
+
+int dtype_code(const Tensor& t) {
+  switch (t.scalar_type()) {
+    case at::kFloat: return SSIM_DTYPE_F32;
+    case at::kHalf: return SSIM_DTYPE_F16;
+    case at::kBFloat16: return SSIM_DTYPE_BF16;
+    default: return -1;
+  }
+}
+
+// a contiguous GPU tensor of one of the three types
+int check(const Tensor& t, const char* name, Py_ssize_t k = -1) {
+  if (!t.device().is_cuda())
+    throw py::type_error(at_index(name, k) + " must be a GPU tensor, got device " + t.device().str());
+  const int code = dtype_code(t);
+  if (code < 0)
+    throw py::type_error(at_index(name, k) + " must be float32, float16 or bfloat16, got " +
+                         c10::toString(t.scalar_type()));
+  if (t.layout() != at::kStrided || !t.is_contiguous())
+    throw py::value_error(at_index(name, k) + " must be contiguous");
+  return code;
+}
+
+void check_device(const Tensor& t, const c10::Device& dev, const char* name, Py_ssize_t k = -1) {
+  if (t.device() != dev)
+    throw py::type_error(at_index(name, k) + " must be a tensor on " + dev.str() + ", got " +
+                         t.device().str());
+}
+
+const Tensor& unpack(PyObject* o, const char* name, Py_ssize_t k = -1) {
+  if (!THPVariable_Check(o)) throw py::type_error(at_index(name, k) + " must be a torch.Tensor");
+  return THPVariable_Unpack(o);
+}
+
+// a list or tuple of tensors
+struct List {
+  py::object fast;
+  const char* name;
+  Py_ssize_t size = 0;
+  List(const py::object& o, const char* name_) : name(name_) {
+    if (THPVariable_Check(o.ptr()) || !(PyList_Check(o.ptr()) || PyTuple_Check(o.ptr())))
+      throw py::type_error(std::string(name) + " must be a list or tuple of tensors");
+    fast = o;
+    size = PySequence_Fast_GET_SIZE(o.ptr());
+  }
+  const Tensor& operator[](Py_ssize_t k) const {
+    return unpack(PySequence_Fast_GET_ITEM(fast.ptr(), k), name, k);
+  }
+  bool none(Py_ssize_t k) const { return PySequence_Fast_GET_ITEM(fast.ptr(), k) == Py_None; }
+};
+
+void* stream_of(const c10::Device& dev) {
+  return c10::hip::getCurrentHIPStream(dev.index()).stream();
+}
+
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
+Tensor scratch(size_t bytes, const c10::Device& dev) {
+  return at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(dev));
+}
+
+// ---- clipping
+Tensor clip(const py::object& grads_, double max_norm, const py::object& out_, bool scales) {
+  const List grads(grads_, "grads");
+  const bool in_place = out_.is_none();
+  const List out(in_place ? grads_ : out_, "out");
+  if (out.size != grads.size) throw py::value_error("out must have as many tensors as grads");
+  if (grads.size == 0) throw py::value_error("grads must hold at least one tensor");
+  if (scales && !(max_norm >= 0.0 && max_norm <= 1.7976931348623157e308))
+    throw py::value_error("max_norm must be a number >= 0");
+  std::vector<ssim_clip_item> items(grads.size);
+  const c10::Device dev = grads[0].device();
+  for (Py_ssize_t k = 0; k < grads.size; ++k) {
+    const Tensor& g = grads[k];
+    ssim_clip_item& it = items[k];
+    it.dtype = check(g, "grads", k);
+    check_device(g, dev, "grads", k);
+    it.grad = g.const_data_ptr();
+    it.n = g.numel();
+    it.reserved = 0;
+    it.out = nullptr;
+    if (!scales) continue;
+    const Tensor& o = out[k];
+    if (!in_place) {
+      check_device(o, dev, "out", k);
+      if (check(o, "out", k) != it.dtype)
+        throw py::type_error(at_index("out", k) + " must have its gradient's dtype");
+      if (o.sizes() != g.sizes())
+        throw py::value_error(at_index("out", k) + " must have its gradient's shape");
+    }
+    it.out = o.data_ptr();
+  }
+  const c10::DeviceGuard guard(dev);
+  Tensor norm = at::empty({}, at::TensorOptions().dtype(at::kFloat).device(dev));
+  const Tensor ws = scratch(ssim_update_workspace_bytes(), dev);
+  float* n = norm.data_ptr<float>();
+  const int rc = scales ? ssim_clip_grads(items.data(), grads.size, max_norm, n, ws.data_ptr(),
+                                          stream_of(dev))
+                        : ssim_grad_norm(items.data(), grads.size, n, ws.data_ptr(), stream_of(dev));
+  if (rc != SSIM_OK) raise(rc, scales ? "ssim_clip_grads" : "ssim_grad_norm");
+  if (scales)
+    for (Py_ssize_t k = 0; k < out.size; ++k) written(out[k]);
+  return norm;
+}
+
+Tensor clip_grads(const py::object& grads, double max_norm, const py::object& out) {
+  return clip(grads, max_norm, out, true);
+}
+Tensor grad_norm(const py::object& grads) { return clip(grads, 0.0, py::none(), false); }
+
+// ---- AdamW
+py::object adamw_step(const py::object& grads_, const py::object& params_, const py::object& m_,
+                      const py::object& v_, const py::object& masters_, const py::object& step_,
+                      const py::object& lr, double beta1, double beta2, double eps,
+                      double weight_decay, const py::object& max_norm) {
+  const List grads(grads_, "grads"), params(params_, "params"), m(m_, "exp_avgs"),
+      v(v_, "exp_avg_sqs");
+  const bool has_masters = !masters_.is_none();
+  const List masters(has_masters ? masters_ : params_, "masters");
+  if (grads.size != params.size)
+    throw py::value_error("grads must have as many entries as params");
+  if (m.size != params.size || v.size != params.size || masters.size != params.size)
+    throw py::value_error("exp_avgs, exp_avg_sqs and masters must have as many tensors as params");
+  if (params.size == 0) throw py::value_error("params must hold at least one tensor");
+  const c10::Device dev = params[0].device();
+  std::vector<ssim_adamw_item> items;
+  items.reserve(params.size);
+  for (Py_ssize_t k = 0; k < params.size; ++k) {
+    if (grads.none(k)) continue;
+    const Tensor &g = grads[k], &p = params[k], &mk = m[k], &vk = v[k];
+    ssim_adamw_item it;
+    it.grad_dtype = check(g, "grads", k);
+    it.param_dtype = check(p, "params", k);
+    const int cm = check(mk, "exp_avgs", k), cv = check(vk, "exp_avg_sqs", k);
+    if (it.grad_dtype != it.param_dtype && it.grad_dtype != SSIM_DTYPE_F32)
+      throw py::type_error(at_index("grads", k) + " must be float32 or have its parameter's dtype");
+    if (cm != SSIM_DTYPE_F32 || cv != SSIM_DTYPE_F32)
+      throw py::type_error(at_index("exp_avgs and exp_avg_sqs", k) + " must be float32");
+    it.n = p.numel();
+    if (g.sizes() != p.sizes() || mk.numel() != it.n || vk.numel() != it.n)
+      throw py::value_error(at_index("grads, exp_avgs and exp_avg_sqs", k) +
+                            " must have their parameter's shape");
+    check_device(g, dev, "grads", k);
+    check_device(p, dev, "params", k);
+    check_device(mk, dev, "exp_avgs", k);
+    check_device(vk, dev, "exp_avg_sqs", k);
+    it.grad = g.const_data_ptr();
+    it.param = p.data_ptr();
+    it.exp_avg = (float*)mk.data_ptr();
+    it.exp_avg_sq = (float*)vk.data_ptr();
+    it.master = nullptr;
+    if (has_masters && !masters.none(k)) {
+      const Tensor& w = masters[k];
+      if (check(w, "masters", k) != SSIM_DTYPE_F32)
+        throw py::type_error(at_index("masters", k) + " must be float32");
+      if (w.numel() != it.n)
+        throw py::value_error(at_index("masters", k) + " must have its parameter's shape");
+      check_device(w, dev, "masters", k);
+      it.master = (float*)w.data_ptr();
+    }
+    items.push_back(it);
+  }
+  const Tensor& step = unpack(step_.ptr(), "step");
+  if (step.scalar_type() != at::kLong || step.numel() != 1)
+    throw py::type_error("step must be one int64");
+  check_device(step, dev, "step");
+  ssim_adamw_options o;
+  o.lr = 0.0;
+  o.lr_device = nullptr;
+  if (THPVariable_Check(lr.ptr())) {
+    const Tensor& t = THPVariable_Unpack(lr.ptr());
+    if (check(t, "lr") != SSIM_DTYPE_F32 || t.numel() != 1)
+      throw py::type_error("lr must be a number or one float32 on the parameters' device");
+    check_device(t, dev, "lr");
+    o.lr_device = t.const_data_ptr<float>();
+  } else {
+    o.lr = lr.cast<double>();
+  }
+  o.beta1 = beta1;
+  o.beta2 = beta2;
+  o.eps = eps;
+  o.weight_decay = weight_decay;
+  const bool clips = !max_norm.is_none();
+  o.max_norm = clips ? max_norm.cast<double>() : HUGE_VAL;
+  const c10::DeviceGuard guard(dev);
+  Tensor norm;
+  if (clips) norm = at::empty({}, at::TensorOptions().dtype(at::kFloat).device(dev));
+  const Tensor ws = scratch(ssim_update_workspace_bytes(), dev);
+  const int rc =
+      ssim_adamw_step(items.data(), (int64_t)items.size(), &o, step.data_ptr<int64_t>(),
+                      clips ? norm.data_ptr<float>() : nullptr, ws.data_ptr(), stream_of(dev));
+  if (rc != SSIM_OK) raise(rc, "ssim_adamw_step");
+  for (Py_ssize_t k = 0; k < params.size; ++k) {
+    if (grads.none(k)) continue;
+    written(params[k]);
+    written(m[k]);
+    written(v[k]);
+    if (has_masters && !masters.none(k)) written(masters[k]);
+  }
+  written(step);
+  if (!clips) return py::none();
+  return py::cast(norm);
+}
+
+// ---- the joint between two blocks
+ssim_block_norm_inputs inputs_of(const Tensor& x, const Tensor& branch, const Tensor& gate,
+                                 const Tensor& scale, const Tensor& post, const Tensor& pre,
+                                 double eps, int act) {
+  ssim_block_norm_inputs in;
+  auto weight = [](const Tensor& t) { return t.defined() ? t.const_data_ptr<float>() : nullptr; };
+  in.x = x.const_data_ptr();
+  in.branch = branch.const_data_ptr();
+  in.gate = gate.defined() ? gate.const_data_ptr() : nullptr;
+  in.scale = weight(scale);
+  in.post_weight = weight(post);
+  in.pre_weight = weight(pre);
+  in.width = x.size(-1);
+  in.rows = x.numel() / in.width;
+  const int64_t gates = gate.defined() ? gate.numel() / in.width : 0;
+  in.gate_rows = gates > 0 && in.rows > 0 ? in.rows / gates : 1;
+  in.eps = eps;
+  in.x_dtype = dtype_code(x);
+  in.branch_dtype = dtype_code(branch);
+  in.gate_act = act;
+  in.reserved = 0;
+  return in;
+}
+
+void forward_into(const ssim_block_norm_inputs& in, const Tensor& residual, const Tensor& normed,
+                  float* stats, const c10::Device& dev) {
+  const int rc = ssim_block_norm_forward(&in, residual.data_ptr(), normed.data_ptr(), stats,
+                                         stream_of(dev));
+  TORCH_CHECK(rc == SSIM_OK, "ssim_block_norm_forward: ", text(rc));
+}
+
+struct BlockNorm : torch::autograd::Function<BlockNorm> {
+  static torch::autograd::variable_list forward(torch::autograd::AutogradContext* ctx,
+                                                const Tensor& x, const Tensor& branch,
+                                                const std::optional<Tensor>& gate_,
+                                                const std::optional<Tensor>& scale_,
+                                                const std::optional<Tensor>& post_,
+                                                const std::optional<Tensor>& pre_, double eps,
+                                                int64_t act, int64_t wants) {
+    const Tensor gate = gate_.value_or(Tensor()), scale = scale_.value_or(Tensor()),
+                 post = post_.value_or(Tensor()), pre = pre_.value_or(Tensor());
+    const c10::Device dev = x.device();
+    const c10::DeviceGuard guard(dev);
+    const ssim_block_norm_inputs in = inputs_of(x, branch, gate, scale, post, pre, eps, (int)act);
+    Tensor residual = at::empty(x.sizes(), x.options());
+    Tensor normed = at::empty(branch.sizes(), branch.options());
+    Tensor stats = at::empty({in.rows, 2}, x.options().dtype(at::kFloat));
+    forward_into(in, residual, normed, stats.data_ptr<float>(), dev);
+    ctx->save_for_backward({x, branch, gate, scale, post, pre, stats});
+    ctx->saved_data["eps"] = eps;
+    ctx->saved_data["act"] = act;
+    ctx->saved_data["wants"] = wants;
+    ctx->set_materialize_grads(false);
+    return {residual, normed};
+  }
+
+  static torch::autograd::variable_list backward(torch::autograd::AutogradContext* ctx,
+                                                 torch::autograd::variable_list upstream) {
+    TORCH_CHECK(!at::GradMode::is_enabled(),
+                "block_norm: the gradient of the gradient is not available (create_graph=True)");
+    const auto saved = ctx->get_saved_variables();
+    const Tensor &x = saved[0], &branch = saved[1], &stats = saved[6];
+    const c10::Device dev = x.device();
+    const c10::DeviceGuard guard(dev);
+    const ssim_block_norm_inputs in =
+        inputs_of(x, branch, saved[2], saved[3], saved[4], saved[5],
+                  ctx->saved_data["eps"].toDouble(), (int)ctx->saved_data["act"].toInt());
+    torch::autograd::variable_list out(9);
+    const int64_t wants = ctx->saved_data["wants"].toInt();
+    auto wanted = [&](int k) -> void* {
+      if (!(wants >> k & 1)) return nullptr;
+      out[k] = in.rows > 0 ? at::empty(saved[k].sizes(), saved[k].options())
+                           : at::zeros(saved[k].sizes(), saved[k].options());
+      return out[k].data_ptr();
+    };
+    ssim_block_norm_grads grads;
+    grads.x = wanted(0);
+    grads.branch = wanted(1);
+    grads.gate = wanted(2);
+    grads.scale = (float*)wanted(3);
+    grads.post_weight = (float*)wanted(4);
+    grads.pre_weight = (float*)wanted(5);
+    if (in.rows == 0) return out;
+    Tensor dr = upstream[0], dh = upstream[1];
+    if (dr.defined()) dr = dr.contiguous();
+    if (dh.defined()) dh = dh.contiguous();
+    const Tensor ws = scratch(ssim_block_norm_workspace_bytes(&in), dev);
+    const int rc = ssim_block_norm_backward(
+        &in, stats.const_data_ptr<float>(), dr.defined() ? dr.const_data_ptr() : nullptr,
+        dh.defined() ? dh.const_data_ptr() : nullptr, &grads, ws.data_ptr(), stream_of(dev));
+    TORCH_CHECK(rc == SSIM_OK, "ssim_block_norm_backward: ", text(rc));
+    return out;
+  }
+};
+
+Tensor optional(const py::object& o, const char* name) {
+  if (o.is_none()) return Tensor();
+  return unpack(o.ptr(), name);
+}
+
+py::tuple block_norm(const py::object& x_, const py::object& branch_, const py::object& gate_,
+                     const py::object& scale_, const py::object& post_, const py::object& pre_,
+                     double eps, int act) {
+  const Tensor x = unpack(x_.ptr(), "x"), branch = unpack(branch_.ptr(), "branch"),
+               gate = optional(gate_, "gate"), scale = optional(scale_, "scale"),
+               post = optional(post_, "post_weight"), pre = optional(pre_, "pre_weight");
+  const int cx = check(x, "x"), cb = check(branch, "branch");
+  const c10::Device dev = x.device();
+  check_device(branch, dev, "branch");
+  if (x.dim() < 1) throw py::value_error("x must have at least one dimension");
+  if (x.sizes() != branch.sizes()) throw py::value_error("x and branch must have the same shape");
+  if (cx != cb && cx != SSIM_DTYPE_F32)
+    throw py::type_error("x must be float32 or have branch's dtype");
+  const int64_t width = x.size(-1);
+  if (width < 1 || width > SSIM_BLOCK_NORM_MAX_WIDTH)
+    throw py::value_error("the last dimension must have 1 to " +
+                          std::to_string(SSIM_BLOCK_NORM_MAX_WIDTH) + " elements, got " +
+                          std::to_string(width));
+  if (!(eps >= 0.0 && eps <= 1.7976931348623157e308))
+    throw py::value_error("eps must be a number >= 0");
+  int64_t wants = 0;  // a bit for each tensor whose gradient is wanted
+  auto want = [&](const Tensor& t, int k) { wants |= (int64_t)t.requires_grad() << k; };
+  want(x, 0);
+  want(branch, 1);
+  if (gate.defined()) {
+    if (check(gate, "gate") != cb) throw py::type_error("gate must have branch's dtype");
+    check_device(gate, dev, "gate");
+    // x's shape, or ones in the place of its last few leading dimensions
+    bool ok = gate.dim() == x.dim() && gate.size(-1) == width, ones = false;
+    for (int64_t k = 0; ok && k + 1 < x.dim(); ++k) {
+      if (gate.size(k) == x.size(k) && !(ones && x.size(k) != 1)) continue;
+      ok = gate.size(k) == 1;
+      ones = true;
+    }
+    if (!ok)
+      throw py::value_error(
+          "gate must have x's shape, or x's shape with ones in the place of the last few "
+          "dimensions before the width");
+    want(gate, 2);
+  }
+  const struct {
+    const Tensor& t;
+    const char* name;
+  } weights[] = {{scale, "scale"}, {post, "post_weight"}, {pre, "pre_weight"}};
+  int k = 2;
+  for (const auto& w : weights) {
+    ++k;
+    if (!w.t.defined()) continue;
+    if (check(w.t, w.name) != SSIM_DTYPE_F32)
+      throw py::type_error(std::string(w.name) + " must be float32");
+    check_device(w.t, dev, w.name);
+    if (w.t.dim() != 1 || w.t.size(0) != width)
+      throw py::value_error(std::string(w.name) + " must have one value for each of the width");
+    want(w.t, k);
+  }
+  if (wants && at::GradMode::is_enabled()) {
+    auto given = [](const Tensor& t) {
+      return t.defined() ? std::optional<Tensor>(t) : std::optional<Tensor>();
+    };
+    const auto out = BlockNorm::apply(x, branch, given(gate), given(scale), given(post), given(pre),
+                                      eps, (int64_t)act, wants);
+    return py::make_tuple(out[0], out[1]);
+  }
+  const c10::DeviceGuard guard(dev);
+  const ssim_block_norm_inputs in = inputs_of(x, branch, gate, scale, post, pre, eps, act);
+  Tensor residual = at::empty(x.sizes(), x.options());
+  Tensor normed = at::empty(branch.sizes(), branch.options());
+  forward_into(in, residual, normed, nullptr, dev);
+  return py::make_tuple(residual, normed);
+}
+
+}  // namespace
+
+PYBIND11_MODULE(_bind, m) {
+  if (ssim_train_abi_version() != SSIM_TRAIN_ABI_VERSION)
+    throw py::import_error("the training library implements ABI version " +
+                           std::to_string(ssim_train_abi_version()) + ", its binding version " +
+                           std::to_string(SSIM_TRAIN_ABI_VERSION) + ": rebuild it");
+  m.def("clip_grads", &clip_grads);
+  m.def("grad_norm", &grad_norm);
+  m.def("adamw_step", &adamw_step);
+  m.def("block_norm", &block_norm);
+  m.def("abi_version", &ssim_train_abi_version);
+  m.def("strerror", &ssim_train_strerror);
+}

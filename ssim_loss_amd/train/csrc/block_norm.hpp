@@ -1,0 +1,562 @@
+// block_norm.hpp -- kernels of the joint between two blocks of a network:
+//   bh = b / sqrt(mean(b^2) + eps)          the norm after a block
+//   r  = x + a c bh                         a = act(gate), c = scale post_weight
+//   h  = r / sqrt(mean(r^2) + eps) pre      the norm before the next block
+// and their gradients.
+//
+// A row stays in registers between its reductions, so each tensor is read and
+// written once; the bound is that traffic.  A row belongs to one wave (narrow
+// rows: the reductions need no barrier) or to one workgroup.  A thread takes
+// I vectors of 16 bytes of the block's type, those of its neighbours beside
+// it; rows start at any element, so odd widths are loaded at full width too
+// and only the row's last vector is taken element by element.  The weights of
+// a thread's columns stay in registers over all rows of the workgroup.
+
+#pragma once
+
+#include "train_common.hpp"
+
+namespace ssim_train {
+
+constexpr int kMaxWaves = 8;    // of a workgroup
+constexpr int kRowWaves = 4;    // rows (waves) of a workgroup where a wave takes a row
+constexpr int kSumColumns = 64; // columns a workgroup of the last sum takes
+constexpr int kSumSlices = 16;  // ... and shares of the partial sums it adds at once
+
+struct NormParams {
+  const void* x;
+  const void* b;
+  const void* gate;
+  const float* scale;
+  const float* post;
+  const float* pre;
+  int64_t rows, gate_rows;
+  int width, act;
+  float eps, inv_width;
+  // forward
+  void* r;
+  void* h;
+  // stats: [rows][2], 1/sqrt(mean(b^2) + eps) and 1/sqrt(mean(r^2) + eps)
+  float* stats;
+  // backward
+  const void* dr;
+  const void* dh;
+  void* dx;
+  void* db;
+  void* dg;
+  float* dscale;
+  float* dpost;
+  float* dpre;
+  // sums over a workgroup's rows, [blocks][width] each: of a e bh, of dh rh,
+  // and, with gate rows shared and cut into parts, of e bh
+  float* part_total;
+  float* part_pre;
+  float* part_gate;
+  int blocks;
+  // gate rows shared: groups of gate_rows rows, each cut into `parts` parts of
+  // part_rows rows
+  int64_t groups, part_rows;
+  int parts;
+};
+
+template <class TX, class TB, int I>
+struct Row {
+  static constexpr int V = 16 / sizeof(TB);
+  static constexpr int E = V * I;
+};
+
+// one vector of a row, as stored; zeros past the row's end
+template <class T, int V>
+__device__ __forceinline__ Vec<T, V> load_cols(const T* row, int col, int width) {
+  if (col + V <= width) return load<T, V>(row + col);
+  Vec<T, V> v = {};
+#pragma unroll
+  for (int k = 0; k < V; ++k)
+    if (col + k < width) v[k] = row[col + k];
+  return v;
+}
+template <class T, int V>
+__device__ __forceinline__ void store_cols(T* row, int col, int width, Wide<V> w) {
+  const Vec<T, V> v = narrow<T, V>(w);
+  if (col + V <= width) {
+    store<T, V>(row + col, v);
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < V; ++k)
+    if (col + k < width) row[col + k] = v[k];
+}
+// a weight's columns; 1 where there is none
+template <int V>
+__device__ __forceinline__ Wide<V> load_weight(const float* w, int col, int width) {
+  if (w) return load_cols<float, V>(w, col, width);
+  Wide<V> one;
+#pragma unroll
+  for (int k = 0; k < V; ++k) one[k] = 1.0f;
+  return one;
+}
+
+// act(g).  fp32 tensors take the exact exponential; for half types the fast
+// one (an error of a few 2^-24 of its argument) is far below their rounding.
+template <class TB>
+__device__ __forceinline__ float activate(float g, int act) {
+  if (act != SSIM_GATE_SIGMOID) return g;
+  if constexpr (sizeof(TB) == 4) return 1.0f / (1.0f + expf(-g));
+  else return __frcp_rn(1.0f + __expf(-g));
+}
+
+// N sums over a row's threads at once.  kRowWave: the row is one wave's;
+// otherwise the workgroup's, with lds[N][kMaxWaves], whose entries past the
+// workgroup's waves are zero.  Two calls that follow each other take different
+// lds arrays: then the barrier within one separates the other's uses.
+template <bool kRowWave, int N>
+__device__ __forceinline__ void row_sums(float (&s)[N], float (*lds)[kMaxWaves]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) s[k] = wave_sum(s[k]);
+  if constexpr (!kRowWave) {
+    if ((threadIdx.x & (kWave - 1)) == 0) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) lds[k][threadIdx.x / kWave] = s[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      float t = 0;
+#pragma unroll
+      for (int w = 0; w < kMaxWaves; ++w) t += lds[k][w];
+      s[k] = t;
+    }
+  }
+}
+
+template <class TX, class TB, int I, bool kRowWave>
+__device__ __forceinline__ void norm_forward(const NormParams& p) {
+  constexpr int V = Row<TX, TB, I>::V;
+  __shared__ float lds[2][1][kMaxWaves];
+  if constexpr (!kRowWave) {
+    if (threadIdx.x < 2 * kMaxWaves) (&lds[0][0][0])[threadIdx.x] = 0;
+    __syncthreads();
+  }
+  const int width = p.width;
+  const int threads = kRowWave ? kWave : (int)blockDim.x;
+  const int q = kRowWave ? (int)threadIdx.x & (kWave - 1) : (int)threadIdx.x;
+  int64_t row = blockIdx.x, stride = gridDim.x;
+  if constexpr (kRowWave) {
+    row = row * kRowWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    stride *= kRowWaves;
+  }
+  Wide<V> c[I], pre[I];
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    const int col = (i * threads + q) * V;
+    c[i] = load_weight<V>(p.scale, col, width) * load_weight<V>(p.post, col, width);
+    pre[i] = load_weight<V>(p.pre, col, width);
+  }
+  for (; row < p.rows; row += stride) {
+    const TX* x = (const TX*)p.x + row * width;
+    const TB* b = (const TB*)p.b + row * width;
+    const int64_t gate_row = p.gate_rows == 1 ? row : row / p.gate_rows;
+    const TB* g = (const TB*)p.gate + (p.gate ? gate_row * width : 0);
+    Vec<TX, V> xr[I];
+    Vec<TB, V> br[I], gr[I];
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int col = (i * threads + q) * V;
+      br[i] = load_cols<TB, V>(b, col, width);
+      xr[i] = load_cols<TX, V>(x, col, width);
+      if (p.gate) gr[i] = load_cols<TB, V>(g, col, width);
+    }
+    float s[1] = {0};
+    Wide<V> v[I];
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      v[i] = widen<TB, V>(br[i]);
+#pragma unroll
+      for (int k = 0; k < V; ++k) s[0] = fmaf(v[i][k], v[i][k], s[0]);
+    }
+    row_sums<kRowWave, 1>(s, lds[0]);
+    const float ib = 1.0f / sqrtf(fmaf(s[0], p.inv_width, p.eps));
+    s[0] = 0;
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const Wide<V> xw = widen<TX, V>(xr[i]);
+      Wide<V> gw = {};
+      if (p.gate) gw = widen<TB, V>(gr[i]);
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        float ac = c[i][k];
+        if (p.gate) ac *= activate<TB>(gw[k], p.act);
+        const float r = fmaf(ac, v[i][k] * ib, xw[k]);
+        v[i][k] = r;
+        s[0] = fmaf(r, r, s[0]);
+      }
+    }
+    // (columns past the row's end hold zeros, so they add nothing)
+    row_sums<kRowWave, 1>(s, lds[1]);
+    const float ir = 1.0f / sqrtf(fmaf(s[0], p.inv_width, p.eps));
+    TX* r = (TX*)p.r + row * width;
+    TB* h = (TB*)p.h + row * width;
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int col = (i * threads + q) * V;
+      if (col >= width) continue;
+      store_cols<TX, V>(r, col, width, v[i]);
+      store_cols<TB, V>(h, col, width, v[i] * ir * pre[i]);
+    }
+    if (p.stats && q == 0) {
+      p.stats[2 * row] = ib;
+      p.stats[2 * row + 1] = ir;
+    }
+  }
+}
+
+// what the backward loads of one vector of a row
+template <class TX, class TB, int V>
+struct Raw {
+  Vec<TX, V> x, dr;
+  Vec<TB, V> b, dh, gate;
+};
+template <class TX, class TB, int V, bool kGrouped>
+__device__ __forceinline__ Raw<TX, TB, V> load_raw(const NormParams& p, int64_t at, int col) {
+  Raw<TX, TB, V> f;
+  f.b = load_cols<TB, V>((const TB*)p.b + at, col, p.width);
+  f.x = load_cols<TX, V>((const TX*)p.x + at, col, p.width);
+  f.gate = 0;
+  f.dr = 0;
+  f.dh = 0;
+  if (!kGrouped && p.gate) f.gate = load_cols<TB, V>((const TB*)p.gate + at, col, p.width);
+  if (p.dr) f.dr = load_cols<TX, V>((const TX*)p.dr + at, col, p.width);
+  if (p.dh) f.dh = load_cols<TB, V>((const TB*)p.dh + at, col, p.width);
+  return f;
+}
+// and forms of it (names as below)
+template <int V>
+struct Terms {
+  Wide<V> bh, rh, u, a;
+};
+template <class TX, class TB, int V, bool kGrouped>
+__device__ __forceinline__ Terms<V> form_terms(const NormParams& p, const Raw<TX, TB, V>& raw,
+                                               Wide<V> dw, float ib, float ir, Wide<V> c,
+                                               Wide<V> pre, Wide<V> group_a) {
+  Terms<V> f;
+  if constexpr (kGrouped) {
+    f.a = group_a;
+  } else if (p.gate) {
+    const Wide<V> g = widen<TB, V>(raw.gate);
+#pragma unroll
+    for (int k = 0; k < V; ++k) f.a[k] = activate<TB>(g[k], p.act);
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k) f.a[k] = 1.0f;
+  }
+  f.bh = widen<TB, V>(raw.b) * ib;
+  const Wide<V> x = widen<TX, V>(raw.x), dr = widen<TX, V>(raw.dr);
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    f.rh[k] = fmaf(f.a[k] * c[k], f.bh[k], x[k]) * ir;
+    f.u[k] = fmaf(ir, dw[k] * pre[k], dr[k]);
+  }
+  return f;
+}
+
+// The gradients.  With wd = dh pre, rh = r ir, u = dr + ir wd:
+//   e  = u - ir rh mean(wd rh)              the gradient of x
+//   t  = e a c,  db = ib (t - bh mean(t bh))
+//   dg = e c bh act'(g)
+//   dscale = post sum_rows(a e bh), dpost = scale (the same sum), dpre = sum_rows(dh rh)
+// mean(t bh) = mean(u ac bh) - ir mean(wd rh) mean(rh ac bh): with the two
+// reciprocal roots kept by the forward, one reduction of three sums serves
+// both norms.  r is formed again from x, so that its rounding to x's type does
+// not enter.
+// kGrouped: one gate row for many rows.  Then only S = sum of e bh is summed
+// over a group's rows, and dg = c act'(g) S, sum of a e bh = a S.
+template <class TX, class TB, int I, bool kRowWave, bool kGrouped>
+__device__ __forceinline__ void norm_backward(const NormParams& p) {
+  constexpr int V = Row<TX, TB, I>::V;
+  // a thread of a very wide row cannot hold it: its vectors are loaded again,
+  // from the caches, after the reduction
+  constexpr bool kReload = Row<TX, TB, I>::E > 16;
+  __shared__ float lds[2][3][kMaxWaves];
+  if constexpr (!kRowWave) {
+    for (int k = threadIdx.x; k < 6 * kMaxWaves; k += blockDim.x) (&lds[0][0][0])[k] = 0;
+    __syncthreads();
+  }
+  const int width = p.width;
+  const int threads = kRowWave ? kWave : (int)blockDim.x;
+  const int q = kRowWave ? (int)threadIdx.x & (kWave - 1) : (int)threadIdx.x;
+  const int wave = kRowWave ? __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) : 0;
+  constexpr int kWorkers = kRowWave ? kRowWaves : 1;
+
+  constexpr int kHeld = kReload ? 1 : I;  // vectors of the weights and of a row that stay
+  Wide<V> c[kHeld], pre[kHeld], total[I], dpre[I], S[kGrouped ? I : 1], a[kGrouped ? I : 1];
+  auto load_weights = [&](int i) {
+    const int col = (i * threads + q) * V, to = kReload ? 0 : i;
+    c[to] = load_weight<V>(p.scale, col, width) * load_weight<V>(p.post, col, width);
+    pre[to] = load_weight<V>(p.pre, col, width);
+  };
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    if constexpr (!kReload) load_weights(i);
+    total[i] = 0;
+    dpre[i] = 0;
+  }
+
+  // the segments of rows this worker takes: all rows, dealt out one by one;
+  // or groups, or parts of a group
+  int64_t seg = 0, segs = 1, seg_stride = 1;
+  int parity = 0;  // of the reductions' lds arrays, over all rows
+  if constexpr (kGrouped) {
+    segs = p.groups * p.parts;
+    seg = blockIdx.x;
+    seg_stride = gridDim.x;
+    if (p.parts == 1) {
+      seg = seg * kWorkers + wave;
+      seg_stride *= kWorkers;
+    }
+  }
+  for (; seg < segs; seg += seg_stride) {
+    int64_t row, end, stride, group = 0;
+    if constexpr (kGrouped) {
+      group = seg / p.parts;
+      const int64_t part = seg - group * p.parts;
+      row = group * p.gate_rows + part * p.part_rows;
+      end = row + p.part_rows;
+      if (end > (group + 1) * p.gate_rows) end = (group + 1) * p.gate_rows;
+      stride = 1;
+      if (p.parts > 1) {
+        row += wave;
+        stride = kWorkers;
+      }
+      const TB* g = (const TB*)p.gate + group * width;
+#pragma unroll
+      for (int i = 0; i < I; ++i) {
+        const int col = (i * threads + q) * V;
+        const Wide<V> gw = widen<TB, V>(load_cols<TB, V>(g, col, width));
+#pragma unroll
+        for (int k = 0; k < V; ++k) a[i][k] = activate<TB>(gw[k], p.act);
+        S[i] = 0;
+      }
+    } else {
+      row = (int64_t)blockIdx.x * kWorkers + wave;
+      stride = (int64_t)gridDim.x * kWorkers;
+      end = p.rows;
+    }
+    for (; row < end; row += stride, parity ^= 1) {
+      const int64_t at = row * width;
+      Raw<TX, TB, V> raw[kHeld];
+      if constexpr (!kReload) {
+#pragma unroll
+        for (int i = 0; i < I; ++i)
+          raw[i] = load_raw<TX, TB, V, kGrouped>(p, at, (i * threads + q) * V);
+      }
+      const float ib = p.stats[2 * row], ir = p.stats[2 * row + 1];
+      float s[3] = {0, 0, 0};
+      Terms<V> terms[kHeld];
+#pragma unroll
+      for (int i = 0; i < I; ++i) {
+        const int j = kReload ? 0 : i;
+        if constexpr (kReload) {
+          load_weights(i);
+          raw[j] = load_raw<TX, TB, V, kGrouped>(p, at, (i * threads + q) * V);
+        }
+        const Wide<V> dw = widen<TB, V>(raw[j].dh);
+        const Terms<V> f = form_terms<TX, TB, V, kGrouped>(p, raw[j], dw, ib, ir, c[j], pre[j],
+                                                           a[kGrouped ? i : 0]);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          const float acbh = f.a[k] * c[j][k] * f.bh[k];
+          s[0] = fmaf(dw[k] * pre[j][k], f.rh[k], s[0]);
+          s[1] = fmaf(f.u[k], acbh, s[1]);
+          s[2] = fmaf(f.rh[k], acbh, s[2]);
+          dpre[i][k] = fmaf(dw[k], f.rh[k], dpre[i][k]);
+        }
+        terms[j] = f;
+      }
+      row_sums<kRowWave, 3>(s, lds[parity]);
+      const float m1 = ir * (s[0] * p.inv_width);
+      const float m2 = s[1] * p.inv_width - m1 * (s[2] * p.inv_width);
+      TX* dx = (TX*)p.dx + (p.dx ? at : 0);
+      TB* db = (TB*)p.db + (p.db ? at : 0);
+      TB* dg = (TB*)p.dg + (p.dg ? at : 0);
+#pragma unroll
+      for (int i = 0; i < I; ++i) {
+        const int col = (i * threads + q) * V, j = kReload ? 0 : i;
+        if constexpr (kReload) {
+          load_weights(i);
+          raw[j] = load_raw<TX, TB, V, kGrouped>(p, at, col);
+          terms[j] = form_terms<TX, TB, V, kGrouped>(p, raw[j], widen<TB, V>(raw[j].dh), ib, ir,
+                                                     c[j], pre[j], a[kGrouped ? i : 0]);
+        }
+        const Terms<V>& f = terms[j];
+        const Wide<V> e = f.u - f.rh * m1, eb = e * f.bh;
+        if constexpr (kGrouped) S[i] += eb;
+        else total[i] += eb * f.a;
+        if (col >= width) continue;
+        if (p.dx) store_cols<TX, V>(dx, col, width, e);
+        if (p.db) store_cols<TB, V>(db, col, width, (e * (f.a * c[j]) - f.bh * m2) * ib);
+        if constexpr (!kGrouped) {
+          if (p.dg) {
+            Wide<V> d = eb * c[j];
+            if (p.act == SSIM_GATE_SIGMOID) d *= f.a * (1.0f - f.a);
+            store_cols<TB, V>(dg, col, width, d);
+          }
+        }
+      }
+    }
+    if constexpr (kGrouped) {
+      TB* dg = (TB*)p.dg + (p.dg ? group * width : 0);
+#pragma unroll
+      for (int i = 0; i < I; ++i) {
+        const int col = (i * threads + q) * V, j = kReload ? 0 : i;
+        total[i] += S[i] * a[i];
+        if (p.parts == 1 && p.dg && col < width) {
+          if constexpr (kReload) load_weights(i);
+          Wide<V> d = S[i] * c[j];
+          if (p.act == SSIM_GATE_SIGMOID) d *= a[i] * (1.0f - a[i]);
+          store_cols<TB, V>(dg, col, width, d);
+        }
+      }
+    }
+  }
+
+  // the workgroup's sums
+  float* out[3] = {p.part_total, p.part_pre, kGrouped && p.parts > 1 ? p.part_gate : nullptr};
+#pragma unroll
+  for (int k = 0; k < (kGrouped ? 3 : 2); ++k) {
+    if (!out[k]) continue;
+    float* to = out[k] + (int64_t)blockIdx.x * width;
+    if constexpr (kRowWave) {
+      __shared__ float waves[kRowWaves][kWave * V * I];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < I; ++i) {
+        Wide<V> v;
+        if constexpr (kGrouped) v = k == 0 ? total[i] : k == 1 ? dpre[i] : S[i];
+        else v = k == 0 ? total[i] : dpre[i];
+#pragma unroll
+        for (int e = 0; e < V; ++e) waves[wave][(i * kWave + q) * V + e] = v[e];
+      }
+      __syncthreads();
+      for (int col = threadIdx.x; col < width; col += kRowWaves * kWave) {
+        float v = 0;
+#pragma unroll
+        for (int w = 0; w < kRowWaves; ++w) v += waves[w][col];
+        to[col] = v;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < I; ++i) {
+        const int col = (i * threads + q) * V;
+        Wide<V> v;
+        if constexpr (kGrouped) v = k == 0 ? total[i] : k == 1 ? dpre[i] : S[i];
+        else v = k == 0 ? total[i] : dpre[i];
+        if (col < width) store_cols<float, V>(to, col, width, v);
+      }
+    }
+  }
+}
+
+// The last sums, in fp64 over the workgroups' partial sums.  blockIdx.y: 0 the
+// scale's and the post weight's gradients, 1 the pre weight's, 2 + g the
+// gradient of gate row g (where its rows were cut into parts).
+template <class TB>
+__device__ __forceinline__ void norm_sums(const NormParams& p) {
+  __shared__ double lds[kSumSlices][kSumColumns];
+  const int lane = threadIdx.x % kSumColumns, slice = threadIdx.x / kSumColumns;
+  const int col = blockIdx.x * kSumColumns + lane;
+  const int job = blockIdx.y;
+  const float* from = job == 0 ? p.part_total : job == 1 ? p.part_pre : p.part_gate;
+  int64_t n = p.blocks;
+  if (job >= 2) {
+    n = p.parts;
+    from += (int64_t)(job - 2) * p.parts * p.width;
+  }
+  if ((job == 0 && !p.dscale && !p.dpost) || (job == 1 && !p.dpre)) return;
+  double s = 0;
+  if (col < p.width) {
+#pragma unroll 8
+    for (int64_t k = slice; k < n; k += kSumSlices) s += (double)from[k * p.width + col];
+  }
+  lds[slice][lane] = s;
+  __syncthreads();
+  if (slice != 0 || col >= p.width) return;
+  s = 0;
+#pragma unroll
+  for (int k = 0; k < kSumSlices; ++k) s += lds[k][lane];
+  if (job == 0) {
+    if (p.dscale) p.dscale[col] = (float)(s * (p.post ? (double)p.post[col] : 1.0));
+    if (p.dpost) p.dpost[col] = (float)(s * (p.scale ? (double)p.scale[col] : 1.0));
+  } else if (job == 1) {
+    p.dpre[col] = (float)s;
+  } else {
+    const int64_t at = (int64_t)(job - 2) * p.width + col;
+    const float a = activate<TB>((float)((const TB*)p.gate)[at], p.act);
+    double d = s * (p.scale ? (double)p.scale[col] : 1.0) * (p.post ? (double)p.post[col] : 1.0);
+    if (p.act == SSIM_GATE_SIGMOID) d *= (double)a * (1.0 - (double)a);
+    ((TB*)p.dg)[at] = (TB)(float)d;
+  }
+}
+
+// ---- the kernels of one block type
+// how a row is spread: over a wave or a workgroup, vectors a thread, threads
+enum NormShape { kWave1, kWave2, kGroup1, kGroup2, kGroup4, kGroup8, kNormShapes };
+
+struct NormTable {
+  const void* forward[2][kNormShapes];      // [x is fp32 beside a half type]
+  const void* backward[2][kNormShapes][2];  // [.. ][gate rows shared]
+  const void* sums;
+};
+
+const NormTable& norm_table_f32();
+const NormTable& norm_table_f16();
+const NormTable& norm_table_bf16();
+
+constexpr int shape_items(int s) {
+  return s == kWave1 || s == kGroup1 ? 1 : s == kGroup4 ? 4 : s == kGroup8 ? 8 : 2;
+}
+constexpr bool shape_wave(int s) { return s == kWave1 || s == kWave2; }
+constexpr int shape_threads(int s) { return (shape_wave(s) ? kRowWaves : kMaxWaves) * kWave; }
+
+template <class TX, class TB, int kShape>
+__global__ __launch_bounds__(shape_threads(kShape)) void ssim_block_norm_fwd_kernel(
+    const NormParams p) {
+  norm_forward<TX, TB, shape_items(kShape), shape_wave(kShape)>(p);
+}
+template <class TX, class TB, int kShape, bool kGrouped>
+__global__ __launch_bounds__(shape_threads(kShape)) void ssim_block_norm_bwd_kernel(
+    const NormParams p) {
+  norm_backward<TX, TB, shape_items(kShape), shape_wave(kShape), kGrouped>(p);
+}
+template <class TB>
+__global__ __launch_bounds__(kSumColumns* kSumSlices) void ssim_block_norm_sums_kernel(
+    const NormParams p) {
+  norm_sums<TB>(p);
+}
+
+template <class TX, class TB, int kShape>
+void fill_shape(NormTable& t, int wide) {
+  if constexpr (!(sizeof(TB) == 2 && kShape == kGroup8)) {
+    t.forward[wide][kShape] = (const void*)ssim_block_norm_fwd_kernel<TX, TB, kShape>;
+    t.backward[wide][kShape][0] = (const void*)ssim_block_norm_bwd_kernel<TX, TB, kShape, false>;
+    t.backward[wide][kShape][1] = (const void*)ssim_block_norm_bwd_kernel<TX, TB, kShape, true>;
+  }
+}
+template <class TX, class TB>
+void fill_types(NormTable& t, int wide) {
+  fill_shape<TX, TB, kWave1>(t, wide);
+  fill_shape<TX, TB, kWave2>(t, wide);
+  fill_shape<TX, TB, kGroup1>(t, wide);
+  fill_shape<TX, TB, kGroup2>(t, wide);
+  fill_shape<TX, TB, kGroup4>(t, wide);
+  fill_shape<TX, TB, kGroup8>(t, wide);
+}
+template <class TB>
+NormTable make_table() {
+  NormTable t = {};
+  fill_types<TB, TB>(t, 0);
+  if constexpr (sizeof(TB) == 2) fill_types<F32, TB>(t, 1);
+  t.sums = (const void*)ssim_block_norm_sums_kernel<TB>;
+  return t;
+}
+
+}  // namespace ssim_train

@@ -1,0 +1,673 @@
+// update.hip -- the gradients of many tensors: their global norm, clipping by
+// it, and AdamW with the clipping fused in.
+//
+// Two launches.  The first sums squares, one fp64 partial sum for each
+// workgroup; every workgroup of the second adds up the partial sums (in one
+// order, so all get the same clipping factor, without an atomic or a value
+// that has to be cleared beforehand) and then scales or updates its share.
+//
+// The tensors reach a kernel as a table of runs in its arguments (no copy to
+// the device, so a call can be captured).  Items that follow each other in
+// memory in all their arrays are one run: a network whose parameters are
+// packed in a bucket is a single run.  A run is cut into chunks of equal
+// size; chunk numbers run through all runs.
+
+#include <math.h>
+
+#include <algorithm>
+#include <vector>
+
+#include "train_common.hpp"
+
+namespace {
+
+using namespace ssim_train;
+
+constexpr int kThreads = 256;
+constexpr int kMaxBlocks = 2048;  // 256 CUs, 8 workgroups of 4 waves each
+constexpr int kWaves = kThreads / kWave;
+
+// What the first launch leaves for the second.
+struct Scratch {
+  double partial[kMaxBlocks];
+  float step_size;  // lr / (1 - beta1^t)
+  float decay;      // 1 - lr weight_decay
+  float inv_bc2;    // 1 / (1 - beta2^t)
+};
+
+struct NormRun {
+  const void* grad;
+  int64_t n;
+  uint32_t first;  // its first chunk
+  int32_t dtype;
+};
+struct ClipRun {
+  const void* grad;
+  void* out;
+  int64_t n;
+  uint32_t first;
+  int32_t dtype;
+};
+struct AdamRun {
+  const void* grad;
+  void* param;
+  float* m;
+  float* v;
+  float* master;
+  int64_t n;
+  uint32_t first;
+  int16_t grad_dtype, param_dtype;
+};
+// tables sized so that a kernel's arguments stay below 4 KB
+constexpr int kNormRuns = 144, kClipRuns = 112, kAdamRuns = 64;
+
+// Advances the count of updates and forms the update's scalars, by one thread.
+struct StepArgs {
+  int64_t* step;  // NULL: no update follows
+  const float* lr_device;
+  double lr, beta1, beta2, weight_decay;
+};
+struct NormArgs {
+  NormRun run[kNormRuns];
+  int count;
+  uint32_t chunks;
+  int add;  // to the partial sums of the launches before
+  Scratch* scratch;
+  StepArgs step;
+};
+struct ClipArgs {
+  ClipRun run[kClipRuns];
+  int count;
+  uint32_t chunks;
+  int partials;
+  double max_norm;
+  float* norm;
+  const Scratch* scratch;
+};
+struct AdamArgs {
+  AdamRun run[kAdamRuns];
+  int count;
+  uint32_t chunks;
+  int partials;  // 0: no clipping
+  double max_norm;
+  float* norm;
+  const Scratch* scratch;
+  float beta1, one_minus_beta1, beta2, one_minus_beta2, eps;
+};
+static_assert(sizeof(NormArgs) <= 4096 && sizeof(ClipArgs) <= 4096 && sizeof(AdamArgs) <= 4096,
+              "kernel arguments");
+
+// the run that holds chunk c
+template <class Run>
+__device__ __forceinline__ int find_run(const Run* run, int count, uint32_t c) {
+  int lo = 0, hi = count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (run[mid].first <= c) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ double block_sum(double v, double* lds) {
+  v = wave_sum(v);
+  if ((threadIdx.x & (kWave - 1)) == 0) lds[threadIdx.x / kWave] = v;
+  __syncthreads();
+  double s = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) s += lds[w];
+  return s;
+}
+
+// ---- the sum of squares.  Reads each gradient once: bound by that read.
+// Squares are formed and added in fp64 (two instructions an element, hidden
+// behind the read), so no gradient's square over- or underflows.
+template <class T, int U>
+__device__ __forceinline__ double squares(const T* g, int64_t n) {
+  constexpr int V = 16 / sizeof(T), C = kThreads * V;
+  double acc[2] = {0, 0};
+  const int64_t at = threadIdx.x * V;
+  if (n >= (int64_t)C * U) {
+    Vec<T, V> x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] = load<T, V>(g + at + u * C);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const Wide<V> w = widen<T, V>(x[u]);
+#pragma unroll
+      for (int k = 0; k < V; ++k) acc[k & 1] = fma((double)w[k], (double)w[k], acc[k & 1]);
+    }
+  } else {
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = at + u * C;
+      for (int k = 0; k < V && i + k < n; ++k) {
+        const double w = (double)(float)g[i + k];
+        acc[0] = fma(w, w, acc[0]);
+      }
+    }
+  }
+  return acc[0] + acc[1];
+}
+
+template <int U>
+__global__ __launch_bounds__(kThreads) void ssim_grad_norm_kernel(const NormArgs a) {
+  __shared__ double lds[kWaves];
+  double acc = 0;
+  for (uint32_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
+    const int r = find_run(a.run, a.count, c);
+    const NormRun& run = a.run[r];
+    const int64_t chunk = (int64_t)(16 / (run.dtype == SSIM_DTYPE_F32 ? 4 : 2)) * kThreads * U;
+    const int64_t i = (int64_t)(c - run.first) * chunk;
+    switch (run.dtype) {
+      case SSIM_DTYPE_F32: acc += squares<F32, U>((const F32*)run.grad + i, run.n - i); break;
+      case SSIM_DTYPE_F16: acc += squares<F16, U>((const F16*)run.grad + i, run.n - i); break;
+      default: acc += squares<BF16, U>((const BF16*)run.grad + i, run.n - i); break;
+    }
+  }
+  acc = block_sum(acc, lds);
+  if (threadIdx.x == 0) {
+    double* p = a.scratch->partial + blockIdx.x;
+    *p = a.add ? *p + acc : acc;
+    if (blockIdx.x == 0 && a.step.step) {
+      const int64_t t = *a.step.step + 1;
+      *a.step.step = t;
+      const double lr = a.step.lr_device ? (double)*a.step.lr_device : a.step.lr;
+      a.scratch->step_size = (float)(lr / (1.0 - pow(a.step.beta1, (double)t)));
+      a.scratch->decay = (float)(1.0 - lr * a.step.weight_decay);
+      a.scratch->inv_bc2 = (float)(1.0 / (1.0 - pow(a.step.beta2, (double)t)));
+    }
+  }
+}
+
+// the norm, from all partial sums, and the clipping factor; every workgroup
+// computes the same
+__device__ __forceinline__ float clip_factor(const Scratch* s, int partials, double max_norm,
+                                             float* norm_out, double* lds) {
+  double v = 0;
+  for (int k = threadIdx.x; k < partials; k += kThreads) v += s->partial[k];
+  const double norm = sqrt(block_sum(v, lds));
+  if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
+  if (isinf(max_norm)) return 1.0f;
+  const double c = max_norm / (norm + 1e-6);
+  return c > 1.0 ? 1.0f : (float)c;  // (a NaN stays one)
+}
+
+__global__ __launch_bounds__(kThreads) void ssim_norm_only_kernel(const Scratch* s, int partials,
+                                                                  float* norm) {
+  __shared__ double lds[kWaves];
+  clip_factor(s, partials, 0.0, norm, lds);
+}
+
+// ---- clipping.  Reads each gradient again and writes it: bound by that.  The
+// chunks are taken from the last to the first, since the first launch read the
+// last ones last and the 256 MB last-level cache still holds them.
+template <class T, int U>
+__device__ __forceinline__ void scale(const T* g, T* out, int64_t n, float c) {
+  constexpr int V = 16 / sizeof(T), C = kThreads * V;
+  const int64_t at = threadIdx.x * V;
+  if (n >= (int64_t)C * U) {
+    Vec<T, V> x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] = load<T, V>(g + at + u * C);
+#pragma unroll
+    for (int u = 0; u < U; ++u) store<T, V>(out + at + u * C, narrow<T, V>(widen<T, V>(x[u]) * c));
+  } else {
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = at + u * C;
+      for (int k = 0; k < V && i + k < n; ++k) out[i + k] = (T)((float)g[i + k] * c);
+    }
+  }
+}
+
+template <int U>
+__global__ __launch_bounds__(kThreads) void ssim_clip_grads_kernel(const ClipArgs a) {
+  __shared__ double lds[kWaves];
+  const float f = clip_factor(a.scratch, a.partials, a.max_norm, a.norm, lds);
+  for (uint32_t k = blockIdx.x; k < a.chunks; k += gridDim.x) {
+    const uint32_t c = a.chunks - 1 - k;
+    const int r = find_run(a.run, a.count, c);
+    const ClipRun& run = a.run[r];
+    if (f == 1.0f && run.grad == run.out) continue;  // in place and not clipped
+    const int64_t chunk = (int64_t)(16 / (run.dtype == SSIM_DTYPE_F32 ? 4 : 2)) * kThreads * U;
+    const int64_t i = (int64_t)(c - run.first) * chunk;
+    switch (run.dtype) {
+      case SSIM_DTYPE_F32:
+        scale<F32, U>((const F32*)run.grad + i, (F32*)run.out + i, run.n - i, f);
+        break;
+      case SSIM_DTYPE_F16:
+        scale<F16, U>((const F16*)run.grad + i, (F16*)run.out + i, run.n - i, f);
+        break;
+      default:
+        scale<BF16, U>((const BF16*)run.grad + i, (BF16*)run.out + i, run.n - i, f);
+        break;
+    }
+  }
+}
+
+// ---- AdamW
+struct Coefs {
+  float clip, step_size, decay, inv_bc2, beta1, omb1, beta2, omb2, eps;
+};
+
+__device__ __forceinline__ void adam_one(const Coefs& k, float g, float& m, float& v, float& w) {
+  g *= k.clip;
+  m = fmaf(k.beta1, m, k.omb1 * g);
+  v = fmaf(k.beta2, v, k.omb2 * g * g);
+  w = w * k.decay - k.step_size * (m / (sqrtf(v * k.inv_bc2) + k.eps));
+}
+
+constexpr int kAdamV = 4;  // elements a thread takes at once: 16 bytes of each fp32 array
+
+// kMaster: the weights are in w and p receives a rounded copy; else they are in p
+template <class TG, class TP, bool kMaster, int U>
+__device__ __forceinline__ void adam_chunk(const Coefs& k, const AdamRun& run, int64_t i0) {
+  constexpr int V = kAdamV, C = kThreads * V;
+  const TG* g = (const TG*)run.grad + i0;
+  TP* p = (TP*)run.param + i0;
+  float* m = run.m + i0;
+  float* v = run.v + i0;
+  float* w = run.master + (kMaster ? i0 : 0);
+  const int64_t n = run.n - i0;
+  const int at = threadIdx.x * V;
+  if (n >= (int64_t)C * U) {
+    Vec<TG, V> xg[U];
+    Vec<TP, V> xp[U];
+    Wide<V> xm[U], xv[U], xw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      xg[u] = load<TG, V>(g + at + u * C);
+      xm[u] = load<float, V>(m + at + u * C);
+      xv[u] = load<float, V>(v + at + u * C);
+      if constexpr (kMaster) xw[u] = load<float, V>(w + at + u * C);
+      else xp[u] = load<TP, V>(p + at + u * C);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if constexpr (!kMaster) xw[u] = widen<TP, V>(xp[u]);
+      const Wide<V> gw = widen<TG, V>(xg[u]);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        float em = xm[u][e], ev = xv[u][e], ew = xw[u][e];
+        adam_one(k, gw[e], em, ev, ew);
+        xm[u][e] = em;
+        xv[u][e] = ev;
+        xw[u][e] = ew;
+      }
+      store<float, V>(m + at + u * C, xm[u]);
+      store<float, V>(v + at + u * C, xv[u]);
+      if constexpr (kMaster) store<float, V>(w + at + u * C, xw[u]);
+      store<TP, V>(p + at + u * C, narrow<TP, V>(xw[u]));
+    }
+  } else {
+    for (int u = 0; u < U; ++u)
+      for (int e = 0; e < V; ++e) {
+        const int64_t i = at + u * C + e;
+        if (i >= n) break;
+        float em = m[i], ev = v[i], ew;
+        if constexpr (kMaster) ew = w[i];
+        else ew = (float)p[i];
+        adam_one(k, (float)g[i], em, ev, ew);
+        m[i] = em;
+        v[i] = ev;
+        if constexpr (kMaster) w[i] = ew;
+        p[i] = (TP)ew;
+      }
+  }
+}
+
+template <class TG, class TP, int U>
+__device__ __forceinline__ void adam_run(const Coefs& k, const AdamRun& run, int64_t i0) {
+  if (run.master) adam_chunk<TG, TP, true, U>(k, run, i0);
+  else adam_chunk<TG, TP, false, U>(k, run, i0);
+}
+
+template <int U>
+__global__ __launch_bounds__(kThreads) void ssim_adamw_kernel(const AdamArgs a) {
+  __shared__ double lds[kWaves];
+  Coefs k;
+  k.clip = a.partials ? clip_factor(a.scratch, a.partials, a.max_norm, a.norm, lds) : 1.0f;
+  k.step_size = a.scratch->step_size;
+  k.decay = a.scratch->decay;
+  k.inv_bc2 = a.scratch->inv_bc2;
+  k.beta1 = a.beta1;
+  k.omb1 = a.one_minus_beta1;
+  k.beta2 = a.beta2;
+  k.omb2 = a.one_minus_beta2;
+  k.eps = a.eps;
+  for (uint32_t b = blockIdx.x; b < a.chunks; b += gridDim.x) {
+    const uint32_t c = a.chunks - 1 - b;
+    const int r = find_run(a.run, a.count, c);
+    const AdamRun& run = a.run[r];
+    const int64_t i = (int64_t)(c - run.first) * (kThreads * kAdamV * U);
+    switch (run.grad_dtype * 4 + run.param_dtype) {
+      case SSIM_DTYPE_F32 * 4 + SSIM_DTYPE_F32: adam_run<F32, F32, U>(k, run, i); break;
+      case SSIM_DTYPE_F16 * 4 + SSIM_DTYPE_F16: adam_run<F16, F16, U>(k, run, i); break;
+      case SSIM_DTYPE_BF16 * 4 + SSIM_DTYPE_BF16: adam_run<BF16, BF16, U>(k, run, i); break;
+      case SSIM_DTYPE_F32 * 4 + SSIM_DTYPE_F16: adam_run<F32, F16, U>(k, run, i); break;
+      default: adam_run<F32, BF16, U>(k, run, i); break;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host side
+struct Span {
+  uintptr_t begin, end;
+  int item;    // items may hold the same array twice only within one clip item
+  bool write;
+};
+
+// no written array may overlap another array (but a clip item's grad equal to
+// its out, which the caller leaves out)
+bool spans_clash(std::vector<Span>& spans) {
+  auto less = [](const Span& a, const Span& b) { return a.begin < b.begin; };
+  if (!std::is_sorted(spans.begin(), spans.end(), less)) std::sort(spans.begin(), spans.end(), less);
+  uintptr_t end = 0, write_end = 0;  // of the arrays so far
+  for (const Span& s : spans) {
+    if (s.begin < write_end || (s.write && s.begin < end)) return true;
+    if (s.end > end) end = s.end;
+    if (s.write && s.end > write_end) write_end = s.end;
+  }
+  return false;
+}
+
+void add_span(std::vector<Span>& spans, const void* p, size_t bytes, bool write) {
+  if (p && bytes) spans.push_back({(uintptr_t)p, (uintptr_t)p + bytes, 0, write});
+}
+
+constexpr int64_t kMaxBytes = (int64_t)1 << 46;
+
+// Groups runs into launches: at most kRuns runs and 2^31 chunks each.
+template <class Run>
+struct Launch {
+  size_t begin, end;
+  uint32_t chunks;
+};
+
+template <class Run, class ChunkOf>
+bool plan(std::vector<Run>& runs, size_t most, ChunkOf chunk_of, std::vector<Launch<Run>>& out) {
+  out.clear();
+  size_t begin = 0;
+  int64_t chunks = 0;
+  for (size_t k = 0; k < runs.size(); ++k) {
+    const int64_t size = chunk_of(runs[k]);
+    const int64_t need = (runs[k].n + size - 1) / size;
+    if (need > 0x7fffffff) return false;
+    if (k - begin == most || chunks + need > 0x7fffffff) {
+      out.push_back({begin, k, (uint32_t)chunks});
+      begin = k;
+      chunks = 0;
+    }
+    runs[k].first = (uint32_t)chunks;
+    chunks += need;
+  }
+  if (begin < runs.size()) out.push_back({begin, runs.size(), (uint32_t)chunks});
+  return true;
+}
+
+int launch_kernel(const void* kernel, int grid, void* args, void* stream) {
+  void* list[] = {args};
+  if (hipLaunchKernel(kernel, dim3(grid), dim3(kThreads), list, 0,
+                      static_cast<hipStream_t>(stream)) != hipSuccess) {
+    (void)hipGetLastError();
+    return SSIM_ERR_HIP;
+  }
+  return SSIM_OK;
+}
+
+int grid_for(uint32_t chunks) { return chunks < (uint32_t)kMaxBlocks ? (int)chunks : kMaxBlocks; }
+
+// Below this many elements a launch of whole chunks of 16 bytes x 4 a thread
+// does not fill the card; a quarter of the chunk does better.
+constexpr int64_t kSmallElements = (int64_t)1 << 22;
+
+// The norm launches.  *partials: how many partial sums they leave.
+int launch_norm(std::vector<NormRun>& runs, int64_t total, Scratch* scratch, const StepArgs& step,
+                int* partials, void* stream) {
+  const bool small = total < kSmallElements;
+  const int U = small ? 1 : 4;
+  std::vector<Launch<NormRun>> launches;
+  if (!plan(runs, kNormRuns,
+            [&](const NormRun& r) { return (int64_t)(16 / elem_bytes(r.dtype)) * kThreads * U; },
+            launches))
+    return SSIM_ERR_OVERFLOW;
+  int grid = 1;
+  for (const auto& l : launches) grid = std::max(grid, grid_for(l.chunks));
+  *partials = grid;
+  if (launches.empty()) launches.push_back({0, 0, 0});
+  NormArgs a;
+  for (size_t k = 0; k < launches.size(); ++k) {
+    const auto& l = launches[k];
+    a.count = (int)(l.end - l.begin);
+    if (a.count) memcpy(a.run, &runs[l.begin], a.count * sizeof(NormRun));
+    a.chunks = l.chunks;
+    a.add = k > 0;
+    a.scratch = scratch;
+    a.step = step;
+    if (k > 0) a.step.step = nullptr;
+    const void* kernel = small ? (const void*)ssim_grad_norm_kernel<1>
+                               : (const void*)ssim_grad_norm_kernel<4>;
+    const int rc = launch_kernel(kernel, grid, &a, stream);
+    if (rc != SSIM_OK) return rc;
+  }
+  return SSIM_OK;
+}
+
+bool follows(const void* a, int64_t n, int bytes, const void* b) {
+  return (const char*)a + n * bytes == (const char*)b;
+}
+
+int clip_impl(const ssim_clip_item* items, int64_t count, bool scales, double max_norm, float* norm,
+              void* workspace, void* stream) {
+  if (count < 0) return SSIM_ERR_SHAPE;
+  if ((count > 0 && !items) || !norm || !workspace) return SSIM_ERR_NULL;
+  if (scales && !(max_norm >= 0.0 && max_norm <= 1.7976931348623157e308)) return SSIM_ERR_VALUE;
+  if (misaligned(norm, 4) || misaligned(workspace, 8)) return SSIM_ERR_SHAPE;
+  std::vector<ClipRun> runs;
+  int64_t total = 0;
+  for (int64_t k = 0; k < count; ++k) {
+    const ssim_clip_item& it = items[k];
+    if (it.n < 0) return SSIM_ERR_SHAPE;
+    if (it.n == 0) continue;
+    if (!known_dtype(it.dtype)) return SSIM_ERR_DTYPE;
+    if (!it.grad || (scales && !it.out)) return SSIM_ERR_NULL;
+    const int eb = elem_bytes(it.dtype);
+    if (misaligned(it.grad, eb) || (scales && misaligned(it.out, eb))) return SSIM_ERR_SHAPE;
+    if (it.n > kMaxBytes / eb || (total += it.n) > kMaxBytes) return SSIM_ERR_OVERFLOW;
+    void* out = scales ? it.out : nullptr;
+    if (!runs.empty()) {
+      ClipRun& r = runs.back();
+      if (r.dtype == it.dtype && follows(r.grad, r.n, eb, it.grad) &&
+          (!scales || follows(r.out, r.n, eb, out))) {
+        r.n += it.n;
+        continue;
+      }
+    }
+    runs.push_back({it.grad, out, it.n, 0, it.dtype});
+  }
+  std::vector<Span> spans;
+  spans.reserve(2 * runs.size() + 2);
+  for (const ClipRun& r : runs) {
+    const size_t bytes = (size_t)r.n * elem_bytes(r.dtype);
+    if (scales) add_span(spans, r.out, bytes, true);
+    if (r.grad != r.out) add_span(spans, r.grad, bytes, false);
+  }
+  add_span(spans, norm, 4, true);
+  add_span(spans, workspace, sizeof(Scratch), true);
+  if (spans_clash(spans)) return SSIM_ERR_ALIAS;
+
+  int cus = 0;
+  int rc = current_device(&cus);
+  if (rc != SSIM_OK) return rc;
+
+  Scratch* scratch = static_cast<Scratch*>(workspace);
+  std::vector<NormRun> norm_runs;
+  norm_runs.reserve(runs.size());
+  for (const ClipRun& r : runs) norm_runs.push_back({r.grad, r.n, 0, r.dtype});
+  StepArgs none;
+  memset(&none, 0, sizeof(none));
+  const bool small = total < kSmallElements;
+  const int U = small ? 1 : 4;
+  std::vector<Launch<ClipRun>> launches;
+  if (scales &&
+      !plan(runs, kClipRuns,
+            [&](const ClipRun& r) { return (int64_t)(16 / elem_bytes(r.dtype)) * kThreads * U; },
+            launches))
+    return SSIM_ERR_OVERFLOW;
+  int partials = 0;
+  rc = launch_norm(norm_runs, total, scratch, none, &partials, stream);
+  if (rc != SSIM_OK) return rc;
+  if (launches.empty()) {
+    ssim_norm_only_kernel<<<dim3(1), dim3(kThreads), 0, static_cast<hipStream_t>(stream)>>>(
+        scratch, partials, norm);
+    return hipGetLastError() == hipSuccess ? SSIM_OK : SSIM_ERR_HIP;
+  }
+  ClipArgs a;
+  // (the last tensors first: see the kernel)
+  for (size_t k = launches.size(); k-- > 0;) {
+    const auto& l = launches[k];
+    a.count = (int)(l.end - l.begin);
+    memcpy(a.run, &runs[l.begin], a.count * sizeof(ClipRun));
+    a.chunks = l.chunks;
+    a.partials = partials;
+    a.max_norm = max_norm;
+    a.norm = k == 0 ? norm : nullptr;
+    a.scratch = scratch;
+    const void* kernel = small ? (const void*)ssim_clip_grads_kernel<1>
+                               : (const void*)ssim_clip_grads_kernel<4>;
+    rc = launch_kernel(kernel, grid_for(l.chunks), &a, stream);
+    if (rc != SSIM_OK) return rc;
+  }
+  return SSIM_OK;
+}
+
+int adamw_impl(const ssim_adamw_item* items, int64_t count, const ssim_adamw_options* o,
+               int64_t* step, float* norm, void* workspace, void* stream) {
+  if (count < 0) return SSIM_ERR_SHAPE;
+  if ((count > 0 && !items) || !o || !step || !workspace) return SSIM_ERR_NULL;
+  const double kMax = 1.7976931348623157e308;
+  const bool clips = !(o->max_norm > kMax);  // (NaN: refused below)
+  if (!(o->max_norm >= 0.0) || !(o->beta1 >= 0.0 && o->beta1 < 1.0) ||
+      !(o->beta2 >= 0.0 && o->beta2 < 1.0) || !(o->eps >= 0.0 && o->eps <= kMax) ||
+      !(o->weight_decay >= 0.0 && o->weight_decay <= kMax) ||
+      (!o->lr_device && !(o->lr >= 0.0 && o->lr <= kMax)))
+    return SSIM_ERR_VALUE;
+  if (clips && !norm) return SSIM_ERR_NULL;
+  if (misaligned(step, 8) || misaligned(norm, 4) || misaligned(workspace, 8) ||
+      misaligned(o->lr_device, 4))
+    return SSIM_ERR_SHAPE;
+  std::vector<AdamRun> runs;
+  int64_t total = 0;
+  for (int64_t k = 0; k < count; ++k) {
+    const ssim_adamw_item& it = items[k];
+    if (it.n < 0) return SSIM_ERR_SHAPE;
+    if (it.n == 0) continue;
+    if (!known_dtype(it.param_dtype) || !known_dtype(it.grad_dtype) ||
+        (it.grad_dtype != it.param_dtype && it.grad_dtype != SSIM_DTYPE_F32))
+      return SSIM_ERR_DTYPE;
+    if (!it.grad || !it.param || !it.exp_avg || !it.exp_avg_sq) return SSIM_ERR_NULL;
+    const int gb = elem_bytes(it.grad_dtype), pb = elem_bytes(it.param_dtype);
+    if (misaligned(it.grad, gb) || misaligned(it.param, pb) || misaligned(it.exp_avg, 4) ||
+        misaligned(it.exp_avg_sq, 4) || misaligned(it.master, 4))
+      return SSIM_ERR_SHAPE;
+    if (it.n > kMaxBytes / 4 || (total += it.n) > kMaxBytes) return SSIM_ERR_OVERFLOW;
+    if (!runs.empty()) {
+      AdamRun& r = runs.back();
+      if (r.grad_dtype == it.grad_dtype && r.param_dtype == it.param_dtype &&
+          follows(r.grad, r.n, gb, it.grad) && follows(r.param, r.n, pb, it.param) &&
+          follows(r.m, r.n, 4, it.exp_avg) && follows(r.v, r.n, 4, it.exp_avg_sq) &&
+          (r.master ? follows(r.master, r.n, 4, it.master) : !it.master)) {
+        r.n += it.n;
+        continue;
+      }
+    }
+    runs.push_back({it.grad, it.param, it.exp_avg, it.exp_avg_sq, it.master, it.n, 0,
+                    (int16_t)it.grad_dtype, (int16_t)it.param_dtype});
+  }
+  std::vector<Span> spans;
+  spans.reserve(5 * runs.size() + 4);
+  for (const AdamRun& r : runs) add_span(spans, r.grad, (size_t)r.n * elem_bytes(r.grad_dtype), false);
+  for (const AdamRun& r : runs) add_span(spans, r.param, (size_t)r.n * elem_bytes(r.param_dtype), true);
+  for (const AdamRun& r : runs) add_span(spans, r.m, (size_t)r.n * 4, true);
+  for (const AdamRun& r : runs) add_span(spans, r.v, (size_t)r.n * 4, true);
+  for (const AdamRun& r : runs) add_span(spans, r.master, (size_t)r.n * 4, true);
+  add_span(spans, step, 8, true);
+  add_span(spans, norm, 4, true);
+  add_span(spans, o->lr_device, 4, false);
+  add_span(spans, workspace, sizeof(Scratch), true);
+  if (spans_clash(spans)) return SSIM_ERR_ALIAS;
+
+  int cus = 0;
+  int rc = current_device(&cus);
+  if (rc != SSIM_OK) return rc;
+
+  Scratch* scratch = static_cast<Scratch*>(workspace);
+  const bool small = total < kSmallElements;
+  const int U = small ? 1 : 2;
+  std::vector<Launch<AdamRun>> launches;
+  if (!plan(runs, kAdamRuns, [&](const AdamRun&) { return (int64_t)kThreads * kAdamV * U; }, launches))
+    return SSIM_ERR_OVERFLOW;
+  std::vector<NormRun> norm_runs;
+  if (norm) {
+    norm_runs.reserve(runs.size());
+    for (const AdamRun& r : runs) norm_runs.push_back({r.grad, r.n, 0, r.grad_dtype});
+  }
+  const StepArgs st = {step, o->lr_device, o->lr, o->beta1, o->beta2, o->weight_decay};
+  int partials = 0;  // (without a norm the first launch forms the scalars only)
+  rc = launch_norm(norm_runs, total, scratch, st, &partials, stream);
+  if (rc != SSIM_OK) return rc;
+  if (launches.empty()) {
+    if (!norm) return SSIM_OK;
+    ssim_norm_only_kernel<<<dim3(1), dim3(kThreads), 0, static_cast<hipStream_t>(stream)>>>(
+        scratch, partials, norm);
+    return hipGetLastError() == hipSuccess ? SSIM_OK : SSIM_ERR_HIP;
+  }
+  AdamArgs a;
+  for (size_t k = launches.size(); k-- > 0;) {
+    const auto& l = launches[k];
+    a.count = (int)(l.end - l.begin);
+    memcpy(a.run, &runs[l.begin], a.count * sizeof(AdamRun));
+    a.chunks = l.chunks;
+    a.partials = norm ? partials : 0;
+    a.max_norm = o->max_norm;
+    a.norm = k == 0 ? norm : nullptr;
+    a.scratch = scratch;
+    a.beta1 = (float)o->beta1;
+    a.one_minus_beta1 = (float)(1.0 - o->beta1);
+    a.beta2 = (float)o->beta2;
+    a.one_minus_beta2 = (float)(1.0 - o->beta2);
+    a.eps = (float)o->eps;
+    rc = launch_kernel(small ? (const void*)ssim_adamw_kernel<1> : (const void*)ssim_adamw_kernel<2>,
+                       grid_for(l.chunks), &a, stream);
+    if (rc != SSIM_OK) return rc;
+  }
+  return SSIM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ssim_update_workspace_bytes(void) { return sizeof(Scratch); }
+
+int ssim_clip_grads(const ssim_clip_item* items, int64_t count, double max_norm, float* norm,
+                    void* workspace, void* stream) try {
+  return clip_impl(items, count, true, max_norm, norm, workspace, stream);
+} catch (...) {
+  return SSIM_ERR_OVERFLOW;  // host memory for the table
+}
+
+int ssim_grad_norm(const ssim_clip_item* items, int64_t count, float* norm, void* workspace,
+                   void* stream) try {
+  return clip_impl(items, count, false, 0.0, norm, workspace, stream);
+} catch (...) {
+  return SSIM_ERR_OVERFLOW;
+}
+
+int ssim_adamw_step(const ssim_adamw_item* items, int64_t count, const ssim_adamw_options* options,
+                    int64_t* step, float* norm, void* workspace, void* stream) try {
+  return adamw_impl(items, count, options, step, norm, workspace, stream);
+} catch (...) {
+  return SSIM_ERR_OVERFLOW;
+}
+
+}  // extern "C"
