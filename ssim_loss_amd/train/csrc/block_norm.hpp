@@ -18,8 +18,9 @@
 
 namespace ssim_train {
 
-constexpr int kMaxWaves = 8;    // of a workgroup
-constexpr int kRowWaves = 4;    // rows (waves) of a workgroup where a wave takes a row
+constexpr int kMaxWaves = 8;     // of a workgroup
+constexpr int kRowWaves = 4;     // rows (waves) of a workgroup where a wave takes a row: forward
+constexpr int kRowWavesBack = 8; // and backward
 constexpr int kSumColumns = 64; // columns a workgroup of the last sum takes
 constexpr int kSumSlices = 16;  // ... and shares of the partial sums it adds at once
 
@@ -65,21 +66,56 @@ struct Row {
   static constexpr int E = V * I;
 };
 
-// one vector of a row, as stored; zeros past the row's end
+// One vector of a row, as stored, with one load and no branch: a vector that
+// would pass the row's end is the row's last V elements instead, and settle()
+// moves them down to where they belong, with zeros behind the row's end.  (A
+// row of less than V elements is taken element by element.)
 template <class T, int V>
 __device__ __forceinline__ Vec<T, V> load_cols(const T* row, int col, int width) {
-  if (col + V <= width) return load<T, V>(row + col);
+  if (width >= V) return load<T, V>(row + min(col, width - V));
   Vec<T, V> v = {};
+  if (col == 0) {
 #pragma unroll
-  for (int k = 0; k < V; ++k)
-    if (col + k < width) v[k] = row[col + k];
+    for (int k = 0; k < V; ++k)
+      if (k < width) v[k] = row[k];
+  }
   return v;
+}
+template <class T, int V>
+__device__ __forceinline__ void settle(Vec<T, V>& v, int col, int width) {
+  int shift = col + V - width;  // elements
+  if (shift <= 0 || width < V) return;
+  constexpr int kWords = V * (int)sizeof(T) / 4;
+  union {
+    Vec<T, V> v;
+    uint32_t w[kWords];
+  } u = {v};
+  if constexpr (sizeof(T) == 2) {
+    if (shift & 1) {
+#pragma unroll
+      for (int k = 0; k < kWords; ++k)
+        u.w[k] = (u.w[k] >> 16) | (k + 1 < kWords ? u.w[k + 1] << 16 : 0u);
+    }
+    shift >>= 1;
+  }
+#pragma unroll
+  for (int step = 1; step < kWords; step *= 2) {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) {
+      const uint32_t from = k + step < kWords ? u.w[k + step] : 0u;
+      u.w[k] = (shift & step) ? from : u.w[k];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kWords; ++k) u.w[k] = shift >= kWords ? 0u : u.w[k];
+  v = u.v;
 }
 template <class T, int V>
 __device__ __forceinline__ void store_cols(T* row, int col, int width, Wide<V> w) {
   const Vec<T, V> v = narrow<T, V>(w);
   if (col + V <= width) {
-    store<T, V>(row + col, v);
+    if constexpr (sizeof(T) == 2) store_once<T, V>(row + col, v);
+    else store<T, V>(row + col, v);
     return;
   }
 #pragma unroll
@@ -89,11 +125,21 @@ __device__ __forceinline__ void store_cols(T* row, int col, int width, Wide<V> w
 // a weight's columns; 1 where there is none
 template <int V>
 __device__ __forceinline__ Wide<V> load_weight(const float* w, int col, int width) {
-  if (w) return load_cols<float, V>(w, col, width);
+  if (w) {
+    Vec<float, V> v = load_cols<float, V>(w, col, width);
+    settle<float, V>(v, col, width);
+    return v;
+  }
   Wide<V> one;
 #pragma unroll
   for (int k = 0; k < V; ++k) one[k] = 1.0f;
   return one;
+}
+
+// a / b of numbers >= 0, which rarely need 64 bits
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
 }
 
 // act(g).  fp32 tensors take the exact exponential; for half types the fast
@@ -106,11 +152,11 @@ __device__ __forceinline__ float activate(float g, int act) {
 }
 
 // N sums over a row's threads at once.  kRowWave: the row is one wave's;
-// otherwise the workgroup's, with lds[N][kMaxWaves], whose entries past the
+// otherwise the workgroup's, with lds[N][kWaves], whose entries past the
 // workgroup's waves are zero.  Two calls that follow each other take different
 // lds arrays: then the barrier within one separates the other's uses.
-template <bool kRowWave, int N>
-__device__ __forceinline__ void row_sums(float (&s)[N], float (*lds)[kMaxWaves]) {
+template <bool kRowWave, int N, int kWaves>
+__device__ __forceinline__ void row_sums(float (&s)[N], float (*lds)[kWaves]) {
 #pragma unroll
   for (int k = 0; k < N; ++k) s[k] = wave_sum(s[k]);
   if constexpr (!kRowWave) {
@@ -123,20 +169,25 @@ __device__ __forceinline__ void row_sums(float (&s)[N], float (*lds)[kMaxWaves])
     for (int k = 0; k < N; ++k) {
       float t = 0;
 #pragma unroll
-      for (int w = 0; w < kMaxWaves; ++w) t += lds[k][w];
+      for (int w = 0; w < kWaves; ++w) t += lds[k][w];
       s[k] = t;
     }
   }
 }
 
-template <class TX, class TB, int I, bool kRowWave>
+// what the forward loads of one vector of a row
+template <class TX, class TB, int V>
+struct FwdRaw {
+  Vec<TX, V> x;
+  Vec<TB, V> b, gate;
+};
+
+// kPrefetch: a row's loads are issued while the row before it is worked on, the
+// first row's before the weights'.
+template <class TX, class TB, int I, bool kRowWave, bool kPrefetch>
 __device__ __forceinline__ void norm_forward(const NormParams& p) {
   constexpr int V = Row<TX, TB, I>::V;
   __shared__ float lds[2][1][kMaxWaves];
-  if constexpr (!kRowWave) {
-    if (threadIdx.x < 2 * kMaxWaves) (&lds[0][0][0])[threadIdx.x] = 0;
-    __syncthreads();
-  }
   const int width = p.width;
   const int threads = kRowWave ? kWave : (int)blockDim.x;
   const int q = kRowWave ? (int)threadIdx.x & (kWave - 1) : (int)threadIdx.x;
@@ -144,6 +195,24 @@ __device__ __forceinline__ void norm_forward(const NormParams& p) {
   if constexpr (kRowWave) {
     row = row * kRowWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     stride *= kRowWaves;
+  }
+  FwdRaw<TX, TB, V> next[I];
+  auto fetch = [&](int64_t of) {
+    const int64_t at = of * width;
+    const int64_t gate_at = (p.gate_rows == 1 ? of : quotient(of, p.gate_rows)) * width;
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int col = (i * threads + q) * V;
+      next[i].b = load_cols<TB, V>((const TB*)p.b + at, col, width);
+      next[i].x = load_cols<TX, V>((const TX*)p.x + at, col, width);
+      next[i].gate = 0;
+      if (p.gate) next[i].gate = load_cols<TB, V>((const TB*)p.gate + gate_at, col, width);
+    }
+  };
+  if (kPrefetch && row < p.rows) fetch(row);
+  if constexpr (!kRowWave) {
+    if (threadIdx.x < 2 * kMaxWaves) (&lds[0][0][0])[threadIdx.x] = 0;
+    __syncthreads();
   }
   Wide<V> c[I], pre[I];
 #pragma unroll
@@ -153,35 +222,32 @@ __device__ __forceinline__ void norm_forward(const NormParams& p) {
     pre[i] = load_weight<V>(p.pre, col, width);
   }
   for (; row < p.rows; row += stride) {
-    const TX* x = (const TX*)p.x + row * width;
-    const TB* b = (const TB*)p.b + row * width;
-    const int64_t gate_row = p.gate_rows == 1 ? row : row / p.gate_rows;
-    const TB* g = (const TB*)p.gate + (p.gate ? gate_row * width : 0);
-    Vec<TX, V> xr[I];
-    Vec<TB, V> br[I], gr[I];
+    FwdRaw<TX, TB, V> raw[I];
+    if (!kPrefetch) fetch(row);
+#pragma unroll
+    for (int i = 0; i < I; ++i) raw[i] = next[i];
+    if (kPrefetch && row + stride < p.rows) fetch(row + stride);
 #pragma unroll
     for (int i = 0; i < I; ++i) {
       const int col = (i * threads + q) * V;
-      br[i] = load_cols<TB, V>(b, col, width);
-      xr[i] = load_cols<TX, V>(x, col, width);
-      if (p.gate) gr[i] = load_cols<TB, V>(g, col, width);
+      settle<TB, V>(raw[i].b, col, width);
+      settle<TX, V>(raw[i].x, col, width);
+      if (p.gate) settle<TB, V>(raw[i].gate, col, width);
     }
     float s[1] = {0};
     Wide<V> v[I];
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      v[i] = widen<TB, V>(br[i]);
+      v[i] = widen<TB, V>(raw[i].b);
 #pragma unroll
       for (int k = 0; k < V; ++k) s[0] = fmaf(v[i][k], v[i][k], s[0]);
     }
-    row_sums<kRowWave, 1>(s, lds[0]);
+    row_sums<kRowWave>(s, lds[0]);
     const float ib = 1.0f / sqrtf(fmaf(s[0], p.inv_width, p.eps));
     s[0] = 0;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const Wide<V> xw = widen<TX, V>(xr[i]);
-      Wide<V> gw = {};
-      if (p.gate) gw = widen<TB, V>(gr[i]);
+      const Wide<V> xw = widen<TX, V>(raw[i].x), gw = widen<TB, V>(raw[i].gate);
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         float ac = c[i][k];
@@ -192,7 +258,7 @@ __device__ __forceinline__ void norm_forward(const NormParams& p) {
       }
     }
     // (columns past the row's end hold zeros, so they add nothing)
-    row_sums<kRowWave, 1>(s, lds[1]);
+    row_sums<kRowWave>(s, lds[1]);
     const float ir = 1.0f / sqrtf(fmaf(s[0], p.inv_width, p.eps));
     TX* r = (TX*)p.r + row * width;
     TB* h = (TB*)p.h + row * width;
@@ -228,6 +294,14 @@ __device__ __forceinline__ Raw<TX, TB, V> load_raw(const NormParams& p, int64_t 
   if (p.dr) f.dr = load_cols<TX, V>((const TX*)p.dr + at, col, p.width);
   if (p.dh) f.dh = load_cols<TB, V>((const TB*)p.dh + at, col, p.width);
   return f;
+}
+template <class TX, class TB, int V, bool kGrouped>
+__device__ __forceinline__ void settle_raw(Raw<TX, TB, V>& f, int col, int width) {
+  settle<TB, V>(f.b, col, width);
+  settle<TX, V>(f.x, col, width);
+  settle<TX, V>(f.dr, col, width);
+  settle<TB, V>(f.dh, col, width);
+  if constexpr (!kGrouped) settle<TB, V>(f.gate, col, width);
 }
 // and forms of it (names as below)
 template <int V>
@@ -276,16 +350,20 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
   // a thread of a very wide row cannot hold it: its vectors are loaded again,
   // from the caches, after the reduction
   constexpr bool kReload = Row<TX, TB, I>::E > 16;
-  __shared__ float lds[2][3][kMaxWaves];
+  constexpr int kWaves = kMaxWaves;
+  // (two vectors of a thread twice over do not fit its registers, unless the
+  // group's are missing)
+  constexpr bool kPrefetch = I == 1 || (I == 2 && kRowWave && !kGrouped);
+  __shared__ float lds[2][3][kWaves];
   if constexpr (!kRowWave) {
-    for (int k = threadIdx.x; k < 6 * kMaxWaves; k += blockDim.x) (&lds[0][0][0])[k] = 0;
+    for (int k = threadIdx.x; k < 6 * kWaves; k += blockDim.x) (&lds[0][0][0])[k] = 0;
     __syncthreads();
   }
   const int width = p.width;
   const int threads = kRowWave ? kWave : (int)blockDim.x;
   const int q = kRowWave ? (int)threadIdx.x & (kWave - 1) : (int)threadIdx.x;
   const int wave = kRowWave ? __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) : 0;
-  constexpr int kWorkers = kRowWave ? kRowWaves : 1;
+  constexpr int kWorkers = kRowWave ? kRowWavesBack : 1;
 
   constexpr int kHeld = kReload ? 1 : I;  // vectors of the weights and of a row that stay
   Wide<V> c[kHeld], pre[kHeld], total[I], dpre[I], S[kGrouped ? I : 1], a[kGrouped ? I : 1];
@@ -317,7 +395,7 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
   for (; seg < segs; seg += seg_stride) {
     int64_t row, end, stride, group = 0;
     if constexpr (kGrouped) {
-      group = seg / p.parts;
+      group = quotient(seg, p.parts);
       const int64_t part = seg - group * p.parts;
       row = group * p.gate_rows + part * p.part_rows;
       end = row + p.part_rows;
@@ -331,7 +409,9 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
 #pragma unroll
       for (int i = 0; i < I; ++i) {
         const int col = (i * threads + q) * V;
-        const Wide<V> gw = widen<TB, V>(load_cols<TB, V>(g, col, width));
+        Vec<TB, V> gr = load_cols<TB, V>(g, col, width);
+        settle<TB, V>(gr, col, width);
+        const Wide<V> gw = widen<TB, V>(gr);
 #pragma unroll
         for (int k = 0; k < V; ++k) a[i][k] = activate<TB>(gw[k], p.act);
         S[i] = 0;
@@ -341,24 +421,40 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
       stride = (int64_t)gridDim.x * kWorkers;
       end = p.rows;
     }
-    for (; row < end; row += stride, parity ^= 1) {
-      const int64_t at = row * width;
-      Raw<TX, TB, V> raw[kHeld];
+    // a row's loads are issued while the row before it is worked on
+    Raw<TX, TB, V> next[kHeld];
+    float next_ib = 0, next_ir = 0;
+    auto fetch = [&](int64_t of) {
       if constexpr (!kReload) {
 #pragma unroll
         for (int i = 0; i < I; ++i)
-          raw[i] = load_raw<TX, TB, V, kGrouped>(p, at, (i * threads + q) * V);
+          next[i] = load_raw<TX, TB, V, kGrouped>(p, of * width, (i * threads + q) * V);
       }
-      const float ib = p.stats[2 * row], ir = p.stats[2 * row + 1];
+      next_ib = p.stats[2 * of];
+      next_ir = p.stats[2 * of + 1];
+    };
+    if (kPrefetch && row < end) fetch(row);
+    for (; row < end; row += stride, parity ^= 1) {
+      const int64_t at = row * width;
+      Raw<TX, TB, V> raw[kHeld];
+      if (!kPrefetch) fetch(row);
+      if constexpr (!kReload) {
+#pragma unroll
+        for (int i = 0; i < I; ++i) raw[i] = next[i];
+      }
+      const float ib = next_ib, ir = next_ir;
+      if (kPrefetch && row + stride < end) fetch(row + stride);
       float s[3] = {0, 0, 0};
       Terms<V> terms[kHeld];
 #pragma unroll
       for (int i = 0; i < I; ++i) {
         const int j = kReload ? 0 : i;
         if constexpr (kReload) {
+          __builtin_amdgcn_sched_barrier(0);  // one vector at a time, for its registers
           load_weights(i);
           raw[j] = load_raw<TX, TB, V, kGrouped>(p, at, (i * threads + q) * V);
         }
+        settle_raw<TX, TB, V, kGrouped>(raw[j], (i * threads + q) * V, width);
         const Wide<V> dw = widen<TB, V>(raw[j].dh);
         const Terms<V> f = form_terms<TX, TB, V, kGrouped>(p, raw[j], dw, ib, ir, c[j], pre[j],
                                                            a[kGrouped ? i : 0]);
@@ -372,7 +468,7 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
         }
         terms[j] = f;
       }
-      row_sums<kRowWave, 3>(s, lds[parity]);
+      row_sums<kRowWave>(s, lds[parity]);
       const float m1 = ir * (s[0] * p.inv_width);
       const float m2 = s[1] * p.inv_width - m1 * (s[2] * p.inv_width);
       TX* dx = (TX*)p.dx + (p.dx ? at : 0);
@@ -382,8 +478,10 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
       for (int i = 0; i < I; ++i) {
         const int col = (i * threads + q) * V, j = kReload ? 0 : i;
         if constexpr (kReload) {
+          __builtin_amdgcn_sched_barrier(0);
           load_weights(i);
           raw[j] = load_raw<TX, TB, V, kGrouped>(p, at, col);
+          settle_raw<TX, TB, V, kGrouped>(raw[j], col, width);
           terms[j] = form_terms<TX, TB, V, kGrouped>(p, raw[j], widen<TB, V>(raw[j].dh), ib, ir,
                                                      c[j], pre[j], a[kGrouped ? i : 0]);
         }
@@ -426,7 +524,7 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
     if (!out[k]) continue;
     float* to = out[k] + (int64_t)blockIdx.x * width;
     if constexpr (kRowWave) {
-      __shared__ float waves[kRowWaves][kWave * V * I];
+      __shared__ float waves[kRowWavesBack][kWave * V * I];
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < I; ++i) {
@@ -437,10 +535,10 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
         for (int e = 0; e < V; ++e) waves[wave][(i * kWave + q) * V + e] = v[e];
       }
       __syncthreads();
-      for (int col = threadIdx.x; col < width; col += kRowWaves * kWave) {
+      for (int col = threadIdx.x; col < width; col += kRowWavesBack * kWave) {
         float v = 0;
 #pragma unroll
-        for (int w = 0; w < kRowWaves; ++w) v += waves[w][col];
+        for (int w = 0; w < kRowWavesBack; ++w) v += waves[w][col];
         to[col] = v;
       }
     } else {
@@ -498,8 +596,30 @@ __device__ __forceinline__ void norm_sums(const NormParams& p) {
 }
 
 // ---- the kernels of one block type
-// how a row is spread: over a wave or a workgroup, vectors a thread, threads
-enum NormShape { kWave1, kWave2, kGroup1, kGroup2, kGroup4, kGroup8, kNormShapes };
+// How a row is spread: over a wave or a workgroup of at most so many waves,
+// vectors a thread.
+enum NormShape {
+  kWave1,   // one wave, one vector
+  kWave2,   // one wave, two
+  kGroup1,  // 4 waves, one
+  kGroup1w, // 8 waves, one
+  kGroup2,  // 8 waves, two
+  kGroup4,  // 8 waves, four
+  kGroup8,  // 8 waves, eight (fp32 blocks)
+  kNormShapes
+};
+constexpr bool shape_wave(int s) { return s == kWave1 || s == kWave2; }
+constexpr int shape_items(int s) {
+  return s == kWave2 || s == kGroup2 ? 2 : s == kGroup4 ? 4 : s == kGroup8 ? 8 : 1;
+}
+constexpr int shape_threads(int s, int row_waves) {
+  return (shape_wave(s) ? row_waves : s == kGroup1 ? 4 : kMaxWaves) * kWave;
+}
+// A workgroup of more than four waves to a row waits at its barriers with few
+// others beside it; there the next row's loads go out early.  Where many waves
+// are resident that gains nothing and costs registers: at 4100 x 1152 in fp16
+// 12.6 us without and 13.3 with, at 16384 x 4096 in bf16 124 and 100.
+constexpr bool shape_prefetch(int s) { return s == kGroup1w || s == kGroup2; }
 
 struct NormTable {
   const void* forward[2][kNormShapes];      // [x is fp32 beside a half type]
@@ -511,19 +631,14 @@ const NormTable& norm_table_f32();
 const NormTable& norm_table_f16();
 const NormTable& norm_table_bf16();
 
-constexpr int shape_items(int s) {
-  return s == kWave1 || s == kGroup1 ? 1 : s == kGroup4 ? 4 : s == kGroup8 ? 8 : 2;
-}
-constexpr bool shape_wave(int s) { return s == kWave1 || s == kWave2; }
-constexpr int shape_threads(int s) { return (shape_wave(s) ? kRowWaves : kMaxWaves) * kWave; }
-
 template <class TX, class TB, int kShape>
-__global__ __launch_bounds__(shape_threads(kShape)) void ssim_block_norm_fwd_kernel(
+__global__ __launch_bounds__(shape_threads(kShape, kRowWaves)) void ssim_block_norm_fwd_kernel(
     const NormParams p) {
-  norm_forward<TX, TB, shape_items(kShape), shape_wave(kShape)>(p);
+  norm_forward<TX, TB, shape_items(kShape), shape_wave(kShape), shape_prefetch(kShape)>(
+      p);
 }
 template <class TX, class TB, int kShape, bool kGrouped>
-__global__ __launch_bounds__(shape_threads(kShape)) void ssim_block_norm_bwd_kernel(
+__global__ __launch_bounds__(shape_threads(kShape, kRowWavesBack)) void ssim_block_norm_bwd_kernel(
     const NormParams p) {
   norm_backward<TX, TB, shape_items(kShape), shape_wave(kShape), kGrouped>(p);
 }
@@ -546,6 +661,7 @@ void fill_types(NormTable& t, int wide) {
   fill_shape<TX, TB, kWave1>(t, wide);
   fill_shape<TX, TB, kWave2>(t, wide);
   fill_shape<TX, TB, kGroup1>(t, wide);
+  fill_shape<TX, TB, kGroup1w>(t, wide);
   fill_shape<TX, TB, kGroup2>(t, wide);
   fill_shape<TX, TB, kGroup4>(t, wide);
   fill_shape<TX, TB, kGroup8>(t, wide);

@@ -19,55 +19,86 @@ const NormTable& table_of(int dtype) {
 
 // How the rows are dealt out.
 struct Plan {
-  int shape, threads, workers;  // workers: rows a workgroup takes at once
   bool wide, grouped;
-  int blocks;  // of the backward
+  int shape;
+  int threads, blocks;            // of the forward
+  int back_threads, back_blocks;  // of the backward
   int parts;
   int64_t groups, part_rows;
 };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Workgroups of `workers` rows at once, about `target` of them, with the same
+// number of rows each.
+int64_t blocks_for(int64_t rows, int64_t workers, int64_t target) {
+  const int64_t need = ceil_div(rows, workers);
+  if (need <= target) return need;
+  const int64_t each = (2 * need + target) / (2 * target);  // to the nearest
+  return ceil_div(need, each);
+}
+
+int threads_of(int shape, int row_waves, int64_t vectors) {
+  if (shape_wave(shape)) return row_waves * kWave;
+  return (int)ceil_div(ceil_div(vectors, shape_items(shape)), kWave) * kWave;
+}
+
 Plan make_plan(const ssim_block_norm_inputs& in) {
   Plan p;
-  const int64_t vectors = ceil_div(in.width, 16 / elem_bytes(in.branch_dtype));
-  p.shape = vectors <= kWave               ? kWave1
-            : vectors <= 2 * kWave         ? kWave2
-            : vectors <= kMaxWaves * kWave ? kGroup1
-            : vectors <= 2 * kMaxWaves * kWave ? kGroup2
-            : vectors <= 4 * kMaxWaves * kWave ? kGroup4
-                                               : kGroup8;
+  const int xb = elem_bytes(in.x_dtype), bb = elem_bytes(in.branch_dtype);
+  const int64_t vectors = ceil_div(in.width, 16 / bb);
+  p.shape = vectors <= kWave       ? kWave1
+            : vectors <= 2 * kWave ? kWave2
+            : vectors <= 4 * kWave ? kGroup1
+            : vectors <= 8 * kWave ? kGroup1w
+            : vectors <= 16 * kWave ? kGroup2
+            : vectors <= 32 * kWave ? kGroup4
+                                    : kGroup8;
+  const bool wave = shape_wave(p.shape);
   p.wide = in.x_dtype != in.branch_dtype;
-  p.workers = shape_wave(p.shape) ? kRowWaves : 1;
-  p.threads = shape_wave(p.shape)
-                  ? kRowWaves * kWave
-                  : (int)ceil_div(ceil_div(vectors, shape_items(p.shape)), kWave) * kWave;
+  p.threads = threads_of(p.shape, kRowWaves, vectors);
+  p.back_threads = threads_of(p.shape, kRowWavesBack, vectors);
   p.grouped = in.gate && in.gate_rows > 1;
-  const int64_t target = (int64_t)kCUs * (1024 / p.threads);
+
+  // Forward: rows in work whose loads are 48 KB on each CU; where a row is a
+  // workgroup's 24 KB, 32 KB with the next row's loads out beside them.  Fewer
+  // leave the memory idle; more read the weights more often and end unevenly.
+  // Measured with 24 and 48 KB: 4100 x 1153 fp16 13.1 and 14.6 us (a workgroup
+  // a row), 65536 x 512 bf16 57.8 and 54.0 us (a wave a row).
+  const int64_t row_bytes = in.width * (xb + bb + (in.gate && !p.grouped ? bb : 0));
+  const int64_t in_work = wave ? 48 << 10 : shape_prefetch(p.shape) ? 32 << 10 : 24 << 10;
+  const int64_t rows_per_cu = ceil_div(in_work, row_bytes);
+  p.blocks = (int)(wave ? blocks_for(in.rows, kRowWaves, kCUs * ceil_div(rows_per_cu, kRowWaves))
+                        : blocks_for(in.rows, 1, kCUs * rows_per_cu));
+
+  // Backward: 16 KB, since each workgroup leaves a row of partial sums.
+  // Measured with 16 and 32 KB: 4100 x 1152 fp16 18.8 and 23.4 us, 32768 x
+  // 2048 bf16 beside fp32 266 and 290 us.  Blocks in fp32 leave room for two
+  // workgroups of eight waves on a CU, and one waits at its barriers too long
+  // (16384 x 2048: 195 us with two, 230 with one).
+  const int workers = wave ? kRowWavesBack : 1;
+  const int64_t back_bytes = in.width * (2 * xb + 2 * bb + (in.gate && !p.grouped ? bb : 0));
+  int64_t per_cu = ceil_div(ceil_div(16 << 10, back_bytes), workers);
+  if (bb == 4 && p.shape <= kGroup2 && per_cu < 1024 / p.back_threads) per_cu = 1024 / p.back_threads;
+  const int64_t target = kCUs * per_cu;
   p.parts = 1;
   p.groups = p.part_rows = 0;
   if (!p.grouped) {
-    const int64_t need = ceil_div(in.rows, p.workers);
-    p.blocks = (int)(need < target ? need : target);
+    p.back_blocks = (int)blocks_for(in.rows, workers, target);
     return p;
   }
   p.groups = in.rows / in.gate_rows;
   p.part_rows = in.gate_rows;
   if (p.groups > 0 && p.groups < target) {
     int64_t parts = target / p.groups;
-    const int64_t most = ceil_div(in.gate_rows, p.workers);
+    const int64_t most = ceil_div(in.gate_rows, workers);
     if (parts > most) parts = most;
     if (parts > 1) {
-      p.part_rows = ceil_div(in.gate_rows, parts);
+      p.part_rows = ceil_div(ceil_div(in.gate_rows, parts), workers) * workers;
       p.parts = (int)ceil_div(in.gate_rows, p.part_rows);
     }
   }
-  if (p.parts > 1) {
-    p.blocks = (int)(p.groups * p.parts);
-  } else {
-    const int64_t need = ceil_div(p.groups, p.workers);
-    p.blocks = (int)(need < target ? need : target);
-  }
+  p.back_blocks = (int)(p.parts > 1 ? p.groups * p.parts : blocks_for(p.groups, workers, target));
   return p;
 }
 
@@ -106,7 +137,7 @@ int check_arrays(const Array* ins, int n_in, const Array* outs, int n_out) {
 
 size_t workspace_bytes(const ssim_block_norm_inputs& in, const Plan& p) {
   const size_t arrays = p.grouped && p.parts > 1 ? 3 : 2;
-  return ((size_t)p.blocks * (size_t)in.width * 4 * arrays + 15) & ~(size_t)15;
+  return ((size_t)p.back_blocks * (size_t)in.width * 4 * arrays + 15) & ~(size_t)15;
 }
 
 NormParams params_of(const ssim_block_norm_inputs& in, const Plan& p) {
@@ -127,7 +158,7 @@ NormParams params_of(const ssim_block_norm_inputs& in, const Plan& p) {
   k.groups = p.groups;
   k.part_rows = p.part_rows;
   k.parts = p.parts;
-  k.blocks = p.blocks;
+  k.blocks = p.back_blocks;
   return k;
 }
 
@@ -168,9 +199,8 @@ int ssim_block_norm_forward(const ssim_block_norm_inputs* in, void* residual, vo
   k.r = residual;
   k.h = normed;
   k.stats = stats;
-  const int64_t need = ceil_div(in->rows, p.workers), most = (int64_t)kCUs * (2048 / p.threads);
-  return launch(table_of(in->branch_dtype).forward[p.wide][p.shape],
-                dim3((unsigned)(need < most ? need : most)), p.threads, k, stream);
+  return launch(table_of(in->branch_dtype).forward[p.wide][p.shape], dim3(p.blocks), p.threads, k,
+                stream);
 }
 
 size_t ssim_block_norm_workspace_bytes(const ssim_block_norm_inputs* in) {
@@ -222,7 +252,7 @@ int ssim_block_norm_backward(const ssim_block_norm_inputs* in, const float* stat
   k.dscale = grads->scale;
   k.dpost = grads->post_weight;
   k.dpre = grads->pre_weight;
-  const size_t part = (size_t)p.blocks * (size_t)in->width;
+  const size_t part = (size_t)p.back_blocks * (size_t)in->width;
   float* ws = static_cast<float*>(workspace);
   const bool cut = p.grouped && p.parts > 1 && grads->gate && rows;
   if (k.dscale || k.dpost) k.part_total = ws;
@@ -230,7 +260,7 @@ int ssim_block_norm_backward(const ssim_block_norm_inputs* in, const float* stat
   if (cut) k.part_gate = ws + 2 * part;
   const NormTable& t = table_of(in->branch_dtype);
   if (rows) {
-    rc = launch(t.backward[p.wide][p.shape][p.grouped], dim3(p.blocks), p.threads, k, stream);
+    rc = launch(t.backward[p.wide][p.shape][p.grouped], dim3(p.back_blocks), p.back_threads, k, stream);
     if (rc != SSIM_OK) return rc;
   }
   if (!weights && !cut) return SSIM_OK;
