@@ -59,11 +59,43 @@ __device__ __forceinline__ Vec<T, N> narrow(Wide<N> v) {  // to nearest even
 }
 
 // ---- reductions: every lane gets the sum, in an order that does not change
+// A value from the lane that kControl names, 0 where kRows leaves a row of 16
+// lanes out (data-parallel primitives: within the vector unit, where a
+// shuffle goes through the LDS at several times the latency).
+template <int kControl, int kRows>
+__device__ __forceinline__ float lane_move(float v) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), kControl, kRows, 0xf, false));
+}
+template <int kControl, int kRows>
+__device__ __forceinline__ double lane_move(double v) {
+  struct Words {
+    int lo, hi;
+  } w = __builtin_bit_cast(Words, v);
+  w.lo = __builtin_amdgcn_update_dpp(0, w.lo, kControl, kRows, 0xf, false);
+  w.hi = __builtin_amdgcn_update_dpp(0, w.hi, kControl, kRows, 0xf, false);
+  return __builtin_bit_cast(double, w);
+}
+__device__ __forceinline__ float last_lane(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), kWave - 1));
+}
+__device__ __forceinline__ double last_lane(double v) {
+  struct Words {
+    int lo, hi;
+  } w = __builtin_bit_cast(Words, v);
+  w.lo = __builtin_amdgcn_readlane(w.lo, kWave - 1);
+  w.hi = __builtin_amdgcn_readlane(w.hi, kWave - 1);
+  return __builtin_bit_cast(double, w);
+}
 template <class T>
 __device__ __forceinline__ T wave_sum(T v) {
-#pragma unroll
-  for (int m = kWave / 2; m > 0; m >>= 1) v += __shfl_xor(v, m, kWave);
-  return v;
+  v += lane_move<0xB1, 0xf>(v);   // the neighbour, of each two lanes
+  v += lane_move<0x4E, 0xf>(v);   // the other two, of four
+  v += lane_move<0x141, 0xf>(v);  // the mirror image, of eight
+  v += lane_move<0x140, 0xf>(v);  // of sixteen
+  v += lane_move<0x142, 0xa>(v);  // rows 1 and 3: the last lane of the row before
+  v += lane_move<0x143, 0xc>(v);  // rows 2 and 3: lane 31
+  return last_lane(v);
 }
 
 // ---- host side
