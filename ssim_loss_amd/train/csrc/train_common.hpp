@@ -49,6 +49,16 @@ template <class T, int N>
 __device__ __forceinline__ void store_once(T* p, Vec<T, N> v) {
   __builtin_nontemporal_store(v, reinterpret_cast<typename Pack<T, N>::Loose*>(p));
 }
+template <bool kOnce, class T, int N>
+__device__ __forceinline__ Vec<T, N> load_as(const T* p) {
+  if constexpr (kOnce) return load_once<T, N>(p);
+  else return load<T, N>(p);
+}
+template <bool kOnce, class T, int N>
+__device__ __forceinline__ void store_as(T* p, Vec<T, N> v) {
+  if constexpr (kOnce) store_once<T, N>(p, v);
+  else store<T, N>(p, v);
+}
 template <class T, int N>
 __device__ __forceinline__ Wide<N> widen(Vec<T, N> v) {
   return __builtin_convertvector(v, typename Pack<T, N>::Wide);
