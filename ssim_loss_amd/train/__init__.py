@@ -174,7 +174,9 @@ class AdamW:
             self.exp_avgs = states(exp_avgs)
             self.exp_avg_sqs = states(exp_avg_sqs)
             self.masters = None if masters is None else list(masters)
-            self._step = torch.tensor(int(step), dtype=torch.int64, device=self.params[0].device)
+            # (the second word is the library's, 0 between calls)
+            self._step = torch.tensor([int(step), 0], dtype=torch.int64,
+                                      device=self.params[0].device)
         for name in ("exp_avgs", "exp_avg_sqs", "masters"):
             held = getattr(self, name)
             if held is not None and len(held) != len(self.params):
@@ -198,7 +200,7 @@ class AdamW:
     @property
     def steps(self) -> int:
         """Updates done (waits for the device)."""
-        return int(self._step.item())
+        return int(self._step[0].item())
 
     def state_dict(self) -> dict:
         """Copies of the state: exp_avgs, exp_avg_sqs, masters, step (waits
@@ -229,7 +231,7 @@ class AdamW:
         with torch.no_grad():
             for to, by in pairs:
                 to.copy_(by)
-            self._step.fill_(int(state["step"]))
+            self._step[0].fill_(int(state["step"]))
 
 
 # --------------------------------------------------------------------------- the joint of two blocks

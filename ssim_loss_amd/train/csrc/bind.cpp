@@ -205,8 +205,8 @@ py::object adamw_step(const py::object& grads_, const py::object& params_, const
     items.push_back(it);
   }
   const Tensor& step = unpack(step_.ptr(), "step");
-  if (step.scalar_type() != at::kLong || step.numel() != 1)
-    throw py::type_error("step must be one int64");
+  if (step.scalar_type() != at::kLong || step.numel() != 2 || !step.is_contiguous())
+    throw py::type_error("step must be two int64");
   check_device(step, dev, "step");
   ssim_adamw_options o;
   o.lr = 0.0;

@@ -108,8 +108,9 @@ typedef struct {
                              graph then follows a schedule) */
 } ssim_adamw_options;
 
-/*   step : device int64, the number of updates done before this one; the call
- *          adds one to it
+/*   step : device int64[2], the number of updates done before this one, to which
+ *          the call adds one, and a word of the library's that is 0 before the
+ *          first call and after every call
  *   norm : device fp32, receives the gradients' norm before clipping; may be
  *          NULL if max_norm is infinite
  * No array of an item may overlap another array of any item, the step, the

@@ -92,8 +92,21 @@ def test_clip_more_tensors_than_a_launch_holds():
     _check_clip(_list(sizes, [F32, BF16, F16], 8), 1.0)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("sizes", [[1, 2, 3, 1, 3, 45], [4096] * 8, [32768], [32769], [4097] * 8,
+                                   [1] * 8, [1] * 9, [5, 32000, 7], [16384, 16384]])
+def test_clip_few_gradients(sizes, dtype):
+    """Lists at and around what one launch takes, out of place in one
+    workgroup and in several, and in place."""
+    say("clip", sizes, dtype)
+    grads = _list(sizes, [dtype], 15)
+    _check_clip(grads, 0.5, [torch.full_like(g, float("nan")) for g in grads])
+    _check_clip(grads, 0.25)
+
+
 def test_clip_large_lists_take_the_large_chunks():
-    _check_clip(_list([3_000_001, 2_000_003], [F32, BF16], 9), 1.0)
+    """More than the last-level cache holds twice over, in both types."""
+    _check_clip(_list([50_000_001, 90_000_003], [F32, BF16], 9), 1.0)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
@@ -264,8 +277,24 @@ def test_adamw_more_tensors_than_a_launch_holds():
     _check_update(net, before, net.optimizer().step(net.grads), 1.0, 4)
 
 
+@pytest.mark.parametrize("dtype,masters,grad", [(F32, False, None), (BF16, True, None),
+                                                (F16, False, F32), (F16, True, F32)])
+@pytest.mark.parametrize("sizes", [[1, 2, 3, 1, 3, 45], [32768], [32769], [4093] * 8, [1] * 9])
+@pytest.mark.parametrize("max_norm", [0.5, None])
+def test_adamw_few_parameters(sizes, dtype, masters, grad, max_norm):
+    """Lists at and around what one launch takes; two updates, so that the
+    count that the workgroups keep is used twice."""
+    say("adamw", sizes, dtype, masters, grad)
+    net = Net(sizes, dtype, masters, 32, grad)
+    opt = net.optimizer(max_norm)
+    for t in (4, 5):
+        before = net.cpu()
+        _check_update(net, before, opt.step(net.grads), max_norm, t)
+    assert opt._step.tolist() == [5, 0]
+
+
 def test_adamw_large_lists_take_the_large_chunks():
-    net = Net([4_000_003, 500_001], F16, True, 23)
+    net = Net([20_000_003, 500_001], F16, True, 23)
     before = net.cpu()
     _check_update(net, before, net.optimizer().step(net.grads), 1.0, 4)
 
