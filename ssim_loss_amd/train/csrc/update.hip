@@ -643,17 +643,25 @@ int launch_kernel(const void* kernel, int grid, void* args, void* stream, int th
 
 int grid_for(uint32_t chunks) { return chunks < (uint32_t)kMaxBlocks ? (int)chunks : kMaxBlocks; }
 
-// A call that moves more than this streams: it takes larger chunks and leaves
-// nothing in the caches but the gradients between the two launches.  Measured
-// on AdamW, kept and streamed: 495 MB 92 and 95 us, 991 MB 214 and 180 us; on
-// clipping: 283 MB 68 and 71 us, 1416 MB 398 and 342 us.
-constexpr int64_t kStreamBytes = (int64_t)512 << 20;
-constexpr int kClipStreamU = 8, kAdamStreamU = 4;
+// A call that moves much streams: it takes larger chunks and leaves nothing in
+// the caches but the gradients between the two launches.  Measured on four
+// lists in turn, kept and streamed: clipping 66 MB of fp32 22.6 and 23.0 us,
+// 141 MB 45.5 and 39.2, 283 MB 88 and 71; AdamW over 115 MB 29 and 28 us, 231 MB
+// 54 and 49, 991 MB 224 and 191.  Larger chunks yet for clipping pay with many of
+// them only (1416 MB: 359 us with two vectors a thread, 339 with eight; 141 MB
+// in bf16: 40 and 52, since the last round of chunks leaves CUs idle).
+constexpr int64_t kClipStreamBytes = (int64_t)96 << 20, kClipLargeBytes = (int64_t)512 << 20;
+constexpr int64_t kAdamStreamBytes = (int64_t)128 << 20;
+constexpr int kClipStreamU = 2, kClipLargeU = 8, kAdamStreamU = 4;
+
+int clip_vectors(int64_t bytes) {
+  return bytes > kClipLargeBytes ? kClipLargeU : bytes > kClipStreamBytes ? kClipStreamU : 1;
+}
 
 // The norm launches.  *partials: how many partial sums they leave.
-int launch_norm(std::vector<NormRun>& runs, bool streams, Scratch* scratch, const StepArgs& step,
+int launch_norm(std::vector<NormRun>& runs, int64_t bytes, Scratch* scratch, const StepArgs& step,
                 int* partials, void* stream) {
-  const int U = streams ? kClipStreamU : 1;
+  const int U = clip_vectors(bytes);
   std::vector<Launch<NormRun>> launches;
   if (!plan(runs, kNormRuns,
             [&](const NormRun& r) { return (int64_t)(16 / elem_bytes(r.dtype)) * kThreads * U; },
@@ -673,8 +681,9 @@ int launch_norm(std::vector<NormRun>& runs, bool streams, Scratch* scratch, cons
     a.scratch = scratch;
     a.step = step;
     if (k > 0) a.step.step = nullptr;
-    const void* kernel = streams ? (const void*)ssim_grad_norm_kernel<kClipStreamU>
-                                 : (const void*)ssim_grad_norm_kernel<1>;
+    const void* kernel = U == 1              ? (const void*)ssim_grad_norm_kernel<1>
+                         : U == kClipStreamU ? (const void*)ssim_grad_norm_kernel<kClipStreamU>
+                                             : (const void*)ssim_grad_norm_kernel<kClipLargeU>;
     const int rc = launch_kernel(kernel, grid, &a, stream);
     if (rc != SSIM_OK) return rc;
   }
@@ -774,8 +783,7 @@ int clip_impl(const ssim_clip_item* items, int64_t count, bool scales, double ma
   for (const ClipRun& r : runs) norm_runs.push_back({r.grad, r.n, 0, r.dtype});
   StepArgs none;
   memset(&none, 0, sizeof(none));
-  const bool streams = bytes > kStreamBytes;
-  const int U = streams ? kClipStreamU : 1;
+  const int U = clip_vectors(bytes);
   std::vector<Launch<ClipRun>> launches;
   if (scales &&
       !plan(runs, kClipRuns,
@@ -783,7 +791,7 @@ int clip_impl(const ssim_clip_item* items, int64_t count, bool scales, double ma
             launches))
     return SSIM_ERR_OVERFLOW;
   int partials = 0;
-  rc = launch_norm(norm_runs, streams, scratch, none, &partials, stream);
+  rc = launch_norm(norm_runs, bytes, scratch, none, &partials, stream);
   if (rc != SSIM_OK) return rc;
   if (launches.empty()) {
     ssim_norm_only_kernel<<<dim3(1), dim3(kThreads), 0, static_cast<hipStream_t>(stream)>>>(
@@ -801,8 +809,9 @@ int clip_impl(const ssim_clip_item* items, int64_t count, bool scales, double ma
     a.max_norm = max_norm;
     a.norm = k == 0 ? norm : nullptr;
     a.scratch = scratch;
-    const void* kernel = streams ? (const void*)ssim_clip_grads_kernel<kClipStreamU>
-                                 : (const void*)ssim_clip_grads_kernel<1>;
+    const void* kernel = U == 1              ? (const void*)ssim_clip_grads_kernel<1>
+                         : U == kClipStreamU ? (const void*)ssim_clip_grads_kernel<kClipStreamU>
+                                             : (const void*)ssim_clip_grads_kernel<kClipLargeU>;
     rc = launch_kernel(kernel, grid_for(l.chunks), &a, stream);
     if (rc != SSIM_OK) return rc;
   }
@@ -839,7 +848,7 @@ int adamw_impl(const ssim_adamw_item* items, int64_t count, const ssim_adamw_opt
       misaligned(o->lr_device, 4))
     return SSIM_ERR_SHAPE;
   std::vector<AdamRun> runs;
-  int64_t total = 0, bytes = 0;
+  int64_t total = 0, bytes = 0, grad_bytes = 0;
   for (int64_t k = 0; k < count; ++k) {
     const ssim_adamw_item& it = items[k];
     if (it.n < 0) return SSIM_ERR_SHAPE;
@@ -853,6 +862,7 @@ int adamw_impl(const ssim_adamw_item* items, int64_t count, const ssim_adamw_opt
         misaligned(it.exp_avg_sq, 4) || misaligned(it.master, 4))
       return SSIM_ERR_SHAPE;
     if (it.n > kMaxBytes / 4 || (total += it.n) > kMaxBytes) return SSIM_ERR_OVERFLOW;
+    grad_bytes += it.n * gb;
     bytes += it.n * (gb + pb + 16 + (it.master ? 8 : pb));
     if (!runs.empty()) {
       AdamRun& r = runs.back();
@@ -905,7 +915,7 @@ int adamw_impl(const ssim_adamw_item* items, int64_t count, const ssim_adamw_opt
   }
 
   Scratch* scratch = static_cast<Scratch*>(workspace);
-  const bool streams = bytes > kStreamBytes;
+  const bool streams = bytes > kAdamStreamBytes;
   const int U = streams ? kAdamStreamU : 1;
   std::vector<Launch<AdamRun>> launches;
   if (!plan(runs, kAdamRuns, [&](const AdamRun&) { return (int64_t)kThreads * kAdamV * U; }, launches))
@@ -916,7 +926,7 @@ int adamw_impl(const ssim_adamw_item* items, int64_t count, const ssim_adamw_opt
     for (const AdamRun& r : runs) norm_runs.push_back({r.grad, r.n, 0, r.grad_dtype});
   }
   int partials = 0;  // (without a norm the first launch forms the scalars only)
-  rc = launch_norm(norm_runs, streams, scratch, st, &partials, stream);
+  rc = launch_norm(norm_runs, 2 * grad_bytes, scratch, st, &partials, stream);
   if (rc != SSIM_OK) return rc;
   if (launches.empty()) {
     if (!norm) return SSIM_OK;
