@@ -68,11 +68,12 @@ struct Row {
 
 // One vector of a row, as stored, with one load and no branch: a vector that
 // would pass the row's end is the row's last V elements instead, and settle()
-// moves them down to where they belong, with zeros behind the row's end.  (A
-// row of less than V elements is taken element by element.)
-template <class T, int V>
+// moves them down to where they belong, with zeros behind the row's end.
+// kNarrow: a row of less than V elements, which is taken element by element (by
+// kernels of its own: in the others that path costs registers and time).
+template <class T, int V, bool kNarrow>
 __device__ __forceinline__ Vec<T, V> load_cols(const T* row, int col, int width) {
-  if (width >= V) return load<T, V>(row + min(col, width - V));
+  if constexpr (!kNarrow) return load<T, V>(row + min(col, width - V));
   Vec<T, V> v = {};
   if (col == 0) {
 #pragma unroll
@@ -81,10 +82,10 @@ __device__ __forceinline__ Vec<T, V> load_cols(const T* row, int col, int width)
   }
   return v;
 }
-template <class T, int V>
+template <class T, int V, bool kNarrow>
 __device__ __forceinline__ void settle(Vec<T, V>& v, int col, int width) {
   int shift = col + V - width;  // elements
-  if (shift <= 0 || width < V) return;
+  if (kNarrow || shift <= 0) return;
   constexpr int kWords = V * (int)sizeof(T) / 4;
   union {
     Vec<T, V> v;
@@ -123,11 +124,11 @@ __device__ __forceinline__ void store_cols(T* row, int col, int width, Wide<V> w
     if (col + k < width) row[col + k] = v[k];
 }
 // a weight's columns; 1 where there is none
-template <int V>
+template <int V, bool kNarrow>
 __device__ __forceinline__ Wide<V> load_weight(const float* w, int col, int width) {
   if (w) {
-    Vec<float, V> v = load_cols<float, V>(w, col, width);
-    settle<float, V>(v, col, width);
+    Vec<float, V> v = load_cols<float, V, kNarrow>(w, col, width);
+    settle<float, V, kNarrow>(v, col, width);
     return v;
   }
   Wide<V> one;
@@ -142,13 +143,29 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   return a / b;
 }
 
-// act(g).  fp32 tensors take the exact exponential; for half types the fast
-// one (an error of a few 2^-24 of its argument) is far below their rounding.
+// act(g).  fp32 tensors take the exact exponential and quotient; for half types
+// the fast ones (errors of one step each, and a few 2^-24 of the argument) are
+// far below their rounding.
 template <class TB>
-__device__ __forceinline__ float activate(float g, int act) {
-  if (act != SSIM_GATE_SIGMOID) return g;
+__device__ __forceinline__ float sigmoid(float g) {
   if constexpr (sizeof(TB) == 4) return 1.0f / (1.0f + expf(-g));
-  else return __frcp_rn(1.0f + __expf(-g));
+  else return __builtin_amdgcn_rcpf(1.0f + __expf(-g));
+}
+// (the branch is once for all: one for each element left nothing to overlap)
+template <class TB, int V>
+__device__ __forceinline__ Wide<V> activate(Wide<V> g, int act) {
+  if (act == SSIM_GATE_SIGMOID) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) g[k] = sigmoid<TB>(g[k]);
+  }
+  return g;
+}
+
+// 1 / sqrt(v), v >= 0, off by a step at most.  The instruction takes subnormal
+// numbers for 0, so they are scaled.
+__device__ __forceinline__ float inv_root(float v) {
+  const bool tiny = v < 0x1p-100f;
+  return __builtin_amdgcn_rsqf(tiny ? v * 0x1p60f : v) * (tiny ? 0x1p30f : 1.0f);
 }
 
 // N sums over a row's threads at once.  kRowWave: the row is one wave's;
@@ -184,7 +201,7 @@ struct FwdRaw {
 
 // kPrefetch: a row's loads are issued while the row before it is worked on, the
 // first row's before the weights'.
-template <class TX, class TB, int I, bool kRowWave, bool kPrefetch>
+template <class TX, class TB, int I, bool kRowWave, bool kPrefetch, bool kNarrow>
 __device__ __forceinline__ void norm_forward(const NormParams& p) {
   constexpr int V = Row<TX, TB, I>::V;
   __shared__ float lds[2][1][kMaxWaves];
@@ -196,17 +213,33 @@ __device__ __forceinline__ void norm_forward(const NormParams& p) {
     row = row * kRowWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     stride *= kRowWaves;
   }
+  // the gate row of the row that is fetched next, and how far into its rows
+  // that one lies; kept by addition, since a quotient costs as much as a row
+  int64_t gate_row = row, gate_at = 0, gate_step = stride, gate_rest = 0;
+  if (p.gate_rows > 1) {
+    gate_row = quotient(row, p.gate_rows);
+    gate_at = row - gate_row * p.gate_rows;
+    gate_step = quotient(stride, p.gate_rows);
+    gate_rest = stride - gate_step * p.gate_rows;
+  }
   FwdRaw<TX, TB, V> next[I];
   auto fetch = [&](int64_t of) {
-    const int64_t at = of * width;
-    const int64_t gate_at = (p.gate_rows == 1 ? of : quotient(of, p.gate_rows)) * width;
+    const TB* b = (const TB*)p.b + of * width;
+    const TX* x = (const TX*)p.x + of * width;
+    const TB* gate = (const TB*)p.gate + gate_row * width;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
       const int col = (i * threads + q) * V;
-      next[i].b = load_cols<TB, V>((const TB*)p.b + at, col, width);
-      next[i].x = load_cols<TX, V>((const TX*)p.x + at, col, width);
+      next[i].b = load_cols<TB, V, kNarrow>(b, col, width);
+      next[i].x = load_cols<TX, V, kNarrow>(x, col, width);
       next[i].gate = 0;
-      if (p.gate) next[i].gate = load_cols<TB, V>((const TB*)p.gate + gate_at, col, width);
+      if (p.gate) next[i].gate = load_cols<TB, V, kNarrow>(gate, col, width);
+    }
+    gate_row += gate_step;
+    gate_at += gate_rest;
+    if (gate_at >= p.gate_rows) {
+      gate_at -= p.gate_rows;
+      ++gate_row;
     }
   };
   if (kPrefetch && row < p.rows) fetch(row);
@@ -218,8 +251,8 @@ __device__ __forceinline__ void norm_forward(const NormParams& p) {
 #pragma unroll
   for (int i = 0; i < I; ++i) {
     const int col = (i * threads + q) * V;
-    c[i] = load_weight<V>(p.scale, col, width) * load_weight<V>(p.post, col, width);
-    pre[i] = load_weight<V>(p.pre, col, width);
+    c[i] = load_weight<V, kNarrow>(p.scale, col, width) * load_weight<V, kNarrow>(p.post, col, width);
+    pre[i] = load_weight<V, kNarrow>(p.pre, col, width);
   }
   for (; row < p.rows; row += stride) {
     FwdRaw<TX, TB, V> raw[I];
@@ -230,36 +263,36 @@ __device__ __forceinline__ void norm_forward(const NormParams& p) {
 #pragma unroll
     for (int i = 0; i < I; ++i) {
       const int col = (i * threads + q) * V;
-      settle<TB, V>(raw[i].b, col, width);
-      settle<TX, V>(raw[i].x, col, width);
-      if (p.gate) settle<TB, V>(raw[i].gate, col, width);
+      settle<TB, V, kNarrow>(raw[i].b, col, width);
+      settle<TX, V, kNarrow>(raw[i].x, col, width);
+      if (p.gate) settle<TB, V, kNarrow>(raw[i].gate, col, width);
     }
     float s[1] = {0};
-    Wide<V> v[I];
+    Wide<V> v[I], ac[I];
 #pragma unroll
     for (int i = 0; i < I; ++i) {
       v[i] = widen<TB, V>(raw[i].b);
 #pragma unroll
       for (int k = 0; k < V; ++k) s[0] = fmaf(v[i][k], v[i][k], s[0]);
+      ac[i] = c[i];
+      if (p.gate) ac[i] *= activate<TB, V>(widen<TB, V>(raw[i].gate), p.act);
     }
     row_sums<kRowWave>(s, lds[0]);
-    const float ib = 1.0f / sqrtf(fmaf(s[0], p.inv_width, p.eps));
+    const float ib = inv_root(fmaf(s[0], p.inv_width, p.eps));
     s[0] = 0;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const Wide<V> xw = widen<TX, V>(raw[i].x), gw = widen<TB, V>(raw[i].gate);
+      const Wide<V> xw = widen<TX, V>(raw[i].x);
 #pragma unroll
       for (int k = 0; k < V; ++k) {
-        float ac = c[i][k];
-        if (p.gate) ac *= activate<TB>(gw[k], p.act);
-        const float r = fmaf(ac, v[i][k] * ib, xw[k]);
+        const float r = fmaf(ac[i][k], v[i][k] * ib, xw[k]);
         v[i][k] = r;
         s[0] = fmaf(r, r, s[0]);
       }
     }
     // (columns past the row's end hold zeros, so they add nothing)
     row_sums<kRowWave>(s, lds[1]);
-    const float ir = 1.0f / sqrtf(fmaf(s[0], p.inv_width, p.eps));
+    const float ir = inv_root(fmaf(s[0], p.inv_width, p.eps));
     TX* r = (TX*)p.r + row * width;
     TB* h = (TB*)p.h + row * width;
 #pragma unroll
@@ -282,26 +315,26 @@ struct Raw {
   Vec<TX, V> x, dr;
   Vec<TB, V> b, dh, gate;
 };
-template <class TX, class TB, int V, bool kGrouped>
+template <class TX, class TB, int V, bool kGrouped, bool kNarrow>
 __device__ __forceinline__ Raw<TX, TB, V> load_raw(const NormParams& p, int64_t at, int col) {
   Raw<TX, TB, V> f;
-  f.b = load_cols<TB, V>((const TB*)p.b + at, col, p.width);
-  f.x = load_cols<TX, V>((const TX*)p.x + at, col, p.width);
+  f.b = load_cols<TB, V, kNarrow>((const TB*)p.b + at, col, p.width);
+  f.x = load_cols<TX, V, kNarrow>((const TX*)p.x + at, col, p.width);
   f.gate = 0;
   f.dr = 0;
   f.dh = 0;
-  if (!kGrouped && p.gate) f.gate = load_cols<TB, V>((const TB*)p.gate + at, col, p.width);
-  if (p.dr) f.dr = load_cols<TX, V>((const TX*)p.dr + at, col, p.width);
-  if (p.dh) f.dh = load_cols<TB, V>((const TB*)p.dh + at, col, p.width);
+  if (!kGrouped && p.gate) f.gate = load_cols<TB, V, kNarrow>((const TB*)p.gate + at, col, p.width);
+  if (p.dr) f.dr = load_cols<TX, V, kNarrow>((const TX*)p.dr + at, col, p.width);
+  if (p.dh) f.dh = load_cols<TB, V, kNarrow>((const TB*)p.dh + at, col, p.width);
   return f;
 }
-template <class TX, class TB, int V, bool kGrouped>
+template <class TX, class TB, int V, bool kGrouped, bool kNarrow>
 __device__ __forceinline__ void settle_raw(Raw<TX, TB, V>& f, int col, int width) {
-  settle<TB, V>(f.b, col, width);
-  settle<TX, V>(f.x, col, width);
-  settle<TX, V>(f.dr, col, width);
-  settle<TB, V>(f.dh, col, width);
-  if constexpr (!kGrouped) settle<TB, V>(f.gate, col, width);
+  settle<TB, V, kNarrow>(f.b, col, width);
+  settle<TX, V, kNarrow>(f.x, col, width);
+  settle<TX, V, kNarrow>(f.dr, col, width);
+  settle<TB, V, kNarrow>(f.dh, col, width);
+  if constexpr (!kGrouped) settle<TB, V, kNarrow>(f.gate, col, width);
 }
 // and forms of it (names as below)
 template <int V>
@@ -316,9 +349,7 @@ __device__ __forceinline__ Terms<V> form_terms(const NormParams& p, const Raw<TX
   if constexpr (kGrouped) {
     f.a = group_a;
   } else if (p.gate) {
-    const Wide<V> g = widen<TB, V>(raw.gate);
-#pragma unroll
-    for (int k = 0; k < V; ++k) f.a[k] = activate<TB>(g[k], p.act);
+    f.a = activate<TB, V>(widen<TB, V>(raw.gate), p.act);
   } else {
 #pragma unroll
     for (int k = 0; k < V; ++k) f.a[k] = 1.0f;
@@ -344,7 +375,7 @@ __device__ __forceinline__ Terms<V> form_terms(const NormParams& p, const Raw<TX
 // not enter.
 // kGrouped: one gate row for many rows.  Then only S = sum of e bh is summed
 // over a group's rows, and dg = c act'(g) S, sum of a e bh = a S.
-template <class TX, class TB, int I, bool kRowWave, bool kGrouped>
+template <class TX, class TB, int I, bool kRowWave, bool kGrouped, bool kNarrow>
 __device__ __forceinline__ void norm_backward(const NormParams& p) {
   constexpr int V = Row<TX, TB, I>::V;
   // a thread of a very wide row cannot hold it: its vectors are loaded again,
@@ -369,8 +400,8 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
   Wide<V> c[kHeld], pre[kHeld], total[I], dpre[I], S[kGrouped ? I : 1], a[kGrouped ? I : 1];
   auto load_weights = [&](int i) {
     const int col = (i * threads + q) * V, to = kReload ? 0 : i;
-    c[to] = load_weight<V>(p.scale, col, width) * load_weight<V>(p.post, col, width);
-    pre[to] = load_weight<V>(p.pre, col, width);
+    c[to] = load_weight<V, kNarrow>(p.scale, col, width) * load_weight<V, kNarrow>(p.post, col, width);
+    pre[to] = load_weight<V, kNarrow>(p.pre, col, width);
   };
 #pragma unroll
   for (int i = 0; i < I; ++i) {
@@ -409,11 +440,9 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
 #pragma unroll
       for (int i = 0; i < I; ++i) {
         const int col = (i * threads + q) * V;
-        Vec<TB, V> gr = load_cols<TB, V>(g, col, width);
-        settle<TB, V>(gr, col, width);
-        const Wide<V> gw = widen<TB, V>(gr);
-#pragma unroll
-        for (int k = 0; k < V; ++k) a[i][k] = activate<TB>(gw[k], p.act);
+        Vec<TB, V> gr = load_cols<TB, V, kNarrow>(g, col, width);
+        settle<TB, V, kNarrow>(gr, col, width);
+        a[i] = activate<TB, V>(widen<TB, V>(gr), p.act);
         S[i] = 0;
       }
     } else {
@@ -428,7 +457,7 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
       if constexpr (!kReload) {
 #pragma unroll
         for (int i = 0; i < I; ++i)
-          next[i] = load_raw<TX, TB, V, kGrouped>(p, of * width, (i * threads + q) * V);
+          next[i] = load_raw<TX, TB, V, kGrouped, kNarrow>(p, of * width, (i * threads + q) * V);
       }
       next_ib = p.stats[2 * of];
       next_ir = p.stats[2 * of + 1];
@@ -452,9 +481,9 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
         if constexpr (kReload) {
           __builtin_amdgcn_sched_barrier(0);  // one vector at a time, for its registers
           load_weights(i);
-          raw[j] = load_raw<TX, TB, V, kGrouped>(p, at, (i * threads + q) * V);
+          raw[j] = load_raw<TX, TB, V, kGrouped, kNarrow>(p, at, (i * threads + q) * V);
         }
-        settle_raw<TX, TB, V, kGrouped>(raw[j], (i * threads + q) * V, width);
+        settle_raw<TX, TB, V, kGrouped, kNarrow>(raw[j], (i * threads + q) * V, width);
         const Wide<V> dw = widen<TB, V>(raw[j].dh);
         const Terms<V> f = form_terms<TX, TB, V, kGrouped>(p, raw[j], dw, ib, ir, c[j], pre[j],
                                                            a[kGrouped ? i : 0]);
@@ -480,8 +509,8 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
         if constexpr (kReload) {
           __builtin_amdgcn_sched_barrier(0);
           load_weights(i);
-          raw[j] = load_raw<TX, TB, V, kGrouped>(p, at, col);
-          settle_raw<TX, TB, V, kGrouped>(raw[j], col, width);
+          raw[j] = load_raw<TX, TB, V, kGrouped, kNarrow>(p, at, col);
+          settle_raw<TX, TB, V, kGrouped, kNarrow>(raw[j], col, width);
           terms[j] = form_terms<TX, TB, V, kGrouped>(p, raw[j], widen<TB, V>(raw[j].dh), ib, ir,
                                                      c[j], pre[j], a[kGrouped ? i : 0]);
         }
@@ -588,7 +617,8 @@ __device__ __forceinline__ void norm_sums(const NormParams& p) {
     p.dpre[col] = (float)s;
   } else {
     const int64_t at = (int64_t)(job - 2) * p.width + col;
-    const float a = activate<TB>((float)((const TB*)p.gate)[at], p.act);
+    const float g = (float)((const TB*)p.gate)[at];
+    const float a = p.act == SSIM_GATE_SIGMOID ? sigmoid<TB>(g) : g;
     double d = s * (p.scale ? (double)p.scale[col] : 1.0) * (p.post ? (double)p.post[col] : 1.0);
     if (p.act == SSIM_GATE_SIGMOID) d *= (double)a * (1.0 - (double)a);
     ((TB*)p.dg)[at] = (TB)(float)d;
@@ -599,6 +629,7 @@ __device__ __forceinline__ void norm_sums(const NormParams& p) {
 // How a row is spread: over a wave or a workgroup of at most so many waves,
 // vectors a thread.
 enum NormShape {
+  kNarrow,  // one wave, less than a vector
   kWave1,   // one wave, one vector
   kWave2,   // one wave, two
   kGroup1,  // 4 waves, one
@@ -608,7 +639,7 @@ enum NormShape {
   kGroup8,  // 8 waves, eight (fp32 blocks)
   kNormShapes
 };
-constexpr bool shape_wave(int s) { return s == kWave1 || s == kWave2; }
+constexpr bool shape_wave(int s) { return s == kNarrow || s == kWave1 || s == kWave2; }
 constexpr int shape_items(int s) {
   return s == kWave2 || s == kGroup2 ? 2 : s == kGroup4 ? 4 : s == kGroup8 ? 8 : 1;
 }
@@ -634,13 +665,13 @@ const NormTable& norm_table_bf16();
 template <class TX, class TB, int kShape>
 __global__ __launch_bounds__(shape_threads(kShape, kRowWaves)) void ssim_block_norm_fwd_kernel(
     const NormParams p) {
-  norm_forward<TX, TB, shape_items(kShape), shape_wave(kShape), shape_prefetch(kShape)>(
-      p);
+  norm_forward<TX, TB, shape_items(kShape), shape_wave(kShape), shape_prefetch(kShape),
+               kShape == kNarrow>(p);
 }
 template <class TX, class TB, int kShape, bool kGrouped>
 __global__ __launch_bounds__(shape_threads(kShape, kRowWavesBack)) void ssim_block_norm_bwd_kernel(
     const NormParams p) {
-  norm_backward<TX, TB, shape_items(kShape), shape_wave(kShape), kGrouped>(p);
+  norm_backward<TX, TB, shape_items(kShape), shape_wave(kShape), kGrouped, kShape == kNarrow>(p);
 }
 template <class TB>
 __global__ __launch_bounds__(kSumColumns* kSumSlices) void ssim_block_norm_sums_kernel(
@@ -658,6 +689,7 @@ void fill_shape(NormTable& t, int wide) {
 }
 template <class TX, class TB>
 void fill_types(NormTable& t, int wide) {
+  fill_shape<TX, TB, kNarrow>(t, wide);
   fill_shape<TX, TB, kWave1>(t, wide);
   fill_shape<TX, TB, kWave2>(t, wide);
   fill_shape<TX, TB, kGroup1>(t, wide);

@@ -47,7 +47,8 @@ Plan make_plan(const ssim_block_norm_inputs& in) {
   Plan p;
   const int xb = elem_bytes(in.x_dtype), bb = elem_bytes(in.branch_dtype);
   const int64_t vectors = ceil_div(in.width, 16 / bb);
-  p.shape = vectors <= kWave       ? kWave1
+  p.shape = in.width < 16 / bb     ? kNarrow
+            : vectors <= kWave     ? kWave1
             : vectors <= 2 * kWave ? kWave2
             : vectors <= 4 * kWave ? kGroup1
             : vectors <= 8 * kWave ? kGroup1w
