@@ -19,6 +19,7 @@
 namespace ssim_train {
 
 constexpr int kMaxWaves = 8;     // of a workgroup
+constexpr int kWideWaves = 16;    // of one whose threads load their vectors twice
 constexpr int kRowWaves = 4;     // rows (waves) of a workgroup where a wave takes a row: forward
 constexpr int kRowWavesBack = 8; // and backward
 constexpr int kSumColumns = 64; // columns a workgroup of the last sum takes
@@ -168,15 +169,15 @@ __device__ __forceinline__ float inv_root(float v) {
   return __builtin_amdgcn_rsqf(tiny ? v * 0x1p60f : v) * (tiny ? 0x1p30f : 1.0f);
 }
 
-// N sums over a row's threads at once.  kRowWave: the row is one wave's;
-// otherwise the workgroup's, with lds[N][kWaves], whose entries past the
+// N sums over a row's threads at once.  kLanes: so many lanes of a wave hold the
+// row; 0: the workgroup does, with lds[N][kWaves], whose entries past the
 // workgroup's waves are zero.  Two calls that follow each other take different
 // lds arrays: then the barrier within one separates the other's uses.
-template <bool kRowWave, int N, int kWaves>
+template <int kLanes, int N, int kWaves>
 __device__ __forceinline__ void row_sums(float (&s)[N], float (*lds)[kWaves]) {
 #pragma unroll
-  for (int k = 0; k < N; ++k) s[k] = wave_sum(s[k]);
-  if constexpr (!kRowWave) {
+  for (int k = 0; k < N; ++k) s[k] = lanes_sum<kLanes ? kLanes : kWave>(s[k]);
+  if constexpr (kLanes == 0) {
     if ((threadIdx.x & (kWave - 1)) == 0) {
 #pragma unroll
       for (int k = 0; k < N; ++k) lds[k][threadIdx.x / kWave] = s[k];
@@ -192,6 +193,15 @@ __device__ __forceinline__ void row_sums(float (&s)[N], float (*lds)[kWaves]) {
   }
 }
 
+// Which of a workgroup's rows this thread works on; a scalar where it is the
+// whole wave's.
+template <int kLanes>
+__device__ __forceinline__ int worker_of() {
+  if constexpr (kLanes == 0) return 0;
+  else if constexpr (kLanes == kWave) return __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  else return (int)threadIdx.x / kLanes;
+}
+
 // what the forward loads of one vector of a row
 template <class TX, class TB, int V>
 struct FwdRaw {
@@ -199,20 +209,19 @@ struct FwdRaw {
   Vec<TB, V> b, gate;
 };
 
-// kPrefetch: a row's loads are issued while the row before it is worked on, the
-// first row's before the weights'.
-template <class TX, class TB, int I, bool kRowWave, bool kPrefetch, bool kNarrow>
+// The first row's loads are issued before the weights', each other's while the
+// row before it is worked on: as soon as that one's registers are free, or
+// (kEarly) at its start.
+template <class TX, class TB, int I, int kLanes, bool kEarly, bool kNarrow>
 __device__ __forceinline__ void norm_forward(const NormParams& p) {
   constexpr int V = Row<TX, TB, I>::V;
   __shared__ float lds[2][1][kMaxWaves];
   const int width = p.width;
-  const int threads = kRowWave ? kWave : (int)blockDim.x;
-  const int q = kRowWave ? (int)threadIdx.x & (kWave - 1) : (int)threadIdx.x;
-  int64_t row = blockIdx.x, stride = gridDim.x;
-  if constexpr (kRowWave) {
-    row = row * kRowWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    stride *= kRowWaves;
-  }
+  const int threads = kLanes ? kLanes : (int)blockDim.x;
+  const int q = kLanes ? (int)threadIdx.x & (kLanes - 1) : (int)threadIdx.x;
+  constexpr int kWorkers = kLanes ? kRowWaves * kWave / kLanes : 1;
+  const int64_t stride = (int64_t)gridDim.x * kWorkers;
+  int64_t row = (int64_t)blockIdx.x * kWorkers + worker_of<kLanes>();
   // the gate row of the row that is fetched next, and how far into its rows
   // that one lies; kept by addition, since a quotient costs as much as a row
   int64_t gate_row = row, gate_at = 0, gate_step = stride, gate_rest = 0;
@@ -242,8 +251,8 @@ __device__ __forceinline__ void norm_forward(const NormParams& p) {
       ++gate_row;
     }
   };
-  if (kPrefetch && row < p.rows) fetch(row);
-  if constexpr (!kRowWave) {
+  if (row < p.rows) fetch(row);
+  if constexpr (kLanes == 0) {
     if (threadIdx.x < 2 * kMaxWaves) (&lds[0][0][0])[threadIdx.x] = 0;
     __syncthreads();
   }
@@ -256,10 +265,10 @@ __device__ __forceinline__ void norm_forward(const NormParams& p) {
   }
   for (; row < p.rows; row += stride) {
     FwdRaw<TX, TB, V> raw[I];
-    if (!kPrefetch) fetch(row);
 #pragma unroll
     for (int i = 0; i < I; ++i) raw[i] = next[i];
-    if (kPrefetch && row + stride < p.rows) fetch(row + stride);
+    const bool more = row + stride < p.rows;
+    if (kEarly && more) fetch(row + stride);
 #pragma unroll
     for (int i = 0; i < I; ++i) {
       const int col = (i * threads + q) * V;
@@ -277,7 +286,7 @@ __device__ __forceinline__ void norm_forward(const NormParams& p) {
       ac[i] = c[i];
       if (p.gate) ac[i] *= activate<TB, V>(widen<TB, V>(raw[i].gate), p.act);
     }
-    row_sums<kRowWave>(s, lds[0]);
+    row_sums<kLanes>(s, lds[0]);
     const float ib = inv_root(fmaf(s[0], p.inv_width, p.eps));
     s[0] = 0;
 #pragma unroll
@@ -291,7 +300,7 @@ __device__ __forceinline__ void norm_forward(const NormParams& p) {
       }
     }
     // (columns past the row's end hold zeros, so they add nothing)
-    row_sums<kRowWave>(s, lds[1]);
+    row_sums<kLanes>(s, lds[1]);
     const float ir = inv_root(fmaf(s[0], p.inv_width, p.eps));
     TX* r = (TX*)p.r + row * width;
     TB* h = (TB*)p.h + row * width;
@@ -306,6 +315,7 @@ __device__ __forceinline__ void norm_forward(const NormParams& p) {
       p.stats[2 * row] = ib;
       p.stats[2 * row + 1] = ir;
     }
+    if (!kEarly && more) fetch(row + stride);
   }
 }
 
@@ -375,37 +385,49 @@ __device__ __forceinline__ Terms<V> form_terms(const NormParams& p, const Raw<TX
 // not enter.
 // kGrouped: one gate row for many rows.  Then only S = sum of e bh is summed
 // over a group's rows, and dg = c act'(g) S, sum of a e bh = a S.
-template <class TX, class TB, int I, bool kRowWave, bool kGrouped, bool kNarrow>
+// kReload: a thread of a very wide row cannot hold it; its vectors, the weights'
+// and the gate's are loaded again, from the caches, after the reduction.
+template <class TX, class TB, int I, int kLanes, bool kGrouped, bool kNarrow, bool kReload>
 __device__ __forceinline__ void norm_backward(const NormParams& p) {
   constexpr int V = Row<TX, TB, I>::V;
-  // a thread of a very wide row cannot hold it: its vectors are loaded again,
-  // from the caches, after the reduction
-  constexpr bool kReload = Row<TX, TB, I>::E > 16;
-  constexpr int kWaves = kMaxWaves;
+  constexpr int kWaves = kReload ? kWideWaves : kMaxWaves;
   // (two vectors of a thread twice over do not fit its registers, unless the
   // group's are missing)
-  constexpr bool kPrefetch = I == 1 || (I == 2 && kRowWave && !kGrouped);
+  constexpr bool kPrefetch = kReload || I == 1 || (I == 2 && kLanes && !kGrouped);
   __shared__ float lds[2][3][kWaves];
-  if constexpr (!kRowWave) {
+  if constexpr (kLanes == 0) {
     for (int k = threadIdx.x; k < 6 * kWaves; k += blockDim.x) (&lds[0][0][0])[k] = 0;
     __syncthreads();
   }
   const int width = p.width;
-  const int threads = kRowWave ? kWave : (int)blockDim.x;
-  const int q = kRowWave ? (int)threadIdx.x & (kWave - 1) : (int)threadIdx.x;
-  const int wave = kRowWave ? __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) : 0;
-  constexpr int kWorkers = kRowWave ? kRowWavesBack : 1;
+  const int threads = kLanes ? kLanes : (int)blockDim.x;
+  const int q = kLanes ? (int)threadIdx.x & (kLanes - 1) : (int)threadIdx.x;
+  const int worker = worker_of<kLanes>();
+  constexpr int kWorkers = kLanes ? kRowWavesBack * kWave / kLanes : 1;
 
+  // The first column of this thread's vector i.  Where vectors are loaded again,
+  // the compiler may not see that it is the same one: it would keep the values,
+  // or their addresses, in registers that are not there.
+  auto col_of = [&](int i) {
+    int at = q;
+    if constexpr (kReload) asm volatile("" : "+v"(at));
+    return (i * threads + at) * V;
+  };
   constexpr int kHeld = kReload ? 1 : I;  // vectors of the weights and of a row that stay
-  Wide<V> c[kHeld], pre[kHeld], total[I], dpre[I], S[kGrouped ? I : 1], a[kGrouped ? I : 1];
-  auto load_weights = [&](int i) {
-    const int col = (i * threads + q) * V, to = kReload ? 0 : i;
+  Wide<V> c[kHeld], pre[kHeld], total[I], dpre[I], S[kGrouped ? I : 1], a[kGrouped ? kHeld : 1];
+  auto load_weights = [&](int i, int col) {
+    const int to = kReload ? 0 : i;
     c[to] = load_weight<V, kNarrow>(p.scale, col, width) * load_weight<V, kNarrow>(p.post, col, width);
     pre[to] = load_weight<V, kNarrow>(p.pre, col, width);
   };
+  auto load_gate = [&](int64_t group, int i, int col) {
+    Vec<TB, V> g = load_cols<TB, V, kNarrow>((const TB*)p.gate + group * width, col, width);
+    settle<TB, V, kNarrow>(g, col, width);
+    a[kReload ? 0 : i] = activate<TB, V>(widen<TB, V>(g), p.act);
+  };
 #pragma unroll
   for (int i = 0; i < I; ++i) {
-    if constexpr (!kReload) load_weights(i);
+    if constexpr (!kReload) load_weights(i, col_of(i));
     total[i] = 0;
     dpre[i] = 0;
   }
@@ -419,7 +441,7 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
     seg = blockIdx.x;
     seg_stride = gridDim.x;
     if (p.parts == 1) {
-      seg = seg * kWorkers + wave;
+      seg = seg * kWorkers + worker;
       seg_stride *= kWorkers;
     }
   }
@@ -433,20 +455,16 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
       if (end > (group + 1) * p.gate_rows) end = (group + 1) * p.gate_rows;
       stride = 1;
       if (p.parts > 1) {
-        row += wave;
+        row += worker;
         stride = kWorkers;
       }
-      const TB* g = (const TB*)p.gate + group * width;
 #pragma unroll
       for (int i = 0; i < I; ++i) {
-        const int col = (i * threads + q) * V;
-        Vec<TB, V> gr = load_cols<TB, V, kNarrow>(g, col, width);
-        settle<TB, V, kNarrow>(gr, col, width);
-        a[i] = activate<TB, V>(widen<TB, V>(gr), p.act);
+        if constexpr (!kReload) load_gate(group, i, col_of(i));
         S[i] = 0;
       }
     } else {
-      row = (int64_t)blockIdx.x * kWorkers + wave;
+      row = (int64_t)blockIdx.x * kWorkers + worker;
       stride = (int64_t)gridDim.x * kWorkers;
       end = p.rows;
     }
@@ -457,7 +475,7 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
       if constexpr (!kReload) {
 #pragma unroll
         for (int i = 0; i < I; ++i)
-          next[i] = load_raw<TX, TB, V, kGrouped, kNarrow>(p, of * width, (i * threads + q) * V);
+          next[i] = load_raw<TX, TB, V, kGrouped, kNarrow>(p, of * width, col_of(i));
       }
       next_ib = p.stats[2 * of];
       next_ir = p.stats[2 * of + 1];
@@ -477,16 +495,17 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
       Terms<V> terms[kHeld];
 #pragma unroll
       for (int i = 0; i < I; ++i) {
-        const int j = kReload ? 0 : i;
+        const int col = col_of(i), j = kReload ? 0 : i;
         if constexpr (kReload) {
           __builtin_amdgcn_sched_barrier(0);  // one vector at a time, for its registers
-          load_weights(i);
-          raw[j] = load_raw<TX, TB, V, kGrouped, kNarrow>(p, at, (i * threads + q) * V);
+          load_weights(i, col);
+          if constexpr (kGrouped) load_gate(group, i, col);
+          raw[j] = load_raw<TX, TB, V, kGrouped, kNarrow>(p, at, col);
         }
-        settle_raw<TX, TB, V, kGrouped, kNarrow>(raw[j], (i * threads + q) * V, width);
+        settle_raw<TX, TB, V, kGrouped, kNarrow>(raw[j], col, width);
         const Wide<V> dw = widen<TB, V>(raw[j].dh);
         const Terms<V> f = form_terms<TX, TB, V, kGrouped>(p, raw[j], dw, ib, ir, c[j], pre[j],
-                                                           a[kGrouped ? i : 0]);
+                                                           a[kGrouped ? j : 0]);
 #pragma unroll
         for (int k = 0; k < V; ++k) {
           const float acbh = f.a[k] * c[j][k] * f.bh[k];
@@ -497,7 +516,7 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
         }
         terms[j] = f;
       }
-      row_sums<kRowWave>(s, lds[parity]);
+      row_sums<kLanes>(s, lds[parity]);
       const float m1 = ir * (s[0] * p.inv_width);
       const float m2 = s[1] * p.inv_width - m1 * (s[2] * p.inv_width);
       TX* dx = (TX*)p.dx + (p.dx ? at : 0);
@@ -505,14 +524,15 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
       TB* dg = (TB*)p.dg + (p.dg ? at : 0);
 #pragma unroll
       for (int i = 0; i < I; ++i) {
-        const int col = (i * threads + q) * V, j = kReload ? 0 : i;
+        const int col = col_of(i), j = kReload ? 0 : i;
         if constexpr (kReload) {
           __builtin_amdgcn_sched_barrier(0);
-          load_weights(i);
+          load_weights(i, col);
+          if constexpr (kGrouped) load_gate(group, i, col);
           raw[j] = load_raw<TX, TB, V, kGrouped, kNarrow>(p, at, col);
           settle_raw<TX, TB, V, kGrouped, kNarrow>(raw[j], col, width);
           terms[j] = form_terms<TX, TB, V, kGrouped>(p, raw[j], widen<TB, V>(raw[j].dh), ib, ir,
-                                                     c[j], pre[j], a[kGrouped ? i : 0]);
+                                                     c[j], pre[j], a[kGrouped ? j : 0]);
         }
         const Terms<V>& f = terms[j];
         const Wide<V> e = f.u - f.rh * m1, eb = e * f.bh;
@@ -534,12 +554,16 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
       TB* dg = (TB*)p.dg + (p.dg ? group * width : 0);
 #pragma unroll
       for (int i = 0; i < I; ++i) {
-        const int col = (i * threads + q) * V, j = kReload ? 0 : i;
-        total[i] += S[i] * a[i];
+        const int col = col_of(i), j = kReload ? 0 : i;
+        if constexpr (kReload) {
+          __builtin_amdgcn_sched_barrier(0);
+          load_weights(i, col);
+          load_gate(group, i, col);
+        }
+        total[i] += S[i] * a[j];
         if (p.parts == 1 && p.dg && col < width) {
-          if constexpr (kReload) load_weights(i);
           Wide<V> d = S[i] * c[j];
-          if (p.act == SSIM_GATE_SIGMOID) d *= a[i] * (1.0f - a[i]);
+          if (p.act == SSIM_GATE_SIGMOID) d *= a[j] * (1.0f - a[j]);
           store_cols<TB, V>(dg, col, width, d);
         }
       }
@@ -552,8 +576,8 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
   for (int k = 0; k < (kGrouped ? 3 : 2); ++k) {
     if (!out[k]) continue;
     float* to = out[k] + (int64_t)blockIdx.x * width;
-    if constexpr (kRowWave) {
-      __shared__ float waves[kRowWavesBack][kWave * V * I];
+    if constexpr (kLanes != 0) {
+      __shared__ float rows[kWorkers][kLanes * V * I];
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < I; ++i) {
@@ -561,13 +585,13 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
         if constexpr (kGrouped) v = k == 0 ? total[i] : k == 1 ? dpre[i] : S[i];
         else v = k == 0 ? total[i] : dpre[i];
 #pragma unroll
-        for (int e = 0; e < V; ++e) waves[wave][(i * kWave + q) * V + e] = v[e];
+        for (int e = 0; e < V; ++e) rows[worker][(i * kLanes + q) * V + e] = v[e];
       }
       __syncthreads();
       for (int col = threadIdx.x; col < width; col += kRowWavesBack * kWave) {
         float v = 0;
 #pragma unroll
-        for (int w = 0; w < kRowWavesBack; ++w) v += waves[w][col];
+        for (int w = 0; w < kWorkers; ++w) v += rows[w][col];
         to[col] = v;
       }
     } else {
@@ -626,11 +650,14 @@ __device__ __forceinline__ void norm_sums(const NormParams& p) {
 }
 
 // ---- the kernels of one block type
-// How a row is spread: over a wave or a workgroup of at most so many waves,
-// vectors a thread.
+// How a row is spread: over so many lanes of a wave, or a workgroup of at most
+// so many waves; vectors a thread.
 enum NormShape {
-  kNarrow,  // one wave, less than a vector
-  kWave1,   // one wave, one vector
+  kNarrow,  // 8 lanes, less than a vector
+  kLanes8,  // 8 lanes, one vector
+  kLanes16, // 16 lanes, one
+  kLanes32, // 32 lanes, one
+  kWave1,   // one wave, one
   kWave2,   // one wave, two
   kGroup1,  // 4 waves, one
   kGroup1w, // 8 waves, one
@@ -639,18 +666,31 @@ enum NormShape {
   kGroup8,  // 8 waves, eight (fp32 blocks)
   kNormShapes
 };
-constexpr bool shape_wave(int s) { return s == kNarrow || s == kWave1 || s == kWave2; }
+constexpr int shape_lanes(int s) {  // 0: a workgroup's row
+  return s <= kLanes8 ? 8 : s == kLanes16 ? 16 : s == kLanes32 ? 32 : s <= kWave2 ? kWave : 0;
+}
 constexpr int shape_items(int s) {
   return s == kWave2 || s == kGroup2 ? 2 : s == kGroup4 ? 4 : s == kGroup8 ? 8 : 1;
 }
 constexpr int shape_threads(int s, int row_waves) {
-  return (shape_wave(s) ? row_waves : s == kGroup1 ? 4 : kMaxWaves) * kWave;
+  return (shape_lanes(s) ? row_waves : s == kGroup1 ? 4 : kMaxWaves) * kWave;
+}
+// A thread of the backward that would hold more than 16 elements of a row has
+// not the registers: workgroups of twice as many threads load them twice.
+// Forward and gradients of 2000 x 16384 in bf16 347 us (with a thread's elements
+// held by eight waves, half of them spilled to memory, 920), of 2000 x 10000 in
+// fp32 448 (700).
+constexpr bool shape_reload(int s, int bytes) { return shape_items(s) * 16 / bytes > 16; }
+constexpr int shape_back_items(int s, int bytes) {
+  return shape_reload(s, bytes) ? shape_items(s) / 2 : shape_items(s);
+}
+constexpr int shape_back_threads(int s, int bytes) {
+  return shape_reload(s, bytes) ? kWideWaves * kWave : shape_threads(s, kRowWavesBack);
 }
 // A workgroup of more than four waves to a row waits at its barriers with few
-// others beside it; there the next row's loads go out early.  Where many waves
-// are resident that gains nothing and costs registers: at 4100 x 1152 in fp16
-// 12.6 us without and 13.3 with, at 16384 x 4096 in bf16 124 and 100.
-constexpr bool shape_prefetch(int s) { return s == kGroup1w || s == kGroup2; }
+// others beside it; there the next row's loads go out at its start.  Where many
+// waves are resident that gains nothing and costs registers.
+constexpr bool shape_early(int s) { return s == kGroup1w || s == kGroup2; }
 
 struct NormTable {
   const void* forward[2][kNormShapes];      // [x is fp32 beside a half type]
@@ -665,13 +705,14 @@ const NormTable& norm_table_bf16();
 template <class TX, class TB, int kShape>
 __global__ __launch_bounds__(shape_threads(kShape, kRowWaves)) void ssim_block_norm_fwd_kernel(
     const NormParams p) {
-  norm_forward<TX, TB, shape_items(kShape), shape_wave(kShape), shape_prefetch(kShape),
+  norm_forward<TX, TB, shape_items(kShape), shape_lanes(kShape), shape_early(kShape),
                kShape == kNarrow>(p);
 }
 template <class TX, class TB, int kShape, bool kGrouped>
-__global__ __launch_bounds__(shape_threads(kShape, kRowWavesBack)) void ssim_block_norm_bwd_kernel(
+__global__ __launch_bounds__(shape_back_threads(kShape, sizeof(TB))) void ssim_block_norm_bwd_kernel(
     const NormParams p) {
-  norm_backward<TX, TB, shape_items(kShape), shape_wave(kShape), kGrouped, kShape == kNarrow>(p);
+  norm_backward<TX, TB, shape_back_items(kShape, sizeof(TB)), shape_lanes(kShape), kGrouped,
+                kShape == kNarrow, shape_reload(kShape, sizeof(TB))>(p);
 }
 template <class TB>
 __global__ __launch_bounds__(kSumColumns* kSumSlices) void ssim_block_norm_sums_kernel(
@@ -690,6 +731,9 @@ void fill_shape(NormTable& t, int wide) {
 template <class TX, class TB>
 void fill_types(NormTable& t, int wide) {
   fill_shape<TX, TB, kNarrow>(t, wide);
+  fill_shape<TX, TB, kLanes8>(t, wide);
+  fill_shape<TX, TB, kLanes16>(t, wide);
+  fill_shape<TX, TB, kLanes32>(t, wide);
   fill_shape<TX, TB, kWave1>(t, wide);
   fill_shape<TX, TB, kWave2>(t, wide);
   fill_shape<TX, TB, kGroup1>(t, wide);

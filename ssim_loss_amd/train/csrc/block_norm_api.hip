@@ -38,9 +38,9 @@ int64_t blocks_for(int64_t rows, int64_t workers, int64_t target) {
   return ceil_div(need, each);
 }
 
-int threads_of(int shape, int row_waves, int64_t vectors) {
-  if (shape_wave(shape)) return row_waves * kWave;
-  return (int)ceil_div(ceil_div(vectors, shape_items(shape)), kWave) * kWave;
+int threads_of(int shape, int row_waves, int items, int64_t vectors) {
+  if (shape_lanes(shape)) return row_waves * kWave;
+  return (int)ceil_div(ceil_div(vectors, items), kWave) * kWave;
 }
 
 Plan make_plan(const ssim_block_norm_inputs& in) {
@@ -48,6 +48,9 @@ Plan make_plan(const ssim_block_norm_inputs& in) {
   const int xb = elem_bytes(in.x_dtype), bb = elem_bytes(in.branch_dtype);
   const int64_t vectors = ceil_div(in.width, 16 / bb);
   p.shape = in.width < 16 / bb     ? kNarrow
+            : vectors <= 8         ? kLanes8
+            : vectors <= 16        ? kLanes16
+            : vectors <= 32        ? kLanes32
             : vectors <= kWave     ? kWave1
             : vectors <= 2 * kWave ? kWave2
             : vectors <= 4 * kWave ? kGroup1
@@ -55,29 +58,30 @@ Plan make_plan(const ssim_block_norm_inputs& in) {
             : vectors <= 16 * kWave ? kGroup2
             : vectors <= 32 * kWave ? kGroup4
                                     : kGroup8;
-  const bool wave = shape_wave(p.shape);
+  const int lanes = shape_lanes(p.shape);
   p.wide = in.x_dtype != in.branch_dtype;
-  p.threads = threads_of(p.shape, kRowWaves, vectors);
-  p.back_threads = threads_of(p.shape, kRowWavesBack, vectors);
+  p.threads = threads_of(p.shape, kRowWaves, shape_items(p.shape), vectors);
+  p.back_threads = threads_of(p.shape, kRowWavesBack, shape_back_items(p.shape, bb), vectors);
   p.grouped = in.gate && in.gate_rows > 1;
 
   // Forward: rows in work whose loads are 48 KB on each CU; where a row is a
-  // workgroup's 24 KB, 32 KB with the next row's loads out beside them.  Fewer
+  // workgroup's 28 KB, 32 KB with the next row's loads out beside them.  Fewer
   // leave the memory idle; more read the weights more often and end unevenly.
-  // Measured with 24 and 48 KB: 4100 x 1153 fp16 13.1 and 14.6 us (a workgroup
-  // a row), 65536 x 512 bf16 57.8 and 54.0 us (a wave a row).
+  // Measured with 24, 28 and 36 KB where a row is a workgroup's: 4100 x 1153 fp16
+  // 12.2, 11.5 and 11.7 us, 32768 x 2048 bf16 beside fp32 163, 163 and 182 us;
+  // with 32 and 48 KB where it is a wave's: 65536 x 512 bf16 63 and 55 us.
   const int64_t row_bytes = in.width * (xb + bb + (in.gate && !p.grouped ? bb : 0));
-  const int64_t in_work = wave ? 48 << 10 : shape_prefetch(p.shape) ? 32 << 10 : 24 << 10;
+  const int64_t in_work = lanes ? 48 << 10 : shape_early(p.shape) ? 32 << 10 : 28 << 10;
   const int64_t rows_per_cu = ceil_div(in_work, row_bytes);
-  p.blocks = (int)(wave ? blocks_for(in.rows, kRowWaves, kCUs * ceil_div(rows_per_cu, kRowWaves))
-                        : blocks_for(in.rows, 1, kCUs * rows_per_cu));
+  const int fwd_workers = lanes ? kRowWaves * kWave / lanes : 1;
+  p.blocks = (int)blocks_for(in.rows, fwd_workers, kCUs * ceil_div(rows_per_cu, fwd_workers));
 
   // Backward: 16 KB, since each workgroup leaves a row of partial sums.
   // Measured with 16 and 32 KB: 4100 x 1152 fp16 18.8 and 23.4 us, 32768 x
   // 2048 bf16 beside fp32 266 and 290 us.  Blocks in fp32 leave room for two
   // workgroups of eight waves on a CU, and one waits at its barriers too long
   // (16384 x 2048: 195 us with two, 230 with one).
-  const int workers = wave ? kRowWavesBack : 1;
+  const int workers = lanes ? kRowWavesBack * kWave / lanes : 1;
   const int64_t back_bytes = in.width * (2 * xb + 2 * bb + (in.gate && !p.grouped ? bb : 0));
   int64_t per_cu = ceil_div(ceil_div(16 << 10, back_bytes), workers);
   if (bb == 4 && p.shape <= kGroup2 && per_cu < 1024 / p.back_threads) per_cu = 1024 / p.back_threads;

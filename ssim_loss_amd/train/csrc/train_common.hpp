@@ -108,6 +108,19 @@ __device__ __forceinline__ T wave_sum(T v) {
   return last_lane(v);
 }
 
+// The sum of each kLanes lanes beside each other, of 8, 16, 32 or the wave's 64.
+template <int kLanes>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if constexpr (kLanes == kWave) return wave_sum(v);
+  v += lane_move<0xB1, 0xf>(v);
+  v += lane_move<0x4E, 0xf>(v);
+  v += lane_move<0x141, 0xf>(v);
+  if constexpr (kLanes >= 16) v += lane_move<0x140, 0xf>(v);
+  if constexpr (kLanes == 32)  // the lane 16 away
+    v += __builtin_bit_cast(float, __builtin_amdgcn_ds_swizzle(__builtin_bit_cast(int, v), 0x401F));
+  return v;
+}
+
 // ---- host side
 inline int elem_bytes(int dtype) { return dtype == SSIM_DTYPE_F32 ? 4 : 2; }
 inline bool known_dtype(int dtype) {

@@ -105,6 +105,17 @@ def test_rows_and_groups(shape, gate, types):
     verify(make(shape, types, gate=gate, act="sigmoid", seed=40))
 
 
+# rows that 8, 16, 32 and 64 lanes take, in either type, with several to a wave:
+# rows left over in the last one, groups that end inside one
+@pytest.mark.parametrize("types", [(F32, F32), (BF16, BF16), (F32, F16)])
+@pytest.mark.parametrize("width", [3, 31, 32, 33, 63, 64, 65, 127, 128, 129, 256, 257])
+def test_several_rows_to_a_wave(width, types):
+    say("joint", width, types)
+    verify(make((2, 1301, width), types, gate=(2, 1301, width), act="sigmoid", seed=width))
+    verify(make((3, 75, width), types, gate=(3, 1, width), act="sigmoid", seed=width + 1))
+    verify(make((1500, 3, width), types, gate=(1500, 1, width), seed=width + 2))
+
+
 @pytest.mark.parametrize("types", [(F32, F32), (F16, F16), (F32, BF16)])
 @pytest.mark.parametrize("width", [640, 1153, 2048])
 def test_tensors_that_start_anywhere(width, types):
