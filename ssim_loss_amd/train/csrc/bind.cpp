@@ -9,9 +9,13 @@
 #include <ATen/ATen.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/core/GradMode.h>
+#include <c10/hip/HIPGraphsC10Utils.h>
 #include <c10/hip/HIPStream.h>
-#include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/function.h>
+#include <torch/csrc/autograd/functions/utils.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/autograd/saved_variable.h>
+#include <torch/csrc/autograd/variable.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include <optional>
@@ -277,48 +281,56 @@ void forward_into(const ssim_block_norm_inputs& in, const Tensor& residual, cons
   TORCH_CHECK(rc == SSIM_OK, "ssim_block_norm_forward: ", text(rc));
 }
 
-struct BlockNorm : torch::autograd::Function<BlockNorm> {
-  static torch::autograd::variable_list forward(torch::autograd::AutogradContext* ctx,
-                                                const Tensor& x, const Tensor& branch,
-                                                const std::optional<Tensor>& gate_,
-                                                const std::optional<Tensor>& scale_,
-                                                const std::optional<Tensor>& post_,
-                                                const std::optional<Tensor>& pre_, double eps,
-                                                int64_t act, int64_t wants) {
-    const Tensor gate = gate_.value_or(Tensor()), scale = scale_.value_or(Tensor()),
-                 post = post_.value_or(Tensor()), pre = pre_.value_or(Tensor());
-    const c10::Device dev = x.device();
-    const c10::DeviceGuard guard(dev);
-    const ssim_block_norm_inputs in = inputs_of(x, branch, gate, scale, post, pre, eps, (int)act);
-    Tensor residual = at::empty(x.sizes(), x.options());
-    Tensor normed = at::empty(branch.sizes(), branch.options());
-    Tensor stats = at::empty({in.rows, 2}, x.options().dtype(at::kFloat));
-    forward_into(in, residual, normed, stats.data_ptr<float>(), dev);
-    ctx->save_for_backward({x, branch, gate, scale, post, pre, stats});
-    ctx->saved_data["eps"] = eps;
-    ctx->saved_data["act"] = act;
-    ctx->saved_data["wants"] = wants;
-    ctx->set_materialize_grads(false);
-    return {residual, normed};
+// A backward pass under capture ends in its inputs' nodes.  Where one of them was
+// made on the default stream, by an eager graph that still lives, that stream
+// would be made to wait for the capturing one, which HIP does not allow and the
+// process does not survive.  So the forward of such a pass is refused.  (Streams
+// are compared by number: torch gives them a device type of its own.)
+void check_capture(const torch::autograd::edge_list& edges, const c10::Device& dev) {
+  if (c10::hip::currentStreamCaptureStatusMayInitCtx() == c10::hip::CaptureStatus::None) return;
+  const c10::StreamId eager = c10::hip::getDefaultHIPStream(dev.index()).id();
+  for (const auto& edge : edges) {
+    if (!edge.function) continue;
+    const auto stream = edge.function->stream();
+    TORCH_CHECK(!stream || stream->id() != eager, "block_norm: captured with gradients, but the node ",
+                edge.function->name(), " of an input belongs to the default stream: let go of "
+                "graphs that were made of it outside the capture, or use torch.no_grad()");
+  }
+}
+
+// The joint's node in an autograd graph.  A node itself, not a Function with a
+// context: that recorded a call in 2.8 us more than this.
+struct BlockNormBackward : torch::autograd::Node {
+  static constexpr int kTensors = 7;  // x, branch, gate, scale, post and pre weight; the row's roots
+  torch::autograd::SavedVariable saved[kTensors];
+  double eps = 0;
+  int act = 0;
+
+  std::string name() const override { return "BlockNormBackward"; }
+
+  void release_variables() override {
+    std::lock_guard<std::mutex> lock(mutex_);
+    for (auto& s : saved) s.reset_data();
   }
 
-  static torch::autograd::variable_list backward(torch::autograd::AutogradContext* ctx,
-                                                 torch::autograd::variable_list upstream) {
+  torch::autograd::variable_list apply(torch::autograd::variable_list&& upstream) override {
+    std::lock_guard<std::mutex> lock(mutex_);
     TORCH_CHECK(!at::GradMode::is_enabled(),
                 "block_norm: the gradient of the gradient is not available (create_graph=True)");
-    const auto saved = ctx->get_saved_variables();
-    const Tensor &x = saved[0], &branch = saved[1], &stats = saved[6];
+    Tensor in_[kTensors];
+    for (int k = 0; k < kTensors; ++k) in_[k] = saved[k].unpack();
+    const Tensor &x = in_[0], &stats = in_[6];
     const c10::Device dev = x.device();
     const c10::DeviceGuard guard(dev);
     const ssim_block_norm_inputs in =
-        inputs_of(x, branch, saved[2], saved[3], saved[4], saved[5],
-                  ctx->saved_data["eps"].toDouble(), (int)ctx->saved_data["act"].toInt());
-    torch::autograd::variable_list out(9);
-    const int64_t wants = ctx->saved_data["wants"].toInt();
+        inputs_of(x, in_[1], in_[2], in_[3], in_[4], in_[5], eps, act);
+    torch::autograd::variable_list out(kTensors - 1);
+    Tensor dr = upstream[0], dh = upstream[1];
+    if (!dr.defined() && !dh.defined()) return out;
     auto wanted = [&](int k) -> void* {
-      if (!(wants >> k & 1)) return nullptr;
-      out[k] = in.rows > 0 ? at::empty(saved[k].sizes(), saved[k].options())
-                           : at::zeros(saved[k].sizes(), saved[k].options());
+      if (!in_[k].defined() || !task_should_compute_output(k)) return nullptr;
+      out[k] = in.rows > 0 ? at::empty(in_[k].sizes(), in_[k].options())
+                           : at::zeros(in_[k].sizes(), in_[k].options());
       return out[k].data_ptr();
     };
     ssim_block_norm_grads grads;
@@ -329,7 +341,6 @@ struct BlockNorm : torch::autograd::Function<BlockNorm> {
     grads.post_weight = (float*)wanted(4);
     grads.pre_weight = (float*)wanted(5);
     if (in.rows == 0) return out;
-    Tensor dr = upstream[0], dh = upstream[1];
     if (dr.defined()) dr = dr.contiguous();
     if (dh.defined()) dh = dh.contiguous();
     const Tensor ws = scratch(ssim_block_norm_workspace_bytes(&in), dev);
@@ -366,10 +377,7 @@ py::tuple block_norm(const py::object& x_, const py::object& branch_, const py::
                           std::to_string(width));
   if (!(eps >= 0.0 && eps <= 1.7976931348623157e308))
     throw py::value_error("eps must be a number >= 0");
-  int64_t wants = 0;  // a bit for each tensor whose gradient is wanted
-  auto want = [&](const Tensor& t, int k) { wants |= (int64_t)t.requires_grad() << k; };
-  want(x, 0);
-  want(branch, 1);
+  bool wants = x.requires_grad() || branch.requires_grad();
   if (gate.defined()) {
     if (check(gate, "gate") != cb) throw py::type_error("gate must have branch's dtype");
     check_device(gate, dev, "gate");
@@ -384,36 +392,48 @@ py::tuple block_norm(const py::object& x_, const py::object& branch_, const py::
       throw py::value_error(
           "gate must have x's shape, or x's shape with ones in the place of the last few "
           "dimensions before the width");
-    want(gate, 2);
+    wants |= gate.requires_grad();
   }
   const struct {
     const Tensor& t;
     const char* name;
   } weights[] = {{scale, "scale"}, {post, "post_weight"}, {pre, "pre_weight"}};
-  int k = 2;
   for (const auto& w : weights) {
-    ++k;
     if (!w.t.defined()) continue;
     if (check(w.t, w.name) != SSIM_DTYPE_F32)
       throw py::type_error(std::string(w.name) + " must be float32");
     check_device(w.t, dev, w.name);
     if (w.t.dim() != 1 || w.t.size(0) != width)
       throw py::value_error(std::string(w.name) + " must have one value for each of the width");
-    want(w.t, k);
-  }
-  if (wants && at::GradMode::is_enabled()) {
-    auto given = [](const Tensor& t) {
-      return t.defined() ? std::optional<Tensor>(t) : std::optional<Tensor>();
-    };
-    const auto out = BlockNorm::apply(x, branch, given(gate), given(scale), given(post), given(pre),
-                                      eps, (int64_t)act, wants);
-    return py::make_tuple(out[0], out[1]);
+    wants |= w.t.requires_grad();
   }
   const c10::DeviceGuard guard(dev);
+  const Tensor* tensors[] = {&x, &branch, &gate, &scale, &post, &pre};
+  torch::autograd::edge_list edges(BlockNormBackward::kTensors - 1);
+  wants = wants && at::GradMode::is_enabled();
+  if (wants) {
+    for (size_t k = 0; k < edges.size(); ++k)
+      if (tensors[k]->defined() && tensors[k]->requires_grad())
+        edges[k] = torch::autograd::impl::gradient_edge(*tensors[k]);
+    check_capture(edges, dev);
+  }
   const ssim_block_norm_inputs in = inputs_of(x, branch, gate, scale, post, pre, eps, act);
   Tensor residual = at::empty(x.sizes(), x.options());
   Tensor normed = at::empty(branch.sizes(), branch.options());
-  forward_into(in, residual, normed, nullptr, dev);
+  Tensor stats;
+  if (wants) stats = at::empty({in.rows, 2}, x.options().dtype(at::kFloat));
+  forward_into(in, residual, normed, wants ? stats.data_ptr<float>() : nullptr, dev);
+  if (wants) {
+    std::shared_ptr<BlockNormBackward> node(new BlockNormBackward(), torch::autograd::deleteNode);
+    for (size_t k = 0; k < edges.size(); ++k)
+      if (tensors[k]->defined()) node->saved[k] = torch::autograd::SavedVariable(*tensors[k], false);
+    node->saved[6] = torch::autograd::SavedVariable(stats, false);
+    node->eps = eps;
+    node->act = act;
+    node->set_next_edges(std::move(edges));
+    torch::autograd::set_history(residual, node);
+    torch::autograd::set_history(normed, node);
+  }
   return py::make_tuple(residual, normed);
 }
 

@@ -301,6 +301,48 @@ def test_captured_in_a_graph(gate):
         assert all(torch.equal(grads[k], grads2[k]) for k in grads)
 
 
+def test_captured_with_gradients_beside_an_eager_graph_is_refused():
+    """The leaves' nodes belong to the default stream as long as the eager
+    graph lives; afterwards the same capture is taken."""
+    t, dr, dh, act = make((3, 40), (F32, F32), gate=(3, 40), seed=70)
+    want = run(t, dr, dh, act)
+    call = lambda: S.block_norm(t["x"], t["branch"], t["gate"], t["scale"], t["post_weight"],
+                                t["pre_weight"], 1e-6, act)
+    eager = call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dr * 2.0
+        with pytest.raises(RuntimeError, match="default stream"):
+            call()
+        with torch.no_grad():
+            r, h = call()
+    say("captured")
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(r, want[0]) and torch.equal(h, want[1])
+    del eager
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(t, dr, dh, act)
+    for replay in range(3):
+        say("replay", replay)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert all(torch.equal(got[2][k], want[2][k]) for k in want[2])
+
+
+def test_two_passes_through_one_graph():
+    t, dr, dh, act = make((3, 40), (F32, F32), seed=71)
+    r, h = S.block_norm(t["x"], t["branch"], scale=t["scale"])
+    leaves = [t["x"], t["branch"], t["scale"]]
+    a = torch.autograd.grad((r, h), leaves, (dr, dh), retain_graph=True)
+    b = torch.autograd.grad((r, h), leaves, (dr, dh))
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+    with pytest.raises(RuntimeError, match="second time"):
+        torch.autograd.grad((r, h), leaves, (dr, dh))
+
+
 def test_refusals():
     x = torch.ones(2, 3, 8, device="cuda")
     w = torch.ones(8, device="cuda")
