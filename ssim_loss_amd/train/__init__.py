@@ -96,13 +96,13 @@ def _native():
 
 # --------------------------------------------------------------------------- clipping
 def clip_grads_(grads, max_norm, out=None):
-    """Scales `grads`, a list of contiguous GPU tensors (float32, float16,
-    bfloat16, mixed as they come), by c = min(1, max_norm / (norm + 1e-6)),
+    """Scales `grads`, a list of GPU tensors (float32, float16, bfloat16, mixed as
+    they come; contiguous, or channels_last or another permutation of it), by c = min(1, max_norm / (norm + 1e-6)),
     where norm is the root of the sum of all their squares, formed in fp64.
 
     Returns the norm before clipping, a 0-d float32 tensor; nothing waits for
-    it.  Writes to `out` (tensors of the same shapes and types) if given, else
-    in place.  A NaN or infinite gradient makes the norm so, and the outputs
+    it.  Writes to `out` (tensors of the same shapes, strides and types) if given,
+    else in place.  A NaN or infinite gradient makes the norm so, and the outputs
     follow the formula.  A tensor may be in the list once."""
     return _native().clip_grads(grads, max_norm, out)
 
@@ -121,7 +121,9 @@ class AdamW:
         m  = beta1 m + (1 - beta1) g'          v = beta2 v + (1 - beta2) g'^2
         w  = (1 - lr weight_decay) w - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
 
-    params:  contiguous GPU tensors of float32, float16 or bfloat16.
+    params:  GPU tensors of float32, float16 or bfloat16, contiguous or a
+             permutation of it such as channels_last; gradients and states have
+             their parameter's strides.
     lr:      a number, which may be changed between steps, or one float32 on
              the parameters' device: a captured graph then follows its value.
     max_norm: None: no clipping, and no norm is formed.
@@ -167,7 +169,7 @@ class AdamW:
         def states(given):
             if given is not None:
                 return list(given)
-            return [torch.zeros_like(p, dtype=torch.float32, memory_format=torch.contiguous_format)
+            return [torch.zeros_like(p, dtype=torch.float32)
                     for p in self.params]
 
         with torch.no_grad():

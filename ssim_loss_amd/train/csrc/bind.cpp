@@ -54,17 +54,29 @@ int dtype_code(const Tensor& t) {
   }
 }
 
-// a contiguous GPU tensor of one of the three types
-int check(const Tensor& t, const char* name, Py_ssize_t k = -1) {
+// a GPU tensor of one of the three types, contiguous or (dense) without gaps in
+// any order of its dimensions
+int check(const Tensor& t, const char* name, Py_ssize_t k = -1, bool dense = false) {
   if (!t.device().is_cuda())
     throw py::type_error(at_index(name, k) + " must be a GPU tensor, got device " + t.device().str());
   const int code = dtype_code(t);
   if (code < 0)
     throw py::type_error(at_index(name, k) + " must be float32, float16 or bfloat16, got " +
                          c10::toString(t.scalar_type()));
-  if (t.layout() != at::kStrided || !t.is_contiguous())
-    throw py::value_error(at_index(name, k) + " must be contiguous");
+  if (t.layout() != at::kStrided || !(t.is_contiguous() || (dense && t.is_non_overlapping_and_dense())))
+    throw py::value_error(at_index(name, k) +
+                          (dense ? " must be contiguous or a permutation of a contiguous tensor"
+                                 : " must be contiguous"));
   return code;
+}
+
+// that the elements of two such tensors of one size lie in the same order
+void check_order(const Tensor& t, const Tensor& by, const char* name, Py_ssize_t k) {
+  if (t.is_contiguous() && by.is_contiguous()) return;
+  bool same = t.sizes() == by.sizes();
+  for (int64_t d = 0; same && d < t.dim(); ++d)
+    same = t.size(d) <= 1 || t.stride(d) == by.stride(d);
+  if (!same) throw py::value_error(at_index(name, k) + " must have the strides of its item's others");
 }
 
 void check_device(const Tensor& t, const c10::Device& dev, const char* name, Py_ssize_t k = -1) {
@@ -121,7 +133,7 @@ Tensor clip(const py::object& grads_, double max_norm, const py::object& out_, b
   for (Py_ssize_t k = 0; k < grads.size; ++k) {
     const Tensor& g = grads[k];
     ssim_clip_item& it = items[k];
-    it.dtype = check(g, "grads", k);
+    it.dtype = check(g, "grads", k, true);
     check_device(g, dev, "grads", k);
     it.grad = g.const_data_ptr();
     it.n = g.numel();
@@ -131,10 +143,11 @@ Tensor clip(const py::object& grads_, double max_norm, const py::object& out_, b
     const Tensor& o = out[k];
     if (!in_place) {
       check_device(o, dev, "out", k);
-      if (check(o, "out", k) != it.dtype)
+      if (check(o, "out", k, true) != it.dtype)
         throw py::type_error(at_index("out", k) + " must have its gradient's dtype");
       if (o.sizes() != g.sizes())
         throw py::value_error(at_index("out", k) + " must have its gradient's shape");
+      check_order(o, g, "out", k);
     }
     it.out = o.data_ptr();
   }
@@ -177,9 +190,9 @@ py::object adamw_step(const py::object& grads_, const py::object& params_, const
     if (grads.none(k)) continue;
     const Tensor &g = grads[k], &p = params[k], &mk = m[k], &vk = v[k];
     ssim_adamw_item it;
-    it.grad_dtype = check(g, "grads", k);
-    it.param_dtype = check(p, "params", k);
-    const int cm = check(mk, "exp_avgs", k), cv = check(vk, "exp_avg_sqs", k);
+    it.grad_dtype = check(g, "grads", k, true);
+    it.param_dtype = check(p, "params", k, true);
+    const int cm = check(mk, "exp_avgs", k, true), cv = check(vk, "exp_avg_sqs", k, true);
     if (it.grad_dtype != it.param_dtype && it.grad_dtype != SSIM_DTYPE_F32)
       throw py::type_error(at_index("grads", k) + " must be float32 or have its parameter's dtype");
     if (cm != SSIM_DTYPE_F32 || cv != SSIM_DTYPE_F32)
@@ -188,6 +201,9 @@ py::object adamw_step(const py::object& grads_, const py::object& params_, const
     if (g.sizes() != p.sizes() || mk.numel() != it.n || vk.numel() != it.n)
       throw py::value_error(at_index("grads, exp_avgs and exp_avg_sqs", k) +
                             " must have their parameter's shape");
+    check_order(g, p, "grads", k);
+    check_order(mk, p, "exp_avgs", k);
+    check_order(vk, p, "exp_avg_sqs", k);
     check_device(g, dev, "grads", k);
     check_device(p, dev, "params", k);
     check_device(mk, dev, "exp_avgs", k);
@@ -199,10 +215,11 @@ py::object adamw_step(const py::object& grads_, const py::object& params_, const
     it.master = nullptr;
     if (has_masters && !masters.none(k)) {
       const Tensor& w = masters[k];
-      if (check(w, "masters", k) != SSIM_DTYPE_F32)
+      if (check(w, "masters", k, true) != SSIM_DTYPE_F32)
         throw py::type_error(at_index("masters", k) + " must be float32");
       if (w.numel() != it.n)
         throw py::value_error(at_index("masters", k) + " must have its parameter's shape");
+      check_order(w, p, "masters", k);
       check_device(w, dev, "masters", k);
       it.master = (float*)w.data_ptr();
     }

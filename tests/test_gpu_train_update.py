@@ -174,8 +174,9 @@ def test_clip_past_32_bit_offsets():
 
 def test_clip_refusals():
     a = torch.ones(8, 8, device="cuda")
-    for call in (lambda: S.clip_grads_([a.t()[:, :4]], 1.0),
+    for call in (lambda: S.clip_grads_([a[:, :4]], 1.0),
                  lambda: S.clip_grads_([a], 1.0, out=[a[:4]]),
+                 lambda: S.clip_grads_([a], 1.0, out=[torch.ones(8, 8, device="cuda").t()]),
                  lambda: S.clip_grads_([a], -1.0)):
         with pytest.raises(ValueError):
             call()
@@ -369,9 +370,12 @@ def test_adamw_marks_its_tensors_as_written():
 def test_adamw_refusals():
     p = torch.zeros(8, device="cuda")
     g = torch.ones(8, device="cuda")
+    a = torch.zeros(4, 2, device="cuda").t()
     for make in (lambda: S.AdamW([p], lr=-1.0), lambda: S.AdamW([p], betas=(1.0, 0.9)),
                  lambda: S.AdamW([p], eps=-1.0), lambda: S.AdamW([p], max_norm=math.nan),
                  lambda: S.AdamW([p], exp_avgs=[]), lambda: S.AdamW([p], step=-1),
+                 lambda: S.AdamW([a]).step([torch.ones(2, 4, device="cuda")]),
+                 lambda: S.AdamW([a], exp_avgs=[torch.zeros(8, device="cuda")]).step([a.clone()]),
                  lambda: S.AdamW([p]).step([g, g]), lambda: S.AdamW([p]).step([g[:4]]),
                  lambda: S.AdamW([torch.zeros(4, 4, device="cuda").t()]).step([g.view(2, 4)])):
         with pytest.raises(ValueError):
@@ -439,3 +443,30 @@ def test_update_captured_in_a_graph_follows_its_step_and_rate():
         for x, y in zip(net.params + net.masters + net.m + net.v,
                         other.params + other.masters + other.m + other.v):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype,masters", [(F32, False), (BF16, True)])
+def test_tensors_in_another_order_of_their_dimensions(dtype, masters):
+    """Convolution weights in channels_last, beside a contiguous one: as their
+    contiguous copies."""
+    shapes = [(16, 8, 3, 3), (5, 1, 3, 3), (24, 7)]
+    rng = torch.Generator(device="cuda").manual_seed(33)
+    last = lambda t: t.to(memory_format=torch.channels_last) if t.dim() == 4 else t.t().contiguous().t()
+    made = [_values(rng, math.prod(s), F32, 0.05).view(s) for s in shapes]
+    grads = [_values(rng, math.prod(s), dtype).view(s) for s in shapes]
+    sides = []
+    for order in (last, lambda t: t.clone()):
+        g = [order(t) for t in grads]
+        params = [order(w.to(dtype)) for w in made]
+        opt = S.AdamW(params, lr=LR, max_norm=0.5, masters=[order(w) for w in made] if masters else None)
+        norm = [opt.step(g), opt.step(g)]
+        clipped_to = [torch.zeros_like(t) for t in g]
+        S.clip_grads_(g, 0.25, out=clipped_to)
+        S.clip_grads_(g, 0.25)
+        sides.append(norm + params + opt.exp_avgs + opt.exp_avg_sqs + (opt.masters or []) + clipped_to + g)
+    assert not sides[0][2].is_contiguous() and sides[0][2].stride() == sides[0][5].stride()
+    for a, b in zip(*sides):
+        if a.dim():
+            assert torch.equal(a, b)
+        else:  # (squares are added in the order of the memory)
+            check_norm(a, b.cpu().double())
