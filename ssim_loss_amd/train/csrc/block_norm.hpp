@@ -162,11 +162,17 @@ __device__ __forceinline__ Wide<V> activate(Wide<V> g, int act) {
   return g;
 }
 
-// 1 / sqrt(v), v >= 0, off by a step at most.  The instruction takes subnormal
-// numbers for 0, so they are scaled.
+// 1 / sqrt(v), v >= 0: the instruction, which is off by a step, and one step of
+// Newton's method, since a root's error is the whole row's.  The instruction
+// takes subnormal numbers for 0, so they are scaled; 0 and infinity stay what it
+// gives.
 __device__ __forceinline__ float inv_root(float v) {
   const bool tiny = v < 0x1p-100f;
-  return __builtin_amdgcn_rsqf(tiny ? v * 0x1p60f : v) * (tiny ? 0x1p30f : 1.0f);
+  const float w = tiny ? v * 0x1p60f : v;
+  const float y = __builtin_amdgcn_rsqf(w);
+  const float rest = fmaf(-w * y, y, 1.0f);
+  const float z = fmaf(0.5f * y, rest, y);
+  return (rest == rest ? z : y) * (tiny ? 0x1p30f : 1.0f);
 }
 
 // N sums over a row's threads at once.  kLanes: so many lanes of a wave hold the
