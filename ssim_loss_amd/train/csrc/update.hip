@@ -58,8 +58,11 @@ struct AdamRun {
   uint32_t first;
   int16_t grad_dtype, param_dtype;
 };
-// tables sized so that a kernel's arguments stay below 4 KB
-constexpr int kNormRuns = 144, kClipRuns = 112, kAdamRuns = 64;
+// Tables sized so that a kernel's arguments stay below 4 KB, and one for few
+// runs: a launch with 256 bytes of arguments costs 3.5 us of host time, with
+// 3.6 KB 3.9 (six tensors of 118000 elements, clipped in two launches: 7.1 us a
+// call with this table, 8.6 with the large one).
+constexpr int kNormRuns = 144, kClipRuns = 112, kAdamRuns = 64, kFewRuns = 8;
 
 // Advances the count of updates and forms the update's scalars, by one thread.
 struct StepArgs {
@@ -67,16 +70,18 @@ struct StepArgs {
   const float* lr_device;
   double lr, beta1, beta2, weight_decay;
 };
+template <int N>
 struct NormArgs {
-  NormRun run[kNormRuns];
+  NormRun run[N];
   int count;
   uint32_t chunks;
   int add;  // to the partial sums of the launches before
   Scratch* scratch;
   StepArgs step;
 };
+template <int N>
 struct ClipArgs {
-  ClipRun run[kClipRuns];
+  ClipRun run[N];
   int count;
   uint32_t chunks;
   int partials;
@@ -84,8 +89,9 @@ struct ClipArgs {
   float* norm;
   const Scratch* scratch;
 };
+template <int N>
 struct AdamArgs {
-  AdamRun run[kAdamRuns];
+  AdamRun run[N];
   int count;
   uint32_t chunks;
   int partials;  // 0: no clipping
@@ -94,12 +100,19 @@ struct AdamArgs {
   const Scratch* scratch;
   float beta1, one_minus_beta1, beta2, one_minus_beta2, eps;
 };
-static_assert(sizeof(NormArgs) <= 4096 && sizeof(ClipArgs) <= 4096 && sizeof(AdamArgs) <= 4096,
+static_assert(sizeof(NormArgs<kNormRuns>) <= 4096 && sizeof(ClipArgs<kClipRuns>) <= 4096 &&
+                  sizeof(AdamArgs<kAdamRuns>) <= 4096,
               "kernel arguments");
 
 // the run that holds chunk c
-template <class Run>
-__device__ __forceinline__ int find_run(const Run* run, int count, uint32_t c) {
+template <class Run, int N>
+__device__ __forceinline__ int find_run(const Run (&run)[N], int count, uint32_t c) {
+  if constexpr (N == kFewRuns) {  // by comparing with all: their loads do not wait for each other
+    int r = 0;
+#pragma unroll
+    for (int k = 1; k < N; ++k) r += k < count && run[k].first <= c ? 1 : 0;
+    return r;
+  }
   int lo = 0, hi = count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -166,8 +179,8 @@ __device__ __forceinline__ double squares(const T* g, int64_t n) {
   return acc[0] + acc[1];
 }
 
-template <int U>
-__global__ __launch_bounds__(kThreads) void ssim_grad_norm_kernel(const NormArgs a) {
+template <int U, int N>
+__global__ __launch_bounds__(kThreads) void ssim_grad_norm_kernel(const NormArgs<N> a) {
   __shared__ double lds[kWaves];
   double acc = 0;
   for (uint32_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
@@ -240,8 +253,8 @@ __device__ __forceinline__ void scale(const T* g, T* out, int64_t n, float c) {
   }
 }
 
-template <int U>
-__global__ __launch_bounds__(kThreads) void ssim_clip_grads_kernel(const ClipArgs a) {
+template <int U, int N>
+__global__ __launch_bounds__(kThreads) void ssim_clip_grads_kernel(const ClipArgs<N> a) {
   __shared__ double lds[kWaves];
   const float f = clip_factor(a.scratch, a.partials, a.max_norm, a.norm, lds);
   for (uint32_t k = blockIdx.x; k < a.chunks; k += gridDim.x) {
@@ -343,8 +356,8 @@ __device__ __forceinline__ void adam_run(const Coefs& k, const AdamRun& run, int
   else adam_chunk<TG, TP, false, U>(k, run, i0);
 }
 
-template <int U>
-__global__ __launch_bounds__(kThreads) void ssim_adamw_kernel(const AdamArgs a) {
+template <int U, int N>
+__global__ __launch_bounds__(kThreads) void ssim_adamw_kernel(const AdamArgs<N> a) {
   __shared__ double lds[kWaves];
   Coefs k;
   k.clip = a.partials ? clip_factor(a.scratch, a.partials, a.max_norm, a.norm, lds) : 1.0f;
@@ -376,7 +389,7 @@ __global__ __launch_bounds__(kThreads) void ssim_adamw_kernel(const AdamArgs a) 
 // squares of all gradients by itself, from the caches, and then scales or
 // updates its own share.  Runs are taken as one sequence of 16-byte vectors; a
 // run's last one may be short.
-constexpr int kSmallThreads = 1024, kSmallRuns = 8;
+constexpr int kSmallThreads = 1024, kSmallRuns = kFewRuns;
 constexpr int kSmallShare = 256;  // vectors that a workgroup of AdamW updates at once
 
 template <class Run>
@@ -658,6 +671,23 @@ int clip_vectors(int64_t bytes) {
   return bytes > kClipLargeBytes ? kClipLargeU : bytes > kClipStreamBytes ? kClipStreamU : 1;
 }
 
+const void* const kNormFew[3] = {(const void*)ssim_grad_norm_kernel<1, kFewRuns>,
+                                 (const void*)ssim_grad_norm_kernel<kClipStreamU, kFewRuns>,
+                                 (const void*)ssim_grad_norm_kernel<kClipLargeU, kFewRuns>};
+const void* const kNormMany[3] = {(const void*)ssim_grad_norm_kernel<1, kNormRuns>,
+                                  (const void*)ssim_grad_norm_kernel<kClipStreamU, kNormRuns>,
+                                  (const void*)ssim_grad_norm_kernel<kClipLargeU, kNormRuns>};
+const void* const kClipFew[3] = {(const void*)ssim_clip_grads_kernel<1, kFewRuns>,
+                                 (const void*)ssim_clip_grads_kernel<kClipStreamU, kFewRuns>,
+                                 (const void*)ssim_clip_grads_kernel<kClipLargeU, kFewRuns>};
+const void* const kClipMany[3] = {(const void*)ssim_clip_grads_kernel<1, kClipRuns>,
+                                  (const void*)ssim_clip_grads_kernel<kClipStreamU, kClipRuns>,
+                                  (const void*)ssim_clip_grads_kernel<kClipLargeU, kClipRuns>};
+const void* const kAdamFew[2] = {(const void*)ssim_adamw_kernel<1, kFewRuns>,
+                                 (const void*)ssim_adamw_kernel<kAdamStreamU, kFewRuns>};
+const void* const kAdamMany[2] = {(const void*)ssim_adamw_kernel<1, kAdamRuns>,
+                                  (const void*)ssim_adamw_kernel<kAdamStreamU, kAdamRuns>};
+
 // The norm launches.  *partials: how many partial sums they leave.
 int launch_norm(std::vector<NormRun>& runs, int64_t bytes, Scratch* scratch, const StepArgs& step,
                 int* partials, void* stream) {
@@ -671,8 +701,7 @@ int launch_norm(std::vector<NormRun>& runs, int64_t bytes, Scratch* scratch, con
   for (const auto& l : launches) grid = std::max(grid, grid_for(l.chunks));
   *partials = grid;
   if (launches.empty()) launches.push_back({0, 0, 0});
-  NormArgs a;
-  for (size_t k = 0; k < launches.size(); ++k) {
+  auto launch = [&](auto& a, const void* const (&kernels)[3], size_t k) {
     const auto& l = launches[k];
     a.count = (int)(l.end - l.begin);
     if (a.count) memcpy(a.run, &runs[l.begin], a.count * sizeof(NormRun));
@@ -681,10 +710,15 @@ int launch_norm(std::vector<NormRun>& runs, int64_t bytes, Scratch* scratch, con
     a.scratch = scratch;
     a.step = step;
     if (k > 0) a.step.step = nullptr;
-    const void* kernel = U == 1              ? (const void*)ssim_grad_norm_kernel<1>
-                         : U == kClipStreamU ? (const void*)ssim_grad_norm_kernel<kClipStreamU>
-                                             : (const void*)ssim_grad_norm_kernel<kClipLargeU>;
-    const int rc = launch_kernel(kernel, grid, &a, stream);
+    return launch_kernel(kernels[U == 1 ? 0 : U == kClipStreamU ? 1 : 2], grid, &a, stream);
+  };
+  if (runs.size() <= kFewRuns && launches.size() == 1) {
+    NormArgs<kFewRuns> a;
+    return launch(a, kNormFew, 0);
+  }
+  for (size_t k = 0; k < launches.size(); ++k) {
+    NormArgs<kNormRuns> a;
+    const int rc = launch(a, kNormMany, k);
     if (rc != SSIM_OK) return rc;
   }
   return SSIM_OK;
@@ -692,8 +726,8 @@ int launch_norm(std::vector<NormRun>& runs, int64_t bytes, Scratch* scratch, con
 
 // The single launch takes up to this many elements (each workgroup reads them
 // all), in at most kSmallRuns runs of one type.  Measured in one launch and in
-// two, fp32: clipping 17700 elements 5.6 and 8.0 us, 29500 7.2 and 8.0, 41300
-// 8.9 and 8.1; AdamW 6.9 and 8.7, 8.4 and 8.8, 10.1 and 8.8.
+// two, fp32: clipping 17700 elements 5.6 and 8.4 us, 32450 7.8 and 9.2; AdamW 6.9
+// and 9.3, 8.9 and 9.4.
 constexpr int64_t kSmallElements = 32 << 10;
 
 // Fills the table if these runs go into a single launch.
@@ -798,9 +832,7 @@ int clip_impl(const ssim_clip_item* items, int64_t count, bool scales, double ma
         scratch, partials, norm);
     return hipGetLastError() == hipSuccess ? SSIM_OK : SSIM_ERR_HIP;
   }
-  ClipArgs a;
-  // (the last tensors first: see the kernel)
-  for (size_t k = launches.size(); k-- > 0;) {
+  auto launch = [&](auto& a, const void* const (&kernels)[3], size_t k) {
     const auto& l = launches[k];
     a.count = (int)(l.end - l.begin);
     memcpy(a.run, &runs[l.begin], a.count * sizeof(ClipRun));
@@ -809,10 +841,17 @@ int clip_impl(const ssim_clip_item* items, int64_t count, bool scales, double ma
     a.max_norm = max_norm;
     a.norm = k == 0 ? norm : nullptr;
     a.scratch = scratch;
-    const void* kernel = U == 1              ? (const void*)ssim_clip_grads_kernel<1>
-                         : U == kClipStreamU ? (const void*)ssim_clip_grads_kernel<kClipStreamU>
-                                             : (const void*)ssim_clip_grads_kernel<kClipLargeU>;
-    rc = launch_kernel(kernel, grid_for(l.chunks), &a, stream);
+    return launch_kernel(kernels[U == 1 ? 0 : U == kClipStreamU ? 1 : 2], grid_for(l.chunks), &a,
+                         stream);
+  };
+  if (runs.size() <= kFewRuns && launches.size() == 1) {
+    ClipArgs<kFewRuns> a;
+    return launch(a, kClipFew, 0);
+  }
+  // (the last tensors first: see the kernel)
+  for (size_t k = launches.size(); k-- > 0;) {
+    ClipArgs<kClipRuns> a;
+    rc = launch(a, kClipMany, k);
     if (rc != SSIM_OK) return rc;
   }
   return SSIM_OK;
@@ -934,8 +973,7 @@ int adamw_impl(const ssim_adamw_item* items, int64_t count, const ssim_adamw_opt
         scratch, partials, norm);
     return hipGetLastError() == hipSuccess ? SSIM_OK : SSIM_ERR_HIP;
   }
-  AdamArgs a;
-  for (size_t k = launches.size(); k-- > 0;) {
+  auto launch = [&](auto& a, const void* const (&kernels)[2], size_t k) {
     const auto& l = launches[k];
     a.count = (int)(l.end - l.begin);
     memcpy(a.run, &runs[l.begin], a.count * sizeof(AdamRun));
@@ -949,9 +987,15 @@ int adamw_impl(const ssim_adamw_item* items, int64_t count, const ssim_adamw_opt
     a.beta2 = (float)o->beta2;
     a.one_minus_beta2 = (float)(1.0 - o->beta2);
     a.eps = (float)o->eps;
-    rc = launch_kernel(streams ? (const void*)ssim_adamw_kernel<kAdamStreamU>
-                               : (const void*)ssim_adamw_kernel<1>,
-                       grid_for(l.chunks), &a, stream);
+    return launch_kernel(kernels[streams], grid_for(l.chunks), &a, stream);
+  };
+  if (runs.size() <= kFewRuns && launches.size() == 1) {
+    AdamArgs<kFewRuns> a;
+    return launch(a, kAdamFew, 0);
+  }
+  for (size_t k = launches.size(); k-- > 0;) {
+    AdamArgs<kAdamRuns> a;
+    rc = launch(a, kAdamMany, k);
     if (rc != SSIM_OK) return rc;
   }
   return SSIM_OK;
