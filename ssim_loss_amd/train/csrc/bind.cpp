@@ -295,7 +295,7 @@ void forward_into(const ssim_block_norm_inputs& in, const Tensor& residual, cons
                   float* stats, const c10::Device& dev) {
   const int rc = ssim_block_norm_forward(&in, residual.data_ptr(), normed.data_ptr(), stats,
                                          stream_of(dev));
-  TORCH_CHECK(rc == SSIM_OK, "ssim_block_norm_forward: ", text(rc));
+  if (rc != SSIM_OK) raise(rc, "ssim_block_norm_forward");
 }
 
 // A backward pass under capture ends in its inputs' nodes.  Where one of them was

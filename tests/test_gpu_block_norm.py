@@ -187,8 +187,9 @@ def test_a_row_that_is_not_finite_stays_alone(bad, width):
     assert torch.isnan(grads["scale"]).any()
 
 
-def test_gates_at_the_ends_of_the_sigmoid():
-    made = make((3, 700), (F32, F32), gate=(3, 700), act="sigmoid", seed=50)
+@pytest.mark.parametrize("types", [(F32, F32), (F16, F16), (F32, BF16)])
+def test_gates_at_the_ends_of_the_sigmoid(types):
+    made = make((3, 700), types, gate=(3, 700), act="sigmoid", seed=50)
     with torch.no_grad():
         made[0]["gate"][0] = 200.0
         made[0]["gate"][1] = -200.0
@@ -361,6 +362,9 @@ def test_refusals():
                  lambda: f(x, x, scale=w.half()), lambda: f(x, x, scale=w.cpu())):
         with pytest.raises(TypeError):
             call()
+    with pytest.raises(S.TrainError) as e:  # a number, but none of fp32
+        f(x, x, eps=1e300)
+    assert e.value.code == -10
     a = x.clone().requires_grad_(True)
     r, h = f(a, x)
     with pytest.raises(RuntimeError, match="create_graph"):
