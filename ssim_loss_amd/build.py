@@ -113,7 +113,7 @@ def build_bind(verbose: bool = False) -> str:
            "-I", INCLUDE, "-I", TRAIN_INCLUDE,
            *(a for d in includes if os.path.isdir(d) for a in ("-isystem", d)),
            "-o", tmp, os.path.join(TRAIN_CSRC, "bind.cpp"),
-           "-L", os.path.join(inside, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch",
+           "-L", os.path.join(inside, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch",
            "-ltorch_python", TRAIN_LIB_PATH, "-Wl,-rpath,$ORIGIN"]
     _run(cmd, verbose)
     os.replace(tmp, BIND_PATH)
