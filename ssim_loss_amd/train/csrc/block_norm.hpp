@@ -394,7 +394,8 @@ __device__ __forceinline__ Terms<V> form_terms(const NormParams& p, const Raw<TX
 // kGrouped: one gate row for many rows.  Then only S = sum of e bh is summed
 // over a group's rows, and dg = c act'(g) S, sum of a e bh = a S.
 // kReload: a thread of a very wide row cannot hold it; its vectors, the weights'
-// and the gate's are loaded again, from the caches, after the reduction.
+// and the gate's are loaded again, from the caches, after the reduction, and its
+// sums over rows lie in LDS.
 template <class TX, class TB, int I, int kLanes, bool kGrouped, bool kNarrow, bool kReload>
 __device__ __forceinline__ void norm_backward(const NormParams& p) {
   constexpr int V = Row<TX, TB, I>::V;
@@ -422,7 +423,27 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
     return (i * threads + at) * V;
   };
   constexpr int kHeld = kReload ? 1 : I;  // vectors of the weights and of a row that stay
-  Wide<V> c[kHeld], pre[kHeld], total[I], dpre[I], S[kGrouped ? I : 1], a[kGrouped ? kHeld : 1];
+  Wide<V> c[kHeld], pre[kHeld], a[kGrouped ? kHeld : 1];
+  // The sums over rows, S and total as above.  kReload: dpre and the one that
+  // grows with each row lie in LDS, each thread's in a place of its own.
+  constexpr int kRowSums = kReload ? 1 : I;
+  Wide<V> dpre[kRowSums], S[kGrouped ? kRowSums : 1], total[kGrouped ? I : kRowSums];
+  __shared__ __attribute__((aligned(32))) float kept[2][kReload ? kWaves * kWave * V * I : 8];
+  auto kept_at = [&](int which, int i) -> Wide<V>& {
+    return *reinterpret_cast<Wide<V>*>(&kept[which][kReload ? (i * threads + q) * V : 0]);
+  };
+  auto dpre_at = [&](int i) -> Wide<V>& {
+    if constexpr (kReload) return kept_at(0, i);
+    else return dpre[i];
+  };
+  auto S_at = [&](int i) -> Wide<V>& {
+    if constexpr (kReload) return kept_at(1, i);
+    else return S[kGrouped ? i : 0];
+  };
+  auto total_at = [&](int i) -> Wide<V>& {
+    if constexpr (kReload && !kGrouped) return kept_at(1, i);
+    else return total[i];
+  };
   auto load_weights = [&](int i, int col) {
     const int to = kReload ? 0 : i;
     c[to] = load_weight<V, kNarrow>(p.scale, col, width) * load_weight<V, kNarrow>(p.post, col, width);
@@ -436,8 +457,8 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
 #pragma unroll
   for (int i = 0; i < I; ++i) {
     if constexpr (!kReload) load_weights(i, col_of(i));
-    total[i] = 0;
-    dpre[i] = 0;
+    total_at(i) = 0;
+    dpre_at(i) = 0;
   }
 
   // the segments of rows this worker takes: all rows, dealt out one by one;
@@ -469,7 +490,7 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
 #pragma unroll
       for (int i = 0; i < I; ++i) {
         if constexpr (!kReload) load_gate(group, i, col_of(i));
-        S[i] = 0;
+        S_at(i) = 0;
       }
     } else {
       row = (int64_t)blockIdx.x * kWorkers + worker;
@@ -514,14 +535,16 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
         const Wide<V> dw = widen<TB, V>(raw[j].dh);
         const Terms<V> f = form_terms<TX, TB, V, kGrouped>(p, raw[j], dw, ib, ir, c[j], pre[j],
                                                            a[kGrouped ? j : 0]);
+        Wide<V> sum = dpre_at(i);
 #pragma unroll
         for (int k = 0; k < V; ++k) {
           const float acbh = f.a[k] * c[j][k] * f.bh[k];
           s[0] = fmaf(dw[k] * pre[j][k], f.rh[k], s[0]);
           s[1] = fmaf(f.u[k], acbh, s[1]);
           s[2] = fmaf(f.rh[k], acbh, s[2]);
-          dpre[i][k] = fmaf(dw[k], f.rh[k], dpre[i][k]);
+          sum[k] = fmaf(dw[k], f.rh[k], sum[k]);
         }
+        dpre_at(i) = sum;
         terms[j] = f;
       }
       row_sums<kLanes>(s, lds[parity]);
@@ -544,8 +567,8 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
         }
         const Terms<V>& f = terms[j];
         const Wide<V> e = f.u - f.rh * m1, eb = e * f.bh;
-        if constexpr (kGrouped) S[i] += eb;
-        else total[i] += eb * f.a;
+        if constexpr (kGrouped) S_at(i) += eb;
+        else total_at(i) += eb * f.a;
         if (col >= width) continue;
         if (p.dx) store_cols<TX, V>(dx, col, width, e);
         if (p.db) store_cols<TB, V>(db, col, width, (e * (f.a * c[j]) - f.bh * m2) * ib);
@@ -568,9 +591,9 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
           load_weights(i, col);
           load_gate(group, i, col);
         }
-        total[i] += S[i] * a[j];
+        total_at(i) += S_at(i) * a[j];
         if (p.parts == 1 && p.dg && col < width) {
-          Wide<V> d = S[i] * c[j];
+          Wide<V> d = S_at(i) * c[j];
           if (p.act == SSIM_GATE_SIGMOID) d *= a[j] * (1.0f - a[j]);
           store_cols<TB, V>(dg, col, width, d);
         }
@@ -590,8 +613,8 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
 #pragma unroll
       for (int i = 0; i < I; ++i) {
         Wide<V> v;
-        if constexpr (kGrouped) v = k == 0 ? total[i] : k == 1 ? dpre[i] : S[i];
-        else v = k == 0 ? total[i] : dpre[i];
+        if constexpr (kGrouped) v = k == 0 ? total_at(i) : k == 1 ? dpre_at(i) : S_at(i);
+        else v = k == 0 ? total_at(i) : dpre_at(i);
 #pragma unroll
         for (int e = 0; e < V; ++e) rows[worker][(i * kLanes + q) * V + e] = v[e];
       }
@@ -607,8 +630,8 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
       for (int i = 0; i < I; ++i) {
         const int col = (i * threads + q) * V;
         Wide<V> v;
-        if constexpr (kGrouped) v = k == 0 ? total[i] : k == 1 ? dpre[i] : S[i];
-        else v = k == 0 ? total[i] : dpre[i];
+        if constexpr (kGrouped) v = k == 0 ? total_at(i) : k == 1 ? dpre_at(i) : S_at(i);
+        else v = k == 0 ? total_at(i) : dpre_at(i);
         if (col < width) store_cols<float, V>(to, col, width, v);
       }
     }
@@ -684,10 +707,11 @@ constexpr int shape_threads(int s, int row_waves) {
   return (shape_lanes(s) ? row_waves : s == kGroup1 ? 4 : kMaxWaves) * kWave;
 }
 // A thread of the backward that would hold more than 16 elements of a row has
-// not the registers: workgroups of twice as many threads load them twice.
-// Forward and gradients of 2000 x 16384 in bf16 347 us (with a thread's elements
-// held by eight waves, half of them spilled to memory, 920), of 2000 x 10000 in
-// fp32 448 (700).
+// not the registers: workgroups of twice as many threads load them twice and keep
+// their sums over rows in 128 KB of LDS.  Forward and gradients of 2000 x 16384 in
+// bf16 201 us (sums in registers, some of them spilled to memory, 346; elements
+// held by eight waves, half of them spilled, 920), of 2000 x 12288 in fp16 without
+// a gate 119 (246).
 constexpr bool shape_reload(int s, int bytes) { return shape_items(s) * 16 / bytes > 16; }
 constexpr int shape_back_items(int s, int bytes) {
   return shape_reload(s, bytes) ? shape_items(s) / 2 : shape_items(s);
