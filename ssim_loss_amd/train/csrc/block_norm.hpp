@@ -220,10 +220,10 @@ struct FwdRaw {
 // The first row's loads are issued before the weights', each other's while the
 // row before it is worked on: as soon as that one's registers are free, or
 // (kEarly) at its start.
-template <class TX, class TB, int I, int kLanes, bool kEarly, bool kNarrow>
+template <class TX, class TB, int I, int kLanes, int kWaves, bool kEarly, bool kNarrow>
 __device__ __forceinline__ void norm_forward(const NormParams& p) {
   constexpr int V = Row<TX, TB, I>::V;
-  __shared__ float lds[2][1][kMaxWaves];
+  __shared__ float lds[2][1][kWaves];
   const int width = p.width;
   const int threads = kLanes ? kLanes : (int)blockDim.x;
   const int q = kLanes ? (int)threadIdx.x & (kLanes - 1) : (int)threadIdx.x;
@@ -261,15 +261,30 @@ __device__ __forceinline__ void norm_forward(const NormParams& p) {
   };
   if (row < p.rows) fetch(row);
   if constexpr (kLanes == 0) {
-    if (threadIdx.x < 2 * kMaxWaves) (&lds[0][0][0])[threadIdx.x] = 0;
+    if (threadIdx.x < 2 * kWaves) (&lds[0][0][0])[threadIdx.x] = 0;
     __syncthreads();
   }
+  // (16 waves have not the registers for the weights: each row's are loaded
+  // anew, and the compiler may not see that they are the same ones)
+  constexpr bool kAnew = kWaves == kWideWaves;
   Wide<V> c[I], pre[I];
-#pragma unroll
-  for (int i = 0; i < I; ++i) {
-    const int col = (i * threads + q) * V;
+  auto load_inner = [&](int i) {
+    int at = q;
+    if constexpr (kAnew) asm volatile("" : "+v"(at));
+    const int col = (i * threads + at) * V;
     c[i] = load_weight<V, kNarrow>(p.scale, col, width) * load_weight<V, kNarrow>(p.post, col, width);
-    pre[i] = load_weight<V, kNarrow>(p.pre, col, width);
+  };
+  auto load_outer = [&](int i) {
+    int at = q;
+    if constexpr (kAnew) asm volatile("" : "+v"(at));
+    pre[i] = load_weight<V, kNarrow>(p.pre, (i * threads + at) * V, width);
+  };
+  if constexpr (!kAnew) {
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      load_inner(i);
+      load_outer(i);
+    }
   }
   for (; row < p.rows; row += stride) {
     FwdRaw<TX, TB, V> raw[I];
@@ -291,6 +306,7 @@ __device__ __forceinline__ void norm_forward(const NormParams& p) {
       v[i] = widen<TB, V>(raw[i].b);
 #pragma unroll
       for (int k = 0; k < V; ++k) s[0] = fmaf(v[i][k], v[i][k], s[0]);
+      if constexpr (kAnew) load_inner(i);
       ac[i] = c[i];
       if (p.gate) ac[i] *= activate<TB, V>(widen<TB, V>(raw[i].gate), p.act);
     }
@@ -316,6 +332,7 @@ __device__ __forceinline__ void norm_forward(const NormParams& p) {
     for (int i = 0; i < I; ++i) {
       const int col = (i * threads + q) * V;
       if (col >= width) continue;
+      if constexpr (kAnew) load_outer(i);
       store_cols<TX, V>(r, col, width, v[i]);
       store_cols<TB, V>(h, col, width, v[i] * ir * pre[i]);
     }
@@ -713,11 +730,20 @@ constexpr int shape_threads(int s, int row_waves) {
 // held by eight waves, half of them spilled, 920), of 2000 x 12288 in fp16 without
 // a gate 119 (246).
 constexpr bool shape_reload(int s, int bytes) { return shape_items(s) * 16 / bytes > 16; }
-constexpr int shape_back_items(int s, int bytes) {
+constexpr int shape_items(int s, int bytes) {
   return shape_reload(s, bytes) ? shape_items(s) / 2 : shape_items(s);
 }
-constexpr int shape_back_threads(int s, int bytes) {
-  return shape_reload(s, bytes) ? kWideWaves * kWave : shape_threads(s, kRowWavesBack);
+constexpr int shape_threads(int s, int row_waves, int bytes) {
+  return shape_reload(s, bytes) ? kWideWaves * kWave : shape_threads(s, row_waves);
+}
+// The forward takes 16 waves for such rows in fp32 (2000 x 10000: 93 us, with eight
+// 201), eight in half types (2000 x 16384 bf16 60 us, with 16 71).
+constexpr bool shape_fwd_wide(int s, int bytes) { return bytes == 4 && shape_reload(s, bytes); }
+constexpr int shape_fwd_items(int s, int bytes) {
+  return shape_fwd_wide(s, bytes) ? shape_items(s, bytes) : shape_items(s);
+}
+constexpr int shape_fwd_threads(int s, int bytes) {
+  return shape_fwd_wide(s, bytes) ? kWideWaves * kWave : shape_threads(s, kRowWaves);
 }
 // A workgroup of more than four waves to a row waits at its barriers with few
 // others beside it; there the next row's loads go out at its start.  Where many
@@ -735,15 +761,16 @@ const NormTable& norm_table_f16();
 const NormTable& norm_table_bf16();
 
 template <class TX, class TB, int kShape>
-__global__ __launch_bounds__(shape_threads(kShape, kRowWaves)) void ssim_block_norm_fwd_kernel(
-    const NormParams p) {
-  norm_forward<TX, TB, shape_items(kShape), shape_lanes(kShape), shape_early(kShape),
+__global__ __launch_bounds__(shape_fwd_threads(kShape, sizeof(TB))) void
+ssim_block_norm_fwd_kernel(const NormParams p) {
+  norm_forward<TX, TB, shape_fwd_items(kShape, sizeof(TB)), shape_lanes(kShape),
+               shape_fwd_wide(kShape, sizeof(TB)) ? kWideWaves : kMaxWaves, shape_early(kShape),
                kShape == kNarrow>(p);
 }
 template <class TX, class TB, int kShape, bool kGrouped>
-__global__ __launch_bounds__(shape_back_threads(kShape, sizeof(TB))) void ssim_block_norm_bwd_kernel(
-    const NormParams p) {
-  norm_backward<TX, TB, shape_back_items(kShape, sizeof(TB)), shape_lanes(kShape), kGrouped,
+__global__ __launch_bounds__(shape_threads(kShape, kRowWavesBack, sizeof(TB))) void
+ssim_block_norm_bwd_kernel(const NormParams p) {
+  norm_backward<TX, TB, shape_items(kShape, sizeof(TB)), shape_lanes(kShape), kGrouped,
                 kShape == kNarrow, shape_reload(kShape, sizeof(TB))>(p);
 }
 template <class TB>

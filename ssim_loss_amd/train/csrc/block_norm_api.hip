@@ -60,8 +60,8 @@ Plan make_plan(const ssim_block_norm_inputs& in) {
                                     : kGroup8;
   const int lanes = shape_lanes(p.shape);
   p.wide = in.x_dtype != in.branch_dtype;
-  p.threads = threads_of(p.shape, kRowWaves, shape_items(p.shape), vectors);
-  p.back_threads = threads_of(p.shape, kRowWavesBack, shape_back_items(p.shape, bb), vectors);
+  p.threads = threads_of(p.shape, kRowWaves, shape_fwd_items(p.shape, bb), vectors);
+  p.back_threads = threads_of(p.shape, kRowWavesBack, shape_items(p.shape, bb), vectors);
   p.grouped = in.gate && in.gate_rows > 1;
 
   // Forward: rows in work whose loads are 48 KB on each CU; where a row is a
