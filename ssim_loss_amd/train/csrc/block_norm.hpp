@@ -736,14 +736,17 @@ constexpr int shape_items(int s, int bytes) {
 constexpr int shape_threads(int s, int row_waves, int bytes) {
   return shape_reload(s, bytes) ? kWideWaves * kWave : shape_threads(s, row_waves);
 }
-// The forward takes 16 waves for such rows in fp32 (2000 x 10000: 93 us, with eight
-// 201), eight in half types (2000 x 16384 bf16 60 us, with 16 71).
-constexpr bool shape_fwd_wide(int s, int bytes) { return bytes == 4 && shape_reload(s, bytes); }
-constexpr int shape_fwd_items(int s, int bytes) {
-  return shape_fwd_wide(s, bytes) ? shape_items(s, bytes) : shape_items(s);
+// The forward takes 16 waves for such rows where x is fp32 (fp32, 2000 x 10000: 93
+// us, with eight 201; bf16 beside fp32, 2000 x 16384: 95 and 104), eight for half
+// types alone (2000 x 16384 bf16 60 us, with 16 64).
+constexpr bool shape_fwd_wide(int s, int x_bytes, int bytes) {
+  return x_bytes == 4 && shape_reload(s, bytes);
 }
-constexpr int shape_fwd_threads(int s, int bytes) {
-  return shape_fwd_wide(s, bytes) ? kWideWaves * kWave : shape_threads(s, kRowWaves);
+constexpr int shape_fwd_items(int s, int x_bytes, int bytes) {
+  return shape_fwd_wide(s, x_bytes, bytes) ? shape_items(s, bytes) : shape_items(s);
+}
+constexpr int shape_fwd_threads(int s, int x_bytes, int bytes) {
+  return shape_fwd_wide(s, x_bytes, bytes) ? kWideWaves * kWave : shape_threads(s, kRowWaves);
 }
 // A workgroup of more than four waves to a row waits at its barriers with few
 // others beside it; there the next row's loads go out at its start.  Where many
@@ -761,10 +764,10 @@ const NormTable& norm_table_f16();
 const NormTable& norm_table_bf16();
 
 template <class TX, class TB, int kShape>
-__global__ __launch_bounds__(shape_fwd_threads(kShape, sizeof(TB))) void
+__global__ __launch_bounds__(shape_fwd_threads(kShape, sizeof(TX), sizeof(TB))) void
 ssim_block_norm_fwd_kernel(const NormParams p) {
-  norm_forward<TX, TB, shape_fwd_items(kShape, sizeof(TB)), shape_lanes(kShape),
-               shape_fwd_wide(kShape, sizeof(TB)) ? kWideWaves : kMaxWaves, shape_early(kShape),
+  norm_forward<TX, TB, shape_fwd_items(kShape, sizeof(TX), sizeof(TB)), shape_lanes(kShape),
+               shape_fwd_wide(kShape, sizeof(TX), sizeof(TB)) ? kWideWaves : kMaxWaves, shape_early(kShape),
                kShape == kNarrow>(p);
 }
 template <class TX, class TB, int kShape, bool kGrouped>

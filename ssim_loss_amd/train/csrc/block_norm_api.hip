@@ -60,7 +60,7 @@ Plan make_plan(const ssim_block_norm_inputs& in) {
                                     : kGroup8;
   const int lanes = shape_lanes(p.shape);
   p.wide = in.x_dtype != in.branch_dtype;
-  p.threads = threads_of(p.shape, kRowWaves, shape_fwd_items(p.shape, bb), vectors);
+  p.threads = threads_of(p.shape, kRowWaves, shape_fwd_items(p.shape, xb, bb), vectors);
   p.back_threads = threads_of(p.shape, kRowWavesBack, shape_items(p.shape, bb), vectors);
   p.grouped = in.gate && in.gate_rows > 1;
 
