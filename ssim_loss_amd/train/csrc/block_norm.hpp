@@ -217,9 +217,8 @@ struct FwdRaw {
   Vec<TB, V> b, gate;
 };
 
-// The first row's loads are issued before the weights', each other's while the
-// row before it is worked on: as soon as that one's registers are free, or
-// (kEarly) at its start.
+// The first row's loads are issued before the weights', each other's at the end
+// of the row before it or (kEarly) at its start.
 template <class TX, class TB, int I, int kLanes, int kWaves, bool kEarly, bool kNarrow>
 __device__ __forceinline__ void norm_forward(const NormParams& p) {
   constexpr int V = Row<TX, TB, I>::V;

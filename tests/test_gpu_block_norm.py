@@ -98,6 +98,9 @@ def test_shared_gates_and_none(gate, width, types):
     ((7, 5, 3, 100), (7, 1, 1, 100)),
     ((5000, 72), (5000, 72)),          # more rows than workgroups
     ((3000, 1200), None),
+    ((300, 2, 8200), (300, 1, 8200)),  # rows loaded twice: several groups to a workgroup
+    ((2, 300, 8200), (2, 1, 8200)),
+    ((600, 8200), (600, 8200)),
 ])
 @pytest.mark.parametrize("types", [(F32, F32), (F32, BF16)])
 def test_rows_and_groups(shape, gate, types):
