@@ -154,6 +154,14 @@ __device__ __forceinline__ float sigmoid(float g) {
   if constexpr (sizeof(TB) == 4) return 1.0f / (1.0f + expf(-g));
   else return __builtin_amdgcn_rcpf(1.0f + __expf(-g));
 }
+// act'(g) of an a = sigmoid(g).  1 - a of an open gate is a exp(-g): taken from
+// the rounded a it would be off by all that a's last bit is of it (g = 12: 0.9%,
+// g = 17: the whole).
+template <class TB>
+__device__ __forceinline__ float sigmoid_slope(float g, float a) {
+  const float e = sizeof(TB) == 4 ? expf(-g) : __expf(-g);
+  return a * (g > 0.0f ? a * e : 1.0f - a);
+}
 // (the branch is once for all: one for each element left nothing to overlap)
 template <class TB, int V>
 __device__ __forceinline__ Wide<V> activate(Wide<V> g, int act) {
@@ -161,6 +169,13 @@ __device__ __forceinline__ Wide<V> activate(Wide<V> g, int act) {
 #pragma unroll
     for (int k = 0; k < V; ++k) g[k] = sigmoid<TB>(g[k]);
   }
+  return g;
+}
+
+template <class TB, int V>
+__device__ __forceinline__ Wide<V> slope(Wide<V> g, Wide<V> a) {
+#pragma unroll
+  for (int k = 0; k < V; ++k) g[k] = sigmoid_slope<TB>(g[k], a[k]);
   return g;
 }
 
@@ -465,10 +480,13 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
     c[to] = load_weight<V, kNarrow>(p.scale, col, width) * load_weight<V, kNarrow>(p.post, col, width);
     pre[to] = load_weight<V, kNarrow>(p.pre, col, width);
   };
-  auto load_gate = [&](int64_t group, int i, int col) {
+  auto group_gate = [&](int64_t group, int col) {
     Vec<TB, V> g = load_cols<TB, V, kNarrow>((const TB*)p.gate + group * width, col, width);
     settle<TB, V, kNarrow>(g, col, width);
-    a[kReload ? 0 : i] = activate<TB, V>(widen<TB, V>(g), p.act);
+    return g;
+  };
+  auto load_gate = [&](int64_t group, int i, int col) {
+    a[kReload ? 0 : i] = activate<TB, V>(widen<TB, V>(group_gate(group, col)), p.act);
   };
 #pragma unroll
   for (int i = 0; i < I; ++i) {
@@ -591,7 +609,7 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
         if constexpr (!kGrouped) {
           if (p.dg) {
             Wide<V> d = eb * c[j];
-            if (p.act == SSIM_GATE_SIGMOID) d *= f.a * (1.0f - f.a);
+            if (p.act == SSIM_GATE_SIGMOID) d *= slope<TB, V>(widen<TB, V>(raw[j].gate), f.a);
             store_cols<TB, V>(dg, col, width, d);
           }
         }
@@ -610,7 +628,7 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
         total_at(i) += S_at(i) * a[j];
         if (p.parts == 1 && p.dg && col < width) {
           Wide<V> d = S_at(i) * c[j];
-          if (p.act == SSIM_GATE_SIGMOID) d *= a[j] * (1.0f - a[j]);
+          if (p.act == SSIM_GATE_SIGMOID) d *= slope<TB, V>(widen<TB, V>(group_gate(group, col)), a[j]);
           store_cols<TB, V>(dg, col, width, d);
         }
       }
@@ -689,9 +707,8 @@ __device__ __forceinline__ void norm_sums(const NormParams& p) {
   } else {
     const int64_t at = (int64_t)(job - 2) * p.width + col;
     const float g = (float)((const TB*)p.gate)[at];
-    const float a = p.act == SSIM_GATE_SIGMOID ? sigmoid<TB>(g) : g;
     double d = s * (p.scale ? (double)p.scale[col] : 1.0) * (p.post ? (double)p.post[col] : 1.0);
-    if (p.act == SSIM_GATE_SIGMOID) d *= (double)a * (1.0 - (double)a);
+    if (p.act == SSIM_GATE_SIGMOID) d *= (double)sigmoid_slope<TB>(g, sigmoid<TB>(g));
     ((TB*)p.dg)[at] = (TB)(float)d;
   }
 }
