@@ -31,7 +31,7 @@ constexpr int kWaves = kThreads / kWave;
 struct Scratch {
   double partial[kMaxBlocks];
   float step_size;  // lr / (1 - beta1^t)
-  float decay;      // 1 - lr weight_decay
+  float decay;      // lr weight_decay
   float inv_bc2;    // 1 / (1 - beta2^t)
 };
 
@@ -145,7 +145,7 @@ __device__ __forceinline__ void form_scalars(const StepArgs& s, int64_t t, float
     b2 *= b2;
   }
   *step_size = (float)(lr / (1.0 - p1));
-  *decay = (float)(1.0 - lr * s.weight_decay);
+  *decay = (float)(lr * s.weight_decay);
   *inv_bc2 = (float)(1.0 / (1.0 - p2));
 }
 
@@ -287,7 +287,11 @@ __device__ __forceinline__ void adam_one(const Coefs& k, float g, float& m, floa
   g *= k.clip;
   m = fmaf(k.beta1, m, k.omb1 * g);
   v = fmaf(k.beta2, v, k.omb2 * g * g);
-  w = w * k.decay - k.step_size * (m / (sqrtf(v * k.inv_bc2) + k.eps));
+  // The decay and the step are added up before they reach w: 1 - lr weight_decay
+  // itself has but multiples of 2^-24 (of 1e-7, 1.2e-7; of 1e-8, none).  (An
+  // infinite weight stays one.)
+  const float step = k.step_size * (m / (sqrtf(v * k.inv_bc2) + k.eps));
+  w -= fmaf(k.decay, isinf(w) ? 0.0f : w, step);
 }
 
 constexpr int kAdamV = 4;  // elements a thread takes at once: 16 bytes of each fp32 array
