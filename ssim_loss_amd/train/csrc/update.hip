@@ -206,15 +206,22 @@ __global__ __launch_bounds__(kThreads) void ssim_grad_norm_kernel(const NormArgs
   }
 }
 
-__device__ __forceinline__ float factor_of(double norm, double max_norm) {
-  if (isinf(max_norm)) return 1.0f;
+// The clipping factor as two, which a gradient is multiplied by one after the
+// other. Of a factor below 2^-126 fp32 holds fewer bits the smaller it is
+// (gradients of 1e38 and more): then the first is a power of two, else 1.
+struct Factor {
+  float power, c;
+};
+__device__ __forceinline__ Factor factor_of(double norm, double max_norm) {
+  if (isinf(max_norm)) return {1.0f, 1.0f};
   const double c = max_norm / (norm + 1e-6);
-  return c > 1.0 ? 1.0f : (float)c;  // (a NaN stays one)
+  if (c < 0x1p-126) return {0x1p-100f, (float)(c * 0x1p100)};
+  return {1.0f, c > 1.0 ? 1.0f : (float)c};  // (a NaN stays one)
 }
 
 // the norm, from all partial sums, and the clipping factor; every workgroup
 // computes the same
-__device__ __forceinline__ float clip_factor(const Scratch* s, int partials, double max_norm,
+__device__ __forceinline__ Factor clip_factor(const Scratch* s, int partials, double max_norm,
                                              float* norm_out, double* lds) {
   double v = 0;
   for (int k = threadIdx.x; k < partials; k += kThreads) v += s->partial[k];
@@ -235,7 +242,7 @@ __global__ __launch_bounds__(kThreads) void ssim_norm_only_kernel(const Scratch*
 // U > 1: a list that the last-level cache does not hold; neither its second
 // read nor the outputs are kept.
 template <class T, int U>
-__device__ __forceinline__ void scale(const T* g, T* out, int64_t n, float c) {
+__device__ __forceinline__ void scale(const T* g, T* out, int64_t n, Factor f) {
   constexpr int V = 16 / sizeof(T), C = kThreads * V;
   const int64_t at = threadIdx.x * V;
   if (n >= (int64_t)C * U) {
@@ -244,11 +251,11 @@ __device__ __forceinline__ void scale(const T* g, T* out, int64_t n, float c) {
     for (int u = 0; u < U; ++u) x[u] = load_as<U != 1, T, V>(g + at + u * C);
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      store_as<U != 1, T, V>(out + at + u * C, narrow<T, V>(widen<T, V>(x[u]) * c));
+      store_as<U != 1, T, V>(out + at + u * C, narrow<T, V>(widen<T, V>(x[u]) * f.power * f.c));
   } else {
     for (int u = 0; u < U; ++u) {
       const int64_t i = at + u * C;
-      for (int k = 0; k < V && i + k < n; ++k) out[i + k] = (T)((float)g[i + k] * c);
+      for (int k = 0; k < V && i + k < n; ++k) out[i + k] = (T)((float)g[i + k] * f.power * f.c);
     }
   }
 }
@@ -256,12 +263,12 @@ __device__ __forceinline__ void scale(const T* g, T* out, int64_t n, float c) {
 template <int U, int N>
 __global__ __launch_bounds__(kThreads) void ssim_clip_grads_kernel(const ClipArgs<N> a) {
   __shared__ double lds[kWaves];
-  const float f = clip_factor(a.scratch, a.partials, a.max_norm, a.norm, lds);
+  const Factor f = clip_factor(a.scratch, a.partials, a.max_norm, a.norm, lds);
   for (uint32_t k = blockIdx.x; k < a.chunks; k += gridDim.x) {
     const uint32_t c = a.chunks - 1 - k;
     const int r = find_run(a.run, a.count, c);
     const ClipRun& run = a.run[r];
-    if (f == 1.0f && run.grad == run.out) continue;  // in place and not clipped
+    if (f.c == 1.0f && f.power == 1.0f && run.grad == run.out) continue;  // in place and not clipped
     const int64_t chunk = (int64_t)(16 / (run.dtype == SSIM_DTYPE_F32 ? 4 : 2)) * kThreads * U;
     const int64_t i = (int64_t)(c - run.first) * chunk;
     switch (run.dtype) {
@@ -280,11 +287,12 @@ __global__ __launch_bounds__(kThreads) void ssim_clip_grads_kernel(const ClipArg
 
 // ---- AdamW
 struct Coefs {
-  float clip, step_size, decay, inv_bc2, beta1, omb1, beta2, omb2, eps;
+  Factor clip;
+  float step_size, decay, inv_bc2, beta1, omb1, beta2, omb2, eps;
 };
 
 __device__ __forceinline__ void adam_one(const Coefs& k, float g, float& m, float& v, float& w) {
-  g *= k.clip;
+  g = g * k.clip.power * k.clip.c;
   m = fmaf(k.beta1, m, k.omb1 * g);
   v = fmaf(k.beta2, v, k.omb2 * g * g);
   // The decay and the step are added up before they reach w: 1 - lr weight_decay
@@ -364,7 +372,7 @@ template <int U, int N>
 __global__ __launch_bounds__(kThreads) void ssim_adamw_kernel(const AdamArgs<N> a) {
   __shared__ double lds[kWaves];
   Coefs k;
-  k.clip = a.partials ? clip_factor(a.scratch, a.partials, a.max_norm, a.norm, lds) : 1.0f;
+  k.clip = a.partials ? clip_factor(a.scratch, a.partials, a.max_norm, a.norm, lds) : Factor{1.0f, 1.0f};
   k.step_size = a.scratch->step_size;
   k.decay = a.scratch->decay;
   k.inv_bc2 = a.scratch->inv_bc2;
@@ -478,7 +486,7 @@ __global__ __launch_bounds__(kSmallThreads) void ssim_clip_small_kernel(const Sm
   __shared__ double lds[kSmallThreads / kWave];
   const double norm = sqrt(small_squares<T, V>(a.table, lds));
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
-  const float f = factor_of(norm, a.max_norm);
+  const Factor f = factor_of(norm, a.max_norm);
   const uint32_t vectors = a.table.first[kSmallRuns];
   for (uint32_t v = blockIdx.x * kSmallThreads + threadIdx.x; v < vectors;
        v += gridDim.x * kSmallThreads) {
@@ -494,9 +502,9 @@ __global__ __launch_bounds__(kSmallThreads) void ssim_clip_small_kernel(const Sm
     const T* g = (const T*)run.grad + i;
     T* out = (T*)run.out + i;
     if (i + V <= run.n) {
-      store<T, V>(out, narrow<T, V>(widen<T, V>(load<T, V>(g)) * f));
+      store<T, V>(out, narrow<T, V>(widen<T, V>(load<T, V>(g)) * f.power * f.c));
     } else {
-      for (int k = 0; i + k < run.n; ++k) out[k] = (T)((float)g[k] * f);
+      for (int k = 0; i + k < run.n; ++k) out[k] = (T)((float)g[k] * f.power * f.c);
     }
   }
 }
@@ -525,7 +533,7 @@ __global__ __launch_bounds__(kSmallThreads) void ssim_adamw_small_kernel(const S
     form_scalars(a.step, t, &scalars[0], &scalars[1], &scalars[2]);
   }
   Coefs k;
-  k.clip = 1.0f;
+  k.clip = {1.0f, 1.0f};
   if (a.norm) {
     const double norm = sqrt(small_squares<TG, V>(a.table, lds));
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
