@@ -255,8 +255,8 @@ def block_norm(x, branch, gate=None, scale=None, post_weight=None, pre_weight=No
 
     Returns (residual, normed) of x's and branch's types; arithmetic is
     float32, and normed is formed from the residual before its rounding.
-    Gradients of all tensor inputs are available, gradients of gradients are
-    not.  Tensors must be contiguous; the width is at most 16384."""
+    Gradients of all tensor inputs are available, gradients of gradients and
+    forward-mode derivatives are not.  Tensors must be contiguous; the width is at most 16384."""
     act = GATE_ACT.get(gate_act)
     if act is None:
         raise ValueError(f"gate_act must be 'none' or 'sigmoid', got {gate_act!r}")

@@ -89,7 +89,12 @@ void check_device(const Tensor& t, const c10::Device& dev, const char* name, Py_
 
 const Tensor& unpack(PyObject* o, const char* name, Py_ssize_t k = -1) {
   if (!THPVariable_Check(o)) throw py::type_error(at_index(name, k) + " must be a torch.Tensor");
-  return THPVariable_Unpack(o);
+  const Tensor& t = THPVariable_Unpack(o);
+  // (it would be left out of the results: these calls do not pass torch's dispatcher)
+  TORCH_CHECK_NOT_IMPLEMENTED(!t._fw_grad(/*level=*/0).defined(), at_index(name, k),
+                              " has a forward-mode tangent: forward-mode derivatives of the "
+                              "training operators are not available");
+  return t;
 }
 
 // a list or tuple of tensors
@@ -239,7 +244,7 @@ py::object adamw_step(const py::object& grads_, const py::object& params_, const
   o.lr = 0.0;
   o.lr_device = nullptr;
   if (THPVariable_Check(lr.ptr())) {
-    const Tensor& t = THPVariable_Unpack(lr.ptr());
+    const Tensor& t = unpack(lr.ptr(), "lr");
     if (check(t, "lr") != SSIM_DTYPE_F32 || t.numel() != 1)
       throw py::type_error("lr must be a number or one float32 on the parameters' device");
     check_device(t, dev, "lr");
