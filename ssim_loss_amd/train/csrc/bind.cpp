@@ -11,6 +11,7 @@
 #include <c10/core/Allocator.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/core/GradMode.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/hip/HIPGraphsC10Utils.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/function.h>
@@ -18,6 +19,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/autograd/saved_variable.h>
 #include <torch/csrc/autograd/variable.h>
+#include <torch/csrc/jit/frontend/tracer.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include <optional>
@@ -97,6 +99,17 @@ const Tensor& unpack(PyObject* o, const char* name, Py_ssize_t k = -1) {
   return t;
 }
 
+// A trace would hold this call's results as constants and follow no new inputs.
+void check_tracing(const char* what) {
+  using c10::impl::TorchDispatchModeTLS;
+  const bool tracing =
+      torch::jit::tracer::isTracing() ||
+      (c10::impl::dispatch_mode_enabled() &&
+       TorchDispatchModeTLS::get_mode(c10::impl::TorchDispatchModeKey::PROXY).has_value());
+  TORCH_CHECK_NOT_IMPLEMENTED(!tracing, what, " cannot be recorded by a tracer (torch.jit.trace, "
+                              "make_fx)");
+}
+
 // a list or tuple of tensors
 struct List {
   py::object fast;
@@ -132,6 +145,7 @@ c10::DataPtr scratch(size_t bytes) { return c10::GetAllocator(c10::kCUDA)->alloc
 
 // ---- clipping
 Tensor clip(const py::object& grads_, double max_norm, const py::object& out_, bool scales) {
+  check_tracing(scales ? "clip_grads_" : "grad_norm");
   const List grads(grads_, "grads");
   const bool in_place = out_.is_none();
   const List out(in_place ? grads_ : out_, "out");
@@ -185,6 +199,7 @@ py::object adamw_step(const py::object& grads_, const py::object& params_, const
                       const py::object& v_, const py::object& masters_, const py::object& step_,
                       const py::object& lr, double beta1, double beta2, double eps,
                       double weight_decay, const py::object& max_norm) {
+  check_tracing("AdamW.step");
   const List grads(grads_, "grads"), params(params_, "params"), m(m_, "exp_avgs"),
       v(v_, "exp_avg_sqs");
   const bool has_masters = !masters_.is_none();
@@ -388,6 +403,7 @@ Tensor optional(const py::object& o, const char* name) {
 py::tuple block_norm(const py::object& x_, const py::object& branch_, const py::object& gate_,
                      const py::object& scale_, const py::object& post_, const py::object& pre_,
                      double eps, int act) {
+  check_tracing("block_norm");
   const Tensor x = unpack(x_.ptr(), "x"), branch = unpack(branch_.ptr(), "branch"),
                gate = optional(gate_, "gate"), scale = optional(scale_, "scale"),
                post = optional(post_, "post_weight"), pre = optional(pre_, "pre_weight");

@@ -4,6 +4,7 @@ operators, so calls within it are refused rather than left out of its result
 import pytest
 import torch
 import torch.autograd.forward_ad as forward_ad
+from torch.fx.experimental.proxy_tensor import make_fx
 
 import ssim_loss_amd as S
 
@@ -34,3 +35,18 @@ def test_tensors_with_a_forward_mode_tangent_are_refused(which):
             calls(torch.ones(4))[which]()
     with pytest.raises(TypeError, match="GPU tensor"):
         calls(dual)[which]()
+
+
+@pytest.mark.parametrize("which", ["x", "clip", "norm", "params"])
+@pytest.mark.parametrize("trace", [lambda f, x: torch.jit.trace(f, (x,)), lambda f, x: make_fx(f)(x)],
+                         ids=["jit", "fx"])
+def test_tracers_are_refused(trace, which):
+    def traced(t):
+        out = t * 2.0
+        calls(t)[which]()
+        return out
+
+    with pytest.raises(NotImplementedError, match="tracer"):
+        trace(traced, torch.ones(4))
+    with pytest.raises(TypeError, match="GPU tensor"):
+        traced(torch.ones(4))
