@@ -52,15 +52,15 @@ struct NormParams {
   float* dpost;
   float* dpre;
   // sums over a workgroup's rows, [blocks][width] each: of a e bh, of dh rh,
-  // and, with gate rows shared and cut into parts, of e bh
+  // and, with gate rows shared and their rows cut, of e bh
   float* part_total;
   float* part_pre;
   float* part_gate;
   int blocks;
-  // gate rows shared: groups of gate_rows rows, each cut into `parts` parts of
-  // part_rows rows
+  // gate rows shared: groups of gate_rows rows, each a worker's; or cut: each in
+  // `parts` parts of part_rows rows, a workgroup's
   int64_t groups, part_rows;
-  int parts;
+  int parts, cut;
 };
 
 template <class TX, class TB, int I>
@@ -503,7 +503,7 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
     segs = p.groups * p.parts;
     seg = blockIdx.x;
     seg_stride = gridDim.x;
-    if (p.parts == 1) {
+    if (!p.cut) {
       seg = seg * kWorkers + worker;
       seg_stride *= kWorkers;
     }
@@ -517,7 +517,7 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
       end = row + p.part_rows;
       if (end > (group + 1) * p.gate_rows) end = (group + 1) * p.gate_rows;
       stride = 1;
-      if (p.parts > 1) {
+      if (p.cut) {
         row += worker;
         stride = kWorkers;
       }
@@ -626,7 +626,7 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
           load_gate(group, i, col);
         }
         total_at(i) += S_at(i) * a[j];
-        if (p.parts == 1 && p.dg && col < width) {
+        if (!p.cut && p.dg && col < width) {
           Wide<V> d = S_at(i) * c[j];
           if (p.act == SSIM_GATE_SIGMOID) d *= slope<TB, V>(widen<TB, V>(group_gate(group, col)), a[j]);
           store_cols<TB, V>(dg, col, width, d);
@@ -636,7 +636,7 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
   }
 
   // the workgroup's sums
-  float* out[3] = {p.part_total, p.part_pre, kGrouped && p.parts > 1 ? p.part_gate : nullptr};
+  float* out[3] = {p.part_total, p.part_pre, kGrouped && p.cut ? p.part_gate : nullptr};
 #pragma unroll
   for (int k = 0; k < (kGrouped ? 3 : 2); ++k) {
     if (!out[k]) continue;

@@ -17,12 +17,16 @@ const NormTable& table_of(int dtype) {
   }
 }
 
+constexpr int64_t kEnds = 8;
+constexpr int64_t kMaxCutGroups = 32768;  // the last sums' grid has a row for each
+
 // How the rows are dealt out.
 struct Plan {
   bool wide, grouped;
   int shape;
   int threads, blocks;            // of the forward
   int back_threads, back_blocks;  // of the backward
+  bool cut;  // a gate row's rows go to whole workgroups (in `parts` parts), not each group to a worker
   int parts;
   int64_t groups, part_rows;
 };
@@ -88,22 +92,37 @@ Plan make_plan(const ssim_block_norm_inputs& in) {
   const int64_t target = kCUs * per_cu;
   p.parts = 1;
   p.groups = p.part_rows = 0;
+  p.cut = false;
   if (!p.grouped) {
     p.back_blocks = (int)blocks_for(in.rows, workers, target);
     return p;
   }
   p.groups = in.rows / in.gate_rows;
   p.part_rows = in.gate_rows;
-  if (p.groups > 0 && p.groups < target) {
-    int64_t parts = target / p.groups;
-    const int64_t most = ceil_div(in.gate_rows, workers);
-    if (parts > most) parts = most;
-    if (parts > 1) {
-      p.part_rows = ceil_div(ceil_div(in.gate_rows, parts), workers) * workers;
-      p.parts = (int)ceil_div(in.gate_rows, p.part_rows);
-    }
+  if (p.groups == 0) {
+    p.back_blocks = 0;
+    return p;
   }
-  p.back_blocks = (int)(p.parts > 1 ? p.groups * p.parts : blocks_for(p.groups, workers, target));
+  int64_t parts = target / p.groups;
+  const int64_t most = ceil_div(in.gate_rows, workers);
+  if (parts > most) parts = most;
+  if (parts > 1) {
+    p.part_rows = ceil_div(ceil_div(in.gate_rows, parts), workers) * workers;
+    p.parts = (int)ceil_div(in.gate_rows, p.part_rows);
+    p.cut = p.parts > 1;
+  }
+  // A group to a worker, or to a workgroup, whose workers share its rows: by the
+  // rows that a worker takes one after another, where a workgroup's beginning and
+  // end (weights, sums) take the time of kEnds.  Forward and gradients in bf16, by
+  // worker and by workgroup: 129 groups of 1024 rows of 64 785 and 36 us, 500 of
+  // 256 of 384 386 and 192, 1000 of 64 of 64 65 and 35; 4000 of 64 of 64 94 and 111,
+  // 500 of 16 of 1000 56 and 65.  (2000 of 64 of 64, 70 and 59, falls to the worker.)
+  if (!p.cut) {
+    p.back_blocks = (int)blocks_for(p.groups, workers, target);
+    const int64_t each = ceil_div(p.groups, (int64_t)p.back_blocks * workers) * in.gate_rows;
+    p.cut = p.groups <= kMaxCutGroups && ceil_div(p.groups, target) * (most + kEnds) < each;
+  }
+  if (p.cut) p.back_blocks = (int)(p.groups * p.parts);
   return p;
 }
 
@@ -141,7 +160,7 @@ int check_arrays(const Array* ins, int n_in, const Array* outs, int n_out) {
 }
 
 size_t workspace_bytes(const ssim_block_norm_inputs& in, const Plan& p) {
-  const size_t arrays = p.grouped && p.parts > 1 ? 3 : 2;
+  const size_t arrays = p.cut ? 3 : 2;
   return ((size_t)p.back_blocks * (size_t)in.width * 4 * arrays + 15) & ~(size_t)15;
 }
 
@@ -162,6 +181,7 @@ NormParams params_of(const ssim_block_norm_inputs& in, const Plan& p) {
   k.inv_width = (float)(1.0 / (double)in.width);
   k.groups = p.groups;
   k.part_rows = p.part_rows;
+  k.cut = p.cut;
   k.parts = p.parts;
   k.blocks = p.back_blocks;
   return k;
@@ -259,7 +279,7 @@ int ssim_block_norm_backward(const ssim_block_norm_inputs* in, const float* stat
   k.dpre = grads->pre_weight;
   const size_t part = (size_t)p.back_blocks * (size_t)in->width;
   float* ws = static_cast<float*>(workspace);
-  const bool cut = p.grouped && p.parts > 1 && grads->gate && rows;
+  const bool cut = p.cut && grads->gate && rows;
   if (k.dscale || k.dpost) k.part_total = ws;
   if (k.dpre) k.part_pre = ws + part;
   if (cut) k.part_gate = ws + 2 * part;
