@@ -20,6 +20,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
@@ -107,7 +108,10 @@ def build_bind(verbose: bool = False) -> str:
                 os.path.join(inside, "include", "torch", "csrc", "api", "include"),
                 os.path.join(os.path.dirname(os.path.dirname(hipcc())), "include"),
                 "/opt/rocm/include", sysconfig.get_paths()["include"]]
-    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-shared",
+    compiler = [shutil.which("g++") or shutil.which("c++")]
+    if compiler == [None]:  # (torch's names are those of g++, and of clang up to this version)
+        compiler = [os.path.join(os.path.dirname(hipcc()), "amdclang++"), "-fclang-abi-compat=17"]
+    cmd = [*compiler, "-O2", "-std=c++17", "-fPIC", "-Wall", "-shared",
            "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", INCLUDE, "-I", TRAIN_INCLUDE,
@@ -121,8 +125,19 @@ def build_bind(verbose: bool = False) -> str:
 
 
 def build_all(verbose: bool = False) -> list[str]:
-    """Both libraries and the binding."""
-    return [build(verbose), build_train(verbose), build_bind(verbose)]
+    """Both libraries, which need hipcc alone, and the binding where torch for
+    ROCm is installed."""
+    built = [build(verbose), build_train(verbose)]
+    try:
+        import torch
+
+        missing = not torch.version.hip
+    except ImportError:
+        missing = True
+    if missing:
+        print("the training operators' binding is not built: it needs torch for ROCm", file=sys.stderr)
+        return built
+    return [*built, build_bind(verbose)]
 
 
 if __name__ == "__main__":
