@@ -656,14 +656,22 @@ bool plan(std::vector<Run>& runs, size_t most, ChunkOf chunk_of, std::vector<Lau
   return true;
 }
 
-int launch_kernel(const void* kernel, int grid, void* args, void* stream, int threads = kThreads) {
-  void* list[] = {args};
+// (the launch's own status: the last error may be another call's)
+int launch_list(const void* kernel, int grid, void** list, void* stream, int threads) {
   if (hipLaunchKernel(kernel, dim3(grid), dim3(threads), list, 0,
                       static_cast<hipStream_t>(stream)) != hipSuccess) {
     (void)hipGetLastError();
     return SSIM_ERR_HIP;
   }
   return SSIM_OK;
+}
+int launch_kernel(const void* kernel, int grid, void* args, void* stream, int threads = kThreads) {
+  void* list[] = {args};
+  return launch_list(kernel, grid, list, stream, threads);
+}
+int launch_norm_only(const Scratch* scratch, int partials, float* norm, void* stream) {
+  void* list[] = {&scratch, &partials, &norm};
+  return launch_list((const void*)ssim_norm_only_kernel, 1, list, stream, kThreads);
 }
 
 int grid_for(uint32_t chunks) { return chunks < (uint32_t)kMaxBlocks ? (int)chunks : kMaxBlocks; }
@@ -839,11 +847,7 @@ int clip_impl(const ssim_clip_item* items, int64_t count, bool scales, double ma
   int partials = 0;
   rc = launch_norm(norm_runs, bytes, scratch, none, &partials, stream);
   if (rc != SSIM_OK) return rc;
-  if (launches.empty()) {
-    ssim_norm_only_kernel<<<dim3(1), dim3(kThreads), 0, static_cast<hipStream_t>(stream)>>>(
-        scratch, partials, norm);
-    return hipGetLastError() == hipSuccess ? SSIM_OK : SSIM_ERR_HIP;
-  }
+  if (launches.empty()) return launch_norm_only(scratch, partials, norm, stream);
   auto launch = [&](auto& a, const void* const (&kernels)[3], size_t k) {
     const auto& l = launches[k];
     a.count = (int)(l.end - l.begin);
@@ -979,12 +983,7 @@ int adamw_impl(const ssim_adamw_item* items, int64_t count, const ssim_adamw_opt
   int partials = 0;  // (without a norm the first launch forms the scalars only)
   rc = launch_norm(norm_runs, 2 * grad_bytes, scratch, st, &partials, stream);
   if (rc != SSIM_OK) return rc;
-  if (launches.empty()) {
-    if (!norm) return SSIM_OK;
-    ssim_norm_only_kernel<<<dim3(1), dim3(kThreads), 0, static_cast<hipStream_t>(stream)>>>(
-        scratch, partials, norm);
-    return hipGetLastError() == hipSuccess ? SSIM_OK : SSIM_ERR_HIP;
-  }
+  if (launches.empty()) return norm ? launch_norm_only(scratch, partials, norm, stream) : SSIM_OK;
   auto launch = [&](auto& a, const void* const (&kernels)[2], size_t k) {
     const auto& l = launches[k];
     a.count = (int)(l.end - l.begin);
