@@ -46,7 +46,8 @@ def _missing(path: str) -> ImportError:
 
 def lib() -> ctypes.CDLL:
     """The C-ABI library, for callers of the C functions.  SSIM_TRAIN_AMD_LIB
-    names another build of the same sources."""
+    names another build of the same sources for them; the operators on tensors
+    run in the one that their binding was linked with."""
     global _lib
     with _lock:
         if _lib is None:

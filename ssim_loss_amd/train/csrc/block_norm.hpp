@@ -12,7 +12,7 @@
 // thread takes I vectors of 16 bytes of the block's type, those of its neighbours
 // beside it; rows start at any element, and all vectors, a row's last one too, are
 // loaded at full width.  The weights of a thread's columns stay in registers over
-// all rows of the workgroup.
+// all rows of the workgroup (but of the widest, see kAnew and kReload).
 
 #pragma once
 
@@ -61,12 +61,6 @@ struct NormParams {
   // `parts` parts of part_rows rows, a workgroup's
   int64_t groups, part_rows;
   int parts, cut;
-};
-
-template <class TX, class TB, int I>
-struct Row {
-  static constexpr int V = 16 / sizeof(TB);
-  static constexpr int E = V * I;
 };
 
 // One vector of a row, as stored, with one load and no branch: a vector that
@@ -236,7 +230,7 @@ struct FwdRaw {
 // of the row before it or (kEarly) at its start.
 template <class TX, class TB, int I, int kLanes, int kWaves, bool kEarly, bool kNarrow>
 __device__ __forceinline__ void norm_forward(const NormParams& p) {
-  constexpr int V = Row<TX, TB, I>::V;
+  constexpr int V = 16 / sizeof(TB);
   __shared__ float lds[2][1][kWaves];
   const int width = p.width;
   const int threads = kLanes ? kLanes : (int)blockDim.x;
@@ -429,7 +423,7 @@ __device__ __forceinline__ Terms<V> form_terms(const NormParams& p, const Raw<TX
 // sums over rows lie in LDS.
 template <class TX, class TB, int I, int kLanes, bool kGrouped, bool kNarrow, bool kReload>
 __device__ __forceinline__ void norm_backward(const NormParams& p) {
-  constexpr int V = Row<TX, TB, I>::V;
+  constexpr int V = 16 / sizeof(TB);
   constexpr int kWaves = kReload ? kWideWaves : kMaxWaves;
   // (two vectors of a thread twice over do not fit its registers, unless the
   // group's are missing)
@@ -674,7 +668,7 @@ __device__ __forceinline__ void norm_backward(const NormParams& p) {
 
 // The last sums, in fp64 over the workgroups' partial sums.  blockIdx.y: 0 the
 // scale's and the post weight's gradients, 1 the pre weight's, 2 + g the
-// gradient of gate row g (where its rows were cut into parts).
+// gradient of gate row g (where its rows were cut).
 template <class TB>
 __device__ __forceinline__ void norm_sums(const NormParams& p) {
   __shared__ double lds[kSumSlices][kSumColumns];
@@ -764,9 +758,10 @@ constexpr int shape_fwd_items(int s, int x_bytes, int bytes) {
 constexpr int shape_fwd_threads(int s, int x_bytes, int bytes) {
   return shape_fwd_wide(s, x_bytes, bytes) ? kWideWaves * kWave : shape_threads(s, kRowWaves);
 }
-// A workgroup of more than four waves to a row waits at its barriers with few
-// others beside it; there the next row's loads go out at its start.  Where many
-// waves are resident that gains nothing and costs registers.
+// A workgroup of eight waves to a row waits at its barriers with few others
+// beside it; there the next row's loads go out at its start, as long as a thread
+// has the registers for them (one or two vectors).  Where many waves are resident
+// that gains nothing.
 constexpr bool shape_early(int s) { return s == kGroup1w || s == kGroup2; }
 
 struct NormTable {

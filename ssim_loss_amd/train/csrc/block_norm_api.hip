@@ -215,8 +215,7 @@ int ssim_block_norm_forward(const ssim_block_norm_inputs* in, void* residual, vo
   const Array outs[] = {{residual, n * xb, xb}, {normed, n * bb, bb}, {stats, 8 * (size_t)in->rows, 4}};
   rc = check_arrays(ins, 6, outs, 3);
   if (rc != SSIM_OK) return rc;
-  int cus = 0;
-  rc = current_device(&cus);
+  rc = check_current_device();
   if (rc != SSIM_OK) return rc;
 
   const Plan p = make_plan(*in);
@@ -263,8 +262,7 @@ int ssim_block_norm_backward(const ssim_block_norm_inputs* in, const float* stat
   rc = check_arrays(ins, 9, outs, 7);
   if (rc != SSIM_OK) return rc;
   if (!weights && !(rows && (grads->x || grads->branch || grads->gate))) return SSIM_OK;
-  int cus = 0;
-  rc = current_device(&cus);
+  rc = check_current_device();
   if (rc != SSIM_OK) return rc;
 
   NormParams k = params_of(*in, p);

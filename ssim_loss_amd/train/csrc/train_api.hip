@@ -7,10 +7,10 @@
 
 namespace ssim_train {
 
-int current_device(int* cus) {
+int check_current_device() {
   struct Known {
     bool ready;
-    int status, cus;
+    int status;
   };
   static std::mutex mu;
   static Known known[64] = {};
@@ -24,10 +24,8 @@ int current_device(int* cus) {
     if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return SSIM_ERR_HIP;
     const bool ok = prop.warpSize == kWave && strncmp(prop.gcnArchName, "gfx950", 6) == 0;
     d.status = ok ? SSIM_OK : SSIM_ERR_DEVICE;
-    d.cus = prop.multiProcessorCount;
     d.ready = true;
   }
-  *cus = d.cus;
   return d.status;
 }
 

@@ -132,7 +132,7 @@ inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t pa = (uintptr_t)a, pb = (uintptr_t)b;
   return pa < pb + nb && pb < pa + na;
 }
-// SSIM_OK if the current device is a gfx950; *cus: its compute units
-int current_device(int* cus);
+// SSIM_OK if the current device is a gfx950
+int check_current_device();
 
 }  // namespace ssim_train

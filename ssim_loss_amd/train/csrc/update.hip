@@ -604,7 +604,6 @@ __global__ __launch_bounds__(kSmallThreads) void ssim_adamw_small_kernel(const S
 // ------------------------------------------------------------------ host side
 struct Span {
   uintptr_t begin, end;
-  int item;    // items may hold the same array twice only within one clip item
   bool write;
 };
 
@@ -623,7 +622,7 @@ bool spans_clash(std::vector<Span>& spans) {
 }
 
 void add_span(std::vector<Span>& spans, const void* p, size_t bytes, bool write) {
-  if (p && bytes) spans.push_back({(uintptr_t)p, (uintptr_t)p + bytes, 0, write});
+  if (p && bytes) spans.push_back({(uintptr_t)p, (uintptr_t)p + bytes, write});
 }
 
 constexpr int64_t kMaxBytes = (int64_t)1 << 46;
@@ -810,8 +809,7 @@ int clip_impl(const ssim_clip_item* items, int64_t count, bool scales, double ma
   add_span(spans, workspace, sizeof(Scratch), true);
   if (spans_clash(spans)) return SSIM_ERR_ALIAS;
 
-  int cus = 0;
-  int rc = current_device(&cus);
+  int rc = check_current_device();
   if (rc != SSIM_OK) return rc;
 
   SmallClipArgs small;
@@ -945,8 +943,7 @@ int adamw_impl(const ssim_adamw_item* items, int64_t count, const ssim_adamw_opt
   add_span(spans, workspace, sizeof(Scratch), true);
   if (spans_clash(spans)) return SSIM_ERR_ALIAS;
 
-  int cus = 0;
-  int rc = current_device(&cus);
+  int rc = check_current_device();
   if (rc != SSIM_OK) return rc;
 
   const StepArgs st = {step, o->lr_device, o->lr, o->beta1, o->beta2, o->weight_decay};

@@ -100,7 +100,7 @@ typedef struct {
 
 typedef struct {
   double lr;           /* >= 0; not looked at if lr_device is given */
-  double beta1, beta2; /* in [0, 1) */
+  double beta1, beta2; /* in [0, 1); they and their complements enter in fp32 */
   double eps;          /* >= 0 */
   double weight_decay; /* >= 0 */
   double max_norm;     /* >= 0; infinity: no clipping */
