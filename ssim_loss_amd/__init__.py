@@ -802,4 +802,5 @@ def fused_ssim3d(vol1, vol2, padding: str = "same", train: bool = True):
 
 # --------------------------------------------------------------------------- the rest of a training step
 from . import train  # noqa: E402
-from .train import AdamW, TrainError, block_norm, clip_grads_, grad_norm  # noqa: E402,F401
+from .train import (AdamW, TrainError, attention, block_norm, clip_grads_, gated_linear,  # noqa: E402,F401
+                    grad_norm, rotary)

@@ -2,7 +2,7 @@
 compiled in parallel with ``hipcc`` for gfx950 and linked into
 ``ssim_loss_amd/libssim_loss_amd.so``, those under train/csrc/ (the training
 operators) into ``ssim_loss_amd/train/libssim_train_amd.so``.  The second
-library's binding to torch, train/csrc/bind.cpp, becomes the Python module
+library's binding to torch, train/csrc/bind*.cpp, becomes the Python module
 ``ssim_loss_amd/train/_bind.so``.
 
 Packed-FP32 instructions are switched off (``-packed-fp32-ops``); the kernels
@@ -40,6 +40,7 @@ TRAIN_INCLUDE = os.path.join(TRAIN, "include")
 TRAIN_SOURCES = sorted(glob.glob(os.path.join(TRAIN_CSRC, "*.hip")))
 TRAIN_LIB_PATH = os.path.join(TRAIN, "libssim_train_amd.so")
 BIND_PATH = os.path.join(TRAIN, "_bind.so")
+BIND_SOURCES = sorted(glob.glob(os.path.join(TRAIN_CSRC, "bind*.cpp")))
 
 
 def hipcc() -> str:
@@ -98,8 +99,8 @@ def build_train(verbose: bool = False, extra: list[str] | None = None,
 
 
 def build_bind(verbose: bool = False) -> str:
-    """Compile train/csrc/bind.cpp against torch's headers and link it with
-    the training library, which it finds beside itself."""
+    """Compile train/csrc/bind*.cpp against torch's headers and link them with
+    the training library, which they find beside themselves."""
     import torch
 
     inside = os.path.dirname(torch.__file__)
@@ -116,7 +117,7 @@ def build_bind(verbose: bool = False) -> str:
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", INCLUDE, "-I", TRAIN_INCLUDE,
            *(a for d in includes if os.path.isdir(d) for a in ("-isystem", d)),
-           "-o", tmp, os.path.join(TRAIN_CSRC, "bind.cpp"),
+           "-o", tmp, *BIND_SOURCES,
            "-L", os.path.join(inside, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch",
            "-ltorch_python", TRAIN_LIB_PATH, "-Wl,-rpath,$ORIGIN"]
     _run(cmd, verbose)

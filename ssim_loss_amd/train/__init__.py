@@ -1,8 +1,9 @@
 """The rest of a training step around the SSIM loss, on AMD MI355X: the global
-gradient norm and clipping by it, AdamW with the clipping fused in, and the
-joint between two blocks of an image network with its gradient.
+gradient norm and clipping by it, AdamW with the clipping fused in, the joint
+between two blocks of an image network, and what lies inside a block: rotary
+positions, attention and the gated layer, all with their gradients.
 
-The C ABI is ``include/ssim_train_amd.h``; ``_bind`` (csrc/bind.cpp) calls it on
+The C ABI is ``include/ssim_train_amd.h``; ``_bind`` (csrc/bind*.cpp) calls it on
 torch tensors, on torch's current stream of their device.  The computation runs
 in the HIP kernels of ``libssim_train_amd.so``; there is no fallback path.
 
@@ -10,6 +11,9 @@ in the HIP kernels of ``libssim_train_amd.so``; there is no fallback path.
   grad_norm(grads)                        -> the norm alone
   AdamW(params, ...).step(grads=None)     -> the norm before clipping, or None
   block_norm(x, branch, gate=..., ...)    -> (residual, normed), with autograd
+  rotary(q, k, positions, axes, ...)      -> (q, k) turned, with autograd
+  attention(q, k, v, ...)                 -> the attended values, with autograd
+  gated_linear(x, w_gate, w_up, ...)      -> act(x w_gate^T) x w_up^T, with autograd
 """
 from __future__ import annotations
 
@@ -21,9 +25,11 @@ from .. import SsimError
 from ..build import BIND_PATH, TRAIN_LIB_PATH
 
 # SSIM_TRAIN_ABI_VERSION of include/ssim_train_amd.h that this package follows
-ABI_VERSION = 1
+ABI_VERSION = 2
 
 GATE_ACT = {"none": 0, "sigmoid": 1}
+PAIRS = {"adjacent": 0, "halves": 1}
+GATED_ACT = {"silu": 0, "gelu": 1, "sigmoid": 2}
 
 _lock = threading.Lock()
 _lib = None
@@ -66,7 +72,17 @@ def lib() -> ctypes.CDLL:
                     ("ssim_adamw_step", i32, [vp, i64, vp, vp, vp, vp, vp]),
                     ("ssim_block_norm_forward", i32, [vp, vp, vp, vp, vp]),
                     ("ssim_block_norm_workspace_bytes", sz, [vp]),
-                    ("ssim_block_norm_backward", i32, [vp, vp, vp, vp, vp, vp, vp])):
+                    ("ssim_block_norm_backward", i32, [vp, vp, vp, vp, vp, vp, vp]),
+                    ("ssim_rotary", i32, [vp, vp, vp, vp]),
+                    ("ssim_attention_workspace_bytes", sz, [vp]),
+                    ("ssim_attention_forward", i32, [vp, vp, vp, vp, vp]),
+                    ("ssim_attention_backward_workspace_bytes", sz, [vp]),
+                    ("ssim_attention_backward", i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+                    ("ssim_gated_linear_saved_elements", sz, [vp]),
+                    ("ssim_gated_linear_workspace_bytes", sz, [vp]),
+                    ("ssim_gated_linear_backward_workspace_bytes", sz, [vp]),
+                    ("ssim_gated_linear_forward", i32, [vp, vp, vp, vp, vp, vp]),
+                    ("ssim_gated_linear_backward", i32, [vp, vp, vp, vp, vp, vp, vp])):
                 function = getattr(L, name)
                 function.restype = result
                 function.argtypes = args
@@ -262,3 +278,73 @@ def block_norm(x, branch, gate=None, scale=None, post_weight=None, pre_weight=No
     if act is None:
         raise ValueError(f"gate_act must be 'none' or 'sigmoid', got {gate_act!r}")
     return _native().block_norm(x, branch, gate, scale, post_weight, pre_weight, eps, act)
+
+
+# --------------------------------------------------------------------------- inside a block
+def rotary(q, k, positions, axes, base=10000.0, pairs="adjacent"):
+    """Queries and keys turned by their positions along several axes, such as
+    (time, height, width), in one launch.
+
+    q, k:      [batch, tokens, heads, dim] (k None: queries alone; its heads may
+               be fewer) of one type, float32, float16 or bfloat16; any strides,
+               such as views of one projection's output.
+    positions: [tokens, axes] or [batch, tokens, axes], float32, int32 or int64;
+               fractions and far positions keep their angle (it is reduced in fp64).
+    axes:      for each of 1 to 4 axes the number of elements of a head that turn
+               by it, one part after the other: even, together at most dim (which
+               is at most 512).  The elements behind them pass as they are.
+    pairs:     pair i of a part of s elements, which turns by
+               position * base^(-2 i / s): "adjacent" elements 2i and 2i + 1, or
+               "halves" elements i and i + s / 2.
+
+    Returns (q, k), new and contiguous.  Gradients of q and k are available,
+    gradients of gradients and of positions are not."""
+    kind = PAIRS.get(pairs)
+    if kind is None:
+        raise ValueError(f"pairs must be 'adjacent' or 'halves', got {pairs!r}")
+    return _native().rotary(q, k, positions, axes, base, kind)
+
+
+def attention(q, k, v, scale=None, causal=False, query_lengths=None, key_lengths=None):
+    """Softmax attention, softmax(scale q k^T) v, without the matrix of scores
+    ever in memory.
+
+    q:     [batch, queries, heads, dim]; k, v: [batch, keys, kv_heads, dim], of one
+           type, float32, float16 or bfloat16.  kv_heads divides heads: query head
+           h uses key head h // (heads / kv_heads).  dim is a multiple of 8 to 128.
+           Any strides: rows that do not lie at multiples of 16 bytes without gaps
+           are copied first.
+    scale: > 0; default dim ** -0.5.
+    query_lengths, key_lengths: int32 [batch] on the same device: sequence b has
+           that many queries and keys (clamped to 0 .. the tensor's); those behind
+           them are not read.  Default: all.
+    causal: query i sees key j <= i + (keys - queries) of its sequence: the last
+           query sees the last key.
+
+    Returns [batch, queries, heads, dim].  A query that sees no key, or is behind
+    its sequence, gives zeros and takes a zero gradient.  A key or value within its
+    sequence's length must be finite also where it is not seen by some queries.
+    Scores and sums are float32; for half types the probabilities (and in the
+    backward, which forms them again, their gradients) are rounded to the type.
+    Gradients of q, k and v are available, the same bits every time; gradients of
+    gradients are not."""
+    return _native().attention(q, k, v, scale, bool(causal), query_lengths, key_lengths)
+
+
+def gated_linear(x, w_gate, w_up, b_gate=None, b_up=None, act="silu"):
+    """The gated layer of a feed-forward block, both projections, the activation
+    and the product in one kernel:
+
+        act(x w_gate^T + b_gate) * (x w_up^T + b_up)
+
+    x: [..., width]; w_gate, w_up: [hidden, width]; b_gate, b_up: [hidden] or None;
+    contiguous, of one type, float32, float16 or bfloat16.
+    act: "silu", "gelu" (with the error function) or "sigmoid".
+
+    Returns [..., hidden].  Sums are float32.  Where gradients are wanted the two
+    projections are kept, rounded to the type, for the backward.  Gradients of all
+    inputs are available, gradients of gradients are not."""
+    kind = GATED_ACT.get(act)
+    if kind is None:
+        raise ValueError(f"act must be 'silu', 'gelu' or 'sigmoid', got {act!r}")
+    return _native().gated_linear(x, w_gate, w_up, b_gate, b_up, kind)

@@ -1,0 +1,661 @@
+// attention.hpp -- kernels of softmax attention and its gradients:
+//   s_ij = q_i . k_j     p_ij = exp(scale s_ij - lse_i)     o_i = sum_j p_ij v_j
+//   ds_ij = p_ij (do_i . v_j - do_i . o_i)
+//   dq_i = scale sum_j ds_ij k_j     dk_j = scale sum_i ds_ij q_i     dv_j = sum_i p_ij do_i
+// over the keys j that row i sees; a row that sees none gives zeros.
+//
+// Scores and probabilities never reach memory.  A wave holds 32 rows' queries (or,
+// for the gradients of keys and values, 32 keys) in registers as one operand and
+// streams the other side through LDS.  A product's result comes out with one of
+// its rows to a lane, so the row's maximum and sum need but one exchange, and is
+// the next product's operand as it stands (mma.hpp).
+
+#pragma once
+
+#include "mma.hpp"
+
+namespace ssim_train {
+
+constexpr int kAttentionThreads = 256;
+constexpr int kRowsOfWave = 32;
+
+struct Strided {
+  const char* p;
+  int64_t batch, head;  // bytes
+  uint32_t token;
+};
+
+struct AttentionParams {
+  Strided q, k, v;
+  const int* q_length;  // NULL: q_tokens
+  const int* k_length;
+  int q_tokens, k_tokens, heads, kv_heads, group, dim, batch;
+  int causal, spread;  // spread: (batch, key head) pairs are dealt out over the XCDs
+  int tiles, splits;   // of rows (or keys); parts of the keys that workgroups of their own take
+  float scale, scale2; // scale2 = scale log2(e)
+  void* out;           // [batch][q_tokens][heads][dim]
+  float* lse;          // [batch][heads][q_tokens], log2 of the row's sum; +inf: no keys.  NULL: not wanted
+  float* part_out;     // [splits][batch][heads][q_tokens][dim], each part's own softmax
+  float* part_lse;     // [splits][batch][heads][q_tokens]; -inf: no keys
+  // backward
+  const void* o;       // as out
+  const void* d_out;
+  float* delta;        // [batch][heads][q_tokens]
+  float* norms;        // fp16: [batch][kv_heads][kNormParts][2], largest |do_i| and |v_j|
+  void* dq;
+  void* dk;
+  void* dv;
+};
+
+// Of a kernel for elements T and heads of at most 32 DB elements.
+template <class T, int DB>
+struct HeadShape {
+  static constexpr int kBytes = DB * 32 * (int)sizeof(T);
+  static constexpr int kRow = kBytes <= 128 ? 128 : kBytes <= 256 ? 256 : 512;  // in LDS
+  static constexpr int kSteps = DB * 32 / kPerStep<T>;
+};
+// a block of 32 rows as an operand: so many steps, of so many registers of a tile
+template <class T>
+constexpr int kAcrossSteps = 32 / kPerStep<T>;
+template <class T>
+constexpr int kAcrossRegs = kPerStep<T> / 2;
+
+// The workgroup's (batch, key head) and its item among theirs.
+struct Where {
+  int b, kvh, item;
+};
+__device__ __forceinline__ Where where(const AttentionParams& p, int items) {
+  const unsigned id = blockIdx.x;
+  unsigned pair, item;
+  if (p.spread) {  // workgroup id goes to XCD id % 8: a pair's keys stay in one XCD's cache
+    const unsigned j = id >> 3;
+    pair = (j / items) * 8 + (id & 7);
+    item = j % items;
+  } else {
+    pair = id / items;
+    item = id % items;
+  }
+  return {(int)(pair / p.kv_heads), (int)(pair % p.kv_heads), (int)item};
+}
+
+// kTile rows of memory, from `from` on, to a tile in LDS; rows from `rows` on and
+// chunks from `chunks` on arrive as zeros.
+template <int kRow, int kTile>
+__device__ __forceinline__ void fetch_tile(const char* from, uint32_t stride, int rows, int chunks, uint32_t to) {
+  constexpr int kChunksOfRow = kRow / 16;
+  constexpr int kRowsAtOnce = kAttentionThreads / kChunksOfRow;
+  static_assert(kTile % kRowsAtOnce == 0, "whole instructions");
+  const int row = threadIdx.x / kChunksOfRow;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const uint32_t size = rows <= 0 ? 0u : (uint32_t)(min(rows, kTile) - 1) * stride + (uint32_t)chunks * 16u;
+  const Descriptor d = describe(from, size);
+#pragma unroll
+  for (int j = 0; j < kTile / kRowsAtOnce; ++j) {
+    const int r = row + j * kRowsAtOnce;
+    const int chunk = (threadIdx.x % kChunksOfRow) ^ swizzle<kRow>(r);
+    const uint32_t offset = chunk < chunks ? (uint32_t)r * stride + (uint32_t)chunk * 16u : kNowhere;
+    load_to_lds(d, offset, to + (uint32_t)(j * kRowsAtOnce * kRow + wave * (kWave * 16)));
+  }
+}
+
+// A lane's chunks of its row: 2 t + h; zeros past the row's chunks and where it is
+// not live (`row` can be read all the same).
+template <class T, int DB>
+__device__ __forceinline__ void load_row(const char* row, bool live, int chunks, Chunk (&to)[HeadShape<T, DB>::kSteps]) {
+  const int h = threadIdx.x >> 5 & 1;
+#pragma unroll
+  for (int t = 0; t < HeadShape<T, DB>::kSteps; ++t) {
+    const int c = 2 * t + h;
+    to[t] = *reinterpret_cast<const Chunk*>(row + (c < chunks ? c : 0) * 16);
+    if (!live || c >= chunks) to[t] = Chunk{0, 0, 0, 0};
+  }
+}
+
+// s = rows `row` .. row + 31 of the tile times the lane's row
+template <class T, int DB>
+__device__ __forceinline__ Sums along(const Lds* tile, int row, const Chunk (&mine)[HeadShape<T, DB>::kSteps]) {
+  constexpr int kRow = HeadShape<T, DB>::kRow;
+  const int lane = threadIdx.x & (kWave - 1);
+  Sums s = {};
+#pragma unroll
+  for (int t = 0; t < HeadShape<T, DB>::kSteps; ++t)
+    multiply<T>(s, lds_chunk(tile, place<kRow>(row + (lane & 31), 2 * t + (lane >> 5))), mine[t]);
+  return s;
+}
+// to[block] += (columns of the tile's rows `row` .. row + 31) times w
+template <class T, int DB>
+__device__ __forceinline__ void across(Sums (&to)[DB], const Lds* tile, int row, const Sums& w) {
+#pragma unroll
+  for (int t = 0; t < kAcrossSteps<T>; ++t) {
+    const Chunk b = operand_of<T>(w, t * kAcrossRegs<T>);
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+      multiply<T>(to[d], lds_across<T, HeadShape<T, DB>::kRow>(tile, row + t * kPerStep<T>, d), b);
+  }
+}
+// the row of a tile's register r
+__device__ __forceinline__ int row_of(int r) { return 8 * (r >> 2) + 4 * (int)(threadIdx.x >> 5 & 1) + (r & 3); }
+
+// A lane's row of the result, of which it holds the columns row_of() of each block.
+template <class T, int DB>
+__device__ __forceinline__ void store_row(T* row, const Sums (&v)[DB], float factor, int dim) {
+  const int h = threadIdx.x >> 5 & 1;
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int column = 32 * d + 8 * k + 4 * h;
+      Wide<4> w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = v[d][4 * k + e] * factor;
+      if (column < dim) store<T, 4>(row + column, narrow<T, 4>(w));
+    }
+}
+
+__device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
+
+// What rows see: of sequence b the first q_length queries, the first k_length
+// keys; with causal order the last query sees the last key.
+struct Seen {
+  int q_length, k_length, shift;  // query i sees keys up to i + shift
+};
+__device__ __forceinline__ Seen seen_of(const AttentionParams& p, int b) {
+  Seen s;
+  s.q_length = p.q_length ? min(max(p.q_length[b], 0), p.q_tokens) : p.q_tokens;
+  s.k_length = p.k_length ? min(max(p.k_length[b], 0), p.k_tokens) : p.k_tokens;
+  s.shift = p.causal ? s.k_length - s.q_length : s.k_length;
+  return s;
+}
+// the last key that query i sees; < 0: none
+__device__ __forceinline__ int last_key(const Seen& s, int i) {
+  return i < s.q_length ? min(s.k_length - 1, i + s.shift) : -1;
+}
+
+// ---------------------------------------------------------------- forward
+// KW waves share rows and take keys in turn: 1, a wave has 32 rows of the
+// workgroup's 128; 4, all have the same 32 (few rows, many keys).
+template <class T, int DB, int KW>
+struct ForwardShape {
+  static constexpr int kKeys = KW == 1 ? 64 : 128;  // of a tile
+  static constexpr int kBlocks = KW == 1 ? 2 : 1;   // of 32 keys, a wave's
+  static constexpr int kRows = KW == 1 ? 128 : 32;  // of the workgroup
+  static constexpr int kTileBytes = kKeys * HeadShape<T, DB>::kRow;
+  static constexpr int kBuffers = 4 * kTileBytes <= 128 << 10 ? 2 : 1;
+  static constexpr int kPitch = DB * 32 + 4;        // floats: of a row where waves' results are joined
+  static constexpr int kJoin = KW == 1 ? 0 : 4 * 32 * kPitch * 4;
+  static constexpr int kTiles = 2 * kBuffers * kTileBytes;
+  static constexpr int kLds = kTiles > kJoin ? kTiles : kJoin;
+};
+
+template <class T, int DB, int KW>
+__global__ void __launch_bounds__(kAttentionThreads, (sizeof(T) == 2 && KW == 1) ? 2 : 1)
+attention_forward(const AttentionParams p) {
+  using Shape = ForwardShape<T, DB, KW>;
+  using Head = HeadShape<T, DB>;
+  __shared__ __attribute__((aligned(1024))) char lds_[Shape::kLds];
+  __shared__ float joined[2][4][32];
+  Lds* lds = (Lds*)lds_;
+  const uint32_t lds_at = lds_address(lds);
+  const Where at = where(p, p.tiles * p.splits);
+  if (at.b >= p.batch) return;
+  // (the last rows see most: first)
+  const int tile = p.tiles - 1 - at.item / p.splits, split = at.item % p.splits;
+  const Seen seen = seen_of(p, at.b);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
+  const int chunks = p.dim / kPerChunk<T>;
+
+  const int rows = p.q_tokens * p.group;
+  const int first_row = tile * Shape::kRows;
+  const int row_ = first_row + (KW == 1 ? wave * kRowsOfWave : 0) + (lane & 31);
+  const bool there = row_ < rows;
+  const int row = there ? row_ : 0;
+  const int token = row / p.group, head = at.kvh * p.group + row % p.group;
+  const int last = there ? last_key(seen, token) : -1;
+  Chunk q[Head::kSteps];
+  load_row<T, DB>(p.q.p + at.b * p.q.batch + (int64_t)token * p.q.token + head * p.q.head,
+                  there && token < seen.q_length, chunks, q);
+
+  // the keys of the workgroup: those that its last row sees, and of them its share
+  const int last_token = min((min(first_row + Shape::kRows, rows) - 1) / p.group, seen.q_length - 1);
+  const int keys = first_row / p.group < seen.q_length ? max(last_key(seen, last_token) + 1, 0) : 0;
+  const int key_tiles = (keys + Shape::kKeys - 1) / Shape::kKeys;
+  const int each = (key_tiles + p.splits - 1) / p.splits;
+  const int begin = min(split * each, key_tiles), end = min(begin + each, key_tiles);
+  // the least that a row of the wave sees, past which scores are compared
+  const int wave_first = (first_row + (KW == 1 ? wave * kRowsOfWave : 0)) / p.group;
+  const int wave_last = min(first_row + (KW == 1 ? wave * kRowsOfWave : 0) + kRowsOfWave, rows) - 1;
+  const int open = wave_last / p.group < seen.q_length && wave_last >= 0 ? last_key(seen, wave_first) : -1;
+
+  const char* k_from = p.k.p + at.b * p.k.batch + at.kvh * p.k.head;
+  const char* v_from = p.v.p + at.b * p.v.batch + at.kvh * p.v.head;
+  auto fetch = [&](int t) {
+    const int key = t * Shape::kKeys;
+    const uint32_t to = lds_at + (t % Shape::kBuffers) * 2 * Shape::kTileBytes;
+    fetch_tile<Head::kRow, Shape::kKeys>(k_from + (int64_t)key * p.k.token, p.k.token, seen.k_length - key, chunks, to);
+    fetch_tile<Head::kRow, Shape::kKeys>(v_from + (int64_t)key * p.v.token, p.v.token, seen.k_length - key, chunks,
+                                         to + Shape::kTileBytes);
+  };
+
+  Sums o[DB] = {};
+  float m = -INFINITY, l = 0.0f;  // the row's maximum so far; the sum of this lane's half
+  if (begin < end) fetch(begin);
+  for (int t = begin; t < end; ++t) {
+    landed_for_all();
+    if (Shape::kBuffers == 2 && t + 1 < end) fetch(t + 1);
+    const Lds* k_tile = lds + (t % Shape::kBuffers) * 2 * Shape::kTileBytes;
+    const Lds* v_tile = k_tile + Shape::kTileBytes;
+    const int in_tile = KW == 1 ? 0 : wave * 32;
+    const int key = t * Shape::kKeys + in_tile;
+    Sums s[Shape::kBlocks];
+#pragma unroll
+    for (int b = 0; b < Shape::kBlocks; ++b) s[b] = along<T, DB>(k_tile, in_tile + 32 * b, q);
+    if (key + 32 * Shape::kBlocks - 1 > open) {
+#pragma unroll
+      for (int b = 0; b < Shape::kBlocks; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          s[b][r] = key + 32 * b + row_of(r) > last ? -INFINITY : s[b][r];
+    }
+    float top = m;
+#pragma unroll
+    for (int b = 0; b < Shape::kBlocks; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[b][r]);
+    top = halves_max(top);
+    const float base = top == -INFINITY ? 0.0f : top * p.scale2;
+    if (__any(top != m)) {
+      const float less = exp2_fast(fmaf(m, p.scale2, -base));
+      l *= less;
+#pragma unroll
+      for (int d = 0; d < DB; ++d) o[d] *= less;
+    }
+    m = top;
+#pragma unroll
+    for (int b = 0; b < Shape::kBlocks; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        s[b][r] = exp2_fast(fmaf(s[b][r], p.scale2, -base));
+        l += s[b][r];
+      }
+#pragma unroll
+    for (int b = 0; b < Shape::kBlocks; ++b) across<T, DB>(o, v_tile, in_tile + 32 * b, s[b]);
+    if (Shape::kBuffers == 1 && t + 1 < end) {
+      landed_for_all();
+      fetch(t + 1);
+    }
+  }
+  l = halves_sum(l);
+
+  if constexpr (KW == 4) {  // the waves' results together
+    if (lane < 32) joined[0][wave][lane] = m;
+    landed_for_all();
+    float top = joined[0][0][lane & 31];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) top = fmaxf(top, joined[0][w][lane & 31]);
+    const float base = top == -INFINITY ? 0.0f : top * p.scale2;
+    const float less = exp2_fast(fmaf(m, p.scale2, -base));
+    l *= less;
+    if (lane < 32) joined[1][wave][lane] = l;
+    float* mine = (float*)lds_ + (wave * 32 + (lane & 31)) * Shape::kPitch;
+#pragma unroll
+    for (int d = 0; d < DB; ++d) o[d] *= less;
+    store_row<float, DB>(mine, o, 1.0f, DB * 32);
+    landed_for_all();
+    l = joined[1][0][lane & 31] + joined[1][1][lane & 31] + joined[1][2][lane & 31] + joined[1][3][lane & 31];
+    m = top;
+  }
+
+  const float inverse = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+  const float lse = l > 0.0f || l != l ? fmaf(m, p.scale2, __builtin_amdgcn_logf(l)) : -INFINITY;
+  const int64_t stat = ((int64_t)at.b * p.heads + head) * p.q_tokens + token;
+  const int64_t part = (int64_t)split * p.batch * p.heads * p.q_tokens;
+  const bool whole = p.splits == 1;
+  if (there && lane < 32 && (KW == 1 || wave == 0)) {
+    if (!whole) p.part_lse[part + stat] = lse;
+    else if (p.lse) p.lse[stat] = lse == -INFINITY ? INFINITY : lse;
+  }
+  T* out = static_cast<T*>(p.out) + (((int64_t)at.b * p.q_tokens + token) * p.heads + head) * p.dim;
+  float* part_out = p.part_out + (part + stat) * p.dim;
+  if constexpr (KW == 1) {
+    if (!there) return;
+    if (whole) store_row<T, DB>(out, o, inverse, p.dim);
+    else store_row<float, DB>(part_out, o, inverse, p.dim);
+  } else {
+    // lane: row lane % 32, four columns of each of the threads' eight groups
+    const int group = threadIdx.x >> 5;
+    if (!there) return;
+#pragma unroll
+    for (int c = 4 * group; c < DB * 32; c += 32) {
+      if (c >= p.dim) break;
+      Wide<4> sum = {};
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        sum += load<float, 4>((const float*)lds_ + (w * 32 + (lane & 31)) * Shape::kPitch + c);
+      sum *= inverse;
+      if (whole) store<T, 4>(out + c, narrow<T, 4>(sum));
+      else store<float, 4>(part_out + c, sum);
+    }
+  }
+}
+
+// The parts of the keys together: a wave to a row.
+template <class T>
+__global__ void __launch_bounds__(kAttentionThreads) attention_join(const AttentionParams p) {
+  const int64_t rows = (int64_t)p.batch * p.heads * p.q_tokens;
+  const int64_t row = (int64_t)blockIdx.x * (kAttentionThreads / kWave) + threadIdx.x / kWave;  // (b, head, token)
+  const int lane = threadIdx.x & (kWave - 1);
+  if (row >= rows) return;
+  float top = -INFINITY;
+  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.part_lse[s * rows + row]);
+  const float base = top == -INFINITY ? 0.0f : top;
+  const int64_t token = row % p.q_tokens, head = row / p.q_tokens % p.heads, b = row / p.q_tokens / p.heads;
+  T* out = static_cast<T*>(p.out) + ((b * p.q_tokens + token) * p.heads + head) * p.dim;
+  float weights = 0.0f;
+  Wide<2> sum = {};
+  for (int s = 0; s < p.splits; ++s) {
+    const float w = exp2_fast(p.part_lse[s * rows + row] - base);
+    weights += w;
+    if (2 * lane < p.dim) sum += w * load<float, 2>(p.part_out + (s * rows + row) * p.dim + 2 * lane);
+  }
+  const float inverse = weights > 0.0f || weights != weights ? 1.0f / weights : 0.0f;
+  if (2 * lane < p.dim) store<T, 2>(out + 2 * lane, narrow<T, 2>(sum * inverse));
+  if (p.lse && lane == 0) p.lse[row] = weights > 0.0f || weights != weights ? base + __builtin_amdgcn_logf(weights) : INFINITY;
+}
+
+// ---------------------------------------------------------------- the range of fp16
+// A long row's ds_ij are far smaller than fp16's normal numbers, and where the
+// gradients are scaled up they may pass its largest.  So they are rounded times
+// 2^e, with |ds_ij| <= 2 max |do_i| max |v_j| kept below 2^15; the products are
+// divided again in fp32.
+constexpr int kNormParts = 16;
+template <class T>
+constexpr bool kScaled = __is_same(T, F16);
+
+// Each of kNormParts workgroups of a (batch, key head) takes a part of its rows and
+// keys, 16 lanes to one.
+template <class T>
+__global__ void __launch_bounds__(kAttentionThreads) attention_norms(const AttentionParams p) {
+  __shared__ float most[2][kAttentionThreads / kWave];
+  const int part = blockIdx.x % kNormParts;
+  const unsigned pair = blockIdx.x / kNormParts;
+  const int b = pair / p.kv_heads, kvh = pair % p.kv_heads;
+  const Seen seen = seen_of(p, b);
+  const int group = threadIdx.x / 16, chunk = threadIdx.x % 16, chunks = p.dim / kPerChunk<T>;
+  auto square = [&](const char* row) {
+    float s = 0.0f;
+    if (chunk < chunks) {
+      const Wide<8> v = widen<T, 8>(load<T, 8>(reinterpret_cast<const T*>(row) + chunk * 8));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s = fmaf(v[k], v[k], s);
+    }
+    return lanes_sum<16>(s);
+  };
+  float top[2] = {0.0f, 0.0f};
+  const int rows = seen.q_length * p.group;
+  for (int r = part * 16 + group; r < rows; r += 16 * kNormParts) {
+    const int64_t at = (((int64_t)b * p.q_tokens + r / p.group) * p.heads + kvh * p.group + r % p.group) * p.dim;
+    top[0] = fmaxf(top[0], square(static_cast<const char*>(p.d_out) + at * (int64_t)sizeof(T)));
+  }
+  for (int j = part * 16 + group; j < seen.k_length; j += 16 * kNormParts)
+    top[1] = fmaxf(top[1], square(p.v.p + b * p.v.batch + kvh * p.v.head + (int64_t)j * p.v.token));
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    for (int step = 16; step < kWave; step *= 2) top[k] = fmaxf(top[k], __shfl_xor(top[k], step));
+    if ((threadIdx.x & (kWave - 1)) == 0) most[k][threadIdx.x / kWave] = top[k];
+  }
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    const float* m = most[threadIdx.x];
+    p.norms[blockIdx.x * 2 + threadIdx.x] = sqrtf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
+  }
+}
+// e, for all lanes of the wave
+template <class T>
+__device__ __forceinline__ int range_of(const AttentionParams& p, const Where& at) {
+  if constexpr (!kScaled<T>) return 0;
+  const float* from = p.norms + ((int64_t)at.b * p.kv_heads + at.kvh) * kNormParts * 2 + 2 * (threadIdx.x % kNormParts);
+  float a = from[0], b = from[1];
+  for (int step = 1; step < kNormParts; step *= 2) {
+    a = fmaxf(a, __shfl_xor(a, step));
+    b = fmaxf(b, __shfl_xor(b, step));
+  }
+  const float most = a * b;
+  if (!(most > 0.0f && most < 0x1p120f)) return 0;
+  return min(13 - __builtin_amdgcn_frexp_expf(most), 100);  // most < 2^exponent
+}
+
+// ---------------------------------------------------------------- gradient of the queries
+// As the forward: a wave has 32 rows, the keys go by.  It forms delta_i = do_i . o_i
+// and leaves it for the other kernel.
+template <class T, int DB>
+struct QueriesShape {
+  static constexpr int kKeys = 64;
+  static constexpr int kRows = 128;
+  static constexpr int kTileBytes = kKeys * HeadShape<T, DB>::kRow;
+};
+
+template <class T, int DB>
+__global__ void __launch_bounds__(kAttentionThreads, sizeof(T) == 2 ? 2 : 1) attention_grad_q(const AttentionParams p) {
+  using Shape = QueriesShape<T, DB>;
+  using Head = HeadShape<T, DB>;
+  __shared__ __attribute__((aligned(1024))) char lds_[4 * Shape::kTileBytes];
+  Lds* lds = (Lds*)lds_;
+  const uint32_t lds_at = lds_address(lds);
+  const Where at = where(p, p.tiles);
+  if (at.b >= p.batch) return;
+  const int tile = p.tiles - 1 - at.item;
+  const Seen seen = seen_of(p, at.b);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
+  const int chunks = p.dim / kPerChunk<T>;
+  const int rows = p.q_tokens * p.group;
+  const int first_row = tile * Shape::kRows;
+  const int row_ = first_row + wave * kRowsOfWave + (lane & 31);
+  const bool there = row_ < rows;
+  const int row = there ? row_ : 0;
+  const int token = row / p.group, head = at.kvh * p.group + row % p.group;
+  const bool live = there && token < seen.q_length;
+  const int last = there ? last_key(seen, token) : -1;
+  const int64_t dense = (((int64_t)at.b * p.q_tokens + token) * p.heads + head) * p.dim;
+  const int64_t stat = ((int64_t)at.b * p.heads + head) * p.q_tokens + token;
+
+  Chunk q[Head::kSteps], d_out[Head::kSteps];
+  load_row<T, DB>(p.q.p + at.b * p.q.batch + (int64_t)token * p.q.token + head * p.q.head, live, chunks, q);
+  load_row<T, DB>((const char*)p.d_out + dense * (int64_t)sizeof(T), live, chunks, d_out);
+  float delta = 0.0f;
+  {
+    Chunk o[Head::kSteps];
+    load_row<T, DB>((const char*)p.o + dense * (int64_t)sizeof(T), live, chunks, o);
+#pragma unroll
+    for (int t = 0; t < Head::kSteps; ++t) {
+      constexpr int N = kPerChunk<T>;
+      const Wide<N> a = widen<T, N>(__builtin_bit_cast(Vec<T, N>, o[t]));
+      const Wide<N> b = widen<T, N>(__builtin_bit_cast(Vec<T, N>, d_out[t]));
+#pragma unroll
+      for (int k = 0; k < N; ++k) delta = fmaf(a[k], b[k], delta);
+    }
+    delta = halves_sum(delta);
+  }
+  if (there && lane < 32) p.delta[stat] = delta;
+  const float lse = there ? p.lse[stat] : INFINITY;
+  const int range = range_of<T>(p, at);
+  const float up = ldexpf(1.0f, range);
+
+  const int last_token = min((min(first_row + Shape::kRows, rows) - 1) / p.group, seen.q_length - 1);
+  const int keys = first_row / p.group < seen.q_length ? max(last_key(seen, last_token) + 1, 0) : 0;
+  const int end = (keys + Shape::kKeys - 1) / Shape::kKeys;
+  const int wave_first = (first_row + wave * kRowsOfWave) / p.group;
+  const int wave_last = min(first_row + wave * kRowsOfWave + kRowsOfWave, rows) - 1;
+  const int open = wave_last / p.group < seen.q_length ? last_key(seen, wave_first) : -1;
+
+  const char* k_from = p.k.p + at.b * p.k.batch + at.kvh * p.k.head;
+  const char* v_from = p.v.p + at.b * p.v.batch + at.kvh * p.v.head;
+  auto fetch = [&](int t) {
+    const int key = t * Shape::kKeys;
+    const uint32_t to = lds_at + (t & 1) * 2 * Shape::kTileBytes;
+    fetch_tile<Head::kRow, Shape::kKeys>(k_from + (int64_t)key * p.k.token, p.k.token, seen.k_length - key, chunks, to);
+    fetch_tile<Head::kRow, Shape::kKeys>(v_from + (int64_t)key * p.v.token, p.v.token, seen.k_length - key, chunks,
+                                         to + Shape::kTileBytes);
+  };
+  Sums dq[DB] = {};
+  if (end > 0) fetch(0);
+  for (int t = 0; t < end; ++t) {
+    landed_for_all();
+    if (t + 1 < end) fetch(t + 1);
+    const Lds* k_tile = lds + (t & 1) * 2 * Shape::kTileBytes;
+    const Lds* v_tile = k_tile + Shape::kTileBytes;
+#pragma unroll
+    for (int b = 0; b < Shape::kKeys / 32; ++b) {
+      Sums s = along<T, DB>(k_tile, 32 * b, q);
+      const Sums dp = along<T, DB>(v_tile, 32 * b, d_out);
+      const int key = t * Shape::kKeys + 32 * b;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        s[r] = exp2_fast(fmaf(s[r], p.scale2, -lse)) * (dp[r] - delta);
+        if constexpr (kScaled<T>) s[r] *= up;
+      }
+      if (key + 31 > open) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          s[r] = key + row_of(r) > last ? 0.0f : s[r];
+      }
+      across<T, DB>(dq, k_tile, 32 * b, s);
+    }
+  }
+  if (there && p.dq) store_row<T, DB>(static_cast<T*>(p.dq) + dense, dq, ldexpf(p.scale, -range), p.dim);
+}
+
+// ---------------------------------------------------------------- gradients of the keys and values
+// A wave has 32 keys; the rows of all heads that share them go by, head after
+// head, in one order: no atomics, the same bits every time.
+template <class T, int DB>
+struct KeysShape {
+  static constexpr int kKeys = 128;
+  static constexpr int kRows = 64 * HeadShape<T, DB>::kRow <= 16 << 10 ? 64 : 32;  // of a tile
+  static constexpr int kTileBytes = kRows * HeadShape<T, DB>::kRow;
+};
+// The probabilities of fp16 are rounded times 2^14: at most 1, most of a long row's
+// would be subnormal.
+template <class T>
+constexpr int kLift = kScaled<T> ? 14 : 0;
+
+template <class T, int DB>
+__global__ void __launch_bounds__(kAttentionThreads, sizeof(T) == 2 ? 2 : 1) attention_grad_kv(const AttentionParams p) {
+  using Shape = KeysShape<T, DB>;
+  using Head = HeadShape<T, DB>;
+  __shared__ __attribute__((aligned(1024))) char lds_[4 * Shape::kTileBytes];
+  __shared__ __attribute__((aligned(16))) float stats[2][2][Shape::kRows];  // [buffer][lse, delta]
+  Lds* lds = (Lds*)lds_;
+  const uint32_t lds_at = lds_address(lds);
+  const Where at = where(p, p.tiles);
+  if (at.b >= p.batch) return;
+  const Seen seen = seen_of(p, at.b);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
+  const int chunks = p.dim / kPerChunk<T>;
+  const int first_key = at.item * Shape::kKeys;
+  const int wave_key = first_key + wave * 32, key = wave_key + (lane & 31);
+  const bool live = key < seen.k_length;
+  const int key_read = min(key, p.k_tokens - 1);
+  Chunk k[Head::kSteps], v[Head::kSteps];
+  load_row<T, DB>(p.k.p + at.b * p.k.batch + at.kvh * p.k.head + (int64_t)key_read * p.k.token, live, chunks, k);
+  load_row<T, DB>(p.v.p + at.b * p.v.batch + at.kvh * p.v.head + (int64_t)key_read * p.v.token, live, chunks, v);
+
+  const int range = range_of<T>(p, at);
+  const float up = ldexpf(1.0f, range - kLift<T>);
+  // tiles of tokens, the first that sees a key of the workgroup's
+  const int first_token = max(0, first_key - seen.shift);
+  const int begin = p.causal ? first_token / Shape::kRows : 0;
+  const int end = first_key < seen.k_length ? (seen.q_length + Shape::kRows - 1) / Shape::kRows : 0;
+  const int per_head = max(end - begin, 0), total = per_head * p.group;
+  const uint32_t dense_stride = (uint32_t)(p.heads * p.dim) * sizeof(T);
+  auto fetch = [&](int n) {
+    const int head = at.kvh * p.group + n / per_head, token = (begin + n % per_head) * Shape::kRows;
+    const uint32_t to = lds_at + (n & 1) * 2 * Shape::kTileBytes;
+    const int count = seen.q_length - token;
+    fetch_tile<Head::kRow, Shape::kRows>(p.q.p + at.b * p.q.batch + head * p.q.head + (int64_t)token * p.q.token,
+                                         p.q.token, count, chunks, to);
+    fetch_tile<Head::kRow, Shape::kRows>(
+        (const char*)p.d_out + (((int64_t)at.b * p.q_tokens + token) * p.heads + head) * p.dim * (int64_t)sizeof(T),
+        dense_stride, count, chunks, to + Shape::kTileBytes);
+    const int64_t stat = ((int64_t)at.b * p.heads + head) * p.q_tokens + token;
+    if (threadIdx.x < Shape::kRows) {
+      const bool in = (int)threadIdx.x < count;
+      stats[n & 1][0][threadIdx.x] = in ? p.lse[stat + threadIdx.x] : INFINITY;
+      stats[n & 1][1][threadIdx.x] = in ? p.delta[stat + threadIdx.x] : 0.0f;
+    }
+  };
+  Sums dk[DB] = {}, dv[DB] = {};
+  if (total > 0) fetch(0);
+  for (int n = 0; n < total; ++n) {
+    landed_for_all();
+    if (n + 1 < total) fetch(n + 1);
+    const Lds* q_tile = lds + (n & 1) * 2 * Shape::kTileBytes;
+    const Lds* d_tile = q_tile + Shape::kTileBytes;
+    const int token = (begin + n % per_head) * Shape::kRows;
+#pragma unroll
+    for (int b = 0; b < Shape::kRows / 32; ++b) {
+      Sums s = along<T, DB>(q_tile, 32 * b, k);
+      Sums ds = along<T, DB>(d_tile, 32 * b, v);
+      const bool open = last_key(seen, token + 32 * b) >= wave_key + 31 && token + 32 * b + 31 < seen.q_length;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int first = 32 * b + row_of(4 * j);
+        const Vec<float, 4> lse = *reinterpret_cast<const Vec<float, 4>*>(&stats[n & 1][0][first]);
+        const Vec<float, 4> delta = *reinterpret_cast<const Vec<float, 4>*>(&stats[n & 1][1][first]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 4 * j + e;
+          float w = exp2_fast(fmaf(s[r], p.scale2, (float)kLift<T> - lse[e]));
+          float g = w * (ds[r] - delta[e]);
+          if constexpr (kScaled<T>) g *= up;
+          if (!open && key > last_key(seen, token + first + e)) w = g = 0.0f;
+          s[r] = w;
+          ds[r] = g;
+        }
+      }
+      across<T, DB>(dv, d_tile, 32 * b, s);
+      across<T, DB>(dk, q_tile, 32 * b, ds);
+    }
+  }
+  if (key >= p.k_tokens) return;
+  const int64_t dense = (((int64_t)at.b * p.k_tokens + key) * p.kv_heads + at.kvh) * p.dim;
+  if (p.dk) store_row<T, DB>(static_cast<T*>(p.dk) + dense, dk, ldexpf(p.scale, -range), p.dim);
+  if (p.dv) store_row<T, DB>(static_cast<T*>(p.dv) + dense, dv, ldexpf(1.0f, -kLift<T>), p.dim);
+}
+
+// ---------------------------------------------------------------- kernels of a type
+struct AttentionTable {
+  const void* forward[4][2];  // [blocks of 32 elements - 1][few rows]
+  const void* grad_q[4];
+  const void* grad_kv[4];
+  const void* join;
+  const void* norms;  // NULL: not needed
+};
+template <class T>
+AttentionTable make_attention_table() {
+  AttentionTable t;
+  t.forward[0][0] = (const void*)attention_forward<T, 1, 1>;
+  t.forward[1][0] = (const void*)attention_forward<T, 2, 1>;
+  t.forward[2][0] = (const void*)attention_forward<T, 3, 1>;
+  t.forward[3][0] = (const void*)attention_forward<T, 4, 1>;
+  t.forward[0][1] = (const void*)attention_forward<T, 1, 4>;
+  t.forward[1][1] = (const void*)attention_forward<T, 2, 4>;
+  t.forward[2][1] = (const void*)attention_forward<T, 3, 4>;
+  t.forward[3][1] = (const void*)attention_forward<T, 4, 4>;
+  t.grad_q[0] = (const void*)attention_grad_q<T, 1>;
+  t.grad_q[1] = (const void*)attention_grad_q<T, 2>;
+  t.grad_q[2] = (const void*)attention_grad_q<T, 3>;
+  t.grad_q[3] = (const void*)attention_grad_q<T, 4>;
+  t.grad_kv[0] = (const void*)attention_grad_kv<T, 1>;
+  t.grad_kv[1] = (const void*)attention_grad_kv<T, 2>;
+  t.grad_kv[2] = (const void*)attention_grad_kv<T, 3>;
+  t.grad_kv[3] = (const void*)attention_grad_kv<T, 4>;
+  t.join = (const void*)attention_join<T>;
+  t.norms = nullptr;
+  if constexpr (kScaled<T>) t.norms = (const void*)attention_norms<T>;
+  return t;
+}
+const AttentionTable& attention_table_f32();
+const AttentionTable& attention_table_f16();
+const AttentionTable& attention_table_bf16();
+
+}  // namespace ssim_train

@@ -1,0 +1,223 @@
+// attention_api.hip -- host side of attention: argument checks, the split of the
+// work, launches.
+
+#include "attention.hpp"
+
+namespace {
+
+using namespace ssim_train;
+
+constexpr int64_t kMaxTokens = (int64_t)1 << 24;
+constexpr int64_t kMaxStride = (int64_t)1 << 24;  // bytes between tokens: a tile's offsets stay below 2^32
+constexpr int64_t kMaxBlocks = (int64_t)1 << 24;
+
+const AttentionTable& table_of(int dtype) {
+  switch (dtype) {
+    case SSIM_DTYPE_F16: return attention_table_f16();
+    case SSIM_DTYPE_BF16: return attention_table_bf16();
+    default: return attention_table_f32();
+  }
+}
+
+struct Plan {
+  bool few;         // all waves of a workgroup have the same 32 rows
+  int tiles, splits;  // of the forward
+  int q_tiles, kv_tiles;  // of the backward
+};
+
+Plan make_plan(const ssim_attention_inputs& in) {
+  Plan p;
+  const int64_t rows = in.q_tokens * (in.heads / in.kv_heads), pairs = in.batch * in.kv_heads;
+  p.few = rows <= 32;
+  p.tiles = (int)ceil_div(rows, p.few ? 32 : 128);
+  // Few workgroups: each takes a part of the keys, two tiles of them at least, and
+  // a second launch joins the parts.
+  const int64_t blocks = p.tiles * pairs, target = p.few && in.dim > 64 ? kCUs : 2 * kCUs;
+  const int64_t most = ceil_div(in.k_tokens, p.few ? 256 : 128);
+  int64_t splits = blocks > 0 ? target / blocks : 1;
+  if (splits > most) splits = most;
+  p.splits = splits < 1 ? 1 : (int)splits;
+  p.q_tiles = (int)ceil_div(rows, 128);
+  p.kv_tiles = (int)ceil_div(in.k_tokens, 128);
+  return p;
+}
+
+bool stride_ok(const int64_t* s, const ssim_attention_inputs& in, int64_t tokens) {
+  const int64_t bytes = elem_bytes(in.dtype);
+  for (int k = 0; k < 3; ++k)
+    if (s[k] < 0 || s[k] > (int64_t)1 << 44 || s[k] * bytes % 16 != 0) return false;
+  return tokens <= 1 || (s[1] >= in.dim && s[1] * bytes < kMaxStride);
+}
+
+int check_inputs(const ssim_attention_inputs* in) {
+  if (!in) return SSIM_ERR_NULL;
+  if (!known_dtype(in->dtype)) return SSIM_ERR_DTYPE;
+  if (in->causal < 0 || in->causal > 1) return SSIM_ERR_VALUE;
+  if (!(in->scale > 0.0 && in->scale <= 3.4028234663852886e37)) return SSIM_ERR_VALUE;  // (times log2 e it is fp32's)
+  if (in->batch < 0 || in->q_tokens < 0 || in->k_tokens < 0 || in->q_tokens >= kMaxTokens ||
+      in->k_tokens >= kMaxTokens)
+    return SSIM_ERR_SHAPE;
+  if (in->heads < 1 || in->heads > 65536 || in->kv_heads < 1 || in->heads % in->kv_heads != 0) return SSIM_ERR_SHAPE;
+  if (in->dim < 8 || in->dim > SSIM_ATTENTION_MAX_DIM || in->dim % 8 != 0) return SSIM_ERR_SHAPE;
+  if (!stride_ok(in->q_stride, *in, in->q_tokens) || !stride_ok(in->k_stride, *in, in->k_tokens) ||
+      !stride_ok(in->v_stride, *in, in->k_tokens))
+    return SSIM_ERR_SHAPE;
+  if (in->batch > 1 << 24) return SSIM_ERR_OVERFLOW;
+  const Plan p = make_plan(*in);
+  const int64_t pairs = in->batch * in->kv_heads, rows = in->q_tokens * (in->heads / in->kv_heads);
+  if (rows >= (int64_t)1 << 31 || pairs > kMaxBlocks / kNormParts || pairs * p.tiles * p.splits > kMaxBlocks ||
+      pairs * p.q_tiles > kMaxBlocks || pairs * p.kv_tiles > kMaxBlocks ||
+      in->batch * in->heads * in->q_tokens > (int64_t)1 << 36)
+    return SSIM_ERR_OVERFLOW;
+  return SSIM_OK;
+}
+
+// bytes from the first element to the last
+size_t span(const int64_t* s, const ssim_attention_inputs& in, int64_t tokens, int64_t heads) {
+  if (in.batch == 0 || tokens == 0) return 0;
+  return (size_t)((in.batch - 1) * s[0] + (tokens - 1) * s[1] + (heads - 1) * s[2] + in.dim) * elem_bytes(in.dtype);
+}
+
+Strided strided(const void* p, const int64_t* s, int bytes) {
+  return {static_cast<const char*>(p), s[0] * bytes, s[2] * bytes, (uint32_t)(s[1] * bytes)};
+}
+
+AttentionParams params_of(const ssim_attention_inputs& in, const Plan& plan) {
+  AttentionParams p;
+  memset(&p, 0, sizeof(p));
+  const int bytes = elem_bytes(in.dtype);
+  p.q = strided(in.q, in.q_stride, bytes);
+  p.k = strided(in.k, in.k_stride, bytes);
+  p.v = strided(in.v, in.v_stride, bytes);
+  p.q_length = in.q_lengths;
+  p.k_length = in.k_lengths;
+  p.q_tokens = (int)in.q_tokens;
+  p.k_tokens = (int)in.k_tokens;
+  p.heads = in.heads;
+  p.kv_heads = in.kv_heads;
+  p.group = in.heads / in.kv_heads;
+  p.dim = in.dim;
+  p.batch = (int)in.batch;
+  p.causal = in.causal;
+  p.spread = in.batch * in.kv_heads % 8 == 0;
+  p.scale = (float)in.scale;
+  p.scale2 = (float)(in.scale * 1.4426950408889634);
+  p.splits = plan.splits;
+  p.tiles = plan.tiles;
+  return p;
+}
+
+size_t rows_of(const ssim_attention_inputs& in) { return (size_t)in.batch * in.heads * in.q_tokens; }
+size_t delta_bytes(const ssim_attention_inputs& in) { return (rows_of(in) * 4 + 15) & ~(size_t)15; }
+size_t norm_bytes(const ssim_attention_inputs& in) {
+  return table_of(in.dtype).norms ? (size_t)in.batch * in.kv_heads * kNormParts * 8 : 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ssim_attention_workspace_bytes(const ssim_attention_inputs* in) {
+  if (check_inputs(in) != SSIM_OK) return 0;
+  const Plan p = make_plan(*in);
+  if (p.splits == 1) return 0;
+  return (rows_of(*in) * p.splits * (in->dim + 1) * 4 + 15) & ~(size_t)15;
+}
+
+int ssim_attention_forward(const ssim_attention_inputs* in, void* out, float* lse, void* workspace,
+                           void* stream) {
+  int rc = check_inputs(in);
+  if (rc != SSIM_OK) return rc;
+  if (in->batch == 0 || in->q_tokens == 0) return SSIM_OK;
+  const size_t ws = ssim_attention_workspace_bytes(in), rows = rows_of(*in);
+  if (!in->q || (in->k_tokens > 0 && (!in->k || !in->v)) || !out || (ws > 0 && !workspace)) return SSIM_ERR_NULL;
+  const int bytes = elem_bytes(in->dtype);
+  const Array ins[] = {{in->q, span(in->q_stride, *in, in->q_tokens, in->heads), 16},
+                       {in->k, span(in->k_stride, *in, in->k_tokens, in->kv_heads), 16},
+                       {in->v, span(in->v_stride, *in, in->k_tokens, in->kv_heads), 16},
+                       {in->q_lengths, 4 * (size_t)in->batch, 4},
+                       {in->k_lengths, 4 * (size_t)in->batch, 4}};
+  const Array outs[] = {{out, rows * in->dim * bytes, bytes}, {lse, rows * 4, 4}, {workspace, ws, ws ? 16 : 1}};
+  rc = check_arrays(ins, 5, outs, 3);
+  if (rc != SSIM_OK) return rc;
+  rc = check_current_device();
+  if (rc != SSIM_OK) return rc;
+
+  const Plan plan = make_plan(*in);
+  AttentionParams p = params_of(*in, plan);
+  p.out = out;
+  p.lse = lse;
+  if (plan.splits > 1) {
+    p.part_out = static_cast<float*>(workspace);
+    p.part_lse = p.part_out + rows * plan.splits * in->dim;
+  }
+  const AttentionTable& t = table_of(in->dtype);
+  const int blocks = (in->dim - 1) / 32;
+  rc = launch(t.forward[blocks][plan.few], dim3((unsigned)(in->batch * in->kv_heads * plan.tiles * plan.splits)),
+              kAttentionThreads, p, stream);
+  if (rc != SSIM_OK || plan.splits == 1) return rc;
+  return launch(t.join, dim3((unsigned)ceil_div(rows, kAttentionThreads / kWave)), kAttentionThreads, p, stream);
+}
+
+size_t ssim_attention_backward_workspace_bytes(const ssim_attention_inputs* in) {
+  if (check_inputs(in) != SSIM_OK) return 0;
+  return delta_bytes(*in) + norm_bytes(*in);
+}
+
+int ssim_attention_backward(const ssim_attention_inputs* in, const void* out, const float* lse,
+                            const void* d_out, void* dq, void* dk, void* dv, void* workspace,
+                            void* stream) {
+  int rc = check_inputs(in);
+  if (rc != SSIM_OK) return rc;
+  if (in->batch == 0) return SSIM_OK;
+  const bool any_q = in->q_tokens > 0, any_k = in->k_tokens > 0;
+  if (!(any_q && dq) && !(any_k && (dk || dv))) return SSIM_OK;
+  if (((any_q || ssim_attention_backward_workspace_bytes(in) > 0) && !workspace) ||
+      (any_q && (!in->q || !out || !lse || !d_out)) || (any_k && (!in->k || !in->v)))
+    return SSIM_ERR_NULL;
+  const int bytes = elem_bytes(in->dtype);
+  const size_t rows = rows_of(*in), keys = (size_t)in->batch * in->k_tokens * in->kv_heads * in->dim * bytes;
+  const size_t ws = ssim_attention_backward_workspace_bytes(in);
+  const Array ins[] = {{in->q, span(in->q_stride, *in, in->q_tokens, in->heads), 16},
+                       {in->k, span(in->k_stride, *in, in->k_tokens, in->kv_heads), 16},
+                       {in->v, span(in->v_stride, *in, in->k_tokens, in->kv_heads), 16},
+                       {in->q_lengths, 4 * (size_t)in->batch, 4},
+                       {in->k_lengths, 4 * (size_t)in->batch, 4},
+                       {out, rows * in->dim * bytes, 16},
+                       {lse, rows * 4, 4},
+                       {d_out, rows * in->dim * bytes, 16}};
+  const Array outs[] = {{dq, rows * in->dim * bytes, bytes}, {dk, keys, bytes}, {dv, keys, bytes},
+                        {workspace, ws, ws ? 16 : 1}};
+  rc = check_arrays(ins, 8, outs, 4);
+  if (rc != SSIM_OK) return rc;
+  rc = check_current_device();
+  if (rc != SSIM_OK) return rc;
+
+  const Plan plan = make_plan(*in);
+  AttentionParams p = params_of(*in, plan);
+  p.o = out;
+  p.lse = const_cast<float*>(lse);
+  p.d_out = d_out;
+  p.delta = static_cast<float*>(workspace);
+  p.dq = dq;
+  p.dk = dk;
+  p.dv = dv;
+  const AttentionTable& t = table_of(in->dtype);
+  const int blocks = (in->dim - 1) / 32;
+  const unsigned pairs = (unsigned)(in->batch * in->kv_heads);
+  if (t.norms) {
+    p.norms = reinterpret_cast<float*>(static_cast<char*>(workspace) + delta_bytes(*in));
+    rc = launch(t.norms, dim3(pairs * kNormParts), kAttentionThreads, p, stream);
+    if (rc != SSIM_OK) return rc;
+  }
+  if (any_q) {  // (it forms delta for the other kernel)
+    p.tiles = plan.q_tiles;
+    rc = launch(t.grad_q[blocks], dim3(pairs * plan.q_tiles), kAttentionThreads, p, stream);
+    if (rc != SSIM_OK) return rc;
+  }
+  if (!any_k || !(dk || dv)) return SSIM_OK;
+  p.tiles = plan.kv_tiles;
+  return launch(t.grad_kv[blocks], dim3(pairs * plan.kv_tiles), kAttentionThreads, p, stream);
+}
+
+}  // extern "C"

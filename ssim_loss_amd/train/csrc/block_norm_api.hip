@@ -7,8 +7,6 @@ namespace {
 
 using namespace ssim_train;
 
-constexpr int kCUs = 256;  // of an MI355X; the workspace's size must not need a device query
-
 const NormTable& table_of(int dtype) {
   switch (dtype) {
     case SSIM_DTYPE_F16: return norm_table_f16();
@@ -30,8 +28,6 @@ struct Plan {
   int parts;
   int64_t groups, part_rows;
 };
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Workgroups of `workers` rows at once, about `target` of them, with the same
 // number of rows each.
@@ -139,26 +135,6 @@ int check_inputs(const ssim_block_norm_inputs* in) {
   return SSIM_OK;
 }
 
-struct Array {
-  const void* p;
-  size_t bytes;
-  int align;
-};
-
-// alignment of all, and no output over an input or another output
-int check_arrays(const Array* ins, int n_in, const Array* outs, int n_out) {
-  for (int k = 0; k < n_in; ++k)
-    if (misaligned(ins[k].p, ins[k].align)) return SSIM_ERR_SHAPE;
-  for (int k = 0; k < n_out; ++k) {
-    if (misaligned(outs[k].p, outs[k].align)) return SSIM_ERR_SHAPE;
-    for (int l = 0; l < n_in; ++l)
-      if (overlaps(outs[k].p, outs[k].bytes, ins[l].p, ins[l].bytes)) return SSIM_ERR_ALIAS;
-    for (int l = 0; l < k; ++l)
-      if (overlaps(outs[k].p, outs[k].bytes, outs[l].p, outs[l].bytes)) return SSIM_ERR_ALIAS;
-  }
-  return SSIM_OK;
-}
-
 size_t workspace_bytes(const ssim_block_norm_inputs& in, const Plan& p) {
   const size_t arrays = p.cut ? 3 : 2;
   return ((size_t)p.back_blocks * (size_t)in.width * 4 * arrays + 15) & ~(size_t)15;
@@ -185,16 +161,6 @@ NormParams params_of(const ssim_block_norm_inputs& in, const Plan& p) {
   k.parts = p.parts;
   k.blocks = p.back_blocks;
   return k;
-}
-
-int launch(const void* kernel, dim3 grid, int threads, NormParams& k, void* stream) {
-  void* args[] = {&k};
-  if (hipLaunchKernel(kernel, grid, dim3(threads), args, 0, static_cast<hipStream_t>(stream)) !=
-      hipSuccess) {
-    (void)hipGetLastError();
-    return SSIM_ERR_HIP;
-  }
-  return SSIM_OK;
 }
 
 }  // namespace

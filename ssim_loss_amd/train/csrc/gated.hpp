@@ -1,0 +1,507 @@
+// gated.hpp -- kernels of the gated layer:
+//   g = x Wg^T + bg,  u = x Wu^T + bu,  h = act(g) u
+//   dg = dh u act'(g),  du = dh act(g)
+//   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x,  db = sums over rows
+//
+// Three products of one kernel's kind.  A workgroup forms a tile of the result,
+// of which a lane has four neighbouring elements of a row at a time: the weights
+// are the left operand.  Both operands go from memory straight to LDS, two tiles
+// in turn, 128 bytes of the axis that is summed over in each.  The forward's left
+// tile is half Wg's and half Wu's rows, so a wave has g and u of the same elements
+// in its registers and neither has to be written for the product.
+
+#pragma once
+
+#include "mma.hpp"
+
+namespace ssim_train {
+
+struct GatedParams {
+  const void* x;        // [rows][x_pitch]
+  const void* w[2];     // gate, up: [hidden][w_pitch]
+  const void* bias[2];  // [hidden] or NULL
+  int64_t rows;
+  int64_t x_pitch, w_pitch, h_pitch;  // elements; of the arrays of g, u, dg, du: h_pitch
+  int width, hidden, act;
+  int width_ext;        // width, or x_pitch where x and w are copies padded with zeros
+  void* out;            // [rows][hidden]
+  void* saved[2];       // g, u: [rows][h_pitch], or NULL
+  // backward
+  const void* d_out;    // [rows][hidden]
+  void* d[2];           // dg, du: [rows][h_pitch], zeros behind hidden
+  float* part_bias;     // [blocks of rows][2][hidden] or NULL
+  int row_blocks;
+  int rows_of_block;
+  void* dx;             // [rows][width]
+  void* dw[2];          // [hidden][width]
+  void* db[2];
+  // tiles of the product
+  int m_tiles, n_tiles;
+  // copies
+  const void* from;
+  void* to;
+  int64_t copy_rows, copy_width, copy_pitch;
+};
+
+// act(g), and act'(g)
+template <class T>
+__device__ __forceinline__ float exp_of(float v) {
+  if constexpr (sizeof(T) == 4) return expf(v);
+  else return __expf(v);
+}
+template <class T>
+__device__ __forceinline__ float quotient_of(float a, float b) {
+  if constexpr (sizeof(T) == 4) return a / b;
+  else return a * __builtin_amdgcn_rcpf(b);
+}
+template <class T>
+__device__ __forceinline__ float act_of(float g, int act) {
+  if (act == SSIM_ACT_GELU) return 0.5f * g * erfcf(g * -0.70710678118654752f);
+  return quotient_of<T>(act == SSIM_ACT_SILU ? g : 1.0f, 1.0f + exp_of<T>(-g));
+}
+template <class T>
+__device__ __forceinline__ void act_slope(float g, int act, float& a, float& slope) {
+  if (act == SSIM_ACT_GELU) {
+    const float phi = 0.5f * erfcf(g * -0.70710678118654752f);
+    a = g * phi;
+    slope = fmaf(g * 0.39894228040143268f, exp_of<T>(-0.5f * g * g), phi);
+    return;
+  }
+  // sigma(g) and sigma(-g), each without cancellation
+  const float e = exp_of<T>(-fabsf(g));
+  const float big = quotient_of<T>(1.0f, 1.0f + e), small = e * big;
+  const float s = g >= 0.0f ? big : g < 0.0f ? small : g, r = g >= 0.0f ? small : big;
+  if (act == SSIM_ACT_SILU) {
+    a = g * s;
+    slope = s * fmaf(g, r, 1.0f);
+  } else {
+    a = s;
+    slope = s * r;
+  }
+}
+
+enum Product { kForward, kGradX, kGradW };
+
+constexpr int kDepthBytes = 128;  // of the summed axis in a tile
+
+// A tile of kBlocksM x kBlocksN blocks of 32 x 32 to a wave, kWavesM x kWavesN waves.
+template <class T, int BM, int BN, int WM, int WN>
+struct ProductShape {
+  static constexpr int kThreads = WM * WN * kWave;
+  static constexpr int kM = BM * WM * 32, kN = BN * WN * 32;
+  static constexpr int kDepth = kDepthBytes / (int)sizeof(T);
+  static constexpr int kSteps = kDepth / kPerStep<T>;
+  static constexpr int kABytes = kM * kDepthBytes, kBBytes = kN * kDepthBytes;
+};
+
+// An operand's tile whose rows are contiguous along the summed axis: kRows rows,
+// 128 bytes each.  `from` is the first row's first byte of the tile; `chunks` are
+// left of the axis.
+template <int kRows, int kThreads>
+__device__ __forceinline__ void fetch_along(const char* from, int64_t pitch, int64_t rows, int chunks, uint32_t to) {
+  constexpr int kAtOnce = kThreads / 8;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int count = (int)(rows < kRows ? rows : kRows);
+  const Descriptor d =
+      describe(from, count <= 0 ? 0u : (uint32_t)(count - 1) * (uint32_t)pitch + (uint32_t)min(chunks, 8) * 16u);
+#pragma unroll
+  for (int j = 0; j < kRows / kAtOnce; ++j) {
+    const int r = threadIdx.x / 8 + j * kAtOnce;
+    const int chunk = (threadIdx.x & 7) ^ swizzle<128>(r);
+    const uint32_t offset = chunk < chunks ? (uint32_t)r * (uint32_t)pitch + (uint32_t)chunk * 16u : kNowhere;
+    load_to_lds(d, offset, to + (uint32_t)(j * kAtOnce * 128 + wave * 1024));
+  }
+}
+// An operand's tile whose rows lie along the other axis: kDepth rows of kColumns
+// elements; `chunks` are left of such a row, `rows` of the summed axis.
+template <class T, int kColumns, int kThreads>
+__device__ __forceinline__ void fetch_across(const char* from, int64_t pitch, int64_t rows, int64_t chunks, uint32_t to) {
+  constexpr int kRow = kColumns * (int)sizeof(T), kChunks = kRow / 16;
+  constexpr int kDepth = kDepthBytes / (int)sizeof(T);
+  constexpr int kAtOnce = kThreads / kChunks;
+  static_assert(kAtOnce >= 1 && kDepth % kAtOnce == 0, "whole instructions");
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int count = (int)(rows < kDepth ? rows : kDepth), left = (int)(chunks < kChunks ? chunks : kChunks);
+  const Descriptor d = describe(from, count <= 0 || left <= 0 ? 0u : (uint32_t)(count - 1) * (uint32_t)pitch + (uint32_t)left * 16u);
+#pragma unroll
+  for (int j = 0; j < kDepth / kAtOnce; ++j) {
+    const int r = threadIdx.x / kChunks + j * kAtOnce;
+    const int chunk = (threadIdx.x % kChunks) ^ swizzle<kRow>(r);
+    const uint32_t offset = chunk < left ? (uint32_t)r * (uint32_t)pitch + (uint32_t)chunk * 16u : kNowhere;
+    load_to_lds(d, offset, to + (uint32_t)(j * kAtOnce * kRow + wave * 1024));
+  }
+}
+
+// The workgroup's tile.  Ids go round the XCDs; each XCD takes a run of tiles that
+// go down eight rows of tiles at a time, so that its cache holds their operands.
+struct TileAt {
+  int m, n;
+};
+__device__ __forceinline__ TileAt tile_at(int m_tiles, int n_tiles) {
+  constexpr unsigned kGroup = 8;
+  const unsigned total = (unsigned)m_tiles * n_tiles, per = (total + 7) / 8, rest = total - (per - 1) * 8;
+  const unsigned xcd = blockIdx.x & 7, j = blockIdx.x >> 3;
+  // (the first `rest` XCDs have a tile more where 8 does not divide the tiles)
+  const unsigned id = xcd < rest ? xcd * per + j : rest * per + (xcd - rest) * (per - 1) + j;
+  const unsigned of_group = kGroup * m_tiles, group = id / of_group, in = id - group * of_group;
+  const unsigned rows = min(kGroup, n_tiles - group * kGroup);
+  return {(int)(in / rows), (int)(group * kGroup + in % rows)};
+}
+
+// Four neighbouring elements of a row, those of them that it has.
+template <class T>
+__device__ __forceinline__ void store_four(T* row, int64_t column, int64_t width, Wide<4> v) {
+  const Vec<T, 4> n = narrow<T, 4>(v);
+  if (column + 4 <= width) {
+    store<T, 4>(row + column, n);
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (column + k < width) row[column + k] = n[k];
+}
+
+template <class T, int kProduct, int BM, int BN, int WM, int WN>
+__global__ void __launch_bounds__(WM* WN* kWave, WM* WN == 4 ? 2 : 1) gated_product(const GatedParams p) {
+  using Shape = ProductShape<T, BM, BN, WM, WN>;
+  __shared__ __attribute__((aligned(1024))) char lds_[2 * (Shape::kABytes + Shape::kBBytes)];
+  Lds* lds = (Lds*)lds_;
+  const uint32_t lds_at = lds_address(lds);
+  const TileAt at = tile_at(p.m_tiles, p.n_tiles);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
+  const int wm = wave % WM, wn = wave / WM, h = lane >> 5;
+  constexpr int kBytes = (int)sizeof(T);
+  constexpr int kHalfM = Shape::kM / 2;  // of the forward: columns of the result in a tile
+
+  // how many tiles of the summed axis there are
+  const int64_t depth = kProduct == kForward ? p.width_ext : kProduct == kGradX ? p.h_pitch : p.rows;
+  const int once = (int)((depth + Shape::kDepth - 1) / Shape::kDepth);
+  const int count = kProduct == kGradX ? 2 * once : once;
+  const int n_half = p.n_tiles / 2;  // gradients of weights: gate's tiles, then up's
+  const int which = kProduct == kGradW ? (at.n >= n_half) : 0;
+  if (kProduct == kGradW && !p.dw[which]) return;
+  const int64_t m0 = (int64_t)at.m * (kProduct == kForward ? kHalfM : Shape::kM);
+  const int64_t n0 = (int64_t)(kProduct == kGradW ? at.n - which * n_half : at.n) * Shape::kN;
+
+  auto fetch = [&](int t) {
+    const uint32_t a_to = lds_at + (t & 1) * (Shape::kABytes + Shape::kBBytes), b_to = a_to + Shape::kABytes;
+    if constexpr (kProduct == kForward) {
+      const int64_t k = (int64_t)t * Shape::kDepth;
+      const int chunks = (int)((p.width_ext - k) / kPerChunk<T>);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        fetch_along<kHalfM, Shape::kThreads>((const char*)p.w[i] + (m0 * p.w_pitch + k) * kBytes, p.w_pitch * kBytes,
+                                             p.hidden - m0, chunks, a_to + i * (kHalfM * 128));
+      fetch_along<Shape::kN, Shape::kThreads>((const char*)p.x + (n0 * p.x_pitch + k) * kBytes, p.x_pitch * kBytes,
+                                              p.rows - n0, chunks, b_to);
+    } else if constexpr (kProduct == kGradX) {
+      const int i = t >= once;
+      const int64_t k = (int64_t)(t - i * once) * Shape::kDepth;
+      fetch_across<T, Shape::kM, Shape::kThreads>((const char*)p.w[i] + (k * p.w_pitch + m0) * kBytes, p.w_pitch * kBytes,
+                                                  p.hidden - k, (p.width_ext - m0 + kPerChunk<T> - 1) / kPerChunk<T>, a_to);
+      fetch_along<Shape::kN, Shape::kThreads>((const char*)p.d[i] + (n0 * p.h_pitch + k) * kBytes, p.h_pitch * kBytes,
+                                              p.rows - n0, (int)((p.h_pitch - k) / kPerChunk<T>), b_to);
+    } else {
+      const int64_t k = (int64_t)t * Shape::kDepth;
+      fetch_across<T, Shape::kM, Shape::kThreads>((const char*)p.x + (k * p.x_pitch + m0) * kBytes, p.x_pitch * kBytes,
+                                                  p.rows - k, (p.width_ext - m0 + kPerChunk<T> - 1) / kPerChunk<T>, a_to);
+      fetch_across<T, Shape::kN, Shape::kThreads>((const char*)p.d[which] + (k * p.h_pitch + n0) * kBytes,
+                                                  p.h_pitch * kBytes, p.rows - k, (p.h_pitch - n0) / kPerChunk<T>, b_to);
+    }
+  };
+
+  Sums c[BM][BN] = {};
+  // the blocks' first rows (or columns) in the tiles; the forward's are g's, then u's
+  auto a_block = [&](int i) {
+    if constexpr (kProduct == kForward) return i < BM / 2 ? wm * (BM / 2) + i : kHalfM / 32 + wm * (BM / 2) + i - BM / 2;
+    else return wm * BM + i;
+  };
+  if (count > 0) fetch(0);
+  for (int t = 0; t < count; ++t) {
+    landed_for_all();
+    if (t + 1 < count) fetch(t + 1);
+    const Lds* a_tile = lds + (t & 1) * (Shape::kABytes + Shape::kBBytes);
+    const Lds* b_tile = a_tile + Shape::kABytes;
+#pragma unroll
+    for (int s = 0; s < Shape::kSteps; ++s) {
+      Chunk a[BM], b[BN];
+#pragma unroll
+      for (int i = 0; i < BM; ++i) {
+        if constexpr (kProduct == kForward)
+          a[i] = lds_chunk(a_tile, place<128>(32 * a_block(i) + (lane & 31), 2 * s + h));
+        else
+          a[i] = lds_across<T, Shape::kM * kBytes, true>(a_tile, s * kPerStep<T>, a_block(i));
+      }
+#pragma unroll
+      for (int i = 0; i < BN; ++i) {
+        if constexpr (kProduct == kGradW)
+          b[i] = lds_across<T, Shape::kN * kBytes, true>(b_tile, s * kPerStep<T>, wn * BN + i);
+        else
+          b[i] = lds_chunk(b_tile, place<128>(32 * (wn * BN + i) + (lane & 31), 2 * s + h));
+      }
+#pragma unroll
+      for (int i = 0; i < BM; ++i)
+#pragma unroll
+        for (int j = 0; j < BN; ++j) multiply<T>(c[i][j], a[i], b[j]);
+    }
+  }
+
+  if constexpr (kProduct == kForward) {
+#pragma unroll
+    for (int i = 0; i < BM / 2; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t column = m0 + 32 * (wm * (BM / 2) + i) + 8 * k + 4 * h;
+        Wide<4> bias[2] = {};
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (p.bias[w] && column + e < p.hidden) bias[w][e] = (float)static_cast<const T*>(p.bias[w])[column + e];
+#pragma unroll
+        for (int j = 0; j < BN; ++j) {
+          const int64_t row = n0 + 32 * (wn * BN + j) + (lane & 31);
+          if (row >= p.rows) continue;
+          Wide<4> g, u, v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            g[e] = c[i][j][4 * k + e] + bias[0][e];
+            u[e] = c[i + BM / 2][j][4 * k + e] + bias[1][e];
+            v[e] = act_of<T>(g[e], p.act) * u[e];
+          }
+          store_four<T>(static_cast<T*>(p.out) + row * p.hidden, column, p.hidden, v);
+          if (p.saved[0] && column < p.h_pitch) {
+            store<T, 4>(static_cast<T*>(p.saved[0]) + row * p.h_pitch + column, narrow<T, 4>(g));
+            store<T, 4>(static_cast<T*>(p.saved[1]) + row * p.h_pitch + column, narrow<T, 4>(u));
+          }
+        }
+      }
+  } else {
+    T* out = static_cast<T*>(kProduct == kGradX ? p.dx : p.dw[which]);
+    const int64_t rows = kProduct == kGradX ? p.rows : p.hidden;
+#pragma unroll
+    for (int j = 0; j < BN; ++j) {
+      const int64_t row = n0 + 32 * (wn * BN + j) + (lane & 31);
+      if (row >= rows) continue;
+#pragma unroll
+      for (int i = 0; i < BM; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          store_four<T>(out + row * p.width, m0 + 32 * (wm * BM + i) + 8 * k + 4 * h, p.width,
+                        Wide<4>{c[i][j][4 * k], c[i][j][4 * k + 1], c[i][j][4 * k + 2], c[i][j][4 * k + 3]});
+    }
+  }
+}
+
+// dg and du, and what they add up to over a block of rows.  A thread has a vector
+// of columns; 64 of them beside each other, four rows at a time.
+template <class T>
+__global__ void __launch_bounds__(256) gated_slopes(const GatedParams p) {
+  constexpr int V = kPerChunk<T>;
+  __shared__ float sums[3][2][kWave * V];
+  const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
+  const int64_t column = ((int64_t)blockIdx.x * kWave + lane) * V;
+  const int64_t first = (int64_t)blockIdx.y * p.rows_of_block;
+  const int64_t end = first + p.rows_of_block < p.rows ? first + p.rows_of_block : p.rows;
+  Wide<V> total[2] = {};
+  if (column < p.h_pitch) {
+    for (int64_t row = first + wave; row < end; row += 4) {
+      const int64_t at = row * p.h_pitch + column;
+      const Wide<V> g = widen<T, V>(load<T, V>(static_cast<const T*>(p.saved[0]) + at));
+      const Wide<V> u = widen<T, V>(load<T, V>(static_cast<const T*>(p.saved[1]) + at));
+      const T* d_row = static_cast<const T*>(p.d_out) + row * p.hidden;
+      Wide<V> d = {};
+      if (column + V <= p.hidden) d = widen<T, V>(load<T, V>(d_row + column));
+      else
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          if (column + k < p.hidden) d[k] = (float)d_row[column + k];
+      Wide<V> dg, du;
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        float a, slope;
+        act_slope<T>(g[k], p.act, a, slope);
+        const bool in = column + k < p.hidden;
+        dg[k] = in ? d[k] * u[k] * slope : 0.0f;
+        du[k] = in ? d[k] * a : 0.0f;
+      }
+      store<T, V>(static_cast<T*>(p.d[0]) + at, narrow<T, V>(dg));
+      store<T, V>(static_cast<T*>(p.d[1]) + at, narrow<T, V>(du));
+      total[0] += dg;
+      total[1] += du;
+    }
+  }
+  if (!p.part_bias) return;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (wave > 0) sums[wave - 1][i][k * kWave + lane] = total[i][k];
+  __syncthreads();
+  if (wave > 0) return;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const float s = ((total[i][k] + sums[0][i][k * kWave + lane]) + sums[1][i][k * kWave + lane]) + sums[2][i][k * kWave + lane];
+      if (column + k < p.hidden) p.part_bias[((int64_t)blockIdx.y * 2 + i) * p.hidden + column + k] = s;
+    }
+}
+
+template <class T>
+__global__ void __launch_bounds__(64) gated_bias_sums(const GatedParams p) {
+  const int column = blockIdx.x * 64 + threadIdx.x, i = blockIdx.y;
+  if (column >= p.hidden || !p.db[i]) return;
+  double sum = 0.0;
+  for (int b = 0; b < p.row_blocks; ++b) sum += p.part_bias[((int64_t)b * 2 + i) * p.hidden + column];
+  static_cast<T*>(p.db[i])[column] = (T)(float)sum;
+}
+
+// Rows of copy_width elements to rows of copy_pitch, zeros behind them.
+template <class T>
+__global__ void __launch_bounds__(256) gated_copy(const GatedParams p) {
+  constexpr int V = kPerChunk<T>;
+  const int64_t chunks = p.copy_pitch / V;
+  for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < p.copy_rows * chunks; id += (int64_t)gridDim.x * 256) {
+    const int64_t row = id / chunks, column = (id - row * chunks) * V;
+    const T* from = static_cast<const T*>(p.from) + row * p.copy_width;
+    Vec<T, V> v = {};
+    if (column + V <= p.copy_width) v = load<T, V>(from + column);
+    else
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (column + k < p.copy_width) v[k] = from[column + k];
+    store<T, V>(static_cast<T*>(p.to) + row * p.copy_pitch + column, v);
+  }
+}
+
+// ---- few rows: the weights go by once, from memory straight to the matrix
+// instruction (16 rows of weights, 16 of x); four waves share the summed axis.
+typedef float Sums4 __attribute__((ext_vector_type(4)));
+template <class T>
+__device__ __forceinline__ void multiply16(Sums4& c, Chunk a, Chunk b) {
+  if constexpr (sizeof(T) == 4) {
+    const Vec<float, 4> x = __builtin_bit_cast(Vec<float, 4>, a), y = __builtin_bit_cast(Vec<float, 4>, b);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[k], y[k], c, 0, 0, 0);
+  } else if constexpr (__is_same(T, F16)) {
+    c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(Vec<F16, 8>, a), __builtin_bit_cast(Vec<F16, 8>, b), c, 0, 0, 0);
+  } else {
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(Vec<BF16, 8>, a), __builtin_bit_cast(Vec<BF16, 8>, b), c, 0, 0, 0);
+  }
+}
+// The chunk of a row at `column`; zeros behind its end, the last one with one load.
+// (rows have a chunk's elements or more)
+template <class T>
+__device__ __forceinline__ Chunk chunk_of_row(const T* row, int column, int width) {
+  constexpr int V = kPerChunk<T>;
+  const int start = min(column, width - V);
+  Chunk c = __builtin_bit_cast(Chunk, load<T, V>(row + start));
+  if (column > start) {  // elements that belong to the chunk before go
+    const int shift = min(column - start, V) * (int)sizeof(T) * 8;  // bits, to 128
+    unsigned __int128 bits = __builtin_bit_cast(unsigned __int128, c);
+    bits = shift >= 128 ? 0 : bits >> shift;
+    c = __builtin_bit_cast(Chunk, bits);
+  }
+  return c;
+}
+
+constexpr int kFewUnroll = 4;
+
+template <class T, int NB>
+__global__ void __launch_bounds__(256) gated_few_rows(const GatedParams p) {
+  __shared__ Sums4 joined[3][2][NB][kWave];
+  const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
+  const int group = lane >> 4;
+  const int m0 = blockIdx.x * 16;
+  const int w_row = min(m0 + (lane & 15), p.hidden - 1);
+  const T* gate = static_cast<const T*>(p.w[0]) + (int64_t)w_row * p.w_pitch;
+  const T* up = static_cast<const T*>(p.w[1]) + (int64_t)w_row * p.w_pitch;
+  const T* x[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j)
+    x[j] = static_cast<const T*>(p.x) + min((int64_t)(16 * j + (lane & 15)), p.rows - 1) * p.x_pitch;
+  constexpr int kStep = 4 * kPerChunk<T>;  // elements that an instruction (fp32: four) sums over
+  constexpr int kAtOnce = kStep * kFewUnroll;
+  Sums4 c[2][NB] = {};
+  for (int k0 = wave * kAtOnce; k0 < p.width; k0 += 4 * kAtOnce) {
+    Chunk a[2][kFewUnroll];
+#pragma unroll
+    for (int s = 0; s < kFewUnroll; ++s) {
+      const int k = k0 + s * kStep + group * kPerChunk<T>;
+      a[0][s] = chunk_of_row<T>(gate, k, p.width);
+      a[1][s] = chunk_of_row<T>(up, k, p.width);
+    }
+#pragma unroll
+    for (int s = 0; s < kFewUnroll; ++s) {
+      const int k = k0 + s * kStep + group * kPerChunk<T>;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const Chunk b = chunk_of_row<T>(x[j], k, p.width);
+        multiply16<T>(c[0][j], a[0][s], b);
+        multiply16<T>(c[1][j], a[1][s], b);
+      }
+    }
+  }
+  if (wave > 0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) joined[wave - 1][i][j][lane] = c[i][j];
+  }
+  __syncthreads();
+  if (wave > 0) return;
+  const int column = m0 + 4 * group;
+  if (column >= p.h_pitch) return;
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) c[i][j] = ((c[i][j] + joined[0][i][j][lane]) + joined[1][i][j][lane]) + joined[2][i][j][lane];
+    const int64_t row = 16 * j + (lane & 15);
+    if (row >= p.rows) continue;
+    Wide<4> g, u, v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool in = column + e < p.hidden;
+      g[e] = c[0][j][e] + (p.bias[0] && in ? (float)static_cast<const T*>(p.bias[0])[column + e] : 0.0f);
+      u[e] = c[1][j][e] + (p.bias[1] && in ? (float)static_cast<const T*>(p.bias[1])[column + e] : 0.0f);
+      v[e] = act_of<T>(g[e], p.act) * u[e];
+    }
+    store_four<T>(static_cast<T*>(p.out) + row * p.hidden, column, p.hidden, v);
+    if (p.saved[0]) {
+      store<T, 4>(static_cast<T*>(p.saved[0]) + row * p.h_pitch + column, narrow<T, 4>(g));
+      store<T, 4>(static_cast<T*>(p.saved[1]) + row * p.h_pitch + column, narrow<T, 4>(u));
+    }
+  }
+}
+
+// ---- kernels of a type
+struct GatedTable {
+  const void* product[3][2];  // [Product][large tiles]
+  const void* few[3];         // 16, 32, 64 rows
+  const void* slopes;
+  const void* bias_sums;
+  const void* copy;
+};
+template <class T>
+GatedTable make_gated_table() {
+  GatedTable t;
+  t.product[kForward][0] = (const void*)gated_product<T, kForward, 2, 2, 2, 2>;
+  t.product[kForward][1] = (const void*)gated_product<T, kForward, 4, 2, 2, 4>;
+  t.product[kGradX][0] = (const void*)gated_product<T, kGradX, 2, 2, 2, 2>;
+  t.product[kGradX][1] = (const void*)gated_product<T, kGradX, 4, 2, 2, 4>;
+  t.product[kGradW][0] = (const void*)gated_product<T, kGradW, 2, 2, 2, 2>;
+  t.product[kGradW][1] = (const void*)gated_product<T, kGradW, 4, 2, 2, 4>;
+  t.few[0] = (const void*)gated_few_rows<T, 1>;
+  t.few[1] = (const void*)gated_few_rows<T, 2>;
+  t.few[2] = (const void*)gated_few_rows<T, 4>;
+  t.slopes = (const void*)gated_slopes<T>;
+  t.bias_sums = (const void*)gated_bias_sums<T>;
+  t.copy = (const void*)gated_copy<T>;
+  return t;
+}
+const GatedTable& gated_table_f32();
+const GatedTable& gated_table_f16();
+const GatedTable& gated_table_bf16();
+
+}  // namespace ssim_train

@@ -1,0 +1,271 @@
+// gated_api.hip -- host side of the gated layer: argument checks, the choice of
+// tiles, launches.
+
+#include "gated.hpp"
+
+namespace {
+
+using namespace ssim_train;
+
+constexpr int64_t kMaxWidth = (int64_t)1 << 20;
+constexpr int64_t kFewRows = 64;
+
+const GatedTable& table_of(int dtype) {
+  switch (dtype) {
+    case SSIM_DTYPE_F16: return gated_table_f16();
+    case SSIM_DTYPE_BF16: return gated_table_bf16();
+    default: return gated_table_f32();
+  }
+}
+
+int per_chunk(const ssim_gated_linear_inputs& in) { return 16 / elem_bytes(in.dtype); }
+int64_t padded(const ssim_gated_linear_inputs& in, int64_t n) { return ceil_div(n, per_chunk(in)) * per_chunk(in); }
+size_t to_16(size_t n) { return (n + 15) & ~(size_t)15; }
+
+bool takes_few(const ssim_gated_linear_inputs& in) { return in.rows <= kFewRows && in.width >= per_chunk(in); }
+
+// The tiled products load whole chunks of 16 bytes at multiples of 16: other
+// widths and tensors that start elsewhere are copied to rows that do first.
+bool needs_copy(const ssim_gated_linear_inputs& in, const void* p) {
+  return in.width % per_chunk(in) != 0 || misaligned(p, 16);
+}
+struct Copies {
+  bool any;
+  size_t x, w;  // bytes of each, 0: not copied
+};
+Copies copies_of(const ssim_gated_linear_inputs& in) {
+  // (all or none: they share a row's length)
+  Copies c = {needs_copy(in, in.x) || needs_copy(in, in.w_gate) || needs_copy(in, in.w_up), 0, 0};
+  if (c.any) {
+    const size_t row = (size_t)padded(in, in.width) * elem_bytes(in.dtype);
+    c.x = (size_t)in.rows * row;
+    c.w = (size_t)in.hidden * row;
+  }
+  return c;
+}
+
+int check_inputs(const ssim_gated_linear_inputs* in) {
+  if (!in) return SSIM_ERR_NULL;
+  if (!known_dtype(in->dtype)) return SSIM_ERR_DTYPE;
+  if (in->act < SSIM_ACT_SILU || in->act > SSIM_ACT_SIGMOID) return SSIM_ERR_VALUE;
+  if (in->rows < 0 || in->width < 1 || in->width > kMaxWidth || in->hidden < 1 || in->hidden > kMaxWidth)
+    return SSIM_ERR_SHAPE;
+  if (in->rows > (int64_t)1 << 30) return SSIM_ERR_OVERFLOW;
+  return SSIM_OK;
+}
+
+GatedParams params_of(const ssim_gated_linear_inputs& in) {
+  GatedParams p;
+  memset(&p, 0, sizeof(p));
+  p.x = in.x;
+  p.w[0] = in.w_gate;
+  p.w[1] = in.w_up;
+  p.bias[0] = in.b_gate;
+  p.bias[1] = in.b_up;
+  p.rows = in.rows;
+  p.x_pitch = p.w_pitch = in.width;
+  p.h_pitch = padded(in, in.hidden);
+  p.width = p.width_ext = (int)in.width;
+  p.hidden = (int)in.hidden;
+  p.act = in.act;
+  return p;
+}
+
+int copy_rows(const GatedTable& t, GatedParams p, const void* from, void* to, int64_t rows, void* stream) {
+  p.from = from;
+  p.to = to;
+  p.copy_rows = rows;
+  p.copy_width = p.width;
+  p.copy_pitch = p.width_ext;
+  const int64_t blocks = ceil_div(rows * p.copy_pitch, 256 * 16);
+  return launch(t.copy, dim3((unsigned)(blocks < 1 ? 1 : blocks < 8 * kCUs ? blocks : 8 * kCUs)), 256, p, stream);
+}
+
+// x and the weights in rows that the tiled products can load, from `ws` on
+int make_copies(const ssim_gated_linear_inputs& in, const Copies& c, const GatedTable& t, GatedParams& p, char*& ws,
+                void* stream) {
+  if (!c.any) return SSIM_OK;
+  p.width_ext = (int)padded(in, in.width);
+  const void* from[] = {in.x, in.w_gate, in.w_up};
+  void* to[3];
+  for (int k = 0; k < 3; ++k) {
+    to[k] = ws;
+    ws += k ? c.w : c.x;
+    const int rc = copy_rows(t, p, from[k], to[k], k ? in.hidden : in.rows, stream);
+    if (rc != SSIM_OK) return rc;
+  }
+  p.x = to[0];
+  p.w[0] = to[1];
+  p.w[1] = to[2];
+  p.x_pitch = p.w_pitch = p.width_ext;
+  return SSIM_OK;
+}
+
+// Tiles of 256 x 256 (one workgroup to a CU) or 128 x 128 (two), whichever ends
+// earlier by the count of rounds; small tiles take a quarter more of the LDS's
+// time for the same work.
+int launch_product(const GatedTable& t, GatedParams& p, int product, int64_t m, int64_t n, int n_factor, void* stream) {
+  const int halved = product == kForward ? 2 : 1;  // a tile's rows are two weights'
+  const int64_t large = ceil_div(m, 256 / halved) * ceil_div(n, 256) * n_factor;
+  const int64_t small = ceil_div(m, 128 / halved) * ceil_div(n, 128) * n_factor;
+  const bool wide = 4.0 * ceil_div(large, kCUs) <= 1.25 * 2.0 * ceil_div(small, 2 * kCUs);
+  const int side = wide ? 256 : 128;
+  p.m_tiles = (int)ceil_div(m, side / halved);
+  p.n_tiles = (int)ceil_div(n, side) * n_factor;
+  const int64_t blocks = (int64_t)p.m_tiles * p.n_tiles;
+  if (blocks > 1 << 22) return SSIM_ERR_OVERFLOW;
+  return launch(t.product[product][wide], dim3((unsigned)blocks), wide ? 512 : 256, p, stream);
+}
+
+struct Slopes {
+  int column_blocks, row_blocks, rows_of_block;
+};
+Slopes slopes_of(const ssim_gated_linear_inputs& in) {
+  Slopes s;
+  s.column_blocks = (int)ceil_div(padded(in, in.hidden), (int64_t)kWave * per_chunk(in));
+  int64_t blocks = ceil_div(8 * kCUs, s.column_blocks);
+  const int64_t most = ceil_div(in.rows, 16);  // four rows to a wave at least
+  if (blocks > most) blocks = most;
+  s.rows_of_block = (int)ceil_div(in.rows, blocks < 1 ? 1 : blocks);
+  s.row_blocks = in.rows > 0 ? (int)ceil_div(in.rows, s.rows_of_block) : 0;
+  return s;
+}
+
+struct BackwardSpace {
+  Copies copies;
+  size_t d, part, total;
+};
+BackwardSpace space_of(const ssim_gated_linear_inputs& in) {
+  BackwardSpace s;
+  s.copies = copies_of(in);
+  s.d = (size_t)in.rows * padded(in, in.hidden) * elem_bytes(in.dtype);
+  s.part = to_16((size_t)slopes_of(in).row_blocks * 2 * in.hidden * 4);
+  s.total = s.copies.x + 2 * s.copies.w + 2 * s.d + s.part;
+  return s;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ssim_gated_linear_saved_elements(const ssim_gated_linear_inputs* in) {
+  if (check_inputs(in) != SSIM_OK) return 0;
+  return (size_t)in->rows * padded(*in, in->hidden);
+}
+
+size_t ssim_gated_linear_workspace_bytes(const ssim_gated_linear_inputs* in) {
+  if (check_inputs(in) != SSIM_OK || in->rows == 0 || takes_few(*in)) return 0;
+  const Copies c = copies_of(*in);
+  return c.x + 2 * c.w;
+}
+
+int ssim_gated_linear_forward(const ssim_gated_linear_inputs* in, void* out, void* g, void* u,
+                              void* workspace, void* stream) {
+  int rc = check_inputs(in);
+  if (rc != SSIM_OK) return rc;
+  if (in->rows == 0) return SSIM_OK;
+  const size_t ws = ssim_gated_linear_workspace_bytes(in);
+  if (!in->x || !in->w_gate || !in->w_up || !out || !g != !u || (ws > 0 && !workspace)) return SSIM_ERR_NULL;
+  const int bytes = elem_bytes(in->dtype);
+  const size_t weight = (size_t)in->hidden * in->width * bytes, saved = ssim_gated_linear_saved_elements(in) * bytes;
+  const Array ins[] = {{in->x, (size_t)in->rows * in->width * bytes, bytes},
+                       {in->w_gate, weight, bytes},
+                       {in->w_up, weight, bytes},
+                       {in->b_gate, (size_t)in->hidden * bytes, bytes},
+                       {in->b_up, (size_t)in->hidden * bytes, bytes}};
+  const Array outs[] = {{out, (size_t)in->rows * in->hidden * bytes, bytes},
+                        {g, saved, 16},
+                        {u, saved, 16},
+                        {workspace, ws, ws ? 16 : 1}};
+  rc = check_arrays(ins, 5, outs, 4);
+  if (rc != SSIM_OK) return rc;
+  rc = check_current_device();
+  if (rc != SSIM_OK) return rc;
+
+  const GatedTable& t = table_of(in->dtype);
+  GatedParams p = params_of(*in);
+  p.out = out;
+  p.saved[0] = g;
+  p.saved[1] = u;
+  if (takes_few(*in))
+    return launch(t.few[in->rows <= 16 ? 0 : in->rows <= 32 ? 1 : 2], dim3((unsigned)ceil_div(in->hidden, 16)), 256, p,
+                  stream);
+  char* at = static_cast<char*>(workspace);
+  rc = make_copies(*in, copies_of(*in), t, p, at, stream);
+  if (rc != SSIM_OK) return rc;
+  return launch_product(t, p, kForward, in->hidden, in->rows, 1, stream);
+}
+
+size_t ssim_gated_linear_backward_workspace_bytes(const ssim_gated_linear_inputs* in) {
+  if (check_inputs(in) != SSIM_OK) return 0;
+  return space_of(*in).total;
+}
+
+int ssim_gated_linear_backward(const ssim_gated_linear_inputs* in, const void* g, const void* u,
+                               const void* d_out, const ssim_gated_linear_grads* grads,
+                               void* workspace, void* stream) {
+  int rc = check_inputs(in);
+  if (rc != SSIM_OK) return rc;
+  if (!grads) return SSIM_ERR_NULL;
+  const bool weights = grads->w_gate || grads->w_up, biases = grads->b_gate || grads->b_up;
+  // a gradient of an input that is not there
+  if ((grads->b_gate && !in->b_gate) || (grads->b_up && !in->b_up)) return SSIM_ERR_NULL;
+  if (!weights && !biases && !(grads->x && in->rows > 0)) return SSIM_OK;
+  if (in->rows > 0 && (!in->x || !in->w_gate || !in->w_up || !g || !u || !d_out || !workspace)) return SSIM_ERR_NULL;
+  const int bytes = elem_bytes(in->dtype);
+  const size_t weight = (size_t)in->hidden * in->width * bytes, bias = (size_t)in->hidden * bytes;
+  const size_t saved = ssim_gated_linear_saved_elements(in) * bytes, xs = (size_t)in->rows * in->width * bytes;
+  const BackwardSpace space = space_of(*in);
+  const bool rows = in->rows > 0;
+  const Array ins[] = {{in->x, xs, bytes},
+                       {in->w_gate, weight, bytes},
+                       {in->w_up, weight, bytes},
+                       {g, saved, rows ? 16 : 1},
+                       {u, saved, rows ? 16 : 1},
+                       {d_out, (size_t)in->rows * in->hidden * bytes, bytes}};
+  const Array outs[] = {{grads->x, xs, bytes},          {grads->w_gate, weight, bytes},
+                        {grads->w_up, weight, bytes},   {grads->b_gate, bias, bytes},
+                        {grads->b_up, bias, bytes},     {workspace, rows ? space.total : 0, rows ? 16 : 1}};
+  rc = check_arrays(ins, 6, outs, 6);
+  if (rc != SSIM_OK) return rc;
+  rc = check_current_device();
+  if (rc != SSIM_OK) return rc;
+
+  const GatedTable& t = table_of(in->dtype);
+  GatedParams p = params_of(*in);
+  p.saved[0] = const_cast<void*>(g);
+  p.saved[1] = const_cast<void*>(u);
+  p.d_out = d_out;
+  p.dx = grads->x;
+  p.dw[0] = grads->w_gate;
+  p.dw[1] = grads->w_up;
+  p.db[0] = grads->b_gate;
+  p.db[1] = grads->b_up;
+  const Slopes s = slopes_of(*in);
+  p.row_blocks = s.row_blocks;
+  p.rows_of_block = s.rows_of_block;
+  char* at = static_cast<char*>(workspace);
+  if (rows) {
+    if (weights || grads->x) {
+      rc = make_copies(*in, space.copies, t, p, at, stream);
+      if (rc != SSIM_OK) return rc;
+    }
+    p.d[0] = at;
+    p.d[1] = at + space.d;
+    p.part_bias = biases ? reinterpret_cast<float*>(at + 2 * space.d) : nullptr;
+    rc = launch(t.slopes, dim3(s.column_blocks, s.row_blocks), 256, p, stream);
+    if (rc != SSIM_OK) return rc;
+  }
+  if (biases) {
+    rc = launch(t.bias_sums, dim3((unsigned)ceil_div(in->hidden, 64), 2), 64, p, stream);
+    if (rc != SSIM_OK) return rc;
+  }
+  if (grads->x && rows) {
+    rc = launch_product(t, p, kGradX, in->width, in->rows, 1, stream);
+    if (rc != SSIM_OK) return rc;
+  }
+  if (weights) return launch_product(t, p, kGradW, in->width, in->hidden, 2, stream);
+  return SSIM_OK;
+}
+
+}  // extern "C"

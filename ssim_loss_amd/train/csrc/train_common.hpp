@@ -135,4 +135,38 @@ inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
 // SSIM_OK if the current device is a gfx950
 int check_current_device();
 
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+constexpr int kCUs = 256;  // of an MI355X; workspaces' sizes must not need a device query
+
+struct Array {
+  const void* p;
+  size_t bytes;
+  int align;
+};
+// alignment of all, and no output over an input or another output
+inline int check_arrays(const Array* ins, int n_in, const Array* outs, int n_out) {
+  for (int k = 0; k < n_in; ++k)
+    if (misaligned(ins[k].p, ins[k].align)) return SSIM_ERR_SHAPE;
+  for (int k = 0; k < n_out; ++k) {
+    if (misaligned(outs[k].p, outs[k].align)) return SSIM_ERR_SHAPE;
+    for (int l = 0; l < n_in; ++l)
+      if (overlaps(outs[k].p, outs[k].bytes, ins[l].p, ins[l].bytes)) return SSIM_ERR_ALIAS;
+    for (int l = 0; l < k; ++l)
+      if (overlaps(outs[k].p, outs[k].bytes, outs[l].p, outs[l].bytes)) return SSIM_ERR_ALIAS;
+  }
+  return SSIM_OK;
+}
+
+template <class Params>
+int launch(const void* kernel, dim3 grid, int threads, Params& params, void* stream) {
+  void* args[] = {&params};
+  if (hipLaunchKernel(kernel, grid, dim3(threads), args, 0, static_cast<hipStream_t>(stream)) !=
+      hipSuccess) {
+    (void)hipGetLastError();
+    return SSIM_ERR_HIP;
+  }
+  return SSIM_OK;
+}
+
 }  // namespace ssim_train

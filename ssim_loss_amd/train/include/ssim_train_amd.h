@@ -1,9 +1,10 @@
 /*
  * ssim_train_amd.h -- C ABI of the training step's operators around the SSIM
  * loss, for AMD Instinct MI355X (gfx950): the global gradient norm and
- * clipping by it, AdamW, and the joint between two blocks of an image network
+ * clipping by it, AdamW, the joint between two blocks of an image network
  * (the norm after a block, its gate, the scaled residual sum and the norm
- * before the next block) with its gradient.
+ * before the next block), and what lies inside a block: rotary positions,
+ * attention and the gated layer; all with their gradients.
  *
  * Conventions, as in ssim_loss_amd.h:
  *   - Tensors are device pointers owned by the caller, contiguous, aligned to
@@ -34,10 +35,11 @@
 extern "C" {
 #endif
 
-#define SSIM_TRAIN_ABI_VERSION 1
+#define SSIM_TRAIN_ABI_VERSION 2
 
 /* a code beside SSIM_ERR_*: a hyperparameter (max_norm, lr, beta1, beta2, eps,
- * weight_decay, gate_act) is not a number or out of its range */
+ * weight_decay, gate_act, base, scale, act or another selector) is not a number
+ * or out of its range */
 enum { SSIM_ERR_VALUE = -10 };
 
 int ssim_train_abi_version(void);
@@ -179,6 +181,150 @@ typedef struct {
 int ssim_block_norm_backward(const ssim_block_norm_inputs* in, const float* stats,
                              const void* d_residual, const void* d_normed,
                              const ssim_block_norm_grads* grads, void* workspace, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions with several axes.  The first elements of each head are
+ * split into parts, one to an axis, of axis_size[a] elements (even); what is
+ * left behind them passes as it is.  Pair i of axis a turns by the angle
+ * positions[.., a] base^(-2 i / axis_size[a]):
+ *   y0 = x0 cos - x1 sin,  y1 = x1 cos + x0 sin
+ * The angle is reduced in fp64, so positions may lie far out and between whole
+ * numbers.
+ */
+enum {
+  SSIM_PAIRS_ADJACENT = 0, /* elements 2 i and 2 i + 1 of the part */
+  SSIM_PAIRS_HALVES = 1    /* elements i and i + axis_size / 2 */
+};
+enum { SSIM_POSITION_F32 = 0, SSIM_POSITION_I32 = 1, SSIM_POSITION_I64 = 2 };
+
+#define SSIM_ROTARY_MAX_AXES 4
+#define SSIM_ROTARY_MAX_DIM 512
+
+typedef struct {
+  const void* q;         /* [batch, tokens, q_heads, dim] of dtype */
+  const void* k;         /* [batch, tokens, k_heads, dim], or NULL: queries alone */
+  const void* positions; /* [batch, tokens, axes] of position_type, the axes beside each other */
+  int64_t q_stride[3];   /* elements from one batch entry, token, head to the next, >= 0 */
+  int64_t k_stride[3];
+  int64_t position_stride[2]; /* ... of batch entries and tokens */
+  int64_t batch, tokens; /* >= 0 */
+  int32_t q_heads, k_heads, dim; /* 1 .. 65536, 1 .. 65536, 1 .. SSIM_ROTARY_MAX_DIM */
+  int32_t axes;          /* 1 .. SSIM_ROTARY_MAX_AXES */
+  int32_t axis_size[SSIM_ROTARY_MAX_AXES];
+  int32_t pairs;         /* SSIM_PAIRS_* */
+  int32_t position_type; /* SSIM_POSITION_* */
+  int32_t dtype;
+  int32_t inverse;       /* 1: by the opposite angle, which is the gradient's way */
+  double base;           /* > 0 */
+} ssim_rotary_inputs;
+
+/* q_out: [batch, tokens, q_heads, dim], contiguous; k_out likewise, or NULL
+ * with k.  They overlap neither the inputs nor each other. */
+int ssim_rotary(const ssim_rotary_inputs* in, void* q_out, void* k_out, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Softmax attention.  Query head h uses key head h / (heads / kv_heads).
+ *   s_ij = scale q_i . k_j,  p_ij = exp(s_ij) / sum_j exp(s_ij),  out_i = sum_j p_ij v_j
+ * over the keys that query i of sequence b sees: with ql = q_lengths[b] and
+ * kl = k_lengths[b] (q_tokens and k_tokens without them; clamped to 0 .. tokens),
+ * none if i >= ql, else j < kl and, with causal order, j <= i + kl - ql.  A query
+ * that sees no key, or whose scores are all minus infinity, gives zeros, and a
+ * query or key that takes no part has a gradient of zeros.  Queries past ql and
+ * keys and values past kl are not read; the other keys and values of a sequence
+ * must be finite also where some queries do not see them.
+ * Scores, sums and statistics are fp32; for half types the probabilities and, in
+ * the gradients, their derivatives are rounded to the type before the products.
+ */
+#define SSIM_ATTENTION_MAX_DIM 128
+
+typedef struct {
+  const void* q;       /* [batch, q_tokens, heads, dim] of dtype */
+  const void* k;       /* [batch, k_tokens, kv_heads, dim] */
+  const void* v;       /* [batch, k_tokens, kv_heads, dim] */
+  const int32_t* q_lengths; /* [batch] on the device, or NULL */
+  const int32_t* k_lengths;
+  int64_t q_stride[3]; /* elements from one batch entry, token, head to the next; */
+  int64_t k_stride[3]; /* each a multiple of 16 bytes, a token's at least dim and less */
+  int64_t v_stride[3]; /* than 2^24 bytes, and q, k, v aligned to 16 bytes */
+  int64_t batch, q_tokens, k_tokens; /* >= 0, tokens < 2^24 */
+  int32_t heads, kv_heads; /* kv_heads divides heads */
+  int32_t dim;         /* a multiple of 8, to SSIM_ATTENTION_MAX_DIM */
+  int32_t causal;
+  int32_t dtype;
+  int32_t reserved;    /* 0 */
+  double scale;        /* > 0 */
+} ssim_attention_inputs;
+
+/* Bytes of the workspace (16-byte aligned) of the forward; 0 also where it needs
+ * none.  Host-only. */
+size_t ssim_attention_workspace_bytes(const ssim_attention_inputs* in);
+
+/* out: [batch, q_tokens, heads, dim], contiguous; lse: NULL, or fp32
+ * [batch, heads, q_tokens] for the backward (log2 of the sum of exp(s_ij), plus
+ * infinity for a query without keys).  workspace may be NULL where it needs none. */
+int ssim_attention_forward(const ssim_attention_inputs* in, void* out, float* lse, void* workspace,
+                           void* stream);
+
+/* Bytes of the backward's workspace (16-byte aligned).  Host-only. */
+size_t ssim_attention_backward_workspace_bytes(const ssim_attention_inputs* in);
+
+/* The gradients for d_out, laid out as out; out and lse are the forward's for the
+ * same inputs.  dq, dk, dv: contiguous, of q's, k's and v's shapes; each may be
+ * NULL: not wanted.  No atomics: the same bits every time. */
+int ssim_attention_backward(const ssim_attention_inputs* in, const void* out, const float* lse,
+                            const void* d_out, void* dq, void* dk, void* dv, void* workspace,
+                            void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The gated layer of a feed-forward block:
+ *   g = x w_gate^T + b_gate,  u = x w_up^T + b_up,  out = act(g) u
+ */
+enum {
+  SSIM_ACT_SILU = 0,    /* g / (1 + exp(-g)) */
+  SSIM_ACT_GELU = 1,    /* g (1 + erf(g / sqrt 2)) / 2 */
+  SSIM_ACT_SIGMOID = 2  /* 1 / (1 + exp(-g)) */
+};
+
+typedef struct {
+  const void* x;      /* [rows, width] */
+  const void* w_gate; /* [hidden, width] */
+  const void* w_up;   /* [hidden, width] */
+  const void* b_gate; /* [hidden], or NULL: 0 */
+  const void* b_up;
+  int64_t rows;       /* >= 0 */
+  int64_t width;      /* 1 .. 2^20 */
+  int64_t hidden;     /* 1 .. 2^20 */
+  int32_t act;        /* SSIM_ACT_* */
+  int32_t dtype;      /* of all tensors */
+} ssim_gated_linear_inputs;
+
+/* Elements of each of the two arrays that the forward keeps for the backward. */
+size_t ssim_gated_linear_saved_elements(const ssim_gated_linear_inputs* in);
+
+/* Bytes of the workspace (16-byte aligned) of the forward, 0 also where it needs
+ * none, and of the backward.  Host-only. */
+size_t ssim_gated_linear_workspace_bytes(const ssim_gated_linear_inputs* in);
+size_t ssim_gated_linear_backward_workspace_bytes(const ssim_gated_linear_inputs* in);
+
+/* out: [rows, hidden].  g, u: NULL, or 16-byte aligned arrays of
+ * ssim_gated_linear_saved_elements elements that receive g and u, rounded to dtype,
+ * for the backward. */
+int ssim_gated_linear_forward(const ssim_gated_linear_inputs* in, void* out, void* g, void* u,
+                              void* workspace, void* stream);
+
+/* The gradients for d_out ([rows, hidden]), each of its input's shape; NULL: not
+ * wanted.  Those of g and u are rounded to dtype before the products. */
+typedef struct {
+  void* x;
+  void* w_gate;
+  void* w_up;
+  void* b_gate;
+  void* b_up;
+} ssim_gated_linear_grads;
+
+int ssim_gated_linear_backward(const ssim_gated_linear_inputs* in, const void* g, const void* u,
+                               const void* d_out, const ssim_gated_linear_grads* grads,
+                               void* workspace, void* stream);
 
 #ifdef __cplusplus
 }
