@@ -341,9 +341,10 @@ def gated_linear(x, w_gate, w_up, b_gate=None, b_up=None, act="silu"):
     contiguous, of one type, float32, float16 or bfloat16.
     act: "silu", "gelu" (with the error function) or "sigmoid".
 
-    Returns [..., hidden].  Sums are float32.  Where gradients are wanted the two
-    projections are kept, rounded to the type, for the backward.  Gradients of all
-    inputs are available, gradients of gradients are not."""
+    Returns [..., hidden].  Sums are float32, and where gradients are wanted the two
+    projections are kept in float32 for the backward, whose gradients of them are
+    rounded to the type before the products.  Gradients of all inputs are
+    available, gradients of gradients are not."""
     kind = GATED_ACT.get(act)
     if kind is None:
         raise ValueError(f"act must be 'silu', 'gelu' or 'sigmoid', got {act!r}")

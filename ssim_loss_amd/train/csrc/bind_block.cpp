@@ -384,8 +384,8 @@ struct GatedLinearBackward : torch::autograd::Node {
     grads.b_up = wanted(4);
     const Tensor d_out = upstream[0].contiguous();
     const c10::DataPtr ws = scratch(ssim_gated_linear_backward_workspace_bytes(&in));
-    const int rc = ssim_gated_linear_backward(&in, t[5].const_data_ptr(), t[6].const_data_ptr(), d_out.const_data_ptr(),
-                                              &grads, ws.get(), stream_of(dev));
+    const int rc = ssim_gated_linear_backward(&in, t[5].const_data_ptr<float>(), t[6].const_data_ptr<float>(),
+                                              d_out.const_data_ptr(), &grads, ws.get(), stream_of(dev));
     TORCH_CHECK(rc == SSIM_OK, "ssim_gated_linear_backward: ", text(rc));
     return out;
   }
@@ -429,13 +429,13 @@ Tensor gated_linear(const py::object& x_, const py::object& w_gate_, const py::o
   Tensor out = fresh(sizes, x.scalar_type(), dev), g, u;
   if (wants) {
     const int64_t n = (int64_t)ssim_gated_linear_saved_elements(&in);
-    g = fresh({n}, x.scalar_type(), dev);
-    u = fresh({n}, x.scalar_type(), dev);
+    g = fresh({n}, at::kFloat, dev);
+    u = fresh({n}, at::kFloat, dev);
   }
   const size_t bytes = ssim_gated_linear_workspace_bytes(&in);
   const c10::DataPtr ws = bytes ? scratch(bytes) : c10::DataPtr();
-  const int rc = ssim_gated_linear_forward(&in, out.data_ptr(), wants ? g.data_ptr() : nullptr,
-                                           wants ? u.data_ptr() : nullptr, ws.get(), stream_of(dev));
+  const int rc = ssim_gated_linear_forward(&in, out.data_ptr(), wants ? g.data_ptr<float>() : nullptr,
+                                           wants ? u.data_ptr<float>() : nullptr, ws.get(), stream_of(dev));
   if (rc != SSIM_OK) raise(rc, "ssim_gated_linear_forward");
   if (wants) {
     std::shared_ptr<GatedLinearBackward> node(new GatedLinearBackward(), torch::autograd::deleteNode);

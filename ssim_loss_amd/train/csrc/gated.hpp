@@ -21,11 +21,11 @@ struct GatedParams {
   const void* w[2];     // gate, up: [hidden][w_pitch]
   const void* bias[2];  // [hidden] or NULL
   int64_t rows;
-  int64_t x_pitch, w_pitch, h_pitch;  // elements; of the arrays of g, u, dg, du: h_pitch
+  int64_t x_pitch, w_pitch, h_pitch;  // elements; of g, u, dg and du: h_pitch
   int width, hidden, act;
   int width_ext;        // width, or x_pitch where x and w are copies padded with zeros
   void* out;            // [rows][hidden]
-  void* saved[2];       // g, u: [rows][h_pitch], or NULL
+  float* saved[2];      // g, u: [rows][h_pitch], or NULL
   // backward
   const void* d_out;    // [rows][hidden]
   void* d[2];           // dg, du: [rows][h_pitch], zeros behind hidden
@@ -35,12 +35,12 @@ struct GatedParams {
   void* dx;             // [rows][width]
   void* dw[2];          // [hidden][width]
   void* db[2];
-  // tiles of the product
-  int m_tiles, n_tiles;
-  // copies
-  const void* from;
-  void* to;
-  int64_t copy_rows, copy_width, copy_pitch;
+  // tiles of the product; parts of its summed axis, each with a sum of its own
+  int m_tiles, n_tiles, splits;
+  float* part;          // [splits][rows of the result][width]
+  // copies of x and the weights
+  const void* from[3];
+  void* to[3];
 };
 
 // act(g), and act'(g)
@@ -137,10 +137,10 @@ __device__ __forceinline__ void fetch_across(const char* from, int64_t pitch, in
 struct TileAt {
   int m, n;
 };
-__device__ __forceinline__ TileAt tile_at(int m_tiles, int n_tiles) {
+__device__ __forceinline__ TileAt tile_at(unsigned block, int m_tiles, int n_tiles) {
   constexpr unsigned kGroup = 8;
   const unsigned total = (unsigned)m_tiles * n_tiles, per = (total + 7) / 8, rest = total - (per - 1) * 8;
-  const unsigned xcd = blockIdx.x & 7, j = blockIdx.x >> 3;
+  const unsigned xcd = block & 7, j = block >> 3;
   // (the first `rest` XCDs have a tile more where 8 does not divide the tiles)
   const unsigned id = xcd < rest ? xcd * per + j : rest * per + (xcd - rest) * (per - 1) + j;
   const unsigned of_group = kGroup * m_tiles, group = id / of_group, in = id - group * of_group;
@@ -148,6 +148,52 @@ __device__ __forceinline__ TileAt tile_at(int m_tiles, int n_tiles) {
   return {(int)(in / rows), (int)(group * kGroup + in % rows)};
 }
 
+// A wave's block of a result, kRows x kColumns, to memory: through its own part of
+// the LDS, so that neighbouring lanes have a row's neighbouring chunks.  Straight
+// from the registers each store would touch 32 rows with 16 bytes of each
+// (16384 x 4096 x 10944 bf16, with g and u: 3419 us, so 2680).
+// In: value(i, j, k), the four columns 32 i + 8 k + 4 h of row 32 j + lane % 32.
+template <class T, int MB, int NB, class Value>
+__device__ __forceinline__ void store_block(Lds* region, T* out, int64_t pitch, int64_t row0, int64_t column0,
+                                            int64_t rows, int64_t columns, Value value) {
+  constexpr int kRow = MB * 32 * 4 < 128 ? 128 : MB * 32 * 4;  // bytes, of fp32
+  static_assert(MB == 1 || MB == 2, "a power of two");
+  const int lane = threadIdx.x & (kWave - 1), h = lane >> 5;
+  typedef __attribute__((address_space(3))) Wide<4>* At;
+#pragma unroll
+  for (int j = 0; j < NB; ++j)
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *(At)(region + place<kRow>(32 * j + (lane & 31), 8 * i + 2 * k + h)) = value(i, j, k);
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // (a wave's own)
+  constexpr int V = kPerChunk<T>;
+  constexpr int kLanes = MB * 32 / V;  // to a row
+  constexpr int kAtOnce = kWave / kLanes;
+#pragma unroll
+  for (int r = 0; r < NB * 32; r += kAtOnce) {
+    const int row = r + lane / kLanes, column = lane % kLanes * V;
+    Wide<V> v;
+#pragma unroll
+    for (int q = 0; q < V / 4; ++q) {
+      const Wide<4> w = *(At)(region + place<kRow>(row, column / 4 + q));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[4 * q + e] = w[e];
+    }
+    if (row0 + row >= rows) continue;
+    T* to = out + (row0 + row) * pitch + column0 + column;
+    const Vec<T, V> n = narrow<T, V>(v);
+    if (column0 + column + V <= columns) {
+      store<T, V>(to, n);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (column0 + column + e < columns) to[e] = n[e];
+    }
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+}
 // Four neighbouring elements of a row, those of them that it has.
 template <class T>
 __device__ __forceinline__ void store_four(T* row, int64_t column, int64_t width, Wide<4> v) {
@@ -163,11 +209,13 @@ __device__ __forceinline__ void store_four(T* row, int64_t column, int64_t width
 
 template <class T, int kProduct, int BM, int BN, int WM, int WN>
 __global__ void __launch_bounds__(WM* WN* kWave, WM* WN == 4 ? 2 : 1) gated_product(const GatedParams p) {
+  // (the smallest tiles leave room for more workgroups than bounds ask for)
   using Shape = ProductShape<T, BM, BN, WM, WN>;
   __shared__ __attribute__((aligned(1024))) char lds_[2 * (Shape::kABytes + Shape::kBBytes)];
   Lds* lds = (Lds*)lds_;
   const uint32_t lds_at = lds_address(lds);
-  const TileAt at = tile_at(p.m_tiles, p.n_tiles);
+  const int split = kProduct == kForward ? 0 : blockIdx.x % p.splits;
+  const TileAt at = tile_at(kProduct == kForward ? blockIdx.x : blockIdx.x / p.splits, p.m_tiles, p.n_tiles);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
   const int wm = wave % WM, wn = wave / WM, h = lane >> 5;
   constexpr int kBytes = (int)sizeof(T);
@@ -176,7 +224,9 @@ __global__ void __launch_bounds__(WM* WN* kWave, WM* WN == 4 ? 2 : 1) gated_prod
   // how many tiles of the summed axis there are
   const int64_t depth = kProduct == kForward ? p.width_ext : kProduct == kGradX ? p.h_pitch : p.rows;
   const int once = (int)((depth + Shape::kDepth - 1) / Shape::kDepth);
-  const int count = kProduct == kGradX ? 2 * once : once;
+  const int whole = kProduct == kGradX ? 2 * once : once, each = (whole + p.splits - 1) / p.splits;
+  const int begin = kProduct == kForward ? 0 : min(split * each, whole);
+  const int end = kProduct == kForward ? whole : min(begin + each, whole);
   const int n_half = p.n_tiles / 2;  // gradients of weights: gate's tiles, then up's
   const int which = kProduct == kGradW ? (at.n >= n_half) : 0;
   if (kProduct == kGradW && !p.dw[which]) return;
@@ -216,10 +266,10 @@ __global__ void __launch_bounds__(WM* WN* kWave, WM* WN == 4 ? 2 : 1) gated_prod
     if constexpr (kProduct == kForward) return i < BM / 2 ? wm * (BM / 2) + i : kHalfM / 32 + wm * (BM / 2) + i - BM / 2;
     else return wm * BM + i;
   };
-  if (count > 0) fetch(0);
-  for (int t = 0; t < count; ++t) {
+  if (begin < end) fetch(begin);
+  for (int t = begin; t < end; ++t) {
     landed_for_all();
-    if (t + 1 < count) fetch(t + 1);
+    if (t + 1 < end) fetch(t + 1);
     const Lds* a_tile = lds + (t & 1) * (Shape::kABytes + Shape::kBBytes);
     const Lds* b_tile = a_tile + Shape::kABytes;
 #pragma unroll
@@ -246,49 +296,83 @@ __global__ void __launch_bounds__(WM* WN* kWave, WM* WN == 4 ? 2 : 1) gated_prod
     }
   }
 
+  landed_for_all();  // the tiles' place is the waves' own now
+  Lds* region = lds + wave * (int)(sizeof(lds_) / (WM * WN));
+  const int64_t row0 = n0 + 32 * wn * BN;
   if constexpr (kProduct == kForward) {
+    constexpr int MB = BM / 2;
+    const int64_t column0 = m0 + 32 * wm * MB;
 #pragma unroll
-    for (int i = 0; i < BM / 2; ++i)
+    for (int i = 0; i < MB; ++i)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int64_t column = m0 + 32 * (wm * (BM / 2) + i) + 8 * k + 4 * h;
-        Wide<4> bias[2] = {};
+      for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int w = 0; w < 2; ++w)
+        for (int e = 0; e < 4; ++e) {
+          const int64_t column = column0 + 32 * i + 8 * k + 4 * h + e;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (p.bias[w] && column + e < p.hidden) bias[w][e] = (float)static_cast<const T*>(p.bias[w])[column + e];
+          for (int w = 0; w < 2; ++w) {
+            const float bias = p.bias[w] && column < p.hidden ? (float)static_cast<const T*>(p.bias[w])[column] : 0.0f;
 #pragma unroll
-        for (int j = 0; j < BN; ++j) {
-          const int64_t row = n0 + 32 * (wn * BN + j) + (lane & 31);
-          if (row >= p.rows) continue;
-          Wide<4> g, u, v;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            g[e] = c[i][j][4 * k + e] + bias[0][e];
-            u[e] = c[i + BM / 2][j][4 * k + e] + bias[1][e];
-            v[e] = act_of<T>(g[e], p.act) * u[e];
-          }
-          store_four<T>(static_cast<T*>(p.out) + row * p.hidden, column, p.hidden, v);
-          if (p.saved[0] && column < p.h_pitch) {
-            store<T, 4>(static_cast<T*>(p.saved[0]) + row * p.h_pitch + column, narrow<T, 4>(g));
-            store<T, 4>(static_cast<T*>(p.saved[1]) + row * p.h_pitch + column, narrow<T, 4>(u));
+            for (int j = 0; j < BN; ++j) c[i + w * MB][j][4 * k + e] += bias;
           }
         }
-      }
+    if (p.saved[0]) {
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+        store_block<float, MB, BN>(region, p.saved[w], p.h_pitch, row0, column0, p.rows, p.h_pitch, [&](int i, int j, int k) {
+          const Sums& s = c[i + w * MB][j];
+          return Wide<4>{s[4 * k], s[4 * k + 1], s[4 * k + 2], s[4 * k + 3]};
+        });
+    }
+    store_block<T, MB, BN>(region, static_cast<T*>(p.out), p.hidden, row0, column0, p.rows, p.hidden, [&](int i, int j, int k) {
+      Wide<4> v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = act_of<T>(c[i][j][4 * k + e], p.act) * c[i + MB][j][4 * k + e];
+      return v;
+    });
   } else {
-    T* out = static_cast<T*>(kProduct == kGradX ? p.dx : p.dw[which]);
     const int64_t rows = kProduct == kGradX ? p.rows : p.hidden;
+    constexpr int MB = BM < 2 ? 1 : 2;  // at once
 #pragma unroll
-    for (int j = 0; j < BN; ++j) {
-      const int64_t row = n0 + 32 * (wn * BN + j) + (lane & 31);
-      if (row >= rows) continue;
-#pragma unroll
-      for (int i = 0; i < BM; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          store_four<T>(out + row * p.width, m0 + 32 * (wm * BM + i) + 8 * k + 4 * h, p.width,
-                        Wide<4>{c[i][j][4 * k], c[i][j][4 * k + 1], c[i][j][4 * k + 2], c[i][j][4 * k + 3]});
+    for (int i0 = 0; i0 < BM; i0 += MB) {
+      const int64_t column0 = m0 + 32 * (wm * BM + i0);
+      auto value = [&](int i, int j, int k) {
+        const Sums& s = c[i0 + i][j];
+        return Wide<4>{s[4 * k], s[4 * k + 1], s[4 * k + 2], s[4 * k + 3]};
+      };
+      if (p.splits > 1) {
+        float* to = p.part + ((int64_t)split * (kProduct == kGradW ? 2 : 1) + which) * rows * p.width;
+        store_block<float, MB, BN>(region, to, p.width, row0, column0, rows, p.width, value);
+      } else {
+        T* to = static_cast<T*>(kProduct == kGradX ? p.dx : p.dw[which]);
+        store_block<T, MB, BN>(region, to, p.width, row0, column0, rows, p.width, value);
+      }
+    }
+  }
+}
+
+// The parts of a product together: `arrays` results beside each other in each part.
+template <class T>
+__global__ void __launch_bounds__(256) gated_join(const GatedParams p) {
+  // dx, or dWg and dWu
+  const bool weights = p.dw[0] || p.dw[1];
+  const int64_t n = (weights ? (int64_t)p.hidden : p.rows) * p.width, arrays = weights ? 2 : 1;
+  const int which = blockIdx.y;
+  T* to = static_cast<T*>(weights ? p.dw[which] : p.dx);
+  if (!to) return;
+  for (int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; at < n; at += (int64_t)gridDim.x * 256 * 4) {
+    const float* from = p.part + which * n + at;
+    if (at + 4 <= n) {
+      Wide<4> sum = load<float, 4>(from);
+#pragma unroll 4
+      for (int s = 1; s < p.splits; ++s) sum += load<float, 4>(from + s * arrays * n);
+      store<T, 4>(to + at, narrow<T, 4>(sum));
+    } else {
+      for (int k = 0; at + k < n; ++k) {
+        float sum = from[k];
+        for (int s = 1; s < p.splits; ++s) sum += from[s * arrays * n + k];
+        to[at + k] = (T)sum;
+      }
     }
   }
 }
@@ -307,8 +391,7 @@ __global__ void __launch_bounds__(256) gated_slopes(const GatedParams p) {
   if (column < p.h_pitch) {
     for (int64_t row = first + wave; row < end; row += 4) {
       const int64_t at = row * p.h_pitch + column;
-      const Wide<V> g = widen<T, V>(load<T, V>(static_cast<const T*>(p.saved[0]) + at));
-      const Wide<V> u = widen<T, V>(load<T, V>(static_cast<const T*>(p.saved[1]) + at));
+      const Wide<V> g = load_once<float, V>(p.saved[0] + at), u = load_once<float, V>(p.saved[1] + at);
       const T* d_row = static_cast<const T*>(p.d_out) + row * p.hidden;
       Wide<V> d = {};
       if (column + V <= p.hidden) d = widen<T, V>(load<T, V>(d_row + column));
@@ -348,30 +431,39 @@ __global__ void __launch_bounds__(256) gated_slopes(const GatedParams p) {
     }
 }
 
+// 64 columns to a workgroup, a quarter of the blocks to each wave.
 template <class T>
-__global__ void __launch_bounds__(64) gated_bias_sums(const GatedParams p) {
-  const int column = blockIdx.x * 64 + threadIdx.x, i = blockIdx.y;
-  if (column >= p.hidden || !p.db[i]) return;
+__global__ void __launch_bounds__(256) gated_bias_sums(const GatedParams p) {
+  __shared__ double sums[4][kWave];
+  const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1), i = blockIdx.y;
+  const int64_t column = (int64_t)blockIdx.x * kWave + lane;
   double sum = 0.0;
-  for (int b = 0; b < p.row_blocks; ++b) sum += p.part_bias[((int64_t)b * 2 + i) * p.hidden + column];
+  if (column < p.hidden) {
+#pragma unroll 8
+    for (int b = wave; b < p.row_blocks; b += 4) sum += p.part_bias[((int64_t)b * 2 + i) * p.hidden + column];
+  }
+  sums[wave][lane] = sum;
+  __syncthreads();
+  if (wave > 0 || column >= p.hidden || !p.db[i]) return;
+  sum = ((sums[0][lane] + sums[1][lane]) + sums[2][lane]) + sums[3][lane];
   static_cast<T*>(p.db[i])[column] = (T)(float)sum;
 }
 
-// Rows of copy_width elements to rows of copy_pitch, zeros behind them.
+// Rows of `width` elements to rows of width_ext, zeros behind them.
 template <class T>
 __global__ void __launch_bounds__(256) gated_copy(const GatedParams p) {
   constexpr int V = kPerChunk<T>;
-  const int64_t chunks = p.copy_pitch / V;
-  for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < p.copy_rows * chunks; id += (int64_t)gridDim.x * 256) {
+  const int64_t chunks = p.width_ext / V, rows = blockIdx.y ? p.hidden : p.rows;
+  for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < rows * chunks; id += (int64_t)gridDim.x * 256) {
     const int64_t row = id / chunks, column = (id - row * chunks) * V;
-    const T* from = static_cast<const T*>(p.from) + row * p.copy_width;
+    const T* from = static_cast<const T*>(p.from[blockIdx.y]) + row * p.width;
     Vec<T, V> v = {};
-    if (column + V <= p.copy_width) v = load<T, V>(from + column);
+    if (column + V <= p.width) v = load<T, V>(from + column);
     else
 #pragma unroll
       for (int k = 0; k < V; ++k)
-        if (column + k < p.copy_width) v[k] = from[column + k];
-    store<T, V>(static_cast<T*>(p.to) + row * p.copy_pitch + column, v);
+        if (column + k < p.width) v[k] = from[column + k];
+    store<T, V>(static_cast<T*>(p.to[blockIdx.y]) + row * p.width_ext + column, v);
   }
 }
 
@@ -469,34 +561,39 @@ __global__ void __launch_bounds__(256) gated_few_rows(const GatedParams p) {
     }
     store_four<T>(static_cast<T*>(p.out) + row * p.hidden, column, p.hidden, v);
     if (p.saved[0]) {
-      store<T, 4>(static_cast<T*>(p.saved[0]) + row * p.h_pitch + column, narrow<T, 4>(g));
-      store<T, 4>(static_cast<T*>(p.saved[1]) + row * p.h_pitch + column, narrow<T, 4>(u));
+      store<float, 4>(p.saved[0] + row * p.h_pitch + column, g);
+      store<float, 4>(p.saved[1] + row * p.h_pitch + column, u);
     }
   }
 }
 
 // ---- kernels of a type
 struct GatedTable {
-  const void* product[3][2];  // [Product][large tiles]
+  const void* product[3][3];  // [Product][tiles of 64, 128, 256 rows]
   const void* few[3];         // 16, 32, 64 rows
   const void* slopes;
   const void* bias_sums;
+  const void* join;
   const void* copy;
 };
 template <class T>
 GatedTable make_gated_table() {
   GatedTable t;
-  t.product[kForward][0] = (const void*)gated_product<T, kForward, 2, 2, 2, 2>;
-  t.product[kForward][1] = (const void*)gated_product<T, kForward, 4, 2, 2, 4>;
-  t.product[kGradX][0] = (const void*)gated_product<T, kGradX, 2, 2, 2, 2>;
-  t.product[kGradX][1] = (const void*)gated_product<T, kGradX, 4, 2, 2, 4>;
-  t.product[kGradW][0] = (const void*)gated_product<T, kGradW, 2, 2, 2, 2>;
-  t.product[kGradW][1] = (const void*)gated_product<T, kGradW, 4, 2, 2, 4>;
+  t.product[kForward][0] = (const void*)gated_product<T, kForward, 2, 1, 2, 2>;
+  t.product[kForward][1] = (const void*)gated_product<T, kForward, 2, 2, 2, 2>;
+  t.product[kForward][2] = (const void*)gated_product<T, kForward, 4, 2, 2, 4>;
+  t.product[kGradX][0] = (const void*)gated_product<T, kGradX, 1, 1, 2, 2>;
+  t.product[kGradX][1] = (const void*)gated_product<T, kGradX, 2, 2, 2, 2>;
+  t.product[kGradX][2] = (const void*)gated_product<T, kGradX, 4, 2, 2, 4>;
+  t.product[kGradW][0] = (const void*)gated_product<T, kGradW, 1, 1, 2, 2>;
+  t.product[kGradW][1] = (const void*)gated_product<T, kGradW, 2, 2, 2, 2>;
+  t.product[kGradW][2] = (const void*)gated_product<T, kGradW, 4, 2, 2, 4>;
   t.few[0] = (const void*)gated_few_rows<T, 1>;
   t.few[1] = (const void*)gated_few_rows<T, 2>;
   t.few[2] = (const void*)gated_few_rows<T, 4>;
   t.slopes = (const void*)gated_slopes<T>;
   t.bias_sums = (const void*)gated_bias_sums<T>;
+  t.join = (const void*)gated_join<T>;
   t.copy = (const void*)gated_copy<T>;
   return t;
 }

@@ -50,7 +50,7 @@ int check_inputs(const ssim_gated_linear_inputs* in) {
   if (in->act < SSIM_ACT_SILU || in->act > SSIM_ACT_SIGMOID) return SSIM_ERR_VALUE;
   if (in->rows < 0 || in->width < 1 || in->width > kMaxWidth || in->hidden < 1 || in->hidden > kMaxWidth)
     return SSIM_ERR_SHAPE;
-  if (in->rows > (int64_t)1 << 30) return SSIM_ERR_OVERFLOW;
+  if (in->rows > (int64_t)1 << 28) return SSIM_ERR_OVERFLOW;
   return SSIM_OK;
 }
 
@@ -71,50 +71,98 @@ GatedParams params_of(const ssim_gated_linear_inputs& in) {
   return p;
 }
 
-int copy_rows(const GatedTable& t, GatedParams p, const void* from, void* to, int64_t rows, void* stream) {
-  p.from = from;
-  p.to = to;
-  p.copy_rows = rows;
-  p.copy_width = p.width;
-  p.copy_pitch = p.width_ext;
-  const int64_t blocks = ceil_div(rows * p.copy_pitch, 256 * 16);
-  return launch(t.copy, dim3((unsigned)(blocks < 1 ? 1 : blocks < 8 * kCUs ? blocks : 8 * kCUs)), 256, p, stream);
-}
-
 // x and the weights in rows that the tiled products can load, from `ws` on
 int make_copies(const ssim_gated_linear_inputs& in, const Copies& c, const GatedTable& t, GatedParams& p, char*& ws,
                 void* stream) {
   if (!c.any) return SSIM_OK;
   p.width_ext = (int)padded(in, in.width);
-  const void* from[] = {in.x, in.w_gate, in.w_up};
-  void* to[3];
+  p.from[0] = in.x;
+  p.from[1] = in.w_gate;
+  p.from[2] = in.w_up;
   for (int k = 0; k < 3; ++k) {
-    to[k] = ws;
+    p.to[k] = ws;
     ws += k ? c.w : c.x;
-    const int rc = copy_rows(t, p, from[k], to[k], k ? in.hidden : in.rows, stream);
-    if (rc != SSIM_OK) return rc;
   }
-  p.x = to[0];
-  p.w[0] = to[1];
-  p.w[1] = to[2];
+  p.x = p.to[0];
+  p.w[0] = p.to[1];
+  p.w[1] = p.to[2];
+  const int64_t most = in.rows > in.hidden ? in.rows : in.hidden;
+  const int64_t blocks = ceil_div(most * p.width_ext, 256 * 2 * per_chunk(in));
+  const int rc = launch(t.copy, dim3((unsigned)(blocks < 8 * kCUs ? blocks : 8 * kCUs), 3), 256, p, stream);
+  if (rc != SSIM_OK) return rc;
   p.x_pitch = p.w_pitch = p.width_ext;
   return SSIM_OK;
 }
 
-// Tiles of 256 x 256 (one workgroup to a CU) or 128 x 128 (two), whichever ends
-// earlier by the count of rounds; small tiles take a quarter more of the LDS's
-// time for the same work.
-int launch_product(const GatedTable& t, GatedParams& p, int product, int64_t m, int64_t n, int n_factor, void* stream) {
-  const int halved = product == kForward ? 2 : 1;  // a tile's rows are two weights'
-  const int64_t large = ceil_div(m, 256 / halved) * ceil_div(n, 256) * n_factor;
-  const int64_t small = ceil_div(m, 128 / halved) * ceil_div(n, 128) * n_factor;
-  const bool wide = 4.0 * ceil_div(large, kCUs) <= 1.25 * 2.0 * ceil_div(small, 2 * kCUs);
-  const int side = wide ? 256 : 128;
-  p.m_tiles = (int)ceil_div(m, side / halved);
-  p.n_tiles = (int)ceil_div(n, side) * n_factor;
-  const int64_t blocks = (int64_t)p.m_tiles * p.n_tiles;
+// Which tiles a product takes, and into how many parts its summed axis is cut.  The
+// time of a choice is taken as its rounds (workgroups that fit on the GPU at once)
+// times a workgroup's share: its tile's elements by the depth, over what the
+// matrix instructions reach with it, and its beginning and end, which are those of
+// kEnds of the depth.  A cut costs the sums' way through memory.
+struct Choice {
+  int tiles;  // 0: 64, 1: 128, 2: 256
+  int splits;
+  int64_t m_tiles, n_tiles;
+};
+constexpr int kMaxSplits = 16;
+
+Choice choose(const ssim_gated_linear_inputs& in, int product) {
+  const int64_t m = product == kForward ? in.hidden : in.width;
+  const int64_t n = product == kGradW ? in.hidden : in.rows;
+  const int factor = product == kGradW ? 2 : 1;  // results
+  const int64_t depth_bytes =
+      (product == kForward ? in.width : product == kGradX ? 2 * in.hidden : in.rows) * elem_bytes(in.dtype);
+  const int64_t depth = ceil_div(depth_bytes, kDepthBytes);
+  // rows of a tile along m and n, workgroups to a CU, and how near the matrix instructions' rate they come
+  struct {
+    int m, n, at_once;
+    double rate;
+  } const shapes[3] = {{product == kForward ? 128 : 64, 64, 2, 0.5}, {128, 128, 2, 0.85}, {256, 256, 1, 1.0}};
+  constexpr double kEnds = 4.0;
+  // (in fp32 the matrix instructions take 16 times as long for the same bytes, and memory is far from it)
+  const double unit = elem_bytes(in.dtype) == 4 ? 8.0 : 1.0;
+  Choice best = {};
+  double least = 1e300;
+  for (int s = 0; s < 3; ++s) {
+    const auto& t = shapes[s];
+    const int64_t mt = ceil_div(m, product == kForward ? t.m / 2 : t.m), nt = ceil_div(n, t.n) * factor;
+    for (int splits = 1; splits <= kMaxSplits; splits *= 2) {
+      if (splits > 1 && (product == kForward || depth < 4 * splits)) break;
+      const double rounds = (double)ceil_div(mt * nt * splits, (int64_t)kCUs * t.at_once) * t.at_once;
+      double time = rounds * t.m * t.n * (ceil_div(depth, splits) / t.rate + kEnds / unit);
+      if (splits > 1) {
+        // 64 elements of a tile's depth take as long as 1.3 bytes of memory traffic a CU's share; and a launch
+        const double bytes = (double)m * n * factor * (8.0 * splits + 4.0) / kCUs;
+        time += (bytes * 50.0 + 256.0 * 256.0 * 2.0) / unit;
+      }
+      if (time < least) {
+        least = time;
+        best = {s, splits, mt, nt};
+      }
+    }
+  }
+  return best;
+}
+size_t part_bytes(const ssim_gated_linear_inputs& in, int product) {
+  const Choice c = choose(in, product);
+  if (c.splits == 1) return 0;
+  return to_16((size_t)(product == kGradW ? 2 * in.hidden : in.rows) * in.width * c.splits * 4);
+}
+
+int launch_product(const ssim_gated_linear_inputs& in, const GatedTable& t, GatedParams p, int product, void* part,
+                   void* stream) {
+  const Choice c = choose(in, product);
+  p.m_tiles = (int)c.m_tiles;
+  p.n_tiles = (int)c.n_tiles;
+  p.splits = c.splits;
+  p.part = static_cast<float*>(part);
+  if (product == kGradX) p.dw[0] = p.dw[1] = nullptr;
+  const int64_t blocks = c.m_tiles * c.n_tiles * c.splits;
   if (blocks > 1 << 22) return SSIM_ERR_OVERFLOW;
-  return launch(t.product[product][wide], dim3((unsigned)blocks), wide ? 512 : 256, p, stream);
+  const int rc = launch(t.product[product][c.tiles], dim3((unsigned)blocks), c.tiles == 2 ? 512 : 256, p, stream);
+  if (rc != SSIM_OK || c.splits == 1) return rc;
+  const int64_t n = (product == kGradW ? in.hidden : in.rows) * in.width, groups = ceil_div(n, 1024);
+  return launch(t.join, dim3((unsigned)(groups < 4 * kCUs ? groups : 4 * kCUs), product == kGradW ? 2 : 1), 256, p, stream);
 }
 
 struct Slopes {
@@ -133,14 +181,16 @@ Slopes slopes_of(const ssim_gated_linear_inputs& in) {
 
 struct BackwardSpace {
   Copies copies;
-  size_t d, part, total;
+  size_t d, bias, part, total;
 };
 BackwardSpace space_of(const ssim_gated_linear_inputs& in) {
   BackwardSpace s;
   s.copies = copies_of(in);
   s.d = (size_t)in.rows * padded(in, in.hidden) * elem_bytes(in.dtype);
-  s.part = to_16((size_t)slopes_of(in).row_blocks * 2 * in.hidden * 4);
-  s.total = s.copies.x + 2 * s.copies.w + 2 * s.d + s.part;
+  s.bias = to_16((size_t)slopes_of(in).row_blocks * 2 * in.hidden * 4);
+  const size_t x = part_bytes(in, kGradX), w = part_bytes(in, kGradW);
+  s.part = x > w ? x : w;  // one after the other
+  s.total = s.copies.x + 2 * s.copies.w + 2 * s.d + s.bias + s.part;
   return s;
 }
 
@@ -159,7 +209,7 @@ size_t ssim_gated_linear_workspace_bytes(const ssim_gated_linear_inputs* in) {
   return c.x + 2 * c.w;
 }
 
-int ssim_gated_linear_forward(const ssim_gated_linear_inputs* in, void* out, void* g, void* u,
+int ssim_gated_linear_forward(const ssim_gated_linear_inputs* in, void* out, float* g, float* u,
                               void* workspace, void* stream) {
   int rc = check_inputs(in);
   if (rc != SSIM_OK) return rc;
@@ -167,7 +217,7 @@ int ssim_gated_linear_forward(const ssim_gated_linear_inputs* in, void* out, voi
   const size_t ws = ssim_gated_linear_workspace_bytes(in);
   if (!in->x || !in->w_gate || !in->w_up || !out || !g != !u || (ws > 0 && !workspace)) return SSIM_ERR_NULL;
   const int bytes = elem_bytes(in->dtype);
-  const size_t weight = (size_t)in->hidden * in->width * bytes, saved = ssim_gated_linear_saved_elements(in) * bytes;
+  const size_t weight = (size_t)in->hidden * in->width * bytes, saved = ssim_gated_linear_saved_elements(in) * 4;
   const Array ins[] = {{in->x, (size_t)in->rows * in->width * bytes, bytes},
                        {in->w_gate, weight, bytes},
                        {in->w_up, weight, bytes},
@@ -193,7 +243,7 @@ int ssim_gated_linear_forward(const ssim_gated_linear_inputs* in, void* out, voi
   char* at = static_cast<char*>(workspace);
   rc = make_copies(*in, copies_of(*in), t, p, at, stream);
   if (rc != SSIM_OK) return rc;
-  return launch_product(t, p, kForward, in->hidden, in->rows, 1, stream);
+  return launch_product(*in, t, p, kForward, nullptr, stream);
 }
 
 size_t ssim_gated_linear_backward_workspace_bytes(const ssim_gated_linear_inputs* in) {
@@ -201,7 +251,7 @@ size_t ssim_gated_linear_backward_workspace_bytes(const ssim_gated_linear_inputs
   return space_of(*in).total;
 }
 
-int ssim_gated_linear_backward(const ssim_gated_linear_inputs* in, const void* g, const void* u,
+int ssim_gated_linear_backward(const ssim_gated_linear_inputs* in, const float* g, const float* u,
                                const void* d_out, const ssim_gated_linear_grads* grads,
                                void* workspace, void* stream) {
   int rc = check_inputs(in);
@@ -214,7 +264,7 @@ int ssim_gated_linear_backward(const ssim_gated_linear_inputs* in, const void* g
   if (in->rows > 0 && (!in->x || !in->w_gate || !in->w_up || !g || !u || !d_out || !workspace)) return SSIM_ERR_NULL;
   const int bytes = elem_bytes(in->dtype);
   const size_t weight = (size_t)in->hidden * in->width * bytes, bias = (size_t)in->hidden * bytes;
-  const size_t saved = ssim_gated_linear_saved_elements(in) * bytes, xs = (size_t)in->rows * in->width * bytes;
+  const size_t saved = ssim_gated_linear_saved_elements(in) * 4, xs = (size_t)in->rows * in->width * bytes;
   const BackwardSpace space = space_of(*in);
   const bool rows = in->rows > 0;
   const Array ins[] = {{in->x, xs, bytes},
@@ -233,8 +283,8 @@ int ssim_gated_linear_backward(const ssim_gated_linear_inputs* in, const void* g
 
   const GatedTable& t = table_of(in->dtype);
   GatedParams p = params_of(*in);
-  p.saved[0] = const_cast<void*>(g);
-  p.saved[1] = const_cast<void*>(u);
+  p.saved[0] = const_cast<float*>(g);
+  p.saved[1] = const_cast<float*>(u);
   p.d_out = d_out;
   p.dx = grads->x;
   p.dw[0] = grads->w_gate;
@@ -257,14 +307,15 @@ int ssim_gated_linear_backward(const ssim_gated_linear_inputs* in, const void* g
     if (rc != SSIM_OK) return rc;
   }
   if (biases) {
-    rc = launch(t.bias_sums, dim3((unsigned)ceil_div(in->hidden, 64), 2), 64, p, stream);
+    rc = launch(t.bias_sums, dim3((unsigned)ceil_div(in->hidden, 64), 2), 256, p, stream);
     if (rc != SSIM_OK) return rc;
   }
+  void* part = rows ? at + 2 * space.d + space.bias : nullptr;
   if (grads->x && rows) {
-    rc = launch_product(t, p, kGradX, in->width, in->rows, 1, stream);
+    rc = launch_product(*in, t, p, kGradX, part, stream);
     if (rc != SSIM_OK) return rc;
   }
-  if (weights) return launch_product(t, p, kGradW, in->width, in->hidden, 2, stream);
+  if (weights) return launch_product(*in, t, p, kGradW, part, stream);
   return SSIM_OK;
 }
 

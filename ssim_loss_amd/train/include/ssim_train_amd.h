@@ -307,9 +307,8 @@ size_t ssim_gated_linear_workspace_bytes(const ssim_gated_linear_inputs* in);
 size_t ssim_gated_linear_backward_workspace_bytes(const ssim_gated_linear_inputs* in);
 
 /* out: [rows, hidden].  g, u: NULL, or 16-byte aligned arrays of
- * ssim_gated_linear_saved_elements elements that receive g and u, rounded to dtype,
- * for the backward. */
-int ssim_gated_linear_forward(const ssim_gated_linear_inputs* in, void* out, void* g, void* u,
+ * ssim_gated_linear_saved_elements floats that receive g and u for the backward. */
+int ssim_gated_linear_forward(const ssim_gated_linear_inputs* in, void* out, float* g, float* u,
                               void* workspace, void* stream);
 
 /* The gradients for d_out ([rows, hidden]), each of its input's shape; NULL: not
@@ -322,7 +321,7 @@ typedef struct {
   void* b_up;
 } ssim_gated_linear_grads;
 
-int ssim_gated_linear_backward(const ssim_gated_linear_inputs* in, const void* g, const void* u,
+int ssim_gated_linear_backward(const ssim_gated_linear_inputs* in, const float* g, const float* u,
                                const void* d_out, const ssim_gated_linear_grads* grads,
                                void* workspace, void* stream);
 

@@ -5,8 +5,8 @@ U = 2^-24 is half a step of fp32.  The bounds count roundings to first order and
 carry them through the formulas by magnitudes, so they hold for every input.  A
 sum of n products is counted with 2 U for each term (a matrix instruction may cut
 where an addition rounds).  Where a half type is rounded to on the way (the
-probabilities, their gradients, the projections kept for the backward), half a
-step of that type is counted; a result adds half a step of its own.
+probabilities, the gradients of scores and projections), half a step of that type
+is counted; a result adds half a step of its own.
 """
 from __future__ import annotations
 
@@ -175,10 +175,7 @@ class Gated:
         self.off = {"out": (h_off + rounding(h, dtype) * SLACK).reshape(shape)}
         if d_out is not None:
             dh = d(d_out).reshape(-1, hidden)
-            tiny = TINY[dtype] / 2
-            g_off, u_off = g_off + t * g.abs() + tiny, u_off + t * u.abs() + tiny
             slope_off = bend * g_off + (16 + 3 * g.abs().clamp(max=100.0)) * U * (slope.abs() + g.abs().clamp(max=1.0))
-            a_off = top * g_off + a_rel * a.abs()
             dg, du = dh * u * slope, dh * a
             dg_off = dh.abs() * (u.abs() * slope_off + u_off * slope.abs()) + 3 * U * dg.abs()
             du_off = dh.abs() * a_off + 2 * U * du.abs()
