@@ -59,23 +59,28 @@ template <class T>
 constexpr int kAcrossSteps = 32 / kPerStep<T>;
 template <class T>
 constexpr int kAcrossRegs = kPerStep<T> / 2;
+// matrix instructions of a step, and reads of an operand across rows
+template <class T>
+constexpr int kInstructions = sizeof(T) == 4 ? 4 : 1;
+template <class T>
+constexpr int kAcrossReads = sizeof(T) == 4 ? 4 : 2;
+constexpr int kAhead = 4;
 
-// The workgroup's (batch, key head) and its item among theirs.
+// The workgroup's (batch, key head) and its item among theirs.  Ids go round the
+// XCDs (id % 8); where the pairs can be dealt out evenly, a pair's keys stay in one
+// XCD's cache.
 struct Where {
   int b, kvh, item;
 };
+template <bool kItemsFirst = false>
 __device__ __forceinline__ Where where(const AttentionParams& p, int items) {
-  const unsigned id = blockIdx.x;
-  unsigned pair, item;
-  if (p.spread) {  // workgroup id goes to XCD id % 8: a pair's keys stay in one XCD's cache
-    const unsigned j = id >> 3;
-    pair = (j / items) * 8 + (id & 7);
-    item = j % items;
-  } else {
-    pair = id / items;
-    item = id % items;
+  const unsigned id = blockIdx.x, step = p.spread ? 8 : 1, j = id / step;
+  if (kItemsFirst && p.causal) {
+    const unsigned pairs = (unsigned)(p.batch * p.kv_heads) / step, pair = j % pairs * step + id % step;
+    return {(int)(pair / p.kv_heads), (int)(pair % p.kv_heads), (int)(j / pairs)};
   }
-  return {(int)(pair / p.kv_heads), (int)(pair % p.kv_heads), (int)item};
+  const unsigned pair = j / items * step + id % step;
+  return {(int)(pair / p.kv_heads), (int)(pair % p.kv_heads), (int)(j % items)};
 }
 
 // kTile rows of memory, from `from` on, to a tile in LDS; rows from `rows` on and
@@ -113,24 +118,32 @@ __device__ __forceinline__ void load_row(const char* row, bool live, int chunks,
 
 // s = rows `row` .. row + 31 of the tile times the lane's row
 template <class T, int DB>
-__device__ __forceinline__ Sums along(const Lds* tile, int row, const Chunk (&mine)[HeadShape<T, DB>::kSteps]) {
-  constexpr int kRow = HeadShape<T, DB>::kRow;
-  const int lane = threadIdx.x & (kWave - 1);
+__device__ __forceinline__ Sums along(const Lds* tile, int offset, int row, const Chunk (&mine)[HeadShape<T, DB>::kSteps]) {
   Sums s = {};
 #pragma unroll
   for (int t = 0; t < HeadShape<T, DB>::kSteps; ++t)
-    multiply<T>(s, lds_chunk(tile, place<kRow>(row + (lane & 31), 2 * t + (lane >> 5))), mine[t]);
+    multiply<T>(s, lds_along<HeadShape<T, DB>::kRow>(tile, offset, row, t), mine[t]);
+  return s;
+}
+// ... where the lane's row is row `other` + lane % 32 of another tile
+template <class T, int DB>
+__device__ __forceinline__ Sums along_both(const Lds* tile, const Lds* others, int offset, int row, int other) {
+  constexpr int kRow = HeadShape<T, DB>::kRow;
+  Sums s = {};
+#pragma unroll
+  for (int t = 0; t < HeadShape<T, DB>::kSteps; ++t)
+    multiply<T>(s, lds_along<kRow>(tile, offset, row, t), lds_along<kRow>(others, offset, other, t));
   return s;
 }
 // to[block] += (columns of the tile's rows `row` .. row + 31) times w
 template <class T, int DB>
-__device__ __forceinline__ void across(Sums (&to)[DB], const Lds* tile, int row, const Sums& w) {
+__device__ __forceinline__ void across(Sums (&to)[DB], const Lds* tile, int offset, int row, const Sums& w) {
 #pragma unroll
   for (int t = 0; t < kAcrossSteps<T>; ++t) {
     const Chunk b = operand_of<T>(w, t * kAcrossRegs<T>);
 #pragma unroll
     for (int d = 0; d < DB; ++d)
-      multiply<T>(to[d], lds_across<T, HeadShape<T, DB>::kRow>(tile, row + t * kPerStep<T>, d), b);
+      multiply<T>(to[d], lds_across<T, HeadShape<T, DB>::kRow>(tile, offset, row + t * kPerStep<T>, d), b);
   }
 }
 // the row of a tile's register r
@@ -236,6 +249,7 @@ attention_forward(const AttentionParams p) {
                                          to + Shape::kTileBytes);
   };
 
+  const int along_at = along_offset<Head::kRow>(), across_at = across_offset<T, Head::kRow>();
   Sums o[DB] = {};
   float m = -INFINITY, l = 0.0f;  // the row's maximum so far; the sum of this lane's half
   if (begin < end) fetch(begin);
@@ -248,7 +262,8 @@ attention_forward(const AttentionParams p) {
     const int key = t * Shape::kKeys + in_tile;
     Sums s[Shape::kBlocks];
 #pragma unroll
-    for (int b = 0; b < Shape::kBlocks; ++b) s[b] = along<T, DB>(k_tile, in_tile + 32 * b, q);
+    for (int b = 0; b < Shape::kBlocks; ++b) s[b] = along<T, DB>(k_tile, fresh(along_at), in_tile + 32 * b, q);
+    read_ahead<kAhead, kInstructions<T>, Shape::kBlocks * Head::kSteps, 1>();
     if (key + 32 * Shape::kBlocks - 1 > open) {
 #pragma unroll
       for (int b = 0; b < Shape::kBlocks; ++b)
@@ -278,7 +293,8 @@ attention_forward(const AttentionParams p) {
         l += s[b][r];
       }
 #pragma unroll
-    for (int b = 0; b < Shape::kBlocks; ++b) across<T, DB>(o, v_tile, in_tile + 32 * b, s[b]);
+    for (int b = 0; b < Shape::kBlocks; ++b) across<T, DB>(o, v_tile, fresh(across_at), in_tile + 32 * b, s[b]);
+    read_ahead<kAhead, kInstructions<T>, Shape::kBlocks * DB * kAcrossSteps<T>, kAcrossReads<T>>();
     if (Shape::kBuffers == 1 && t + 1 < end) {
       landed_for_all();
       fetch(t + 1);
@@ -496,6 +512,7 @@ __global__ void __launch_bounds__(kAttentionThreads, sizeof(T) == 2 ? 2 : 1) att
     fetch_tile<Head::kRow, Shape::kKeys>(v_from + (int64_t)key * p.v.token, p.v.token, seen.k_length - key, chunks,
                                          to + Shape::kTileBytes);
   };
+  const int along_at = along_offset<Head::kRow>(), across_at = across_offset<T, Head::kRow>();
   Sums dq[DB] = {};
   if (end > 0) fetch(0);
   for (int t = 0; t < end; ++t) {
@@ -505,8 +522,9 @@ __global__ void __launch_bounds__(kAttentionThreads, sizeof(T) == 2 ? 2 : 1) att
     const Lds* v_tile = k_tile + Shape::kTileBytes;
 #pragma unroll
     for (int b = 0; b < Shape::kKeys / 32; ++b) {
-      Sums s = along<T, DB>(k_tile, 32 * b, q);
-      const Sums dp = along<T, DB>(v_tile, 32 * b, d_out);
+      Sums s = along<T, DB>(k_tile, fresh(along_at), 32 * b, q);
+      const Sums dp = along<T, DB>(v_tile, fresh(along_at), 32 * b, d_out);
+      read_ahead<kAhead, kInstructions<T>, 2 * Head::kSteps, 1>();
       const int key = t * Shape::kKeys + 32 * b;
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
@@ -518,7 +536,8 @@ __global__ void __launch_bounds__(kAttentionThreads, sizeof(T) == 2 ? 2 : 1) att
         for (int r = 0; r < 16; ++r)
           s[r] = key + row_of(r) > last ? 0.0f : s[r];
       }
-      across<T, DB>(dq, k_tile, 32 * b, s);
+      across<T, DB>(dq, k_tile, fresh(across_at), 32 * b, s);
+      read_ahead<kAhead, kInstructions<T>, DB * kAcrossSteps<T>, kAcrossReads<T>>();
     }
   }
   if (there && p.dq) store_row<T, DB>(static_cast<T*>(p.dq) + dense, dq, ldexpf(p.scale, -range), p.dim);
@@ -530,8 +549,13 @@ __global__ void __launch_bounds__(kAttentionThreads, sizeof(T) == 2 ? 2 : 1) att
 template <class T, int DB>
 struct KeysShape {
   static constexpr int kKeys = 128;
-  static constexpr int kRows = 64 * HeadShape<T, DB>::kRow <= 16 << 10 ? 64 : 32;  // of a tile
+  // Of half types' widest heads the values are read from LDS each time: with them
+  // in registers as well, 224 of 256 are taken and each read from LDS is waited for
+  // (4 x 4096 x 16 x 128 bf16: 375, so 300 us).
+  static constexpr bool kValuesInLds = sizeof(T) == 2 && DB == 4;
+  static constexpr int kRows = !kValuesInLds && 64 * HeadShape<T, DB>::kRow <= 16 << 10 ? 64 : 32;  // of a tile
   static constexpr int kTileBytes = kRows * HeadShape<T, DB>::kRow;
+  static constexpr int kValueBytes = kValuesInLds ? kKeys * HeadShape<T, DB>::kRow : 0;
 };
 // The probabilities of fp16 are rounded times 2^14: at most 1, most of a long row's
 // would be subnormal.
@@ -542,11 +566,11 @@ template <class T, int DB>
 __global__ void __launch_bounds__(kAttentionThreads, sizeof(T) == 2 ? 2 : 1) attention_grad_kv(const AttentionParams p) {
   using Shape = KeysShape<T, DB>;
   using Head = HeadShape<T, DB>;
-  __shared__ __attribute__((aligned(1024))) char lds_[4 * Shape::kTileBytes];
-  __shared__ __attribute__((aligned(16))) float stats[2][2][Shape::kRows];  // [buffer][lse, delta]
+  __shared__ __attribute__((aligned(1024))) char lds_[4 * Shape::kTileBytes + Shape::kValueBytes];
+  __shared__ __attribute__((aligned(16))) float stats[2][2][kWave];  // [buffer][lse, delta][row of the tile]
   Lds* lds = (Lds*)lds_;
-  const uint32_t lds_at = lds_address(lds);
-  const Where at = where(p, p.tiles);
+  const uint32_t lds_at = lds_address(lds), stats_at = lds_address((Lds*)&stats[0][0][0]);
+  const Where at = where<true>(p, p.tiles);
   if (at.b >= p.batch) return;
   const Seen seen = seen_of(p, at.b);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
@@ -555,9 +579,12 @@ __global__ void __launch_bounds__(kAttentionThreads, sizeof(T) == 2 ? 2 : 1) att
   const int wave_key = first_key + wave * 32, key = wave_key + (lane & 31);
   const bool live = key < seen.k_length;
   const int key_read = min(key, p.k_tokens - 1);
-  Chunk k[Head::kSteps], v[Head::kSteps];
+  Chunk k[Head::kSteps], v[Shape::kValuesInLds ? 1 : Head::kSteps];
   load_row<T, DB>(p.k.p + at.b * p.k.batch + at.kvh * p.k.head + (int64_t)key_read * p.k.token, live, chunks, k);
-  load_row<T, DB>(p.v.p + at.b * p.v.batch + at.kvh * p.v.head + (int64_t)key_read * p.v.token, live, chunks, v);
+  const char* v_from = p.v.p + at.b * p.v.batch + at.kvh * p.v.head;
+  const Lds* v_tile = lds + 4 * Shape::kTileBytes;
+  if constexpr (!Shape::kValuesInLds)
+    load_row<T, DB>(v_from + (int64_t)key_read * p.v.token, live, chunks, v);
 
   const int range = range_of<T>(p, at);
   const float up = ldexpf(1.0f, range - kLift<T>);
@@ -567,8 +594,13 @@ __global__ void __launch_bounds__(kAttentionThreads, sizeof(T) == 2 ? 2 : 1) att
   const int end = first_key < seen.k_length ? (seen.q_length + Shape::kRows - 1) / Shape::kRows : 0;
   const int per_head = max(end - begin, 0), total = per_head * p.group;
   const uint32_t dense_stride = (uint32_t)(p.heads * p.dim) * sizeof(T);
+  int next_head = at.kvh * p.group, next_tile = begin;  // what fetch takes
   auto fetch = [&](int n) {
-    const int head = at.kvh * p.group + n / per_head, token = (begin + n % per_head) * Shape::kRows;
+    const int head = next_head, token = next_tile * Shape::kRows;
+    if (++next_tile == end) {
+      next_tile = begin;
+      ++next_head;
+    }
     const uint32_t to = lds_at + (n & 1) * 2 * Shape::kTileBytes;
     const int count = seen.q_length - token;
     fetch_tile<Head::kRow, Shape::kRows>(p.q.p + at.b * p.q.batch + head * p.q.head + (int64_t)token * p.q.token,
@@ -577,25 +609,34 @@ __global__ void __launch_bounds__(kAttentionThreads, sizeof(T) == 2 ? 2 : 1) att
         (const char*)p.d_out + (((int64_t)at.b * p.q_tokens + token) * p.heads + head) * p.dim * (int64_t)sizeof(T),
         dense_stride, count, chunks, to + Shape::kTileBytes);
     const int64_t stat = ((int64_t)at.b * p.heads + head) * p.q_tokens + token;
-    if (threadIdx.x < Shape::kRows) {
-      const bool in = (int)threadIdx.x < count;
-      stats[n & 1][0][threadIdx.x] = in ? p.lse[stat + threadIdx.x] : INFINITY;
-      stats[n & 1][1][threadIdx.x] = in ? p.delta[stat + threadIdx.x] : 0.0f;
-    }
+    // (rows that are not there arrive as zeros, and their queries and gradients with them)
+    if (wave < 2)
+      load_words_to_lds(describe((wave ? p.delta : p.lse) + stat, count <= 0 ? 0 : 4 * min(count, Shape::kRows)),
+                        4 * (threadIdx.x & (kWave - 1)), stats_at + ((n & 1) * 2 + wave) * (kWave * 4));
   };
+  const int along_at = along_offset<Head::kRow>(), across_at = across_offset<T, Head::kRow>();
   Sums dk[DB] = {}, dv[DB] = {};
-  if (total > 0) fetch(0);
-  for (int n = 0; n < total; ++n) {
+  if (total > 0) {
+    if constexpr (Shape::kValuesInLds)
+      fetch_tile<Head::kRow, Shape::kKeys>(v_from + (int64_t)first_key * p.v.token, p.v.token, seen.k_length - first_key,
+                                           chunks, lds_at + 4 * Shape::kTileBytes);
+    fetch(0);
+  }
+  for (int n = 0, now = begin; n < total; ++n) {
     landed_for_all();
     if (n + 1 < total) fetch(n + 1);
     const Lds* q_tile = lds + (n & 1) * 2 * Shape::kTileBytes;
     const Lds* d_tile = q_tile + Shape::kTileBytes;
-    const int token = (begin + n % per_head) * Shape::kRows;
+    const int token = now * Shape::kRows;
+    if (++now == end) now = begin;
 #pragma unroll
     for (int b = 0; b < Shape::kRows / 32; ++b) {
-      Sums s = along<T, DB>(q_tile, 32 * b, k);
-      Sums ds = along<T, DB>(d_tile, 32 * b, v);
-      const bool open = last_key(seen, token + 32 * b) >= wave_key + 31 && token + 32 * b + 31 < seen.q_length;
+      Sums s = along<T, DB>(q_tile, fresh(along_at), 32 * b, k);
+      Sums ds;
+      if constexpr (Shape::kValuesInLds) ds = along_both<T, DB>(d_tile, v_tile, fresh(along_at), 32 * b, wave * 32);
+      else ds = along<T, DB>(d_tile, fresh(along_at), 32 * b, v);
+      read_ahead<kAhead, kInstructions<T>, Head::kSteps, 1, Head::kSteps, Shape::kValuesInLds ? 2 : 1>();
+      __builtin_amdgcn_sched_barrier(0);  // (the statistics' reads are none of these)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int first = 32 * b + row_of(4 * j);
@@ -604,16 +645,22 @@ __global__ void __launch_bounds__(kAttentionThreads, sizeof(T) == 2 ? 2 : 1) att
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int r = 4 * j + e;
-          float w = exp2_fast(fmaf(s[r], p.scale2, (float)kLift<T> - lse[e]));
-          float g = w * (ds[r] - delta[e]);
-          if constexpr (kScaled<T>) g *= up;
-          if (!open && key > last_key(seen, token + first + e)) w = g = 0.0f;
-          s[r] = w;
-          ds[r] = g;
+          s[r] = exp2_fast(fmaf(s[r], p.scale2, (float)kLift<T> - lse[e]));
+          ds[r] = s[r] * (ds[r] - delta[e]);
+          if constexpr (kScaled<T>) ds[r] *= up;
         }
       }
-      across<T, DB>(dv, d_tile, 32 * b, s);
-      across<T, DB>(dk, q_tile, 32 * b, ds);
+      if (last_key(seen, token + 32 * b) < wave_key + 31 || token + 32 * b + 31 >= seen.q_length) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const bool hidden = key > last_key(seen, token + 32 * b + row_of(r));
+          s[r] = hidden ? 0.0f : s[r];
+          ds[r] = hidden ? 0.0f : ds[r];
+        }
+      }
+      across<T, DB>(dv, d_tile, fresh(across_at), 32 * b, s);
+      across<T, DB>(dk, q_tile, fresh(across_at), 32 * b, ds);
+      read_ahead<kAhead, kInstructions<T>, 2 * DB * kAcrossSteps<T>, kAcrossReads<T>>();
     }
   }
   if (key >= p.k_tokens) return;

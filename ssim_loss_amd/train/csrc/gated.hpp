@@ -266,6 +266,8 @@ __global__ void __launch_bounds__(WM* WN* kWave, WM* WN == 4 ? 2 : 1) gated_prod
     if constexpr (kProduct == kForward) return i < BM / 2 ? wm * (BM / 2) + i : kHalfM / 32 + wm * (BM / 2) + i - BM / 2;
     else return wm * BM + i;
   };
+  const int a_at = kProduct == kForward ? along_offset<128>() : across_offset<T, Shape::kM * kBytes, true>();
+  const int b_at = kProduct == kGradW ? across_offset<T, Shape::kN * kBytes, true>() : along_offset<128>();
   if (begin < end) fetch(begin);
   for (int t = begin; t < end; ++t) {
     landed_for_all();
@@ -278,16 +280,16 @@ __global__ void __launch_bounds__(WM* WN* kWave, WM* WN == 4 ? 2 : 1) gated_prod
 #pragma unroll
       for (int i = 0; i < BM; ++i) {
         if constexpr (kProduct == kForward)
-          a[i] = lds_chunk(a_tile, place<128>(32 * a_block(i) + (lane & 31), 2 * s + h));
+          a[i] = lds_along<128>(a_tile, a_at, 32 * a_block(i), s);
         else
-          a[i] = lds_across<T, Shape::kM * kBytes, true>(a_tile, s * kPerStep<T>, a_block(i));
+          a[i] = lds_across<T, Shape::kM * kBytes, true>(a_tile, a_at, s * kPerStep<T>, a_block(i));
       }
 #pragma unroll
       for (int i = 0; i < BN; ++i) {
         if constexpr (kProduct == kGradW)
-          b[i] = lds_across<T, Shape::kN * kBytes, true>(b_tile, s * kPerStep<T>, wn * BN + i);
+          b[i] = lds_across<T, Shape::kN * kBytes, true>(b_tile, b_at, s * kPerStep<T>, wn * BN + i);
         else
-          b[i] = lds_chunk(b_tile, place<128>(32 * (wn * BN + i) + (lane & 31), 2 * s + h));
+          b[i] = lds_along<128>(b_tile, b_at, 32 * (wn * BN + i), s);
       }
 #pragma unroll
       for (int i = 0; i < BM; ++i)

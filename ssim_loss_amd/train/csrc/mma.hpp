@@ -77,42 +77,86 @@ __device__ __forceinline__ Chunk lds_chunk(const Lds* p, int at) {
   return *reinterpret_cast<const __attribute__((address_space(3))) Chunk*>(p + at);
 }
 
+// Where a lane reads: its offsets in a tile (at a multiple of kRow), of which the
+// other reads' are an exclusive or and a constant away.  Left to itself the compiler
+// keeps each of them in a register through a loop; fresh() makes it form them
+// anew, one instruction each.
+__device__ __forceinline__ int fresh(int offset) {
+  asm("" : "+v"(offset));
+  return offset;
+}
+// rows as they lie: row lane % 32, chunk 2 t + h
+template <int kRow>
+__device__ __forceinline__ int along_offset() {
+  const int lane = threadIdx.x & (kWave - 1);
+  return place<kRow>(lane & 31, lane >> 5);
+}
+template <int kRow>
+__device__ __forceinline__ Chunk lds_along(const Lds* tile, int offset, int row, int t) {
+  return lds_chunk(tile, (offset ^ (t << 5)) + row * kRow);
+}
+
 // The operand whose rows are columns of the tile: lane's column 32 block +
-// lane % 32, and a step's rows from `row` on (half types: 16; fp32: 8), in the
-// order in which operand_of's step holds them or, kPlain, in that of a row read
-// as it lies.
+// lane % 32, and a step's rows from `row` on (half types: 16; fp32: 8; `row` a
+// multiple of them), in the order in which operand_of's step holds them or, kPlain,
+// in that of a row read as it lies.
 template <class T, int kRow, bool kPlain = false>
-__device__ __forceinline__ Chunk lds_across(const Lds* tile, int row, int block) {
+__device__ __forceinline__ int across_offset() {
   const int lane = threadIdx.x & (kWave - 1), h = lane >> 5;
+  if constexpr (sizeof(T) == 4) return place<kRow>(4 * h, (lane & 31) >> 2) + ((lane & 3) << 2);
+  // each 16 lanes read 4 rows of 16 columns and get a column's 4 values each
+  const int i = lane & 15;
+  return place<kRow>((kPlain ? 8 : 4) * h + (i >> 2), (lane >> 4 & 1) * 2 + (i >> 1 & 1)) + ((i & 1) << 3);
+}
+template <class T, int kRow, bool kPlain = false>
+__device__ __forceinline__ Chunk lds_across(const Lds* tile, int offset, int row, int block) {
   if constexpr (sizeof(T) == 4) {
     Vec<float, 4> v;
-    const int column = 32 * block + (lane & 31);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int at = place<kRow>(row + 4 * h + k, column >> 2) + ((column & 3) << 2);
+      const int turned = (kRow == 128 ? k >> 1 : k) << 6;
+      const int at = (offset ^ (block << 7) ^ turned ^ ((row >> 3 & 1) << 5)) + (row + k) * kRow;
       v[k] = *reinterpret_cast<const __attribute__((address_space(3))) float*>(tile + at);
     }
     return __builtin_bit_cast(Chunk, v);
   } else {
-    // each 16 lanes read 4 rows of 16 columns and get a column's 4 values each
-    const int i = lane & 15;
-    const int chunk = 4 * block + (lane >> 4 & 1) * 2 + (i >> 1 & 1);
-    const int r = row + (kPlain ? 8 : 4) * h + (i >> 2), part = (i & 1) << 3;
     typedef __attribute__((address_space(3))) Quad* At;
+    constexpr int kTurned = kPlain ? 1 << 4 : 1 << 5, kNext = kPlain ? 4 : 8;
+    const int at = offset ^ (block << 6);
     union {
       Quad q[2];
       Chunk c;
     } u;
-    u.q[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((At)(tile + place<kRow>(r, chunk) + part));
-    u.q[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((At)(tile + place<kRow>(r + (kPlain ? 4 : 8), chunk) + part));
+    u.q[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((At)(tile + at + row * kRow));
+    u.q[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((At)(tile + (at ^ kTurned) + (row + kNext) * kRow));
     return u.c;
+  }
+}
+
+// ---- order of instructions.  Left alone the compiler reads an operand from LDS just
+// before the instruction that needs it and waits.  These lines, behind a sequence of
+// products in the same basic block, ask for kAhead products' reads before the first
+// and for each product's reads kAhead products early.
+// Two stretches, of N products (kEach instructions and R reads) each; N1 may be 0.
+template <int kAhead, int kEach, int N0, int R0, int N1 = 0, int R1 = 0>
+__device__ __forceinline__ void read_ahead() {
+  constexpr int kLdsRead = 0x100, kMatrix = 0x8;
+#pragma unroll
+  for (int i = -kAhead; i < N0 + N1; ++i) {
+    if (i >= 0) __builtin_amdgcn_sched_group_barrier(kMatrix, kEach, 0);
+    if (i + kAhead < N0) {
+      if constexpr (R0 > 0) __builtin_amdgcn_sched_group_barrier(kLdsRead, R0, 0);
+    } else if (i + kAhead < N0 + N1) {
+      if constexpr (R1 > 0) __builtin_amdgcn_sched_group_barrier(kLdsRead, R1, 0);
+    }
   }
 }
 
 // ---- memory to LDS, without registers between: 64 lanes' chunks go to 1024
 // bytes at `to` (the same for the wave), lane after lane.  A chunk past the
-// descriptor's bytes arrives as zeros.  The compiler does not count these
-// loads; landed() waits for all of them.
+// descriptor's bytes arrives as zeros.  In asm, since the compiler waits for its own
+// form of these loads before any read of the LDS; it does not count them:
+// landed_for_all() waits.  (m0 is written here; nothing else in these kernels uses it.)
 typedef unsigned Descriptor __attribute__((ext_vector_type(4)));
 
 // of `bytes` (< 2^32, counted in whole chunks) from p on, which is the same for the wave
@@ -136,7 +180,16 @@ __device__ __forceinline__ void load_to_lds(Descriptor from, uint32_t offset, ui
       : "s"(to), "v"(offset), "s"(from)
       : "memory");
 }
-__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// ... and 64 lanes' words to 256 bytes
+__device__ __forceinline__ void load_words_to_lds(Descriptor from, uint32_t offset, uint32_t to) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n"
+      "s_nop 0\n"
+      "buffer_load_dword %1, %2, 0 offen lds"
+      :
+      : "s"(to), "v"(offset), "s"(from)
+      : "memory");
+}
 
 __device__ __forceinline__ uint32_t lds_address(const Lds* p) { return (uint32_t)(uintptr_t)p; }
 
