@@ -85,10 +85,10 @@ __device__ __forceinline__ Where where(const AttentionParams& p, int items) {
 
 // kTile rows of memory, from `from` on, to a tile in LDS; rows from `rows` on and
 // chunks from `chunks` on arrive as zeros.
-template <int kRow, int kTile>
+template <int kRow, int kTile, int kThreads = kAttentionThreads>
 __device__ __forceinline__ void fetch_tile(const char* from, uint32_t stride, int rows, int chunks, uint32_t to) {
   constexpr int kChunksOfRow = kRow / 16;
-  constexpr int kRowsAtOnce = kAttentionThreads / kChunksOfRow;
+  constexpr int kRowsAtOnce = kThreads / kChunksOfRow;
   static_assert(kTile % kRowsAtOnce == 0, "whole instructions");
   const int row = threadIdx.x / kChunksOfRow;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -102,6 +102,9 @@ __device__ __forceinline__ void fetch_tile(const char* from, uint32_t stride, in
     load_to_lds(d, offset, to + (uint32_t)(j * kRowsAtOnce * kRow + wave * (kWave * 16)));
   }
 }
+
+template <int kRow, int kTile, int kThreads>
+constexpr int kLoadsOfTile = kTile * kRow / (kThreads * 16);  // a wave's
 
 // A lane's chunks of its row: 2 t + h; zeros past the row's chunks and where it is
 // not live (`row` can be read all the same).
@@ -185,25 +188,33 @@ __device__ __forceinline__ int last_key(const Seen& s, int i) {
 }
 
 // ---------------------------------------------------------------- forward
-// KW waves share rows and take keys in turn: 1, a wave has 32 rows of the
-// workgroup's 128; 4, all have the same 32 (few rows, many keys).
-template <class T, int DB, int KW>
+// NW waves.  KW of them share rows and take keys in turn: 1, a wave has 32 rows of
+// its own; 4, all have the same 32 (few rows, many keys).
+//
+// Tiles of keys are loaded kBuffers - 1 ahead.  Eight waves with four buffers, one
+// workgroup to a CU, ask the caches for half of what two workgroups of four waves do
+// and wait less for it (heads of 65 to 128 in a half type with rows enough:
+// 16384 x 16 x 128 bf16 2080, so 1900 us).
+template <class T, int DB, int KW, int NW>
 struct ForwardShape {
+  static constexpr int kThreads = NW * kWave;
   static constexpr int kKeys = KW == 1 ? 64 : 128;  // of a tile
   static constexpr int kBlocks = KW == 1 ? 2 : 1;   // of 32 keys, a wave's
-  static constexpr int kRows = KW == 1 ? 128 : 32;  // of the workgroup
+  static constexpr int kRows = NW / KW * 32;        // of the workgroup
   static constexpr int kTileBytes = kKeys * HeadShape<T, DB>::kRow;
-  static constexpr int kBuffers = 4 * kTileBytes <= 128 << 10 ? 2 : 1;
+  static constexpr int kRoom = NW == 8 || KW == 4 || sizeof(T) == 4 ? 128 << 10 : DB > 2 ? 64 << 10 : 48 << 10;
+  static constexpr int kBuffers = kRoom / (2 * kTileBytes) > 4 ? 4 : kRoom / (2 * kTileBytes);
+  static constexpr int kLoads = 2 * kLoadsOfTile<HeadShape<T, DB>::kRow, kKeys, kThreads>;
   static constexpr int kPitch = DB * 32 + 4;        // floats: of a row where waves' results are joined
   static constexpr int kJoin = KW == 1 ? 0 : 4 * 32 * kPitch * 4;
   static constexpr int kTiles = 2 * kBuffers * kTileBytes;
   static constexpr int kLds = kTiles > kJoin ? kTiles : kJoin;
 };
 
-template <class T, int DB, int KW>
-__global__ void __launch_bounds__(kAttentionThreads, (sizeof(T) == 2 && KW == 1) ? 2 : 1)
+template <class T, int DB, int KW, int NW>
+__global__ void __launch_bounds__(NW* kWave, (sizeof(T) == 2 && KW == 1) ? 2 : 1)
 attention_forward(const AttentionParams p) {
-  using Shape = ForwardShape<T, DB, KW>;
+  using Shape = ForwardShape<T, DB, KW, NW>;
   using Head = HeadShape<T, DB>;
   __shared__ __attribute__((aligned(1024))) char lds_[Shape::kLds];
   __shared__ float joined[2][4][32];
@@ -241,29 +252,40 @@ attention_forward(const AttentionParams p) {
 
   const char* k_from = p.k.p + at.b * p.k.batch + at.kvh * p.k.head;
   const char* v_from = p.v.p + at.b * p.v.batch + at.kvh * p.v.head;
-  auto fetch = [&](int t) {
-    const int key = t * Shape::kKeys;
-    const uint32_t to = lds_at + (t % Shape::kBuffers) * 2 * Shape::kTileBytes;
-    fetch_tile<Head::kRow, Shape::kKeys>(k_from + (int64_t)key * p.k.token, p.k.token, seen.k_length - key, chunks, to);
-    fetch_tile<Head::kRow, Shape::kKeys>(v_from + (int64_t)key * p.v.token, p.v.token, seen.k_length - key, chunks,
-                                         to + Shape::kTileBytes);
+  auto fetch = [&](int t) {  // (none past the end: their loads are counted all the same)
+    const int key = t * Shape::kKeys, left = t < end ? seen.k_length - key : 0;
+    const uint32_t to = lds_at + ((t - begin) % Shape::kBuffers) * 2 * Shape::kTileBytes;
+    fetch_tile<Head::kRow, Shape::kKeys, Shape::kThreads>(k_from + (int64_t)key * p.k.token, p.k.token, left, chunks, to);
+    fetch_tile<Head::kRow, Shape::kKeys, Shape::kThreads>(v_from + (int64_t)key * p.v.token, p.v.token, left, chunks,
+                                                          to + Shape::kTileBytes);
   };
 
   const int along_at = along_offset<Head::kRow>(), across_at = across_offset<T, Head::kRow>();
   Sums o[DB] = {};
-  float m = -INFINITY, l = 0.0f;  // the row's maximum so far; the sum of this lane's half
-  if (begin < end) fetch(begin);
+  // The row's reference, a maximum so far: p = exp2(scale2 s - base).  It is raised, and
+  // the sums with it, only where scores pass it by 2^8 in p, which both types and the
+  // sums hold: in a long row seldom, where a larger maximum comes with every other tile.
+  float m = -INFINITY, base = 0.0f, limit = -INFINITY;
+  const float slack = 8.0f / p.scale2;
+  float l = 0.0f;  // the sum of this lane's half
+  constexpr int kEarly = Shape::kBuffers > 1 ? Shape::kBuffers - 1 : 1;
+  if (begin < end) {
+#pragma unroll
+    for (int t = 0; t < kEarly; ++t) fetch(begin + t);
+  }
   for (int t = begin; t < end; ++t) {
-    landed_for_all();
-    if (Shape::kBuffers == 2 && t + 1 < end) fetch(t + 1);
-    const Lds* k_tile = lds + (t % Shape::kBuffers) * 2 * Shape::kTileBytes;
+    landed_for_all<(kEarly - 1) * Shape::kLoads>();
+    if constexpr (Shape::kBuffers > 1) fetch(t + kEarly);
+    const Lds* k_tile = lds + ((t - begin) % Shape::kBuffers) * 2 * Shape::kTileBytes;
     const Lds* v_tile = k_tile + Shape::kTileBytes;
     const int in_tile = KW == 1 ? 0 : wave * 32;
     const int key = t * Shape::kKeys + in_tile;
     Sums s[Shape::kBlocks];
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int b = 0; b < Shape::kBlocks; ++b) s[b] = along<T, DB>(k_tile, fresh(along_at), in_tile + 32 * b, q);
     read_ahead<kAhead, kInstructions<T>, Shape::kBlocks * Head::kSteps, 1>();
+    __builtin_amdgcn_s_setprio(0);
     if (key + 32 * Shape::kBlocks - 1 > open) {
 #pragma unroll
       for (int b = 0; b < Shape::kBlocks; ++b)
@@ -271,20 +293,22 @@ attention_forward(const AttentionParams p) {
         for (int r = 0; r < 16; ++r)
           s[b][r] = key + 32 * b + row_of(r) > last ? -INFINITY : s[b][r];
     }
-    float top = m;
+    float top = -INFINITY;
 #pragma unroll
     for (int b = 0; b < Shape::kBlocks; ++b)
 #pragma unroll
       for (int r = 0; r < 16; ++r) top = fmaxf(top, s[b][r]);
     top = halves_max(top);
-    const float base = top == -INFINITY ? 0.0f : top * p.scale2;
-    if (__any(top != m)) {
-      const float less = exp2_fast(fmaf(m, p.scale2, -base));
+    if (__any(top > limit)) {
+      const float before = m == -INFINITY ? -INFINITY : base;
+      m = fmaxf(m, top);
+      base = m == -INFINITY ? 0.0f : m * p.scale2;
+      limit = m + slack;
+      const float less = exp2_fast(before - base);
       l *= less;
 #pragma unroll
       for (int d = 0; d < DB; ++d) o[d] *= less;
     }
-    m = top;
 #pragma unroll
     for (int b = 0; b < Shape::kBlocks; ++b)
 #pragma unroll
@@ -295,11 +319,12 @@ attention_forward(const AttentionParams p) {
 #pragma unroll
     for (int b = 0; b < Shape::kBlocks; ++b) across<T, DB>(o, v_tile, fresh(across_at), in_tile + 32 * b, s[b]);
     read_ahead<kAhead, kInstructions<T>, Shape::kBlocks * DB * kAcrossSteps<T>, kAcrossReads<T>>();
-    if (Shape::kBuffers == 1 && t + 1 < end) {
+    if constexpr (Shape::kBuffers == 1) {
       landed_for_all();
       fetch(t + 1);
     }
   }
+  landed_for_all();  // what was fetched past the end, too
   l = halves_sum(l);
 
   if constexpr (KW == 4) {  // the waves' results together
@@ -308,8 +333,9 @@ attention_forward(const AttentionParams p) {
     float top = joined[0][0][lane & 31];
 #pragma unroll
     for (int w = 1; w < 4; ++w) top = fmaxf(top, joined[0][w][lane & 31]);
-    const float base = top == -INFINITY ? 0.0f : top * p.scale2;
-    const float less = exp2_fast(fmaf(m, p.scale2, -base));
+    const float before = m == -INFINITY ? -INFINITY : base;
+    base = top == -INFINITY ? 0.0f : top * p.scale2;
+    const float less = exp2_fast(before - base);
     l *= less;
     if (lane < 32) joined[1][wave][lane] = l;
     float* mine = (float*)lds_ + (wave * 32 + (lane & 31)) * Shape::kPitch;
@@ -318,11 +344,10 @@ attention_forward(const AttentionParams p) {
     store_row<float, DB>(mine, o, 1.0f, DB * 32);
     landed_for_all();
     l = joined[1][0][lane & 31] + joined[1][1][lane & 31] + joined[1][2][lane & 31] + joined[1][3][lane & 31];
-    m = top;
   }
 
   const float inverse = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-  const float lse = l > 0.0f || l != l ? fmaf(m, p.scale2, __builtin_amdgcn_logf(l)) : -INFINITY;
+  const float lse = l > 0.0f || l != l ? base + __builtin_amdgcn_logf(l) : -INFINITY;
   const int64_t stat = ((int64_t)at.b * p.heads + head) * p.q_tokens + token;
   const int64_t part = (int64_t)split * p.batch * p.heads * p.q_tokens;
   const bool whole = p.splits == 1;
@@ -443,18 +468,22 @@ __device__ __forceinline__ int range_of(const AttentionParams& p, const Where& a
 // ---------------------------------------------------------------- gradient of the queries
 // As the forward: a wave has 32 rows, the keys go by.  It forms delta_i = do_i . o_i
 // and leaves it for the other kernel.
-template <class T, int DB>
+template <class T, int DB, int NW>
 struct QueriesShape {
+  static constexpr int kThreads = NW * kWave;
   static constexpr int kKeys = 64;
-  static constexpr int kRows = 128;
+  static constexpr int kRows = NW * 32;
   static constexpr int kTileBytes = kKeys * HeadShape<T, DB>::kRow;
+  static constexpr int kRoom = NW == 8 || sizeof(T) == 4 ? 128 << 10 : DB > 2 ? 64 << 10 : 48 << 10;
+  static constexpr int kBuffers = kRoom / (2 * kTileBytes) > 4 ? 4 : kRoom / (2 * kTileBytes);
+  static constexpr int kLoads = 2 * kLoadsOfTile<HeadShape<T, DB>::kRow, kKeys, kThreads>;
 };
 
-template <class T, int DB>
-__global__ void __launch_bounds__(kAttentionThreads, sizeof(T) == 2 ? 2 : 1) attention_grad_q(const AttentionParams p) {
-  using Shape = QueriesShape<T, DB>;
+template <class T, int DB, int NW>
+__global__ void __launch_bounds__(NW* kWave, sizeof(T) == 2 ? 2 : 1) attention_grad_q(const AttentionParams p) {
+  using Shape = QueriesShape<T, DB, NW>;
   using Head = HeadShape<T, DB>;
-  __shared__ __attribute__((aligned(1024))) char lds_[4 * Shape::kTileBytes];
+  __shared__ __attribute__((aligned(1024))) char lds_[2 * Shape::kBuffers * Shape::kTileBytes];
   Lds* lds = (Lds*)lds_;
   const uint32_t lds_at = lds_address(lds);
   const Where at = where(p, p.tiles);
@@ -506,19 +535,23 @@ __global__ void __launch_bounds__(kAttentionThreads, sizeof(T) == 2 ? 2 : 1) att
   const char* k_from = p.k.p + at.b * p.k.batch + at.kvh * p.k.head;
   const char* v_from = p.v.p + at.b * p.v.batch + at.kvh * p.v.head;
   auto fetch = [&](int t) {
-    const int key = t * Shape::kKeys;
-    const uint32_t to = lds_at + (t & 1) * 2 * Shape::kTileBytes;
-    fetch_tile<Head::kRow, Shape::kKeys>(k_from + (int64_t)key * p.k.token, p.k.token, seen.k_length - key, chunks, to);
-    fetch_tile<Head::kRow, Shape::kKeys>(v_from + (int64_t)key * p.v.token, p.v.token, seen.k_length - key, chunks,
-                                         to + Shape::kTileBytes);
+    const int key = t * Shape::kKeys, left = t < end ? seen.k_length - key : 0;
+    const uint32_t to = lds_at + (t % Shape::kBuffers) * 2 * Shape::kTileBytes;
+    fetch_tile<Head::kRow, Shape::kKeys, Shape::kThreads>(k_from + (int64_t)key * p.k.token, p.k.token, left, chunks, to);
+    fetch_tile<Head::kRow, Shape::kKeys, Shape::kThreads>(v_from + (int64_t)key * p.v.token, p.v.token, left, chunks,
+                                                          to + Shape::kTileBytes);
   };
   const int along_at = along_offset<Head::kRow>(), across_at = across_offset<T, Head::kRow>();
   Sums dq[DB] = {};
-  if (end > 0) fetch(0);
+  constexpr int kEarly = Shape::kBuffers - 1;
+  if (end > 0) {
+#pragma unroll
+    for (int t = 0; t < kEarly; ++t) fetch(t);
+  }
   for (int t = 0; t < end; ++t) {
-    landed_for_all();
-    if (t + 1 < end) fetch(t + 1);
-    const Lds* k_tile = lds + (t & 1) * 2 * Shape::kTileBytes;
+    landed_for_all<(kEarly - 1) * Shape::kLoads>();
+    fetch(t + kEarly);
+    const Lds* k_tile = lds + (t % Shape::kBuffers) * 2 * Shape::kTileBytes;
     const Lds* v_tile = k_tile + Shape::kTileBytes;
 #pragma unroll
     for (int b = 0; b < Shape::kKeys / 32; ++b) {
@@ -540,36 +573,43 @@ __global__ void __launch_bounds__(kAttentionThreads, sizeof(T) == 2 ? 2 : 1) att
       read_ahead<kAhead, kInstructions<T>, DB * kAcrossSteps<T>, kAcrossReads<T>>();
     }
   }
+  landed_for_all();  // what was fetched past the end, too
   if (there && p.dq) store_row<T, DB>(static_cast<T*>(p.dq) + dense, dq, ldexpf(p.scale, -range), p.dim);
 }
 
 // ---------------------------------------------------------------- gradients of the keys and values
 // A wave has 32 keys; the rows of all heads that share them go by, head after
 // head, in one order: no atomics, the same bits every time.
-template <class T, int DB>
+template <class T, int DB, int NW>
 struct KeysShape {
-  static constexpr int kKeys = 128;
+  static constexpr int kThreads = NW * kWave;
+  static constexpr int kKeys = NW * 32;
   // Of half types' widest heads the values are read from LDS each time: with them
   // in registers as well, 224 of 256 are taken and each read from LDS is waited for
-  // (4 x 4096 x 16 x 128 bf16: 375, so 300 us).
+  // (4 x 4096 x 16 x 128 bf16: 489, so 431 us).
   static constexpr bool kValuesInLds = sizeof(T) == 2 && DB == 4;
   static constexpr int kRows = !kValuesInLds && 64 * HeadShape<T, DB>::kRow <= 16 << 10 ? 64 : 32;  // of a tile
   static constexpr int kTileBytes = kRows * HeadShape<T, DB>::kRow;
   static constexpr int kValueBytes = kValuesInLds ? kKeys * HeadShape<T, DB>::kRow : 0;
+  static constexpr int kRoom = (NW == 8 ? 128 << 10 : sizeof(T) == 4 || DB > 2 ? 64 << 10 : 48 << 10) - kValueBytes;
+  static constexpr int kBuffers = kRoom / (2 * kTileBytes) > 4 ? 4 : kRoom / (2 * kTileBytes);
+  static constexpr int kLoads = 2 * kLoadsOfTile<HeadShape<T, DB>::kRow, kRows, kThreads> + 1;
 };
 // The probabilities of fp16 are rounded times 2^14: at most 1, most of a long row's
 // would be subnormal.
 template <class T>
 constexpr int kLift = kScaled<T> ? 14 : 0;
 
-template <class T, int DB>
-__global__ void __launch_bounds__(kAttentionThreads, sizeof(T) == 2 ? 2 : 1) attention_grad_kv(const AttentionParams p) {
-  using Shape = KeysShape<T, DB>;
+template <class T, int DB, int NW>
+__global__ void __launch_bounds__(NW* kWave, sizeof(T) == 2 ? 2 : 1) attention_grad_kv(const AttentionParams p) {
+  using Shape = KeysShape<T, DB, NW>;
   using Head = HeadShape<T, DB>;
-  __shared__ __attribute__((aligned(1024))) char lds_[4 * Shape::kTileBytes + Shape::kValueBytes];
-  __shared__ __attribute__((aligned(16))) float stats[2][2][kWave];  // [buffer][lse, delta][row of the tile]
+  __shared__ __attribute__((aligned(1024))) char lds_[2 * Shape::kBuffers * Shape::kTileBytes + Shape::kValueBytes];
+  __shared__ __attribute__((aligned(16))) float stats[Shape::kBuffers][2][kWave];  // [lse, delta][row of the tile]
   Lds* lds = (Lds*)lds_;
+  __shared__ float nowhere[kWave];
   const uint32_t lds_at = lds_address(lds), stats_at = lds_address((Lds*)&stats[0][0][0]);
+  const uint32_t nowhere_at = lds_address((Lds*)nowhere);
   const Where at = where<true>(p, p.tiles);
   if (at.b >= p.batch) return;
   const Seen seen = seen_of(p, at.b);
@@ -582,7 +622,7 @@ __global__ void __launch_bounds__(kAttentionThreads, sizeof(T) == 2 ? 2 : 1) att
   Chunk k[Head::kSteps], v[Shape::kValuesInLds ? 1 : Head::kSteps];
   load_row<T, DB>(p.k.p + at.b * p.k.batch + at.kvh * p.k.head + (int64_t)key_read * p.k.token, live, chunks, k);
   const char* v_from = p.v.p + at.b * p.v.batch + at.kvh * p.v.head;
-  const Lds* v_tile = lds + 4 * Shape::kTileBytes;
+  const Lds* v_tile = lds + 2 * Shape::kBuffers * Shape::kTileBytes;
   if constexpr (!Shape::kValuesInLds)
     load_row<T, DB>(v_from + (int64_t)key_read * p.v.token, live, chunks, v);
 
@@ -594,38 +634,44 @@ __global__ void __launch_bounds__(kAttentionThreads, sizeof(T) == 2 ? 2 : 1) att
   const int end = first_key < seen.k_length ? (seen.q_length + Shape::kRows - 1) / Shape::kRows : 0;
   const int per_head = max(end - begin, 0), total = per_head * p.group;
   const uint32_t dense_stride = (uint32_t)(p.heads * p.dim) * sizeof(T);
-  int next_head = at.kvh * p.group, next_tile = begin;  // what fetch takes
-  auto fetch = [&](int n) {
-    const int head = next_head, token = next_tile * Shape::kRows;
+  int next = 0, next_head = at.kvh * p.group, next_tile = begin;  // what fetch takes
+  auto fetch = [&]() {
+    const int head = min(next_head, p.heads - 1), token = next_tile * Shape::kRows, buffer = next % Shape::kBuffers;
+    const int count = next < total ? seen.q_length - token : 0;
+    ++next;
     if (++next_tile == end) {
       next_tile = begin;
       ++next_head;
     }
-    const uint32_t to = lds_at + (n & 1) * 2 * Shape::kTileBytes;
-    const int count = seen.q_length - token;
-    fetch_tile<Head::kRow, Shape::kRows>(p.q.p + at.b * p.q.batch + head * p.q.head + (int64_t)token * p.q.token,
-                                         p.q.token, count, chunks, to);
-    fetch_tile<Head::kRow, Shape::kRows>(
+    const uint32_t to = lds_at + buffer * 2 * Shape::kTileBytes;
+    fetch_tile<Head::kRow, Shape::kRows, Shape::kThreads>(
+        p.q.p + at.b * p.q.batch + head * p.q.head + (int64_t)token * p.q.token, p.q.token, count, chunks, to);
+    fetch_tile<Head::kRow, Shape::kRows, Shape::kThreads>(
         (const char*)p.d_out + (((int64_t)at.b * p.q_tokens + token) * p.heads + head) * p.dim * (int64_t)sizeof(T),
         dense_stride, count, chunks, to + Shape::kTileBytes);
+    // (rows that are not there arrive as zeros, and their queries and gradients with them; all but two waves
+    // load nothing, since loads are counted alike)
     const int64_t stat = ((int64_t)at.b * p.heads + head) * p.q_tokens + token;
-    // (rows that are not there arrive as zeros, and their queries and gradients with them)
-    if (wave < 2)
-      load_words_to_lds(describe((wave ? p.delta : p.lse) + stat, count <= 0 ? 0 : 4 * min(count, Shape::kRows)),
-                        4 * (threadIdx.x & (kWave - 1)), stats_at + ((n & 1) * 2 + wave) * (kWave * 4));
+    load_words_to_lds(describe((wave ? p.delta : p.lse) + stat, count <= 0 || wave > 1 ? 0 : 4 * min(count, Shape::kRows)),
+                      4 * (threadIdx.x & (kWave - 1)),
+                      wave > 1 ? nowhere_at : stats_at + (buffer * 2 + wave) * (kWave * 4));
   };
   const int along_at = along_offset<Head::kRow>(), across_at = across_offset<T, Head::kRow>();
   Sums dk[DB] = {}, dv[DB] = {};
+  constexpr int kEarly = Shape::kBuffers - 1;
   if (total > 0) {
     if constexpr (Shape::kValuesInLds)
-      fetch_tile<Head::kRow, Shape::kKeys>(v_from + (int64_t)first_key * p.v.token, p.v.token, seen.k_length - first_key,
-                                           chunks, lds_at + 4 * Shape::kTileBytes);
-    fetch(0);
+      fetch_tile<Head::kRow, Shape::kKeys, Shape::kThreads>(v_from + (int64_t)first_key * p.v.token, p.v.token,
+                                                            seen.k_length - first_key, chunks,
+                                                            lds_at + 2 * Shape::kBuffers * Shape::kTileBytes);
+#pragma unroll
+    for (int t = 0; t < kEarly; ++t) fetch();
   }
   for (int n = 0, now = begin; n < total; ++n) {
-    landed_for_all();
-    if (n + 1 < total) fetch(n + 1);
-    const Lds* q_tile = lds + (n & 1) * 2 * Shape::kTileBytes;
+    landed_for_all<(kEarly - 1) * Shape::kLoads>();
+    fetch();
+    const int buffer = n % Shape::kBuffers;
+    const Lds* q_tile = lds + buffer * 2 * Shape::kTileBytes;
     const Lds* d_tile = q_tile + Shape::kTileBytes;
     const int token = now * Shape::kRows;
     if (++now == end) now = begin;
@@ -640,8 +686,8 @@ __global__ void __launch_bounds__(kAttentionThreads, sizeof(T) == 2 ? 2 : 1) att
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int first = 32 * b + row_of(4 * j);
-        const Vec<float, 4> lse = *reinterpret_cast<const Vec<float, 4>*>(&stats[n & 1][0][first]);
-        const Vec<float, 4> delta = *reinterpret_cast<const Vec<float, 4>*>(&stats[n & 1][1][first]);
+        const Vec<float, 4> lse = *reinterpret_cast<const Vec<float, 4>*>(&stats[buffer][0][first]);
+        const Vec<float, 4> delta = *reinterpret_cast<const Vec<float, 4>*>(&stats[buffer][1][first]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int r = 4 * j + e;
@@ -663,6 +709,7 @@ __global__ void __launch_bounds__(kAttentionThreads, sizeof(T) == 2 ? 2 : 1) att
       read_ahead<kAhead, kInstructions<T>, 2 * DB * kAcrossSteps<T>, kAcrossReads<T>>();
     }
   }
+  landed_for_all();  // what was fetched past the end, too
   if (key >= p.k_tokens) return;
   const int64_t dense = (((int64_t)at.b * p.k_tokens + key) * p.kv_heads + at.kvh) * p.dim;
   if (p.dk) store_row<T, DB>(static_cast<T*>(p.dk) + dense, dk, ldexpf(p.scale, -range), p.dim);
@@ -671,31 +718,35 @@ __global__ void __launch_bounds__(kAttentionThreads, sizeof(T) == 2 ? 2 : 1) att
 
 // ---------------------------------------------------------------- kernels of a type
 struct AttentionTable {
-  const void* forward[4][2];  // [blocks of 32 elements - 1][few rows]
-  const void* grad_q[4];
-  const void* grad_kv[4];
+  // [blocks of 32 elements - 1]; of rows' kernels the last index is 0: four waves of 32 rows, 1: eight, 2 (forward):
+  // four that share 32 rows.  NULL: there is none.
+  const void* forward[4][3];
+  const void* grad_q[4][2];
+  const void* grad_kv[4][2];
   const void* join;
   const void* norms;  // NULL: not needed
 };
+template <class T, int DB>
+void fill_attention_table(AttentionTable& t) {
+  constexpr int k = DB - 1;
+  t.forward[k][0] = (const void*)attention_forward<T, DB, 1, 4>;
+  t.forward[k][2] = (const void*)attention_forward<T, DB, 4, 4>;
+  t.grad_q[k][0] = (const void*)attention_grad_q<T, DB, 4>;
+  t.grad_kv[k][0] = (const void*)attention_grad_kv<T, DB, 4>;
+  t.forward[k][1] = t.grad_q[k][1] = t.grad_kv[k][1] = nullptr;
+  if constexpr (sizeof(T) == 2 && DB > 2) {
+    t.forward[k][1] = (const void*)attention_forward<T, DB, 1, 8>;
+    t.grad_q[k][1] = (const void*)attention_grad_q<T, DB, 8>;
+    t.grad_kv[k][1] = (const void*)attention_grad_kv<T, DB, 8>;
+  }
+}
 template <class T>
 AttentionTable make_attention_table() {
   AttentionTable t;
-  t.forward[0][0] = (const void*)attention_forward<T, 1, 1>;
-  t.forward[1][0] = (const void*)attention_forward<T, 2, 1>;
-  t.forward[2][0] = (const void*)attention_forward<T, 3, 1>;
-  t.forward[3][0] = (const void*)attention_forward<T, 4, 1>;
-  t.forward[0][1] = (const void*)attention_forward<T, 1, 4>;
-  t.forward[1][1] = (const void*)attention_forward<T, 2, 4>;
-  t.forward[2][1] = (const void*)attention_forward<T, 3, 4>;
-  t.forward[3][1] = (const void*)attention_forward<T, 4, 4>;
-  t.grad_q[0] = (const void*)attention_grad_q<T, 1>;
-  t.grad_q[1] = (const void*)attention_grad_q<T, 2>;
-  t.grad_q[2] = (const void*)attention_grad_q<T, 3>;
-  t.grad_q[3] = (const void*)attention_grad_q<T, 4>;
-  t.grad_kv[0] = (const void*)attention_grad_kv<T, 1>;
-  t.grad_kv[1] = (const void*)attention_grad_kv<T, 2>;
-  t.grad_kv[2] = (const void*)attention_grad_kv<T, 3>;
-  t.grad_kv[3] = (const void*)attention_grad_kv<T, 4>;
+  fill_attention_table<T, 1>(t);
+  fill_attention_table<T, 2>(t);
+  fill_attention_table<T, 3>(t);
+  fill_attention_table<T, 4>(t);
   t.join = (const void*)attention_join<T>;
   t.norms = nullptr;
   if constexpr (kScaled<T>) t.norms = (const void*)attention_norms<T>;

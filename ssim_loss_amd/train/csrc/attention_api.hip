@@ -2,6 +2,7 @@
 // work, launches.
 
 #include "attention.hpp"
+#include <stdlib.h>
 
 namespace {
 
@@ -20,25 +21,35 @@ const AttentionTable& table_of(int dtype) {
 }
 
 struct Plan {
-  bool few;         // all waves of a workgroup have the same 32 rows
-  int tiles, splits;  // of the forward
-  int q_tiles, kv_tiles;  // of the backward
+  int shape;  // of the forward: AttentionTable's index
+  int tiles, splits;
+  int q_shape, q_tiles, kv_shape, kv_tiles;  // of the backward
 };
+
+// Eight waves to a workgroup where they are built and there is more than one for
+// every CU.
+int shape_of(const void* eight, int64_t rows, int64_t pairs) {
+  return eight && getenv("A8") && ceil_div(rows, 256) * pairs > kCUs ? 1 : 0;
+}
 
 Plan make_plan(const ssim_attention_inputs& in) {
   Plan p;
   const int64_t rows = in.q_tokens * (in.heads / in.kv_heads), pairs = in.batch * in.kv_heads;
-  p.few = rows <= 32;
-  p.tiles = (int)ceil_div(rows, p.few ? 32 : 128);
+  const AttentionTable& t = table_of(in.dtype);
+  const int blocks = (in.dim - 1) / 32;
+  p.shape = rows <= 32 ? 2 : shape_of(t.forward[blocks][1], rows, pairs);
+  p.tiles = (int)ceil_div(rows, p.shape == 2 ? 32 : p.shape ? 256 : 128);
   // Few workgroups: each takes a part of the keys, two tiles of them at least, and
   // a second launch joins the parts.
-  const int64_t blocks = p.tiles * pairs, target = p.few && in.dim > 64 ? kCUs : 2 * kCUs;
-  const int64_t most = ceil_div(in.k_tokens, p.few ? 256 : 128);
-  int64_t splits = blocks > 0 ? target / blocks : 1;
+  const int64_t groups = p.tiles * pairs, target = p.shape == 2 && in.dim > 64 ? kCUs : 2 * kCUs;
+  const int64_t most = ceil_div(in.k_tokens, p.shape == 2 ? 256 : 128);
+  int64_t splits = groups > 0 ? target / groups : 1;
   if (splits > most) splits = most;
-  p.splits = splits < 1 ? 1 : (int)splits;
-  p.q_tiles = (int)ceil_div(rows, 128);
-  p.kv_tiles = (int)ceil_div(in.k_tokens, 128);
+  p.splits = splits < 1 || p.shape == 1 ? 1 : (int)splits;
+  p.q_shape = shape_of(t.grad_q[blocks][1], rows, pairs);
+  p.q_tiles = (int)ceil_div(rows, p.q_shape ? 256 : 128);
+  p.kv_shape = shape_of(t.grad_kv[blocks][1], in.k_tokens, pairs);
+  p.kv_tiles = (int)ceil_div(in.k_tokens, p.kv_shape ? 256 : 128);
   return p;
 }
 
@@ -153,8 +164,8 @@ int ssim_attention_forward(const ssim_attention_inputs* in, void* out, float* ls
   }
   const AttentionTable& t = table_of(in->dtype);
   const int blocks = (in->dim - 1) / 32;
-  rc = launch(t.forward[blocks][plan.few], dim3((unsigned)(in->batch * in->kv_heads * plan.tiles * plan.splits)),
-              kAttentionThreads, p, stream);
+  rc = launch(t.forward[blocks][plan.shape], dim3((unsigned)(in->batch * in->kv_heads * plan.tiles * plan.splits)),
+              plan.shape == 1 ? 512 : 256, p, stream);
   if (rc != SSIM_OK || plan.splits == 1) return rc;
   return launch(t.join, dim3((unsigned)ceil_div(rows, kAttentionThreads / kWave)), kAttentionThreads, p, stream);
 }
@@ -212,12 +223,12 @@ int ssim_attention_backward(const ssim_attention_inputs* in, const void* out, co
   }
   if (any_q) {  // (it forms delta for the other kernel)
     p.tiles = plan.q_tiles;
-    rc = launch(t.grad_q[blocks], dim3(pairs * plan.q_tiles), kAttentionThreads, p, stream);
+    rc = launch(t.grad_q[blocks][plan.q_shape], dim3(pairs * plan.q_tiles), plan.q_shape ? 512 : 256, p, stream);
     if (rc != SSIM_OK) return rc;
   }
   if (!any_k || !(dk || dv)) return SSIM_OK;
   p.tiles = plan.kv_tiles;
-  return launch(t.grad_kv[blocks], dim3(pairs * plan.kv_tiles), kAttentionThreads, p, stream);
+  return launch(t.grad_kv[blocks][plan.kv_shape], dim3(pairs * plan.kv_tiles), plan.kv_shape ? 512 : 256, p, stream);
 }
 
 }  // extern "C"

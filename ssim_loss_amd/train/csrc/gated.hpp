@@ -54,15 +54,34 @@ __device__ __forceinline__ float quotient_of(float a, float b) {
   if constexpr (sizeof(T) == 4) return a / b;
   else return a * __builtin_amdgcn_rcpf(b);
 }
+// The normal distribution's share below g.  For half types exp(x^2) erfc(x) = t P(t),
+// t = 1 / (1 + 0.44 x), with P fitted to 1.9e-7 of the value over x = 0 .. 10 (5e-7
+// evaluated in fp32), a third of the library function's instructions (4100 x 1153
+// x 2997 fp16: 108, so 92 us).
+template <class T>
+__device__ __forceinline__ float normal_share(float g) {
+  if constexpr (sizeof(T) == 4) return 0.5f * erfcf(g * -0.70710678118654752f);
+  const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(g), 0.44f * 0.70710678118654752f, 1.0f));
+  float v = 0.07122284919023514f;
+  v = fmaf(v, t, -0.2779455780982971f);
+  v = fmaf(v, t, 0.29668352007865906f);
+  v = fmaf(v, t, -0.02017728053033352f);
+  v = fmaf(v, t, 0.21581058204174042f);
+  v = fmaf(v, t, 0.2173140048980713f);
+  v = fmaf(v, t, 0.2488711178302765f);
+  v = fmaf(v, t, 0.24822095036506653f);
+  const float half = 0.5f * t * v * __expf(-0.5f * g * g);
+  return g > 0.0f ? 1.0f - half : half;
+}
 template <class T>
 __device__ __forceinline__ float act_of(float g, int act) {
-  if (act == SSIM_ACT_GELU) return 0.5f * g * erfcf(g * -0.70710678118654752f);
+  if (act == SSIM_ACT_GELU) return g * normal_share<T>(g);
   return quotient_of<T>(act == SSIM_ACT_SILU ? g : 1.0f, 1.0f + exp_of<T>(-g));
 }
 template <class T>
 __device__ __forceinline__ void act_slope(float g, int act, float& a, float& slope) {
   if (act == SSIM_ACT_GELU) {
-    const float phi = 0.5f * erfcf(g * -0.70710678118654752f);
+    const float phi = normal_share<T>(g);
     a = g * phi;
     slope = fmaf(g * 0.39894228040143268f, exp_of<T>(-0.5f * g * g), phi);
     return;

@@ -193,9 +193,11 @@ __device__ __forceinline__ void load_words_to_lds(Descriptor from, uint32_t offs
 
 __device__ __forceinline__ uint32_t lds_address(const Lds* p) { return (uint32_t)(uintptr_t)p; }
 
-// All waves' LDS reads are done and their loads to LDS landed.
+// All waves' LDS reads are done, and of their loads to LDS all but the last kLater
+// have landed.
+template <int kLater = 0>
 __device__ __forceinline__ void landed_for_all() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kLater) : "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }

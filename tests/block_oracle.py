@@ -167,6 +167,10 @@ class Gated:
         a, slope, top, bend = act_of(g, act)
         # the activation: a fast exponential is off by its argument's rounding, the quotient and products
         a_rel = (12 + 3 * g.abs().clamp(max=100.0)) * U
+        if act == "gelu" and t > 0:
+            # a half type's error function: 8 U of itself (a fit's error and its evaluation), and its
+            # exponential's argument g^2 / 2 log2 e < 0.73 g^2 rounded twice
+            a_rel = a_rel + (8 + 1.5 * (g * g).clamp(max=400.0)) * U
         a_off = top * g_off + a_rel * a.abs()
         h = a * u
         h_off = a_off * u.abs() + a.abs() * u_off + 2 * U * h.abs()
