@@ -75,9 +75,9 @@ def lib() -> ctypes.CDLL:
                     ("ssim_block_norm_backward", i32, [vp, vp, vp, vp, vp, vp, vp]),
                     ("ssim_rotary", i32, [vp, vp, vp, vp]),
                     ("ssim_attention_workspace_bytes", sz, [vp]),
-                    ("ssim_attention_forward", i32, [vp, vp, vp, vp, vp]),
+                    ("ssim_attention_forward", i32, [vp, vp, vp, vp, vp, vp]),
                     ("ssim_attention_backward_workspace_bytes", sz, [vp]),
-                    ("ssim_attention_backward", i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+                    ("ssim_attention_backward", i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
                     ("ssim_gated_linear_saved_elements", sz, [vp]),
                     ("ssim_gated_linear_workspace_bytes", sz, [vp]),
                     ("ssim_gated_linear_backward_workspace_bytes", sz, [vp]),

@@ -34,11 +34,13 @@ struct AttentionParams {
   int tiles, splits;   // of rows (or keys); parts of the keys that workgroups of their own take
   float scale, scale2; // scale2 = scale log2(e)
   void* out;           // [batch][q_tokens][heads][dim]
+  void* rest;          // as out: what out's rounding left, rounded itself; NULL: not wanted, or fp32
   float* lse;          // [batch][heads][q_tokens], log2 of the row's sum; +inf: no keys.  NULL: not wanted
   float* part_out;     // [splits][batch][heads][q_tokens][dim], each part's own softmax
   float* part_lse;     // [splits][batch][heads][q_tokens]; -inf: no keys
   // backward
-  const void* o;       // as out
+  const void* o;       // as out and rest
+  const void* o_rest;
   const void* d_out;
   float* delta;        // [batch][heads][q_tokens]
   float* norms;        // fp16: [batch][kv_heads][kNormParts][2], largest |do_i| and |v_j|
@@ -152,9 +154,20 @@ __device__ __forceinline__ void across(Sums (&to)[DB], const Lds* tile, int offs
 // the row of a tile's register r
 __device__ __forceinline__ int row_of(int r) { return 8 * (r >> 2) + 4 * (int)(threadIdx.x >> 5 & 1) + (r & 3); }
 
+// Four elements of a result and, where it is wanted, what their rounding leaves: the
+// backward's delta_i = do_i . o_i is the difference of numbers that may be far
+// larger than ds_ij / p_ij, and with o_i rounded to bf16 a third of dq's error came of
+// it (4 x 4096 x 16 x 128: 2.6e-3 of the norm to 2.4e-3).
+template <class T>
+__device__ __forceinline__ void store_with_rest(T* to, T* rest, Wide<4> v) {
+  const Vec<T, 4> n = narrow<T, 4>(v);
+  store<T, 4>(to, n);
+  if constexpr (sizeof(T) == 2)
+    if (rest) store<T, 4>(rest, narrow<T, 4>(v - widen<T, 4>(n)));
+}
 // A lane's row of the result, of which it holds the columns row_of() of each block.
 template <class T, int DB>
-__device__ __forceinline__ void store_row(T* row, const Sums (&v)[DB], float factor, int dim) {
+__device__ __forceinline__ void store_row(T* row, const Sums (&v)[DB], float factor, int dim, T* rest = nullptr) {
   const int h = threadIdx.x >> 5 & 1;
 #pragma unroll
   for (int d = 0; d < DB; ++d)
@@ -164,7 +177,7 @@ __device__ __forceinline__ void store_row(T* row, const Sums (&v)[DB], float fac
       Wide<4> w;
 #pragma unroll
       for (int e = 0; e < 4; ++e) w[e] = v[d][4 * k + e] * factor;
-      if (column < dim) store<T, 4>(row + column, narrow<T, 4>(w));
+      if (column < dim) store_with_rest<T>(row + column, rest ? rest + column : nullptr, w);
     }
 }
 
@@ -187,6 +200,33 @@ __device__ __forceinline__ int last_key(const Seen& s, int i) {
   return i < s.q_length ? min(s.k_length - 1, i + s.shift) : -1;
 }
 
+// ---- four waves' sums of the same 32 rows together, through the LDS
+template <int DB>
+struct JoinShape {
+  static constexpr int kPitch = DB * 32 + 4;  // floats of a row
+  static constexpr int kBytes = 4 * 32 * kPitch * 4;
+};
+// A wave's own; landed_for_all() comes before and after.
+template <int DB>
+__device__ __forceinline__ void give_to_join(char* lds, const Sums (&v)[DB]) {
+  const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
+  store_row<float, DB>((float*)lds + (wave * 32 + (lane & 31)) * JoinShape<DB>::kPitch, v, 1.0f, DB * 32);
+}
+// The sums of row lane % 32, four columns at a time: take(column, sum).
+template <int DB, class Take>
+__device__ __forceinline__ void take_joined(const char* lds, int dim, Take take) {
+  const int row = threadIdx.x & 31;
+#pragma unroll
+  for (int c = 4 * (threadIdx.x >> 5); c < DB * 32; c += 32) {
+    if (c >= dim) break;
+    const float* from = (const float*)lds + row * JoinShape<DB>::kPitch + c;
+    Wide<4> sum = {};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) sum += load<float, 4>(from + w * 32 * JoinShape<DB>::kPitch);
+    take(c, sum);
+  }
+}
+
 // ---------------------------------------------------------------- forward
 // NW waves.  KW of them share rows and take keys in turn: 1, a wave has 32 rows of
 // its own; 4, all have the same 32 (few rows, many keys).
@@ -205,8 +245,7 @@ struct ForwardShape {
   static constexpr int kRoom = NW == 8 || KW == 4 || sizeof(T) == 4 ? 128 << 10 : DB > 2 ? 64 << 10 : 48 << 10;
   static constexpr int kBuffers = kRoom / (2 * kTileBytes) > 4 ? 4 : kRoom / (2 * kTileBytes);
   static constexpr int kLoads = 2 * kLoadsOfTile<HeadShape<T, DB>::kRow, kKeys, kThreads>;
-  static constexpr int kPitch = DB * 32 + 4;        // floats: of a row where waves' results are joined
-  static constexpr int kJoin = KW == 1 ? 0 : 4 * 32 * kPitch * 4;
+  static constexpr int kJoin = KW == 1 ? 0 : JoinShape<DB>::kBytes;
   static constexpr int kTiles = 2 * kBuffers * kTileBytes;
   static constexpr int kLds = kTiles > kJoin ? kTiles : kJoin;
 };
@@ -338,10 +377,9 @@ attention_forward(const AttentionParams p) {
     const float less = exp2_fast(before - base);
     l *= less;
     if (lane < 32) joined[1][wave][lane] = l;
-    float* mine = (float*)lds_ + (wave * 32 + (lane & 31)) * Shape::kPitch;
 #pragma unroll
     for (int d = 0; d < DB; ++d) o[d] *= less;
-    store_row<float, DB>(mine, o, 1.0f, DB * 32);
+    give_to_join<DB>(lds_, o);
     landed_for_all();
     l = joined[1][0][lane & 31] + joined[1][1][lane & 31] + joined[1][2][lane & 31] + joined[1][3][lane & 31];
   }
@@ -355,27 +393,21 @@ attention_forward(const AttentionParams p) {
     if (!whole) p.part_lse[part + stat] = lse;
     else if (p.lse) p.lse[stat] = lse == -INFINITY ? INFINITY : lse;
   }
-  T* out = static_cast<T*>(p.out) + (((int64_t)at.b * p.q_tokens + token) * p.heads + head) * p.dim;
+  const int64_t dense = (((int64_t)at.b * p.q_tokens + token) * p.heads + head) * p.dim;
+  T* out = static_cast<T*>(p.out) + dense;
+  T* rest = p.rest ? static_cast<T*>(p.rest) + dense : nullptr;
   float* part_out = p.part_out + (part + stat) * p.dim;
   if constexpr (KW == 1) {
     if (!there) return;
-    if (whole) store_row<T, DB>(out, o, inverse, p.dim);
+    if (whole) store_row<T, DB>(out, o, inverse, p.dim, rest);
     else store_row<float, DB>(part_out, o, inverse, p.dim);
   } else {
-    // lane: row lane % 32, four columns of each of the threads' eight groups
-    const int group = threadIdx.x >> 5;
     if (!there) return;
-#pragma unroll
-    for (int c = 4 * group; c < DB * 32; c += 32) {
-      if (c >= p.dim) break;
-      Wide<4> sum = {};
-#pragma unroll
-      for (int w = 0; w < 4; ++w)
-        sum += load<float, 4>((const float*)lds_ + (w * 32 + (lane & 31)) * Shape::kPitch + c);
+    take_joined<DB>(lds_, p.dim, [&](int c, Wide<4> sum) {
       sum *= inverse;
-      if (whole) store<T, 4>(out + c, narrow<T, 4>(sum));
+      if (whole) store_with_rest<T>(out + c, rest ? rest + c : nullptr, sum);
       else store<float, 4>(part_out + c, sum);
-    }
+    });
   }
 }
 
@@ -390,16 +422,22 @@ __global__ void __launch_bounds__(kAttentionThreads) attention_join(const Attent
   for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.part_lse[s * rows + row]);
   const float base = top == -INFINITY ? 0.0f : top;
   const int64_t token = row % p.q_tokens, head = row / p.q_tokens % p.heads, b = row / p.q_tokens / p.heads;
-  T* out = static_cast<T*>(p.out) + ((b * p.q_tokens + token) * p.heads + head) * p.dim;
+  const int64_t dense = ((b * p.q_tokens + token) * p.heads + head) * p.dim;
   float weights = 0.0f;
-  Wide<2> sum = {};
-  for (int s = 0; s < p.splits; ++s) {
+  const int column = 4 * (lane & 31), half = lane >> 5;  // each half of the wave takes every second part
+  Wide<4> sum = {};
+  for (int s = half; s < p.splits; s += 2) {
     const float w = exp2_fast(p.part_lse[s * rows + row] - base);
     weights += w;
-    if (2 * lane < p.dim) sum += w * load<float, 2>(p.part_out + (s * rows + row) * p.dim + 2 * lane);
+    if (column < p.dim) sum += w * load<float, 4>(p.part_out + (s * rows + row) * p.dim + column);
   }
+  weights = halves_sum(weights);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) sum[k] = halves_sum(sum[k]);
   const float inverse = weights > 0.0f || weights != weights ? 1.0f / weights : 0.0f;
-  if (2 * lane < p.dim) store<T, 2>(out + 2 * lane, narrow<T, 2>(sum * inverse));
+  if (half == 0 && column < p.dim)
+    store_with_rest<T>(static_cast<T*>(p.out) + dense + column,
+                       p.rest ? static_cast<T*>(p.rest) + dense + column : nullptr, sum * inverse);
   if (p.lse && lane == 0) p.lse[row] = weights > 0.0f || weights != weights ? base + __builtin_amdgcn_logf(weights) : INFINITY;
 }
 
@@ -468,22 +506,25 @@ __device__ __forceinline__ int range_of(const AttentionParams& p, const Where& a
 // ---------------------------------------------------------------- gradient of the queries
 // As the forward: a wave has 32 rows, the keys go by.  It forms delta_i = do_i . o_i
 // and leaves it for the other kernel.
-template <class T, int DB, int NW>
+template <class T, int DB, int KW, int NW>
 struct QueriesShape {
   static constexpr int kThreads = NW * kWave;
-  static constexpr int kKeys = 64;
-  static constexpr int kRows = NW * 32;
+  static constexpr int kKeys = KW == 1 ? 64 : 128;
+  static constexpr int kRows = NW / KW * 32;
   static constexpr int kTileBytes = kKeys * HeadShape<T, DB>::kRow;
-  static constexpr int kRoom = NW == 8 || sizeof(T) == 4 ? 128 << 10 : DB > 2 ? 64 << 10 : 48 << 10;
+  static constexpr int kRoom = NW == 8 || KW == 4 || sizeof(T) == 4 ? 128 << 10 : DB > 2 ? 64 << 10 : 48 << 10;
   static constexpr int kBuffers = kRoom / (2 * kTileBytes) > 4 ? 4 : kRoom / (2 * kTileBytes);
   static constexpr int kLoads = 2 * kLoadsOfTile<HeadShape<T, DB>::kRow, kKeys, kThreads>;
+  static constexpr int kJoin = KW == 1 ? 0 : JoinShape<DB>::kBytes;
+  static constexpr int kTiles = 2 * kBuffers * kTileBytes;
+  static constexpr int kLds = kTiles > kJoin ? kTiles : kJoin;
 };
 
-template <class T, int DB, int NW>
-__global__ void __launch_bounds__(NW* kWave, sizeof(T) == 2 ? 2 : 1) attention_grad_q(const AttentionParams p) {
-  using Shape = QueriesShape<T, DB, NW>;
+template <class T, int DB, int KW, int NW>
+__global__ void __launch_bounds__(NW* kWave, sizeof(T) == 2 && KW == 1 ? 2 : 1) attention_grad_q(const AttentionParams p) {
+  using Shape = QueriesShape<T, DB, KW, NW>;
   using Head = HeadShape<T, DB>;
-  __shared__ __attribute__((aligned(1024))) char lds_[2 * Shape::kBuffers * Shape::kTileBytes];
+  __shared__ __attribute__((aligned(1024))) char lds_[Shape::kLds];
   Lds* lds = (Lds*)lds_;
   const uint32_t lds_at = lds_address(lds);
   const Where at = where(p, p.tiles);
@@ -494,7 +535,8 @@ __global__ void __launch_bounds__(NW* kWave, sizeof(T) == 2 ? 2 : 1) attention_g
   const int chunks = p.dim / kPerChunk<T>;
   const int rows = p.q_tokens * p.group;
   const int first_row = tile * Shape::kRows;
-  const int row_ = first_row + wave * kRowsOfWave + (lane & 31);
+  const int row_of_wave = first_row + (KW == 1 ? wave * kRowsOfWave : 0);
+  const int row_ = row_of_wave + (lane & 31);
   const bool there = row_ < rows;
   const int row = there ? row_ : 0;
   const int token = row / p.group, head = at.kvh * p.group + row % p.group;
@@ -508,19 +550,22 @@ __global__ void __launch_bounds__(NW* kWave, sizeof(T) == 2 ? 2 : 1) attention_g
   load_row<T, DB>((const char*)p.d_out + dense * (int64_t)sizeof(T), live, chunks, d_out);
   float delta = 0.0f;
   {
-    Chunk o[Head::kSteps];
+    constexpr int N = kPerChunk<T>;
+    constexpr bool kRest = sizeof(T) == 2;
+    Chunk o[Head::kSteps], o_rest[kRest ? Head::kSteps : 1];
     load_row<T, DB>((const char*)p.o + dense * (int64_t)sizeof(T), live, chunks, o);
+    if constexpr (kRest) load_row<T, DB>((const char*)p.o_rest + dense * (int64_t)sizeof(T), live, chunks, o_rest);
 #pragma unroll
     for (int t = 0; t < Head::kSteps; ++t) {
-      constexpr int N = kPerChunk<T>;
-      const Wide<N> a = widen<T, N>(__builtin_bit_cast(Vec<T, N>, o[t]));
+      Wide<N> a = widen<T, N>(__builtin_bit_cast(Vec<T, N>, o[t]));
+      if constexpr (kRest) a += widen<T, N>(__builtin_bit_cast(Vec<T, N>, o_rest[t]));
       const Wide<N> b = widen<T, N>(__builtin_bit_cast(Vec<T, N>, d_out[t]));
 #pragma unroll
       for (int k = 0; k < N; ++k) delta = fmaf(a[k], b[k], delta);
     }
     delta = halves_sum(delta);
   }
-  if (there && lane < 32) p.delta[stat] = delta;
+  if (there && lane < 32 && (KW == 1 || wave == 0)) p.delta[stat] = delta;
   const float lse = there ? p.lse[stat] : INFINITY;
   const int range = range_of<T>(p, at);
   const float up = ldexpf(1.0f, range);
@@ -528,8 +573,8 @@ __global__ void __launch_bounds__(NW* kWave, sizeof(T) == 2 ? 2 : 1) attention_g
   const int last_token = min((min(first_row + Shape::kRows, rows) - 1) / p.group, seen.q_length - 1);
   const int keys = first_row / p.group < seen.q_length ? max(last_key(seen, last_token) + 1, 0) : 0;
   const int end = (keys + Shape::kKeys - 1) / Shape::kKeys;
-  const int wave_first = (first_row + wave * kRowsOfWave) / p.group;
-  const int wave_last = min(first_row + wave * kRowsOfWave + kRowsOfWave, rows) - 1;
+  const int wave_first = row_of_wave / p.group;
+  const int wave_last = min(row_of_wave + kRowsOfWave, rows) - 1;
   const int open = wave_last / p.group < seen.q_length ? last_key(seen, wave_first) : -1;
 
   const char* k_from = p.k.p + at.b * p.k.batch + at.kvh * p.k.head;
@@ -543,22 +588,23 @@ __global__ void __launch_bounds__(NW* kWave, sizeof(T) == 2 ? 2 : 1) attention_g
   };
   const int along_at = along_offset<Head::kRow>(), across_at = across_offset<T, Head::kRow>();
   Sums dq[DB] = {};
-  constexpr int kEarly = Shape::kBuffers - 1;
+  constexpr int kEarly = Shape::kBuffers > 1 ? Shape::kBuffers - 1 : 1;
   if (end > 0) {
 #pragma unroll
     for (int t = 0; t < kEarly; ++t) fetch(t);
   }
   for (int t = 0; t < end; ++t) {
     landed_for_all<(kEarly - 1) * Shape::kLoads>();
-    fetch(t + kEarly);
+    if constexpr (Shape::kBuffers > 1) fetch(t + kEarly);
     const Lds* k_tile = lds + (t % Shape::kBuffers) * 2 * Shape::kTileBytes;
     const Lds* v_tile = k_tile + Shape::kTileBytes;
 #pragma unroll
-    for (int b = 0; b < Shape::kKeys / 32; ++b) {
-      Sums s = along<T, DB>(k_tile, fresh(along_at), 32 * b, q);
-      const Sums dp = along<T, DB>(v_tile, fresh(along_at), 32 * b, d_out);
+    for (int b = 0; b < (KW == 1 ? Shape::kKeys / 32 : 1); ++b) {
+      const int in_tile = KW == 1 ? 32 * b : 32 * wave;
+      Sums s = along<T, DB>(k_tile, fresh(along_at), in_tile, q);
+      const Sums dp = along<T, DB>(v_tile, fresh(along_at), in_tile, d_out);
       read_ahead<kAhead, kInstructions<T>, 2 * Head::kSteps, 1>();
-      const int key = t * Shape::kKeys + 32 * b;
+      const int key = t * Shape::kKeys + in_tile;
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         s[r] = exp2_fast(fmaf(s[r], p.scale2, -lse)) * (dp[r] - delta);
@@ -569,43 +615,62 @@ __global__ void __launch_bounds__(NW* kWave, sizeof(T) == 2 ? 2 : 1) attention_g
         for (int r = 0; r < 16; ++r)
           s[r] = key + row_of(r) > last ? 0.0f : s[r];
       }
-      across<T, DB>(dq, k_tile, fresh(across_at), 32 * b, s);
+      across<T, DB>(dq, k_tile, fresh(across_at), in_tile, s);
       read_ahead<kAhead, kInstructions<T>, DB * kAcrossSteps<T>, kAcrossReads<T>>();
+    }
+    if constexpr (Shape::kBuffers == 1) {
+      landed_for_all();
+      fetch(t + 1);
     }
   }
   landed_for_all();  // what was fetched past the end, too
-  if (there && p.dq) store_row<T, DB>(static_cast<T*>(p.dq) + dense, dq, ldexpf(p.scale, -range), p.dim);
+  T* to = static_cast<T*>(p.dq) + dense;
+  const float factor = ldexpf(p.scale, -range);
+  if constexpr (KW == 1) {
+    if (there && p.dq) store_row<T, DB>(to, dq, factor, p.dim);
+  } else {
+    give_to_join<DB>(lds_, dq);
+    landed_for_all();
+    if (there && p.dq)
+      take_joined<DB>(lds_, p.dim, [&](int c, Wide<4> sum) { store<T, 4>(to + c, narrow<T, 4>(sum * factor)); });
+  }
 }
 
 // ---------------------------------------------------------------- gradients of the keys and values
 // A wave has 32 keys; the rows of all heads that share them go by, head after
 // head, in one order: no atomics, the same bits every time.
-template <class T, int DB, int NW>
+// KW: 4, all waves have the same 32 keys and take the rows in turn.
+template <class T, int DB, int KW, int NW>
 struct KeysShape {
   static constexpr int kThreads = NW * kWave;
-  static constexpr int kKeys = NW * 32;
+  static constexpr int kKeys = NW / KW * 32;
   // Of half types' widest heads the values are read from LDS each time: with them
   // in registers as well, 224 of 256 are taken and each read from LDS is waited for
   // (4 x 4096 x 16 x 128 bf16: 489, so 431 us).
-  static constexpr bool kValuesInLds = sizeof(T) == 2 && DB == 4;
-  static constexpr int kRows = !kValuesInLds && 64 * HeadShape<T, DB>::kRow <= 16 << 10 ? 64 : 32;  // of a tile
+  static constexpr bool kValuesInLds = sizeof(T) == 2 && DB == 4 && KW == 1;
+  static constexpr int kRows =
+      KW == 4 ? 128 : !kValuesInLds && 64 * HeadShape<T, DB>::kRow <= 16 << 10 ? 64 : 32;  // of a tile
   static constexpr int kTileBytes = kRows * HeadShape<T, DB>::kRow;
   static constexpr int kValueBytes = kValuesInLds ? kKeys * HeadShape<T, DB>::kRow : 0;
-  static constexpr int kRoom = (NW == 8 ? 128 << 10 : sizeof(T) == 4 || DB > 2 ? 64 << 10 : 48 << 10) - kValueBytes;
+  static constexpr int kRoom = (NW == 8 || KW == 4 ? 128 << 10 : sizeof(T) == 4 || DB > 2 ? 64 << 10 : 48 << 10) - kValueBytes;
   static constexpr int kBuffers = kRoom / (2 * kTileBytes) > 4 ? 4 : kRoom / (2 * kTileBytes);
   static constexpr int kLoads = 2 * kLoadsOfTile<HeadShape<T, DB>::kRow, kRows, kThreads> + 1;
+  static constexpr int kStats = kRows < kWave ? kWave : kRows;  // rows that there is room for
+  static constexpr int kJoin = KW == 1 ? 0 : JoinShape<DB>::kBytes;
+  static constexpr int kTiles = 2 * kBuffers * kTileBytes + kValueBytes;
+  static constexpr int kLds = kTiles > kJoin ? kTiles : kJoin;
 };
 // The probabilities of fp16 are rounded times 2^14: at most 1, most of a long row's
 // would be subnormal.
 template <class T>
 constexpr int kLift = kScaled<T> ? 14 : 0;
 
-template <class T, int DB, int NW>
-__global__ void __launch_bounds__(NW* kWave, sizeof(T) == 2 ? 2 : 1) attention_grad_kv(const AttentionParams p) {
-  using Shape = KeysShape<T, DB, NW>;
+template <class T, int DB, int KW, int NW>
+__global__ void __launch_bounds__(NW* kWave, sizeof(T) == 2 && KW == 1 ? 2 : 1) attention_grad_kv(const AttentionParams p) {
+  using Shape = KeysShape<T, DB, KW, NW>;
   using Head = HeadShape<T, DB>;
-  __shared__ __attribute__((aligned(1024))) char lds_[2 * Shape::kBuffers * Shape::kTileBytes + Shape::kValueBytes];
-  __shared__ __attribute__((aligned(16))) float stats[Shape::kBuffers][2][kWave];  // [lse, delta][row of the tile]
+  __shared__ __attribute__((aligned(1024))) char lds_[Shape::kLds];
+  __shared__ __attribute__((aligned(16))) float stats[Shape::kBuffers][2][Shape::kStats];  // [lse, delta][row of the tile]
   Lds* lds = (Lds*)lds_;
   __shared__ float nowhere[kWave];
   const uint32_t lds_at = lds_address(lds), stats_at = lds_address((Lds*)&stats[0][0][0]);
@@ -616,7 +681,7 @@ __global__ void __launch_bounds__(NW* kWave, sizeof(T) == 2 ? 2 : 1) attention_g
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
   const int chunks = p.dim / kPerChunk<T>;
   const int first_key = at.item * Shape::kKeys;
-  const int wave_key = first_key + wave * 32, key = wave_key + (lane & 31);
+  const int wave_key = first_key + (KW == 1 ? wave * 32 : 0), key = wave_key + (lane & 31);
   const bool live = key < seen.k_length;
   const int key_read = min(key, p.k_tokens - 1);
   Chunk k[Head::kSteps], v[Shape::kValuesInLds ? 1 : Head::kSteps];
@@ -649,16 +714,17 @@ __global__ void __launch_bounds__(NW* kWave, sizeof(T) == 2 ? 2 : 1) attention_g
     fetch_tile<Head::kRow, Shape::kRows, Shape::kThreads>(
         (const char*)p.d_out + (((int64_t)at.b * p.q_tokens + token) * p.heads + head) * p.dim * (int64_t)sizeof(T),
         dense_stride, count, chunks, to + Shape::kTileBytes);
-    // (rows that are not there arrive as zeros, and their queries and gradients with them; all but two waves
-    // load nothing, since loads are counted alike)
+    // 64 rows' statistics to a wave, lse or delta.  (Rows that are not there arrive as zeros, and their queries and
+    // gradients with them; waves that have none load nothing, since loads are counted alike.)
     const int64_t stat = ((int64_t)at.b * p.heads + head) * p.q_tokens + token;
-    load_words_to_lds(describe((wave ? p.delta : p.lse) + stat, count <= 0 || wave > 1 ? 0 : 4 * min(count, Shape::kRows)),
+    const int which = wave & 1, first = (wave >> 1) * kWave, some = first < Shape::kStats ? min(count, Shape::kRows) - first : 0;
+    load_words_to_lds(describe((which ? p.delta : p.lse) + stat + first, some <= 0 ? 0 : 4 * min(some, kWave)),
                       4 * (threadIdx.x & (kWave - 1)),
-                      wave > 1 ? nowhere_at : stats_at + (buffer * 2 + wave) * (kWave * 4));
+                      first < Shape::kStats ? stats_at + ((buffer * 2 + which) * Shape::kStats + first) * 4 : nowhere_at);
   };
   const int along_at = along_offset<Head::kRow>(), across_at = across_offset<T, Head::kRow>();
   Sums dk[DB] = {}, dv[DB] = {};
-  constexpr int kEarly = Shape::kBuffers - 1;
+  constexpr int kEarly = Shape::kBuffers > 1 ? Shape::kBuffers - 1 : 1;
   if (total > 0) {
     if constexpr (Shape::kValuesInLds)
       fetch_tile<Head::kRow, Shape::kKeys, Shape::kThreads>(v_from + (int64_t)first_key * p.v.token, p.v.token,
@@ -669,23 +735,24 @@ __global__ void __launch_bounds__(NW* kWave, sizeof(T) == 2 ? 2 : 1) attention_g
   }
   for (int n = 0, now = begin; n < total; ++n) {
     landed_for_all<(kEarly - 1) * Shape::kLoads>();
-    fetch();
+    if constexpr (Shape::kBuffers > 1) fetch();
     const int buffer = n % Shape::kBuffers;
     const Lds* q_tile = lds + buffer * 2 * Shape::kTileBytes;
     const Lds* d_tile = q_tile + Shape::kTileBytes;
     const int token = now * Shape::kRows;
     if (++now == end) now = begin;
 #pragma unroll
-    for (int b = 0; b < Shape::kRows / 32; ++b) {
-      Sums s = along<T, DB>(q_tile, fresh(along_at), 32 * b, k);
+    for (int b = 0; b < (KW == 1 ? Shape::kRows / 32 : 1); ++b) {
+      const int in_tile = KW == 1 ? 32 * b : 32 * wave;
+      Sums s = along<T, DB>(q_tile, fresh(along_at), in_tile, k);
       Sums ds;
-      if constexpr (Shape::kValuesInLds) ds = along_both<T, DB>(d_tile, v_tile, fresh(along_at), 32 * b, wave * 32);
-      else ds = along<T, DB>(d_tile, fresh(along_at), 32 * b, v);
+      if constexpr (Shape::kValuesInLds) ds = along_both<T, DB>(d_tile, v_tile, fresh(along_at), in_tile, wave * 32);
+      else ds = along<T, DB>(d_tile, fresh(along_at), in_tile, v);
       read_ahead<kAhead, kInstructions<T>, Head::kSteps, 1, Head::kSteps, Shape::kValuesInLds ? 2 : 1>();
       __builtin_amdgcn_sched_barrier(0);  // (the statistics' reads are none of these)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int first = 32 * b + row_of(4 * j);
+        const int first = in_tile + row_of(4 * j);
         const Vec<float, 4> lse = *reinterpret_cast<const Vec<float, 4>*>(&stats[buffer][0][first]);
         const Vec<float, 4> delta = *reinterpret_cast<const Vec<float, 4>*>(&stats[buffer][1][first]);
 #pragma unroll
@@ -696,33 +763,51 @@ __global__ void __launch_bounds__(NW* kWave, sizeof(T) == 2 ? 2 : 1) attention_g
           if constexpr (kScaled<T>) ds[r] *= up;
         }
       }
-      if (last_key(seen, token + 32 * b) < wave_key + 31 || token + 32 * b + 31 >= seen.q_length) {
+      if (last_key(seen, token + in_tile) < wave_key + 31 || token + in_tile + 31 >= seen.q_length) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          const bool hidden = key > last_key(seen, token + 32 * b + row_of(r));
+          const bool hidden = key > last_key(seen, token + in_tile + row_of(r));
           s[r] = hidden ? 0.0f : s[r];
           ds[r] = hidden ? 0.0f : ds[r];
         }
       }
-      across<T, DB>(dv, d_tile, fresh(across_at), 32 * b, s);
-      across<T, DB>(dk, q_tile, fresh(across_at), 32 * b, ds);
+      across<T, DB>(dv, d_tile, fresh(across_at), in_tile, s);
+      across<T, DB>(dk, q_tile, fresh(across_at), in_tile, ds);
       read_ahead<kAhead, kInstructions<T>, 2 * DB * kAcrossSteps<T>, kAcrossReads<T>>();
+    }
+    if constexpr (Shape::kBuffers == 1) {
+      landed_for_all();
+      fetch();
     }
   }
   landed_for_all();  // what was fetched past the end, too
-  if (key >= p.k_tokens) return;
-  const int64_t dense = (((int64_t)at.b * p.k_tokens + key) * p.kv_heads + at.kvh) * p.dim;
-  if (p.dk) store_row<T, DB>(static_cast<T*>(p.dk) + dense, dk, ldexpf(p.scale, -range), p.dim);
-  if (p.dv) store_row<T, DB>(static_cast<T*>(p.dv) + dense, dv, ldexpf(1.0f, -kLift<T>), p.dim);
+  const int64_t dense = (((int64_t)at.b * p.k_tokens + key_read) * p.kv_heads + at.kvh) * p.dim;
+  T *to_k = p.dk ? static_cast<T*>(p.dk) + dense : nullptr, *to_v = p.dv ? static_cast<T*>(p.dv) + dense : nullptr;
+  const float k_factor = ldexpf(p.scale, -range), v_factor = ldexpf(1.0f, -kLift<T>);
+  const bool there = key < p.k_tokens;
+  if constexpr (KW == 1) {
+    if (there && to_k) store_row<T, DB>(to_k, dk, k_factor, p.dim);
+    if (there && to_v) store_row<T, DB>(to_v, dv, v_factor, p.dim);
+  } else {
+    give_to_join<DB>(lds_, dk);
+    landed_for_all();
+    if (there && to_k)
+      take_joined<DB>(lds_, p.dim, [&](int c, Wide<4> sum) { store<T, 4>(to_k + c, narrow<T, 4>(sum * k_factor)); });
+    landed_for_all();
+    give_to_join<DB>(lds_, dv);
+    landed_for_all();
+    if (there && to_v)
+      take_joined<DB>(lds_, p.dim, [&](int c, Wide<4> sum) { store<T, 4>(to_v + c, narrow<T, 4>(sum * v_factor)); });
+  }
 }
 
 // ---------------------------------------------------------------- kernels of a type
 struct AttentionTable {
-  // [blocks of 32 elements - 1]; of rows' kernels the last index is 0: four waves of 32 rows, 1: eight, 2 (forward):
-  // four that share 32 rows.  NULL: there is none.
+  // [blocks of 32 elements - 1][0: four waves of 32 rows (or keys) each, 1: eight, 2: four that share 32].  NULL:
+  // there is none.
   const void* forward[4][3];
-  const void* grad_q[4][2];
-  const void* grad_kv[4][2];
+  const void* grad_q[4][3];
+  const void* grad_kv[4][3];
   const void* join;
   const void* norms;  // NULL: not needed
 };
@@ -731,13 +816,15 @@ void fill_attention_table(AttentionTable& t) {
   constexpr int k = DB - 1;
   t.forward[k][0] = (const void*)attention_forward<T, DB, 1, 4>;
   t.forward[k][2] = (const void*)attention_forward<T, DB, 4, 4>;
-  t.grad_q[k][0] = (const void*)attention_grad_q<T, DB, 4>;
-  t.grad_kv[k][0] = (const void*)attention_grad_kv<T, DB, 4>;
+  t.grad_q[k][0] = (const void*)attention_grad_q<T, DB, 1, 4>;
+  t.grad_q[k][2] = (const void*)attention_grad_q<T, DB, 4, 4>;
+  t.grad_kv[k][0] = (const void*)attention_grad_kv<T, DB, 1, 4>;
+  t.grad_kv[k][2] = (const void*)attention_grad_kv<T, DB, 4, 4>;
   t.forward[k][1] = t.grad_q[k][1] = t.grad_kv[k][1] = nullptr;
   if constexpr (sizeof(T) == 2 && DB > 2) {
     t.forward[k][1] = (const void*)attention_forward<T, DB, 1, 8>;
-    t.grad_q[k][1] = (const void*)attention_grad_q<T, DB, 8>;
-    t.grad_kv[k][1] = (const void*)attention_grad_kv<T, DB, 8>;
+    t.grad_q[k][1] = (const void*)attention_grad_q<T, DB, 1, 8>;
+    t.grad_kv[k][1] = (const void*)attention_grad_kv<T, DB, 1, 8>;
   }
 }
 template <class T>

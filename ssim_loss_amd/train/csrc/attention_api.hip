@@ -2,7 +2,6 @@
 // work, launches.
 
 #include "attention.hpp"
-#include <stdlib.h>
 
 namespace {
 
@@ -20,36 +19,43 @@ const AttentionTable& table_of(int dtype) {
   }
 }
 
-struct Plan {
-  int shape;  // of the forward: AttentionTable's index
-  int tiles, splits;
-  int q_shape, q_tiles, kv_shape, kv_tiles;  // of the backward
+// A kernel's shape (AttentionTable's index), and how many workgroups a (batch, key
+// head) takes: by its rows (queries of all heads that share the keys, or keys).
+struct Shape {
+  int shape, tiles;
+  int threads() const { return shape == 1 ? 512 : 256; }
 };
-
-// Eight waves to a workgroup where they are built and there is more than one for
-// every CU.
-int shape_of(const void* eight, int64_t rows, int64_t pairs) {
-  return eight && getenv("A8") && ceil_div(rows, 256) * pairs > kCUs ? 1 : 0;
+Shape shape_of(const void* const (&kernels)[3], int64_t rows, int64_t pairs, bool causal) {
+  // Where 32 rows to a workgroup do not fill the GPU, its waves take the other axis in
+  // turn: 2 x 257 x 6 x 64 fp32, gradients of queries XX us, of 128 rows XX.
+  if (rows <= 32 || ceil_div(rows, 32) * pairs <= kCUs) return {2, (int)ceil_div(rows, 32)};
+  // Eight waves: half the caches' traffic, but coarser.  1 x 16384 x 16 x 128 bf16,
+  // forward: 1948, of four waves 2044 us; causal, 4 x 4096: 183 and 156.
+  if (kernels[1] && !causal && ceil_div(rows, 256) * pairs >= 4 * kCUs) return {1, (int)ceil_div(rows, 256)};
+  return {0, (int)ceil_div(rows, 128)};
 }
+
+struct Plan {
+  Shape forward, grad_q, grad_kv;
+  int splits;  // of the forward's keys
+};
 
 Plan make_plan(const ssim_attention_inputs& in) {
   Plan p;
   const int64_t rows = in.q_tokens * (in.heads / in.kv_heads), pairs = in.batch * in.kv_heads;
   const AttentionTable& t = table_of(in.dtype);
   const int blocks = (in.dim - 1) / 32;
-  p.shape = rows <= 32 ? 2 : shape_of(t.forward[blocks][1], rows, pairs);
-  p.tiles = (int)ceil_div(rows, p.shape == 2 ? 32 : p.shape ? 256 : 128);
+  p.forward = shape_of(t.forward[blocks], rows, pairs, in.causal);
+  p.grad_q = shape_of(t.grad_q[blocks], rows, pairs, in.causal);
+  p.grad_kv = shape_of(t.grad_kv[blocks], in.k_tokens, pairs, in.causal);
   // Few workgroups: each takes a part of the keys, two tiles of them at least, and
   // a second launch joins the parts.
-  const int64_t groups = p.tiles * pairs, target = p.shape == 2 && in.dim > 64 ? kCUs : 2 * kCUs;
-  const int64_t most = ceil_div(in.k_tokens, p.shape == 2 ? 256 : 128);
+  const int64_t groups = p.forward.tiles * pairs;
+  const int64_t target = p.forward.shape == 2 && in.dim * elem_bytes(in.dtype) > 128 ? kCUs : 2 * kCUs;
+  const int64_t most = ceil_div(in.k_tokens, p.forward.shape == 2 ? 256 : 128);
   int64_t splits = groups > 0 ? target / groups : 1;
   if (splits > most) splits = most;
-  p.splits = splits < 1 || p.shape == 1 ? 1 : (int)splits;
-  p.q_shape = shape_of(t.grad_q[blocks][1], rows, pairs);
-  p.q_tiles = (int)ceil_div(rows, p.q_shape ? 256 : 128);
-  p.kv_shape = shape_of(t.grad_kv[blocks][1], in.k_tokens, pairs);
-  p.kv_tiles = (int)ceil_div(in.k_tokens, p.kv_shape ? 256 : 128);
+  p.splits = splits < 1 ? 1 : (int)splits;
   return p;
 }
 
@@ -76,8 +82,8 @@ int check_inputs(const ssim_attention_inputs* in) {
   if (in->batch > 1 << 24) return SSIM_ERR_OVERFLOW;
   const Plan p = make_plan(*in);
   const int64_t pairs = in->batch * in->kv_heads, rows = in->q_tokens * (in->heads / in->kv_heads);
-  if (rows >= (int64_t)1 << 31 || pairs > kMaxBlocks / kNormParts || pairs * p.tiles * p.splits > kMaxBlocks ||
-      pairs * p.q_tiles > kMaxBlocks || pairs * p.kv_tiles > kMaxBlocks ||
+  if (rows >= (int64_t)1 << 31 || pairs > kMaxBlocks / kNormParts || pairs * p.forward.tiles * p.splits > kMaxBlocks ||
+      pairs * p.grad_q.tiles > kMaxBlocks || pairs * p.grad_kv.tiles > kMaxBlocks ||
       in->batch * in->heads * in->q_tokens > (int64_t)1 << 36)
     return SSIM_ERR_OVERFLOW;
   return SSIM_OK;
@@ -114,7 +120,7 @@ AttentionParams params_of(const ssim_attention_inputs& in, const Plan& plan) {
   p.scale = (float)in.scale;
   p.scale2 = (float)(in.scale * 1.4426950408889634);
   p.splits = plan.splits;
-  p.tiles = plan.tiles;
+  p.tiles = plan.forward.tiles;
   return p;
 }
 
@@ -135,8 +141,8 @@ size_t ssim_attention_workspace_bytes(const ssim_attention_inputs* in) {
   return (rows_of(*in) * p.splits * (in->dim + 1) * 4 + 15) & ~(size_t)15;
 }
 
-int ssim_attention_forward(const ssim_attention_inputs* in, void* out, float* lse, void* workspace,
-                           void* stream) {
+int ssim_attention_forward(const ssim_attention_inputs* in, void* out, float* lse, void* rest,
+                           void* workspace, void* stream) {
   int rc = check_inputs(in);
   if (rc != SSIM_OK) return rc;
   if (in->batch == 0 || in->q_tokens == 0) return SSIM_OK;
@@ -148,8 +154,9 @@ int ssim_attention_forward(const ssim_attention_inputs* in, void* out, float* ls
                        {in->v, span(in->v_stride, *in, in->k_tokens, in->kv_heads), 16},
                        {in->q_lengths, 4 * (size_t)in->batch, 4},
                        {in->k_lengths, 4 * (size_t)in->batch, 4}};
-  const Array outs[] = {{out, rows * in->dim * bytes, bytes}, {lse, rows * 4, 4}, {workspace, ws, ws ? 16 : 1}};
-  rc = check_arrays(ins, 5, outs, 3);
+  const Array outs[] = {{out, rows * in->dim * bytes, bytes}, {lse, rows * 4, 4}, {rest, rows * in->dim * bytes, bytes},
+                        {workspace, ws, ws ? 16 : 1}};
+  rc = check_arrays(ins, 5, outs, 4);
   if (rc != SSIM_OK) return rc;
   rc = check_current_device();
   if (rc != SSIM_OK) return rc;
@@ -158,14 +165,15 @@ int ssim_attention_forward(const ssim_attention_inputs* in, void* out, float* ls
   AttentionParams p = params_of(*in, plan);
   p.out = out;
   p.lse = lse;
+  if (in->dtype != SSIM_DTYPE_F32) p.rest = rest;
   if (plan.splits > 1) {
     p.part_out = static_cast<float*>(workspace);
     p.part_lse = p.part_out + rows * plan.splits * in->dim;
   }
   const AttentionTable& t = table_of(in->dtype);
   const int blocks = (in->dim - 1) / 32;
-  rc = launch(t.forward[blocks][plan.shape], dim3((unsigned)(in->batch * in->kv_heads * plan.tiles * plan.splits)),
-              plan.shape == 1 ? 512 : 256, p, stream);
+  rc = launch(t.forward[blocks][plan.forward.shape],
+              dim3((unsigned)(in->batch * in->kv_heads * plan.forward.tiles * plan.splits)), plan.forward.threads(), p, stream);
   if (rc != SSIM_OK || plan.splits == 1) return rc;
   return launch(t.join, dim3((unsigned)ceil_div(rows, kAttentionThreads / kWave)), kAttentionThreads, p, stream);
 }
@@ -176,7 +184,7 @@ size_t ssim_attention_backward_workspace_bytes(const ssim_attention_inputs* in) 
 }
 
 int ssim_attention_backward(const ssim_attention_inputs* in, const void* out, const float* lse,
-                            const void* d_out, void* dq, void* dk, void* dv, void* workspace,
+                            const void* rest, const void* d_out, void* dq, void* dk, void* dv, void* workspace,
                             void* stream) {
   int rc = check_inputs(in);
   if (rc != SSIM_OK) return rc;
@@ -184,7 +192,7 @@ int ssim_attention_backward(const ssim_attention_inputs* in, const void* out, co
   const bool any_q = in->q_tokens > 0, any_k = in->k_tokens > 0;
   if (!(any_q && dq) && !(any_k && (dk || dv))) return SSIM_OK;
   if (((any_q || ssim_attention_backward_workspace_bytes(in) > 0) && !workspace) ||
-      (any_q && (!in->q || !out || !lse || !d_out)) || (any_k && (!in->k || !in->v)))
+      (any_q && (!in->q || !out || !lse || !d_out || (in->dtype != SSIM_DTYPE_F32 && !rest))) || (any_k && (!in->k || !in->v)))
     return SSIM_ERR_NULL;
   const int bytes = elem_bytes(in->dtype);
   const size_t rows = rows_of(*in), keys = (size_t)in->batch * in->k_tokens * in->kv_heads * in->dim * bytes;
@@ -196,10 +204,11 @@ int ssim_attention_backward(const ssim_attention_inputs* in, const void* out, co
                        {in->k_lengths, 4 * (size_t)in->batch, 4},
                        {out, rows * in->dim * bytes, 16},
                        {lse, rows * 4, 4},
+                       {rest, rows * in->dim * bytes, 16},
                        {d_out, rows * in->dim * bytes, 16}};
   const Array outs[] = {{dq, rows * in->dim * bytes, bytes}, {dk, keys, bytes}, {dv, keys, bytes},
                         {workspace, ws, ws ? 16 : 1}};
-  rc = check_arrays(ins, 8, outs, 4);
+  rc = check_arrays(ins, 9, outs, 4);
   if (rc != SSIM_OK) return rc;
   rc = check_current_device();
   if (rc != SSIM_OK) return rc;
@@ -207,6 +216,7 @@ int ssim_attention_backward(const ssim_attention_inputs* in, const void* out, co
   const Plan plan = make_plan(*in);
   AttentionParams p = params_of(*in, plan);
   p.o = out;
+  p.o_rest = rest;
   p.lse = const_cast<float*>(lse);
   p.d_out = d_out;
   p.delta = static_cast<float*>(workspace);
@@ -222,13 +232,13 @@ int ssim_attention_backward(const ssim_attention_inputs* in, const void* out, co
     if (rc != SSIM_OK) return rc;
   }
   if (any_q) {  // (it forms delta for the other kernel)
-    p.tiles = plan.q_tiles;
-    rc = launch(t.grad_q[blocks][plan.q_shape], dim3(pairs * plan.q_tiles), plan.q_shape ? 512 : 256, p, stream);
+    p.tiles = plan.grad_q.tiles;
+    rc = launch(t.grad_q[blocks][plan.grad_q.shape], dim3(pairs * plan.grad_q.tiles), plan.grad_q.threads(), p, stream);
     if (rc != SSIM_OK) return rc;
   }
   if (!any_k || !(dk || dv)) return SSIM_OK;
-  p.tiles = plan.kv_tiles;
-  return launch(t.grad_kv[blocks][plan.kv_shape], dim3(pairs * plan.kv_tiles), plan.kv_shape ? 512 : 256, p, stream);
+  p.tiles = plan.grad_kv.tiles;
+  return launch(t.grad_kv[blocks][plan.grad_kv.shape], dim3(pairs * plan.grad_kv.tiles), plan.grad_kv.threads(), p, stream);
 }
 
 }  // extern "C"

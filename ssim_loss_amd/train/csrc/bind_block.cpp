@@ -235,7 +235,7 @@ struct AttentionCall {
 };
 
 struct AttentionBackward : torch::autograd::Node {
-  static constexpr int kTensors = 7;  // q, k, v, the lengths, out, lse
+  static constexpr int kTensors = 8;  // q, k, v, the lengths, out, lse, rest
   SavedVariable saved[kTensors];
   AttentionPlan plan;
 
@@ -266,7 +266,7 @@ struct AttentionBackward : torch::autograd::Node {
     if ((uintptr_t)d_out.const_data_ptr() % 16 != 0) d_out = dense_copy(d_out, dev);
     const c10::DataPtr ws = scratch(ssim_attention_backward_workspace_bytes(&call.in));
     const int rc = ssim_attention_backward(&call.in, t[5].const_data_ptr(), t[6].const_data_ptr<float>(),
-                                           d_out.const_data_ptr(), grads[0], grads[1], grads[2], ws.get(), stream_of(dev));
+                                           t[7].defined() ? t[7].const_data_ptr() : nullptr, d_out.const_data_ptr(), grads[0], grads[1], grads[2], ws.get(), stream_of(dev));
     TORCH_CHECK(rc == SSIM_OK, "ssim_attention_backward: ", text(rc));
     return out;
   }
@@ -311,12 +311,13 @@ Tensor attention(const py::object& q_, const py::object& k_, const py::object& v
     check_capture(edges, dev, "attention");
   }
   const AttentionCall call(q, k, v, q_lengths, k_lengths, plan, dev);
-  Tensor out = fresh(q.sizes(), q.scalar_type(), dev), lse;
+  Tensor out = fresh(q.sizes(), q.scalar_type(), dev), lse, rest;
   if (wants) lse = fresh({q.size(0), q.size(2), q.size(1)}, at::kFloat, dev);
+  if (wants && q.scalar_type() != at::kFloat) rest = fresh(q.sizes(), q.scalar_type(), dev);
   const size_t bytes = ssim_attention_workspace_bytes(&call.in);
   const c10::DataPtr ws = bytes ? scratch(bytes) : c10::DataPtr();
-  const int rc = ssim_attention_forward(&call.in, out.data_ptr(), wants ? lse.data_ptr<float>() : nullptr, ws.get(),
-                                        stream_of(dev));
+  const int rc = ssim_attention_forward(&call.in, out.data_ptr(), wants ? lse.data_ptr<float>() : nullptr,
+                                        rest.defined() ? rest.data_ptr() : nullptr, ws.get(), stream_of(dev));
   if (rc != SSIM_OK) raise(rc, "ssim_attention_forward");
   if (wants) {
     std::shared_ptr<AttentionBackward> node(new AttentionBackward(), torch::autograd::deleteNode);
@@ -328,6 +329,7 @@ Tensor attention(const py::object& q_, const py::object& k_, const py::object& v
       if (tensors[n]->defined()) node->saved[n] = SavedVariable(*tensors[n], false);
     node->saved[5] = SavedVariable(out, true);
     node->saved[6] = SavedVariable(lse, false);
+    if (rest.defined()) node->saved[7] = SavedVariable(rest, false);
   }
   return out;
 }

@@ -261,18 +261,20 @@ size_t ssim_attention_workspace_bytes(const ssim_attention_inputs* in);
 
 /* out: [batch, q_tokens, heads, dim], contiguous; lse: NULL, or fp32
  * [batch, heads, q_tokens] for the backward (log2 of the sum of exp(s_ij), plus
- * infinity for a query without keys).  workspace may be NULL where it needs none. */
-int ssim_attention_forward(const ssim_attention_inputs* in, void* out, float* lse, void* workspace,
-                           void* stream);
+ * infinity for a query without keys); rest: NULL, or an array as out for the
+ * backward, what out's rounding left (fp32: not looked at).  workspace may be NULL
+ * where it needs none. */
+int ssim_attention_forward(const ssim_attention_inputs* in, void* out, float* lse, void* rest,
+                           void* workspace, void* stream);
 
 /* Bytes of the backward's workspace (16-byte aligned).  Host-only. */
 size_t ssim_attention_backward_workspace_bytes(const ssim_attention_inputs* in);
 
-/* The gradients for d_out, laid out as out; out and lse are the forward's for the
- * same inputs.  dq, dk, dv: contiguous, of q's, k's and v's shapes; each may be
+/* The gradients for d_out, laid out as out; out, lse and rest (fp32: not looked at)
+ * are the forward's for the same inputs, and these and d_out are aligned to 16 bytes.  dq, dk, dv: contiguous, of q's, k's and v's shapes; each may be
  * NULL: not wanted.  No atomics: the same bits every time. */
 int ssim_attention_backward(const ssim_attention_inputs* in, const void* out, const float* lse,
-                            const void* d_out, void* dq, void* dk, void* dv, void* workspace,
+                            const void* rest, const void* d_out, void* dq, void* dk, void* dv, void* workspace,
                             void* stream);
 
 /* ---------------------------------------------------------------------------

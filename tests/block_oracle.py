@@ -118,7 +118,8 @@ class Attention:
                 dv_off = (p * (rel_p + 2 * n * heads * U)).t() @ do.abs() + (tiny * 2.0 ** -14 + LEAST) * (seen.double().t() @ do.abs()) + LEAST
                 dp, dp_mag = do @ V.t(), do.abs() @ V.abs().t()
                 delta, delta_mag = (do * o).sum(1, keepdim=True), (do * o).abs().sum(1, keepdim=True)
-                o_err = (do.abs() * (o_off + rounding(o, dtype))).sum(1, keepdim=True)
+                # (delta takes the output with what its rounding left)
+                o_err = (do.abs() * (o_off + (t * t if t else U) * o.abs() + TINY[dtype])).sum(1, keepdim=True)
                 ds = p * (dp - delta)
                 ds_off = p * ((dp.abs() + delta.abs()) * (rel_p + 4 * U) + 2 * dim * U * (dp_mag + delta_mag) + o_err)
                 ds_off = ds_off + t * ds.abs() + torch.where(seen, tiny + LEAST * (1 + dp.abs() + delta.abs()), 0.0)
