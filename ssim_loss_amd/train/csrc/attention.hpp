@@ -53,7 +53,9 @@ struct AttentionParams {
 template <class T, int DB>
 struct HeadShape {
   static constexpr int kBytes = DB * 32 * (int)sizeof(T);
-  static constexpr int kRow = kBytes <= 128 ? 128 : kBytes <= 256 ? 256 : 512;  // in LDS
+  // In LDS.  (192 where 256 left room for two workgroups to a CU, not three: 4 x 1025 x
+  // 16 x 72 fp16 54.8, so XX us.)
+  static constexpr int kRow = kBytes <= 128 ? 128 : kBytes == 192 ? 192 : kBytes <= 256 ? 256 : 512;
   static constexpr int kSteps = DB * 32 / kPerStep<T>;
 };
 // a block of 32 rows as an operand: so many steps, of so many registers of a tile
@@ -90,21 +92,18 @@ __device__ __forceinline__ Where where(const AttentionParams& p, int items) {
 template <int kRow, int kTile, int kThreads = kAttentionThreads>
 __device__ __forceinline__ void fetch_tile(const char* from, uint32_t stride, int rows, int chunks, uint32_t to) {
   constexpr int kChunksOfRow = kRow / 16;
-  constexpr int kRowsAtOnce = kThreads / kChunksOfRow;
-  static_assert(kTile % kRowsAtOnce == 0, "whole instructions");
-  const int row = threadIdx.x / kChunksOfRow;
+  static_assert(kTile * kChunksOfRow % kThreads == 0, "whole instructions");
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const uint32_t size = rows <= 0 ? 0u : (uint32_t)(min(rows, kTile) - 1) * stride + (uint32_t)chunks * 16u;
   const Descriptor d = describe(from, size);
 #pragma unroll
-  for (int j = 0; j < kTile / kRowsAtOnce; ++j) {
-    const int r = row + j * kRowsAtOnce;
-    const int chunk = (threadIdx.x % kChunksOfRow) ^ swizzle<kRow>(r);
+  for (int j = 0; j < kTile * kChunksOfRow / kThreads; ++j) {
+    const int slot = j * kThreads + threadIdx.x, r = slot / kChunksOfRow;
+    const int chunk = (slot % kChunksOfRow) ^ swizzle<kRow>(r);
     const uint32_t offset = chunk < chunks ? (uint32_t)r * stride + (uint32_t)chunk * 16u : kNowhere;
-    load_to_lds(d, offset, to + (uint32_t)(j * kRowsAtOnce * kRow + wave * (kWave * 16)));
+    load_to_lds(d, offset, to + (uint32_t)(j * kThreads * 16 + wave * (kWave * 16)));
   }
 }
-
 template <int kRow, int kTile, int kThreads>
 constexpr int kLoadsOfTile = kTile * kRow / (kThreads * 16);  // a wave's
 
@@ -233,8 +232,8 @@ __device__ __forceinline__ void take_joined(const char* lds, int dim, Take take)
 //
 // Tiles of keys are loaded kBuffers - 1 ahead.  Eight waves with four buffers, one
 // workgroup to a CU, ask the caches for half of what two workgroups of four waves do
-// and wait less for it (heads of 65 to 128 in a half type with rows enough:
-// 16384 x 16 x 128 bf16 2080, so 1900 us).
+// and wait less for it (heads of 97 to 128 in a half type with rows enough:
+// 16384 x 16 x 128 bf16 2044, so 1948 us).
 template <class T, int DB, int KW, int NW>
 struct ForwardShape {
   static constexpr int kThreads = NW * kWave;
@@ -821,7 +820,7 @@ void fill_attention_table(AttentionTable& t) {
   t.grad_kv[k][0] = (const void*)attention_grad_kv<T, DB, 1, 4>;
   t.grad_kv[k][2] = (const void*)attention_grad_kv<T, DB, 4, 4>;
   t.forward[k][1] = t.grad_q[k][1] = t.grad_kv[k][1] = nullptr;
-  if constexpr (sizeof(T) == 2 && DB > 2) {
+  if constexpr (sizeof(T) == 2 && DB == 4) {
     t.forward[k][1] = (const void*)attention_forward<T, DB, 1, 8>;
     t.grad_q[k][1] = (const void*)attention_grad_q<T, DB, 1, 8>;
     t.grad_kv[k][1] = (const void*)attention_grad_kv<T, DB, 1, 8>;

@@ -48,11 +48,11 @@ Plan make_plan(const ssim_attention_inputs& in) {
   p.forward = shape_of(t.forward[blocks], rows, pairs, in.causal);
   p.grad_q = shape_of(t.grad_q[blocks], rows, pairs, in.causal);
   p.grad_kv = shape_of(t.grad_kv[blocks], in.k_tokens, pairs, in.causal);
-  // Few workgroups: each takes a part of the keys, two tiles of them at least, and
-  // a second launch joins the parts.
+  // Few workgroups: each takes a part of the keys, 512 of them at least, and a second
+  // launch joins the parts.
   const int64_t groups = p.forward.tiles * pairs;
   const int64_t target = p.forward.shape == 2 && in.dim * elem_bytes(in.dtype) > 128 ? kCUs : 2 * kCUs;
-  const int64_t most = ceil_div(in.k_tokens, p.forward.shape == 2 ? 256 : 128);
+  const int64_t most = in.k_tokens / 512;
   int64_t splits = groups > 0 ? target / groups : 1;
   if (splits > most) splits = most;
   p.splits = splits < 1 ? 1 : (int)splits;

@@ -57,14 +57,22 @@ __device__ __forceinline__ Chunk operand_of(const Sums& c, int first) {
   }
 }
 
-// ---- tiles in LDS: rows of kRow bytes (a power of two, 128 or more), whose
+// ---- tiles in LDS: rows of kRow bytes (192 or a power of two, 128 or more), whose
 // chunks are permuted within 256 bytes by the row's number: neither 16 rows'
 // chunks of one column (read as they lie) nor 64 bytes of each of 4 rows (read
-// transposed) meet in a bank.
+// transposed) meet in a bank.  (Rows of 192 bytes begin 64 apart by themselves.)
 template <int kRow>
 __device__ __forceinline__ int swizzle(int row) {
   if constexpr (kRow == 128) return ((row >> 1 & 1) << 2) | (row >> 2 & 3);
+  else if constexpr (kRow == 192) return row >> 2 & 3;
   else return ((row & 3) << 2) | (row >> 2 & 3);
+}
+// an offset `bytes` along a row from `offset`, in the first chunks of its row; only where rows begin at multiples of
+// 256 bytes are the higher bits permuted, too
+template <int kRow>
+__device__ __forceinline__ int along_row(int offset, int bytes) {
+  if constexpr (kRow == 192) return (offset ^ (bytes & 63)) + (bytes & ~63);
+  else return offset ^ bytes;
 }
 template <int kRow>
 __device__ __forceinline__ int place(int row, int chunk) {  // byte offset of a chunk
@@ -77,7 +85,7 @@ __device__ __forceinline__ Chunk lds_chunk(const Lds* p, int at) {
   return *reinterpret_cast<const __attribute__((address_space(3))) Chunk*>(p + at);
 }
 
-// Where a lane reads: its offsets in a tile (at a multiple of kRow), of which the
+// Where a lane reads: its offsets in a tile (at a multiple of 256 or kRow), of which the
 // other reads' are an exclusive or and a constant away.  Left to itself the compiler
 // keeps each of them in a register through a loop; fresh() makes it form them
 // anew, one instruction each.
@@ -93,7 +101,7 @@ __device__ __forceinline__ int along_offset() {
 }
 template <int kRow>
 __device__ __forceinline__ Chunk lds_along(const Lds* tile, int offset, int row, int t) {
-  return lds_chunk(tile, (offset ^ (t << 5)) + row * kRow);
+  return lds_chunk(tile, along_row<kRow>(offset, t << 5) + row * kRow);
 }
 
 // The operand whose rows are columns of the tile: lane's column 32 block +
@@ -122,13 +130,13 @@ __device__ __forceinline__ Chunk lds_across(const Lds* tile, int offset, int row
   } else {
     typedef __attribute__((address_space(3))) Quad* At;
     constexpr int kTurned = kPlain ? 1 << 4 : 1 << 5, kNext = kPlain ? 4 : 8;
-    const int at = offset ^ (block << 6);
+    const int at = along_row<kRow>(offset, block << 6);
     union {
       Quad q[2];
       Chunk c;
     } u;
     u.q[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((At)(tile + at + row * kRow));
-    u.q[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((At)(tile + (at ^ kTurned) + (row + kNext) * kRow));
+    u.q[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((At)(tile + along_row<kRow>(offset ^ kTurned, block << 6) + (row + kNext) * kRow));
     return u.c;
   }
 }
