@@ -35,9 +35,12 @@ struct GatedParams {
   void* dx;             // [rows][width]
   void* dw[2];          // [hidden][width]
   void* db[2];
-  // tiles of the product; parts of its summed axis, each with a sum of its own
-  int m_tiles, n_tiles, splits;
-  float* part;          // [splits][rows of the result][width]
+  // Of the products (Product; two gradients may be one launch's, that of x first):
+  // tiles; parts of the summed axis, and where their sums go, [splits][rows of the
+  // result][width]
+  int m_tiles[3], n_tiles[3], splits[3];
+  float* part[3];
+  int x_blocks;
   // copies of x and the weights
   const void* from[3];
   void* to[3];
@@ -101,43 +104,46 @@ __device__ __forceinline__ void act_slope(float g, int act, float& a, float& slo
 
 enum Product { kForward, kGradX, kGradW };
 
-constexpr int kDepthBytes = 128;  // of the summed axis in a tile
+constexpr int kDepthBytes = 128;  // of the summed axis, by which the host counts
 
-// A tile of kBlocksM x kBlocksN blocks of 32 x 32 to a wave, kWavesM x kWavesN waves.
-template <class T, int BM, int BN, int WM, int WN>
+// A product's tiles: BM x BN blocks of 32 x 32 to a wave, WM x WN waves, kDepthOf
+// bytes of the summed axis at a time, kStages of them in LDS.
+template <class T, int BM, int BN, int WM, int WN, int kDepthOf, int kStages_>
 struct ProductShape {
   static constexpr int kThreads = WM * WN * kWave;
   static constexpr int kM = BM * WM * 32, kN = BN * WN * 32;
-  static constexpr int kDepth = kDepthBytes / (int)sizeof(T);
+  static constexpr int kRow = kDepthOf;
+  static constexpr int kDepth = kDepthOf / (int)sizeof(T);
   static constexpr int kSteps = kDepth / kPerStep<T>;
-  static constexpr int kABytes = kM * kDepthBytes, kBBytes = kN * kDepthBytes;
+  static constexpr int kStages = kStages_;
+  static constexpr int kABytes = kM * kDepthOf, kBBytes = kN * kDepthOf, kBytes = kABytes + kBBytes;
+  static constexpr int kLoads = kBytes / (kThreads * 16);  // a wave's, of a stage
 };
 
-// An operand's tile whose rows are contiguous along the summed axis: kRows rows,
-// 128 bytes each.  `from` is the first row's first byte of the tile; `chunks` are
-// left of the axis.
-template <int kRows, int kThreads>
+// An operand's tile whose rows are contiguous along the summed axis: kRows rows of
+// kRow bytes.  `from` is the first row's first byte of the tile; `chunks` are left of
+// the axis.
+template <int kRows, int kRow, int kThreads>
 __device__ __forceinline__ void fetch_along(const char* from, int64_t pitch, int64_t rows, int chunks, uint32_t to) {
-  constexpr int kAtOnce = kThreads / 8;
+  constexpr int kChunks = kRow / 16, kAtOnce = kThreads / kChunks;
+  static_assert(kRows % kAtOnce == 0, "whole instructions");
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int count = (int)(rows < kRows ? rows : kRows);
+  const int count = chunks <= 0 ? 0 : (int)(rows < kRows ? rows : kRows);
   const Descriptor d =
-      describe(from, count <= 0 ? 0u : (uint32_t)(count - 1) * (uint32_t)pitch + (uint32_t)min(chunks, 8) * 16u);
+      describe(from, count <= 0 ? 0u : (uint32_t)(count - 1) * (uint32_t)pitch + (uint32_t)min(chunks, kChunks) * 16u);
 #pragma unroll
   for (int j = 0; j < kRows / kAtOnce; ++j) {
-    const int r = threadIdx.x / 8 + j * kAtOnce;
-    const int chunk = (threadIdx.x & 7) ^ swizzle<128>(r);
+    const int r = threadIdx.x / kChunks + j * kAtOnce;
+    const int chunk = (threadIdx.x % kChunks) ^ swizzle<kRow>(r);
     const uint32_t offset = chunk < chunks ? (uint32_t)r * (uint32_t)pitch + (uint32_t)chunk * 16u : kNowhere;
-    load_to_lds(d, offset, to + (uint32_t)(j * kAtOnce * 128 + wave * 1024));
+    load_to_lds(d, offset, to + (uint32_t)(j * kThreads * 16 + wave * 1024));
   }
 }
-// An operand's tile whose rows lie along the other axis: kDepth rows of kColumns
-// elements; `chunks` are left of such a row, `rows` of the summed axis.
-template <class T, int kColumns, int kThreads>
+// An operand's tile whose rows lie along the other axis: kDepth rows of kRow bytes;
+// `chunks` are left of such a row, `rows` of the summed axis.
+template <int kDepth, int kRow, int kThreads>
 __device__ __forceinline__ void fetch_across(const char* from, int64_t pitch, int64_t rows, int64_t chunks, uint32_t to) {
-  constexpr int kRow = kColumns * (int)sizeof(T), kChunks = kRow / 16;
-  constexpr int kDepth = kDepthBytes / (int)sizeof(T);
-  constexpr int kAtOnce = kThreads / kChunks;
+  constexpr int kChunks = kRow / 16, kAtOnce = kThreads / kChunks;
   static_assert(kAtOnce >= 1 && kDepth % kAtOnce == 0, "whole instructions");
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int count = (int)(rows < kDepth ? rows : kDepth), left = (int)(chunks < kChunks ? chunks : kChunks);
@@ -147,17 +153,17 @@ __device__ __forceinline__ void fetch_across(const char* from, int64_t pitch, in
     const int r = threadIdx.x / kChunks + j * kAtOnce;
     const int chunk = (threadIdx.x % kChunks) ^ swizzle<kRow>(r);
     const uint32_t offset = chunk < left ? (uint32_t)r * (uint32_t)pitch + (uint32_t)chunk * 16u : kNowhere;
-    load_to_lds(d, offset, to + (uint32_t)(j * kAtOnce * kRow + wave * 1024));
+    load_to_lds(d, offset, to + (uint32_t)(j * kThreads * 16 + wave * 1024));
   }
 }
 
 // The workgroup's tile.  Ids go round the XCDs; each XCD takes a run of tiles that
-// go down eight rows of tiles at a time, so that its cache holds their operands.
+// go down four rows of tiles at a time, so that its cache holds their operands (eight: 2% longer).
 struct TileAt {
   int m, n;
 };
 __device__ __forceinline__ TileAt tile_at(unsigned block, int m_tiles, int n_tiles) {
-  constexpr unsigned kGroup = 8;
+  constexpr unsigned kGroup = 4;
   const unsigned total = (unsigned)m_tiles * n_tiles, per = (total + 7) / 8, rest = total - (per - 1) * 8;
   const unsigned xcd = block & 7, j = block >> 3;
   // (the first `rest` XCDs have a tile more where 8 does not divide the tiles)
@@ -226,15 +232,14 @@ __device__ __forceinline__ void store_four(T* row, int64_t column, int64_t width
     if (column + k < width) row[column + k] = n[k];
 }
 
-template <class T, int kProduct, int BM, int BN, int WM, int WN>
-__global__ void __launch_bounds__(WM* WN* kWave, WM* WN == 4 ? 2 : 1) gated_product(const GatedParams p) {
-  // (the smallest tiles leave room for more workgroups than bounds ask for)
-  using Shape = ProductShape<T, BM, BN, WM, WN>;
-  __shared__ __attribute__((aligned(1024))) char lds_[2 * (Shape::kABytes + Shape::kBBytes)];
+template <class T, int kProduct, int BM, int BN, int WM, int WN, int kDepthOf, int kStages>
+__device__ __forceinline__ void product_tile(const GatedParams& p, unsigned block, char* lds_) {
+  using Shape = ProductShape<T, BM, BN, WM, WN, kDepthOf, kStages>;
   Lds* lds = (Lds*)lds_;
   const uint32_t lds_at = lds_address(lds);
-  const int split = kProduct == kForward ? 0 : blockIdx.x % p.splits;
-  const TileAt at = tile_at(kProduct == kForward ? blockIdx.x : blockIdx.x / p.splits, p.m_tiles, p.n_tiles);
+  const int splits = p.splits[kProduct], n_tiles = p.n_tiles[kProduct];
+  const int split = kProduct == kForward ? 0 : block % splits;
+  const TileAt at = tile_at(kProduct == kForward ? block : block / splits, p.m_tiles[kProduct], n_tiles);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
   const int wm = wave % WM, wn = wave / WM, h = lane >> 5;
   constexpr int kBytes = (int)sizeof(T);
@@ -243,39 +248,41 @@ __global__ void __launch_bounds__(WM* WN* kWave, WM* WN == 4 ? 2 : 1) gated_prod
   // how many tiles of the summed axis there are
   const int64_t depth = kProduct == kForward ? p.width_ext : kProduct == kGradX ? p.h_pitch : p.rows;
   const int once = (int)((depth + Shape::kDepth - 1) / Shape::kDepth);
-  const int whole = kProduct == kGradX ? 2 * once : once, each = (whole + p.splits - 1) / p.splits;
+  const int whole = kProduct == kGradX ? 2 * once : once, each = (whole + splits - 1) / splits;
   const int begin = kProduct == kForward ? 0 : min(split * each, whole);
   const int end = kProduct == kForward ? whole : min(begin + each, whole);
-  const int n_half = p.n_tiles / 2;  // gradients of weights: gate's tiles, then up's
+  const int n_half = n_tiles / 2;  // gradients of weights: gate's tiles, then up's
   const int which = kProduct == kGradW ? (at.n >= n_half) : 0;
   if (kProduct == kGradW && !p.dw[which]) return;
   const int64_t m0 = (int64_t)at.m * (kProduct == kForward ? kHalfM : Shape::kM);
   const int64_t n0 = (int64_t)(kProduct == kGradW ? at.n - which * n_half : at.n) * Shape::kN;
 
   auto fetch = [&](int t) {
-    const uint32_t a_to = lds_at + (t & 1) * (Shape::kABytes + Shape::kBBytes), b_to = a_to + Shape::kABytes;
+    // (none past the end: their loads are counted all the same)
+    const uint32_t a_to = lds_at + ((t - begin) % kStages) * Shape::kBytes, b_to = a_to + Shape::kABytes;
+    const bool there = t < end;
     if constexpr (kProduct == kForward) {
       const int64_t k = (int64_t)t * Shape::kDepth;
-      const int chunks = (int)((p.width_ext - k) / kPerChunk<T>);
+      const int chunks = there ? (int)((p.width_ext - k) / kPerChunk<T>) : 0;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        fetch_along<kHalfM, Shape::kThreads>((const char*)p.w[i] + (m0 * p.w_pitch + k) * kBytes, p.w_pitch * kBytes,
+        fetch_along<kHalfM, Shape::kRow, Shape::kThreads>((const char*)p.w[i] + (m0 * p.w_pitch + k) * kBytes, p.w_pitch * kBytes,
                                              p.hidden - m0, chunks, a_to + i * (kHalfM * 128));
-      fetch_along<Shape::kN, Shape::kThreads>((const char*)p.x + (n0 * p.x_pitch + k) * kBytes, p.x_pitch * kBytes,
+      fetch_along<Shape::kN, Shape::kRow, Shape::kThreads>((const char*)p.x + (n0 * p.x_pitch + k) * kBytes, p.x_pitch * kBytes,
                                               p.rows - n0, chunks, b_to);
     } else if constexpr (kProduct == kGradX) {
       const int i = t >= once;
       const int64_t k = (int64_t)(t - i * once) * Shape::kDepth;
-      fetch_across<T, Shape::kM, Shape::kThreads>((const char*)p.w[i] + (k * p.w_pitch + m0) * kBytes, p.w_pitch * kBytes,
-                                                  p.hidden - k, (p.width_ext - m0 + kPerChunk<T> - 1) / kPerChunk<T>, a_to);
-      fetch_along<Shape::kN, Shape::kThreads>((const char*)p.d[i] + (n0 * p.h_pitch + k) * kBytes, p.h_pitch * kBytes,
-                                              p.rows - n0, (int)((p.h_pitch - k) / kPerChunk<T>), b_to);
+      fetch_across<Shape::kDepth, Shape::kM * kBytes, Shape::kThreads>((const char*)p.w[i] + (k * p.w_pitch + m0) * kBytes, p.w_pitch * kBytes,
+                                                  there ? p.hidden - k : 0, (p.width_ext - m0 + kPerChunk<T> - 1) / kPerChunk<T>, a_to);
+      fetch_along<Shape::kN, Shape::kRow, Shape::kThreads>((const char*)p.d[i] + (n0 * p.h_pitch + k) * kBytes, p.h_pitch * kBytes,
+                                              p.rows - n0, there ? (int)((p.h_pitch - k) / kPerChunk<T>) : 0, b_to);
     } else {
       const int64_t k = (int64_t)t * Shape::kDepth;
-      fetch_across<T, Shape::kM, Shape::kThreads>((const char*)p.x + (k * p.x_pitch + m0) * kBytes, p.x_pitch * kBytes,
-                                                  p.rows - k, (p.width_ext - m0 + kPerChunk<T> - 1) / kPerChunk<T>, a_to);
-      fetch_across<T, Shape::kN, Shape::kThreads>((const char*)p.d[which] + (k * p.h_pitch + n0) * kBytes,
-                                                  p.h_pitch * kBytes, p.rows - k, (p.h_pitch - n0) / kPerChunk<T>, b_to);
+      fetch_across<Shape::kDepth, Shape::kM * kBytes, Shape::kThreads>((const char*)p.x + (k * p.x_pitch + m0) * kBytes, p.x_pitch * kBytes,
+                                                  there ? p.rows - k : 0, (p.width_ext - m0 + kPerChunk<T> - 1) / kPerChunk<T>, a_to);
+      fetch_across<Shape::kDepth, Shape::kN * kBytes, Shape::kThreads>((const char*)p.d[which] + (k * p.h_pitch + n0) * kBytes,
+                                                  p.h_pitch * kBytes, there ? p.rows - k : 0, (p.h_pitch - n0) / kPerChunk<T>, b_to);
     }
   };
 
@@ -285,13 +292,16 @@ __global__ void __launch_bounds__(WM* WN* kWave, WM* WN == 4 ? 2 : 1) gated_prod
     if constexpr (kProduct == kForward) return i < BM / 2 ? wm * (BM / 2) + i : kHalfM / 32 + wm * (BM / 2) + i - BM / 2;
     else return wm * BM + i;
   };
-  const int a_at = kProduct == kForward ? along_offset<128>() : across_offset<T, Shape::kM * kBytes, true>();
-  const int b_at = kProduct == kGradW ? across_offset<T, Shape::kN * kBytes, true>() : along_offset<128>();
-  if (begin < end) fetch(begin);
+  const int a_at = kProduct == kForward ? along_offset<Shape::kRow>() : across_offset<T, Shape::kM * kBytes, true>();
+  const int b_at = kProduct == kGradW ? across_offset<T, Shape::kN * kBytes, true>() : along_offset<Shape::kRow>();
+  if (begin < end) {
+#pragma unroll
+    for (int t = 0; t < kStages - 1; ++t) fetch(begin + t);
+  }
   for (int t = begin; t < end; ++t) {
-    landed_for_all();
-    if (t + 1 < end) fetch(t + 1);
-    const Lds* a_tile = lds + (t & 1) * (Shape::kABytes + Shape::kBBytes);
+    landed_for_all<(kStages - 2) * Shape::kLoads>();
+    fetch(t + kStages - 1);
+    const Lds* a_tile = lds + ((t - begin) % kStages) * Shape::kBytes;
     const Lds* b_tile = a_tile + Shape::kABytes;
 #pragma unroll
     for (int s = 0; s < Shape::kSteps; ++s) {
@@ -299,7 +309,7 @@ __global__ void __launch_bounds__(WM* WN* kWave, WM* WN == 4 ? 2 : 1) gated_prod
 #pragma unroll
       for (int i = 0; i < BM; ++i) {
         if constexpr (kProduct == kForward)
-          a[i] = lds_along<128>(a_tile, a_at, 32 * a_block(i), s);
+          a[i] = lds_along<Shape::kRow>(a_tile, a_at, 32 * a_block(i), s);
         else
           a[i] = lds_across<T, Shape::kM * kBytes, true>(a_tile, a_at, s * kPerStep<T>, a_block(i));
       }
@@ -308,7 +318,7 @@ __global__ void __launch_bounds__(WM* WN* kWave, WM* WN == 4 ? 2 : 1) gated_prod
         if constexpr (kProduct == kGradW)
           b[i] = lds_across<T, Shape::kN * kBytes, true>(b_tile, b_at, s * kPerStep<T>, wn * BN + i);
         else
-          b[i] = lds_along<128>(b_tile, b_at, 32 * (wn * BN + i), s);
+          b[i] = lds_along<Shape::kRow>(b_tile, b_at, 32 * (wn * BN + i), s);
       }
 #pragma unroll
       for (int i = 0; i < BM; ++i)
@@ -318,7 +328,7 @@ __global__ void __launch_bounds__(WM* WN* kWave, WM* WN == 4 ? 2 : 1) gated_prod
   }
 
   landed_for_all();  // the tiles' place is the waves' own now
-  Lds* region = lds + wave * (int)(sizeof(lds_) / (WM * WN));
+  Lds* region = lds + wave * (kStages * Shape::kBytes / (WM * WN));
   const int64_t row0 = n0 + 32 * wn * BN;
   if constexpr (kProduct == kForward) {
     constexpr int MB = BM / 2;
@@ -361,8 +371,8 @@ __global__ void __launch_bounds__(WM* WN* kWave, WM* WN == 4 ? 2 : 1) gated_prod
         const Sums& s = c[i0 + i][j];
         return Wide<4>{s[4 * k], s[4 * k + 1], s[4 * k + 2], s[4 * k + 3]};
       };
-      if (p.splits > 1) {
-        float* to = p.part + ((int64_t)split * (kProduct == kGradW ? 2 : 1) + which) * rows * p.width;
+      if (splits > 1) {
+        float* to = p.part[kProduct] + ((int64_t)split * (kProduct == kGradW ? 2 : 1) + which) * rows * p.width;
         store_block<float, MB, BN>(region, to, p.width, row0, column0, rows, p.width, value);
       } else {
         T* to = static_cast<T*>(kProduct == kGradX ? p.dx : p.dw[which]);
@@ -372,29 +382,71 @@ __global__ void __launch_bounds__(WM* WN* kWave, WM* WN == 4 ? 2 : 1) gated_prod
   }
 }
 
-// The parts of a product together: `arrays` results beside each other in each part.
+template <class T, int kProduct, int BM, int BN, int WM, int WN, int kDepthOf, int kStages>
+__global__ void __launch_bounds__(WM* WN* kWave, WM* WN == 4 ? 2 : 1) gated_product(const GatedParams p) {
+  __shared__ __attribute__((aligned(1024))) char lds[kStages * ProductShape<T, BM, BN, WM, WN, kDepthOf, kStages>::kBytes];
+  product_tile<T, kProduct, BM, BN, WM, WN, kDepthOf, kStages>(p, blockIdx.x, lds);
+}
+// Both gradients' small tiles in one launch: neither fills the GPU for long.
 template <class T>
-__global__ void __launch_bounds__(256) gated_join(const GatedParams p) {
-  // dx, or dWg and dWu
-  const bool weights = p.dw[0] || p.dw[1];
-  const int64_t n = (weights ? (int64_t)p.hidden : p.rows) * p.width, arrays = weights ? 2 : 1;
-  const int which = blockIdx.y;
-  T* to = static_cast<T*>(weights ? p.dw[which] : p.dx);
-  if (!to) return;
+__global__ void __launch_bounds__(256, 2) gated_both(const GatedParams p) {
+  __shared__ __attribute__((aligned(1024))) char lds[3 * ProductShape<T, 1, 1, 2, 2, 128, 3>::kBytes];
+  if ((int)blockIdx.x < p.x_blocks) product_tile<T, kGradX, 1, 1, 2, 2, 128, 3>(p, blockIdx.x, lds);
+  else product_tile<T, kGradW, 1, 1, 2, 2, 128, 3>(p, blockIdx.x - p.x_blocks, lds);
+}
+
+// `splits` parts of n elements, `step` apart, together.
+template <class T>
+__device__ __forceinline__ void join_parts(const float* part, T* to, int64_t n, int64_t step, int splits) {
   for (int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; at < n; at += (int64_t)gridDim.x * 256 * 4) {
-    const float* from = p.part + which * n + at;
+    const float* from = part + at;
     if (at + 4 <= n) {
       Wide<4> sum = load<float, 4>(from);
 #pragma unroll 4
-      for (int s = 1; s < p.splits; ++s) sum += load<float, 4>(from + s * arrays * n);
+      for (int s = 1; s < splits; ++s) sum += load<float, 4>(from + s * step);
       store<T, 4>(to + at, narrow<T, 4>(sum));
     } else {
       for (int k = 0; at + k < n; ++k) {
         float sum = from[k];
-        for (int s = 1; s < p.splits; ++s) sum += from[s * arrays * n + k];
+        for (int s = 1; s < splits; ++s) sum += from[s * step + k];
         to[at + k] = (T)sum;
       }
     }
+  }
+}
+// The blocks' sums of a bias together: 64 columns at a time, a quarter of the blocks
+// to each wave.
+template <class T>
+__device__ __forceinline__ void bias_sums(const GatedParams& p, int i) {
+  __shared__ double sums[4][kWave];
+  const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
+  for (int64_t first = (int64_t)blockIdx.x * kWave; first < p.hidden; first += (int64_t)gridDim.x * kWave) {
+    const int64_t column = first + lane;
+    double sum = 0.0;
+    if (column < p.hidden) {
+#pragma unroll 8
+      for (int b = wave; b < p.row_blocks; b += 4) sum += p.part_bias[((int64_t)b * 2 + i) * p.hidden + column];
+    }
+    sums[wave][lane] = sum;
+    __syncthreads();
+    if (wave == 0 && column < p.hidden)
+      static_cast<T*>(p.db[i])[column] = (T)(float)(((sums[0][lane] + sums[1][lane]) + sums[2][lane]) + sums[3][lane]);
+    __syncthreads();
+  }
+}
+// What is left of the gradients, blockIdx.y: the parts of dx, dWg, dWu; the biases.
+template <class T>
+__global__ void __launch_bounds__(256) gated_finish(const GatedParams p) {
+  const int64_t x = p.rows * p.width, w = (int64_t)p.hidden * p.width;
+  const int what = blockIdx.y;
+  if (what == 0) {
+    if (p.dx && p.splits[kGradX] > 1) join_parts<T>(p.part[kGradX], static_cast<T*>(p.dx), x, x, p.splits[kGradX]);
+  } else if (what <= 2) {
+    const int i = what - 1;
+    if (p.dw[i] && p.splits[kGradW] > 1)
+      join_parts<T>(p.part[kGradW] + i * w, static_cast<T*>(p.dw[i]), w, 2 * w, p.splits[kGradW]);
+  } else if (p.db[what - 3]) {
+    bias_sums<T>(p, what - 3);
   }
 }
 
@@ -450,24 +502,6 @@ __global__ void __launch_bounds__(256) gated_slopes(const GatedParams p) {
       const float s = ((total[i][k] + sums[0][i][k * kWave + lane]) + sums[1][i][k * kWave + lane]) + sums[2][i][k * kWave + lane];
       if (column + k < p.hidden) p.part_bias[((int64_t)blockIdx.y * 2 + i) * p.hidden + column + k] = s;
     }
-}
-
-// 64 columns to a workgroup, a quarter of the blocks to each wave.
-template <class T>
-__global__ void __launch_bounds__(256) gated_bias_sums(const GatedParams p) {
-  __shared__ double sums[4][kWave];
-  const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1), i = blockIdx.y;
-  const int64_t column = (int64_t)blockIdx.x * kWave + lane;
-  double sum = 0.0;
-  if (column < p.hidden) {
-#pragma unroll 8
-    for (int b = wave; b < p.row_blocks; b += 4) sum += p.part_bias[((int64_t)b * 2 + i) * p.hidden + column];
-  }
-  sums[wave][lane] = sum;
-  __syncthreads();
-  if (wave > 0 || column >= p.hidden || !p.db[i]) return;
-  sum = ((sums[0][lane] + sums[1][lane]) + sums[2][lane]) + sums[3][lane];
-  static_cast<T*>(p.db[i])[column] = (T)(float)sum;
 }
 
 // Rows of `width` elements to rows of width_ext, zeros behind them.
@@ -593,28 +627,28 @@ struct GatedTable {
   const void* product[3][3];  // [Product][tiles of 64, 128, 256 rows]
   const void* few[3];         // 16, 32, 64 rows
   const void* slopes;
-  const void* bias_sums;
-  const void* join;
+  const void* both;
+  const void* finish;
   const void* copy;
 };
 template <class T>
 GatedTable make_gated_table() {
   GatedTable t;
-  t.product[kForward][0] = (const void*)gated_product<T, kForward, 2, 1, 2, 2>;
-  t.product[kForward][1] = (const void*)gated_product<T, kForward, 2, 2, 2, 2>;
-  t.product[kForward][2] = (const void*)gated_product<T, kForward, 4, 2, 2, 4>;
-  t.product[kGradX][0] = (const void*)gated_product<T, kGradX, 1, 1, 2, 2>;
-  t.product[kGradX][1] = (const void*)gated_product<T, kGradX, 2, 2, 2, 2>;
-  t.product[kGradX][2] = (const void*)gated_product<T, kGradX, 4, 2, 2, 4>;
-  t.product[kGradW][0] = (const void*)gated_product<T, kGradW, 1, 1, 2, 2>;
-  t.product[kGradW][1] = (const void*)gated_product<T, kGradW, 2, 2, 2, 2>;
-  t.product[kGradW][2] = (const void*)gated_product<T, kGradW, 4, 2, 2, 4>;
+  t.product[kForward][0] = (const void*)gated_product<T, kForward, 2, 1, 2, 2, 128, 3>;
+  t.product[kForward][1] = (const void*)gated_product<T, kForward, 2, 2, 2, 2, 128, 2>;
+  t.product[kForward][2] = (const void*)gated_product<T, kForward, 4, 2, 2, 4, 64, 4>;
+  t.product[kGradX][0] = (const void*)gated_product<T, kGradX, 1, 1, 2, 2, 128, 3>;
+  t.product[kGradX][1] = (const void*)gated_product<T, kGradX, 2, 2, 2, 2, 128, 2>;
+  t.product[kGradX][2] = (const void*)gated_product<T, kGradX, 4, 2, 2, 4, 64, 4>;
+  t.product[kGradW][0] = (const void*)gated_product<T, kGradW, 1, 1, 2, 2, 128, 3>;
+  t.product[kGradW][1] = (const void*)gated_product<T, kGradW, 2, 2, 2, 2, 128, 2>;
+  t.product[kGradW][2] = (const void*)gated_product<T, kGradW, 4, 2, 2, 4, 64, 4>;
   t.few[0] = (const void*)gated_few_rows<T, 1>;
   t.few[1] = (const void*)gated_few_rows<T, 2>;
   t.few[2] = (const void*)gated_few_rows<T, 4>;
   t.slopes = (const void*)gated_slopes<T>;
-  t.bias_sums = (const void*)gated_bias_sums<T>;
-  t.join = (const void*)gated_join<T>;
+  t.both = (const void*)gated_both<T>;
+  t.finish = (const void*)gated_finish<T>;
   t.copy = (const void*)gated_copy<T>;
   return t;
 }

@@ -3,6 +3,8 @@
 
 #include "gated.hpp"
 
+#include <algorithm>
+
 namespace {
 
 using namespace ssim_train;
@@ -103,6 +105,7 @@ struct Choice {
   int tiles;  // 0: 64, 1: 128, 2: 256
   int splits;
   int64_t m_tiles, n_tiles;
+  int64_t blocks() const { return m_tiles * n_tiles * splits; }
 };
 constexpr int kMaxSplits = 16;
 
@@ -117,7 +120,7 @@ Choice choose(const ssim_gated_linear_inputs& in, int product) {
   struct {
     int m, n, at_once;
     double rate;
-  } const shapes[3] = {{product == kForward ? 128 : 64, 64, 2, 0.5}, {128, 128, 2, 0.85}, {256, 256, 1, 1.0}};
+  } const shapes[3] = {{product == kForward ? 128 : 64, 64, product == kForward ? 2 : 3, 0.5}, {128, 128, 2, 0.85}, {256, 256, 1, 1.0}};
   constexpr double kEnds = 4.0;
   // (in fp32 the matrix instructions take 16 times as long for the same bytes, and memory is far from it)
   const double unit = elem_bytes(in.dtype) == 4 ? 8.0 : 1.0;
@@ -149,20 +152,17 @@ size_t part_bytes(const ssim_gated_linear_inputs& in, int product) {
   return to_16((size_t)(product == kGradW ? 2 * in.hidden : in.rows) * in.width * c.splits * 4);
 }
 
-int launch_product(const ssim_gated_linear_inputs& in, const GatedTable& t, GatedParams p, int product, void* part,
-                   void* stream) {
-  const Choice c = choose(in, product);
-  p.m_tiles = (int)c.m_tiles;
-  p.n_tiles = (int)c.n_tiles;
-  p.splits = c.splits;
-  p.part = static_cast<float*>(part);
-  if (product == kGradX) p.dw[0] = p.dw[1] = nullptr;
-  const int64_t blocks = c.m_tiles * c.n_tiles * c.splits;
-  if (blocks > 1 << 22) return SSIM_ERR_OVERFLOW;
-  const int rc = launch(t.product[product][c.tiles], dim3((unsigned)blocks), c.tiles == 2 ? 512 : 256, p, stream);
-  if (rc != SSIM_OK || c.splits == 1) return rc;
-  const int64_t n = (product == kGradW ? in.hidden : in.rows) * in.width, groups = ceil_div(n, 1024);
-  return launch(t.join, dim3((unsigned)(groups < 4 * kCUs ? groups : 4 * kCUs), product == kGradW ? 2 : 1), 256, p, stream);
+void set_product(GatedParams& p, const Choice& c, int product, void* part) {
+  p.m_tiles[product] = (int)c.m_tiles;
+  p.n_tiles[product] = (int)c.n_tiles;
+  p.splits[product] = c.splits;
+  p.part[product] = static_cast<float*>(part);
+}
+constexpr int64_t kMaxBlocks = 1 << 22;
+
+int launch_product(const GatedTable& t, GatedParams& p, const Choice& c, int product, void* stream) {
+  if (c.blocks() > kMaxBlocks) return SSIM_ERR_OVERFLOW;
+  return launch(t.product[product][c.tiles], dim3((unsigned)c.blocks()), c.tiles == 2 ? 512 : 256, p, stream);
 }
 
 struct Slopes {
@@ -181,16 +181,17 @@ Slopes slopes_of(const ssim_gated_linear_inputs& in) {
 
 struct BackwardSpace {
   Copies copies;
-  size_t d, bias, part, total;
+  size_t d, bias, part[3], total;
 };
 BackwardSpace space_of(const ssim_gated_linear_inputs& in) {
   BackwardSpace s;
   s.copies = copies_of(in);
   s.d = (size_t)in.rows * padded(in, in.hidden) * elem_bytes(in.dtype);
   s.bias = to_16((size_t)slopes_of(in).row_blocks * 2 * in.hidden * 4);
-  const size_t x = part_bytes(in, kGradX), w = part_bytes(in, kGradW);
-  s.part = x > w ? x : w;  // one after the other
-  s.total = s.copies.x + 2 * s.copies.w + 2 * s.d + s.bias + s.part;
+  s.part[kForward] = 0;
+  s.part[kGradX] = part_bytes(in, kGradX);
+  s.part[kGradW] = part_bytes(in, kGradW);
+  s.total = s.copies.x + 2 * s.copies.w + 2 * s.d + s.bias + s.part[kGradX] + s.part[kGradW];
   return s;
 }
 
@@ -243,7 +244,9 @@ int ssim_gated_linear_forward(const ssim_gated_linear_inputs* in, void* out, flo
   char* at = static_cast<char*>(workspace);
   rc = make_copies(*in, copies_of(*in), t, p, at, stream);
   if (rc != SSIM_OK) return rc;
-  return launch_product(*in, t, p, kForward, nullptr, stream);
+  const Choice c = choose(*in, kForward);
+  set_product(p, c, kForward, nullptr);
+  return launch_product(t, p, c, kForward, stream);
 }
 
 size_t ssim_gated_linear_backward_workspace_bytes(const ssim_gated_linear_inputs* in) {
@@ -306,17 +309,25 @@ int ssim_gated_linear_backward(const ssim_gated_linear_inputs* in, const float* 
     rc = launch(t.slopes, dim3(s.column_blocks, s.row_blocks), 256, p, stream);
     if (rc != SSIM_OK) return rc;
   }
-  if (biases) {
-    rc = launch(t.bias_sums, dim3((unsigned)ceil_div(in->hidden, 64), 2), 256, p, stream);
-    if (rc != SSIM_OK) return rc;
+  char* part = at + 2 * space.d + space.bias;
+  const Choice x = choose(*in, kGradX), w = choose(*in, kGradW);
+  set_product(p, x, kGradX, part);
+  set_product(p, w, kGradW, part + space.part[kGradX]);
+  const bool x_wanted = grads->x && rows;
+  if (x_wanted && weights && x.tiles == 0 && w.tiles == 0 && x.blocks() + w.blocks() <= kMaxBlocks) {
+    p.x_blocks = (int)x.blocks();
+    rc = launch(t.both, dim3((unsigned)(x.blocks() + w.blocks())), 256, p, stream);
+  } else {
+    if (x_wanted) rc = launch_product(t, p, x, kGradX, stream);
+    if (rc == SSIM_OK && weights) rc = launch_product(t, p, w, kGradW, stream);
   }
-  void* part = rows ? at + 2 * space.d + space.bias : nullptr;
-  if (grads->x && rows) {
-    rc = launch_product(*in, t, p, kGradX, part, stream);
-    if (rc != SSIM_OK) return rc;
-  }
-  if (weights) return launch_product(*in, t, p, kGradW, part, stream);
-  return SSIM_OK;
+  if (rc != SSIM_OK) return rc;
+  const bool join_x = x_wanted && x.splits > 1, join_w = weights && w.splits > 1;
+  if (!join_x && !join_w && !biases) return SSIM_OK;
+  int64_t groups = ceil_div(in->hidden, kWave);
+  if (join_x) groups = std::max(groups, ceil_div(in->rows * in->width, 1024));
+  if (join_w) groups = std::max(groups, ceil_div(in->hidden * in->width, 1024));
+  return launch(t.finish, dim3((unsigned)std::min<int64_t>(groups, 4 * kCUs), 5), 256, p, stream);
 }
 
 }  // extern "C"

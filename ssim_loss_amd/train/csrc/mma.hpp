@@ -57,21 +57,21 @@ __device__ __forceinline__ Chunk operand_of(const Sums& c, int first) {
   }
 }
 
-// ---- tiles in LDS: rows of kRow bytes (192 or a power of two, 128 or more), whose
+// ---- tiles in LDS: rows of kRow bytes (192 or a power of two, 64 or more), whose
 // chunks are permuted within 256 bytes by the row's number: neither 16 rows'
 // chunks of one column (read as they lie) nor 64 bytes of each of 4 rows (read
-// transposed) meet in a bank.  (Rows of 192 bytes begin 64 apart by themselves.)
+// transposed) meet in a bank.  (Rows of 192 and 64 bytes begin 64 apart by themselves.)
 template <int kRow>
 __device__ __forceinline__ int swizzle(int row) {
   if constexpr (kRow == 128) return ((row >> 1 & 1) << 2) | (row >> 2 & 3);
-  else if constexpr (kRow == 192) return row >> 2 & 3;
+  else if constexpr (kRow == 192 || kRow == 64) return row >> 2 & 3;
   else return ((row & 3) << 2) | (row >> 2 & 3);
 }
 // an offset `bytes` along a row from `offset`, in the first chunks of its row; only where rows begin at multiples of
 // 256 bytes are the higher bits permuted, too
 template <int kRow>
 __device__ __forceinline__ int along_row(int offset, int bytes) {
-  if constexpr (kRow == 192) return (offset ^ (bytes & 63)) + (bytes & ~63);
+  if constexpr (kRow == 192 || kRow == 64) return (offset ^ (bytes & 63)) + (bytes & ~63);
   else return offset ^ bytes;
 }
 template <int kRow>
