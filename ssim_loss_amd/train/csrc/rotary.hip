@@ -231,8 +231,8 @@ int check_inputs(const ssim_rotary_inputs* in) {
   if (sum > in->dim) return SSIM_ERR_SHAPE;
   if (!strides_ok(in->q_stride, 3) || !strides_ok(in->position_stride, 2) || (in->k && !strides_ok(in->k_stride, 3)))
     return SSIM_ERR_SHAPE;
-  if (in->batch > 0 && in->tokens > ((int64_t)1 << 46) / in->batch / 65536 / SSIM_ROTARY_MAX_DIM)
-    return SSIM_ERR_OVERFLOW;
+  const int64_t heads = in->k && in->k_heads > in->q_heads ? in->k_heads : in->q_heads;
+  if (in->batch > 0 && in->tokens > ((int64_t)1 << 44) / in->batch / (heads * in->dim)) return SSIM_ERR_OVERFLOW;
   return SSIM_OK;
 }
 
@@ -316,6 +316,8 @@ extern "C" int ssim_rotary(const ssim_rotary_inputs* in, void* q_out, void* k_ou
   const int64_t groups = ceil_div(n, at_once);
   if (groups * parts < 2 * kCUs) parts = ceil_div(2 * kCUs, groups);
   if (parts > ceil_div(of_token * at_once, kThreads)) parts = ceil_div(of_token * at_once, kThreads);
+  constexpr int64_t kMaxBlocks = ((int64_t)1 << 32) / kThreads - 1;
+  if (groups * parts > kMaxBlocks) parts = ceil_div(of_token * at_once, 64 * kThreads * kUnits);  // (longer workgroups)
   p.heads_of_part = (int)ceil_div(heads, parts);
   p.head_parts = (int)ceil_div(heads, p.heads_of_part);
   auto inverse_of = [](int64_t d) { return d == 1 ? 0u : (unsigned)((((uint64_t)1 << 32) + d - 1) / d); };
@@ -323,7 +325,7 @@ extern "C" int ssim_rotary(const ssim_rotary_inputs* in, void* q_out, void* k_ou
   p.by_heads = inverse_of(p.heads_of_part);
   p.by_pairs = inverse_of(p.pairs);
   const int64_t blocks = groups * p.head_parts;
-  if (blocks > 0x7fffffff / kThreads * 2) return SSIM_ERR_OVERFLOW;
+  if (blocks > kMaxBlocks) return SSIM_ERR_OVERFLOW;
   const void* kernel = in->dtype == SSIM_DTYPE_F32   ? kernel_of<F32>(v, halves)
                        : in->dtype == SSIM_DTYPE_F16 ? kernel_of<F16>(v, halves)
                                                      : kernel_of<BF16>(v, halves);
