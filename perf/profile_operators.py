@@ -1,15 +1,18 @@
-"""Times and profiles of the training operators over the cases of operators.py.
+"""Times and profiles of the training operators over the cases of operators.py,
+or, with --block, of the operators inside a block over those of more_operators.py.
 
-  python3 perf/profile_operators.py --time [--only NAME,NAME]
+  python3 perf/profile_operators.py [--block] --time [--only NAME,NAME]
         microseconds of a pass among others, and captured in a graph where the
         pass can be; inputs change from pass to pass
-  python3 perf/profile_operators.py --profile DIR
+  python3 perf/profile_operators.py [--block] --profile DIR
         the rocprofv3 passes, each a child with a time limit of its own
-  python3 perf/profile_operators.py --summarize DIR
-        profiles/train_operators_*.md from what --profile left in DIR
+  python3 perf/profile_operators.py [--block] --summarize DIR
+        profiles/train_operators_*.md (block_operators_*.md) from what --profile
+        left in DIR
 """
 import argparse
 import csv
+import importlib
 import os
 import re
 import statistics
@@ -23,34 +26,43 @@ sys.path.insert(0, ROOT)
 TRACED, COUNTED = 30, 6  # passes of a case in the trace, in a counter run
 SEEDS = 3
 COUNTERS = {"fetch": ["FETCH_SIZE"], "write": ["WRITE_SIZE"], "sq": ["SQ_INSTS_VALU"]}
+BLOCK = False  # the operators inside a block
+MATRIX, ACTIVE = "SQ_VALU_MFMA_BUSY_CYCLES", "GRBM_GUI_ACTIVE"
+SIMDS, XCDS = 1024, 8
 FETCH_UNIT = 2.0  # a large copy reads this many bytes for each that the counter names
 CUS = 256
 
 
-def cases(only=None):
-    from perf import operators
+def module():
+    return importlib.import_module("perf.more_operators" if BLOCK else "perf.operators")
 
+
+def counters():
+    return {**COUNTERS, "sq": [*COUNTERS["sq"], MATRIX, ACTIVE]} if BLOCK else COUNTERS
+
+
+def cases(only=None):
+    operators = module()
     operators.own = True
     return [c for c in operators.listed() if not only or c["name"] in only]
 
 
 def large():
     """The cases whose traffic counts: 10 MB and more."""
-    from perf import operators
-
+    operators = module()
     return [c["name"] for c in cases() if operators.work(c)["bytes"] >= 10e6]
 
 
 def states(case):
-    from perf import operators
-
+    operators = module()
     return [operators.prepare(case, seed) for seed in range(SEEDS)]
 
 
 def run_cases(names, passes):
     """The profiled program."""
     import torch
-    from perf import operators
+
+    operators = module()
 
     for case in cases(names):
         made = states(case)
@@ -83,7 +95,8 @@ def best_of(call, passes, rounds=5):
 def captured(made):
     """A graph of five passes for each state."""
     import torch
-    from perf import operators
+
+    operators = module()
 
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -102,8 +115,7 @@ def captured(made):
 
 
 def time_cases(names):
-    from perf import operators
-
+    operators = module()
     for case in cases(names):
         made = states(case)
         eager = best_of(lambda k: operators.run(made[k % SEEDS]), 60)
@@ -120,16 +132,26 @@ def profile(outdir):
 
     def run(name, limit, options, names, passes):
         command = ["timeout", "-s", "KILL", str(limit), "rocprofv3", *options, "--output-format", "csv", "-d",
-                   os.path.join(outdir, name), "-o", "t", "--", "python3", me, "--run", ",".join(names), str(passes)]
+                   os.path.join(outdir, name), "-o", "t", "--", "python3", me, *(["--block"] if BLOCK else []), "--run", ",".join(names), str(passes)]
         print(name, flush=True)
         subprocess.run(command, check=True)
 
     run("trace", 100, ["--kernel-trace", "--stats"], [c["name"] for c in cases()], TRACED)
-    for name, counters in COUNTERS.items():
-        run(name, 60, ["--pmc", *counters], large(), COUNTED)
+    for name, some in counters().items():
+        run(name, 60, ["--pmc", *some], large(), COUNTED)
 
 
 def kernel_of(row):
+    if BLOCK:
+        name = row["Kernel_Name"]
+        found = re.search(r"attention_(?:forward|join|norms|grad_kv|grad_q)|gated_(?:product|both|finish|slopes|few_rows|copy)|"
+                          r"rotary_kernel", name)
+        if not found or found[0] != "gated_product":
+            return found and found[0]
+        # (the tool writes the second product's name with its type and number garbled)
+        which = re.search(r"gated_product(?:I(?:DF16b|DF16_|f)Li|<float, )(\d)", name)
+        return "gated_product, " + ("forward", "gradient of x", "gradients of weights")[int(which[1]) if which else
+                                                                                       2 if "EL, int" in name else 1]
     found = re.search(r"ssim_(?:grad_norm|norm_only|clip|adamw|block_norm)\w*?_kernel", row["Kernel_Name"])
     return found and found[0]
 
@@ -156,8 +178,7 @@ def read(outdir, name, file, order):
 
 
 def summarize(outdir):
-    from perf import operators
-
+    operators = module()
     times, lines = {}, []
     trace = read(outdir, "trace", "t_kernel_trace.csv", "Start_Timestamp")
     for case, launches in by_case(trace, [c["name"] for c in cases()]).items():
@@ -172,10 +193,11 @@ def summarize(outdir):
             lines.append("| %s | %s | %d | %.2f | %.2f | %d x %s, %d | %s | %s |" % (
                 case, kernel, len(us), times[case, kernel], min(us), int(r["Grid_Size_X"]) // threads,
                 r["Grid_Size_Y"], threads, r["VGPR_Count"], r["Scratch_Size"]))
-    with open(os.path.join(PROFILES, "train_operators_kernel_trace.md"), "w") as f:
-        f.write(f"""# Kernel times of the training operators (rocprofv3 --kernel-trace), MI355X
+    what, file = ("operators inside a block", "block") if BLOCK else ("training operators", "train")
+    with open(os.path.join(PROFILES, file + "_operators_kernel_trace.md"), "w") as f:
+        f.write(f"""# Kernel times of the {what} (rocprofv3 --kernel-trace), MI355X
 
-By `perf/profile_operators.py`: one process, each case of `perf/operators.py` {TRACED} times over {SEEDS} sets
+By `perf/profile_operators.py`: one process, each case of `perf/{module().__name__[5:]}.py` {TRACED} times over {SEEDS} sets
 of inputs in turn. Times in microseconds. Profiled kernels of a few microseconds read 0.3 to 1 us
 longer than unprofiled ones.
 
@@ -184,7 +206,7 @@ longer than unprofiled ones.
 """ + "\n".join(lines) + "\n")
 
     counts = {}
-    for name in COUNTERS:
+    for name in counters():
         for case, launches in by_case(read(outdir, name, "t_counter_collection.csv", "Dispatch_Id"), large()).items():
             found = {}
             for kernel, row in launches:
@@ -204,29 +226,38 @@ longer than unprofiled ones.
             lines.append("| %s | %s | %.1f | %.1f | %.0f | %.2f |" % (
                 case, kernel, fetched, written, (fetched + written) / us * 1e3,
                 counts[case, kernel, "SQ_INSTS_VALU"] / CUS / (us * 1e3)))
-        lines.append("| %s | all; the case needs %.1f | %.1f | | | |" % (case, need[case], total))
-    with open(os.path.join(PROFILES, "train_operators_counters.md"), "w") as f:
-        f.write(f"""# Traffic and vector instructions of the training operators (rocprofv3 --pmc), MI355X
+            if BLOCK:
+                busy, active = (counts[case, kernel, c] for c in (MATRIX, ACTIVE))
+                lines[-1] += " %.0f%% | %.2f |" % (100 * busy / SIMDS / (active / XCDS), active / XCDS / us / 1e3)
+        lines.append("| %s | all; the case needs %.1f | %.1f | | | |" % (case, need[case], total) + " | |" * BLOCK)
+    matrix = """ The share of the kernel's
+cycles in which a matrix instruction runs, over all SIMDs, and the cycles in GHz of its time in the trace (the
+counter run's own is a little longer).""" if BLOCK else ""
+    more = (" matrix | GHz |", "---|---|") if BLOCK else ("", "")
+    with open(os.path.join(PROFILES, file + "_operators_counters.md"), "w") as f:
+        f.write(f"""# Traffic and vector instructions of the {what} (rocprofv3 --pmc), MI355X
 
 By `perf/profile_operators.py`. FETCH_SIZE (times {FETCH_UNIT:g}, as a copy calibrates it) and WRITE_SIZE in MB
 per call of a kernel (between the L2s and the memory side, whose 256 MB cache answers some of it), their
-sum over the kernel's median time in `train_operators_kernel_trace.md` in GB/s, and vector wave
+sum over the kernel's median time in `{file}_operators_kernel_trace.md` in GB/s, and vector wave
 instructions per compute unit and nanosecond (streams of them reach 3.2 to 4.1). Each counter in a run of
-its own, over {SEEDS} sets of inputs in turn, {COUNTED} times a case.
+its own, over {SEEDS} sets of inputs in turn, {COUNTED} times a case.{matrix}
 
-| case | kernel | read MB | written MB | GB/s | VALU per CU per ns |
-|---|---|---|---|---|---|
+| case | kernel | read MB | written MB | GB/s | VALU per CU per ns |{more[0]}
+|---|---|---|---|---|---|{more[1]}
 """ + "\n".join(lines) + "\n")
 
 
 if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
+    ap.add_argument("--block", action="store_true", help="the operators inside a block")
     ap.add_argument("--time", action="store_true")
     ap.add_argument("--only", default="", help="cases of --time, by name (default: all)")
     ap.add_argument("--profile", metavar="DIR")
     ap.add_argument("--summarize", metavar="DIR")
     ap.add_argument("--run", nargs=2, metavar=("CASES", "PASSES"), help=argparse.SUPPRESS)
     a = ap.parse_args()
+    BLOCK = a.block
     if a.run:
         run_cases(a.run[0].split(","), int(a.run[1]))
     elif a.time:

@@ -54,7 +54,7 @@ template <class T, int DB>
 struct HeadShape {
   static constexpr int kBytes = DB * 32 * (int)sizeof(T);
   // In LDS.  (192 where 256 left room for two workgroups to a CU, not three: 4 x 1025 x
-  // 16 x 72 fp16 54.8, so XX us.)
+  // 16 x 72 fp16 54.8, so 46.4 us.)
   static constexpr int kRow = kBytes <= 128 ? 128 : kBytes == 192 ? 192 : kBytes <= 256 ? 256 : 512;
   static constexpr int kSteps = DB * 32 / kPerStep<T>;
 };

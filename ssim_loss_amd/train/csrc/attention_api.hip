@@ -27,7 +27,7 @@ struct Shape {
 };
 Shape shape_of(const void* const (&kernels)[3], int64_t rows, int64_t pairs, bool causal) {
   // Where 32 rows to a workgroup do not fill the GPU, its waves take the other axis in
-  // turn: 2 x 257 x 6 x 64 fp32, gradients of queries XX us, of 128 rows XX.
+  // turn: 2 x 257 x 6 x 64 fp32, gradients of queries 19.1, with 128 rows to one 40.3 us.
   if (rows <= 32 || ceil_div(rows, 32) * pairs <= kCUs) return {2, (int)ceil_div(rows, 32)};
   // Eight waves: half the caches' traffic, but coarser.  1 x 16384 x 16 x 128 bf16,
   // forward: 1948, of four waves 2044 us; causal, 4 x 4096: 183 and 156.

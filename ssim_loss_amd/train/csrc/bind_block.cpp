@@ -142,6 +142,8 @@ py::tuple rotary(const py::object& q_, const py::object& k_, const py::object& p
     if (k.size(0) != q.size(0) || k.size(1) != q.size(1) || k.size(3) != q.size(3))
       throw py::value_error("k must have q's batch, tokens and dim");
   }
+  if (q.size(2) < 1 || q.size(3) < 1 || (k.defined() && k.size(2) < 1))
+    throw py::value_error("q and k must have at least one head of one element");
   RotaryPlan plan;
   plan.base = base;
   plan.pairs = pairs;

@@ -60,7 +60,7 @@ __device__ __forceinline__ float quotient_of(float a, float b) {
 // The normal distribution's share below g.  For half types exp(x^2) erfc(x) = t P(t),
 // t = 1 / (1 + 0.44 x), with P fitted to 1.9e-7 of the value over x = 0 .. 10 (5e-7
 // evaluated in fp32), a third of the library function's instructions (4100 x 1153
-// x 2997 fp16: 108, so 92 us).
+// x 2997 fp16: 108, so 98 us).
 template <class T>
 __device__ __forceinline__ float normal_share(float g) {
   if constexpr (sizeof(T) == 4) return 0.5f * erfcf(g * -0.70710678118654752f);

@@ -164,7 +164,8 @@ __device__ __forceinline__ void read_ahead() {
 // bytes at `to` (the same for the wave), lane after lane.  A chunk past the
 // descriptor's bytes arrives as zeros.  In asm, since the compiler waits for its own
 // form of these loads before any read of the LDS; it does not count them:
-// landed_for_all() waits.  (m0 is written here; nothing else in these kernels uses it.)
+// landed_for_all() waits.  (m0 is written here; nothing else in these kernels uses it.
+// The wait between is for a descriptor that the vector unit has just written.)
 typedef unsigned Descriptor __attribute__((ext_vector_type(4)));
 
 // of `bytes` (< 2^32, counted in whole chunks) from p on, which is the same for the wave
@@ -182,7 +183,7 @@ constexpr uint32_t kNowhere = 0xfffffff0u;  // an offset past any descriptor's b
 __device__ __forceinline__ void load_to_lds(Descriptor from, uint32_t offset, uint32_t to) {
   asm volatile(
       "s_mov_b32 m0, %0\n"
-      "s_nop 0\n"
+      "s_nop 4\n"
       "buffer_load_dwordx4 %1, %2, 0 offen lds"
       :
       : "s"(to), "v"(offset), "s"(from)
@@ -192,7 +193,7 @@ __device__ __forceinline__ void load_to_lds(Descriptor from, uint32_t offset, ui
 __device__ __forceinline__ void load_words_to_lds(Descriptor from, uint32_t offset, uint32_t to) {
   asm volatile(
       "s_mov_b32 m0, %0\n"
-      "s_nop 0\n"
+      "s_nop 4\n"
       "buffer_load_dword %1, %2, 0 offen lds"
       :
       : "s"(to), "v"(offset), "s"(from)

@@ -167,7 +167,7 @@ def test_refusals():
     q, p = torch.zeros(2, 3, 4, 8, device="cuda"), torch.zeros(3, 1, device="cuda")
     f = S.rotary
     for call in (lambda: f(q[0], None, p, (8,)), lambda: f(q, q[:1], p, (8,)), lambda: f(q, q[:, :2], p, (8,)),
-                 lambda: f(q, q[..., :4], p, (8,)), lambda: f(q, None, p, (7,)), lambda: f(q, None, p, (10,)),
+                 lambda: f(q, q[..., :4], p, (8,)), lambda: f(q[:, :, :0], q, p, (8,)), lambda: f(q, q[:, :, :0], p, (8,)), lambda: f(q, None, p, (7,)), lambda: f(q, None, p, (10,)),
                  lambda: f(q, None, p, (0,)), lambda: f(q, None, p, ()), lambda: f(q, None, p, (4, 4)),
                  lambda: f(q, None, torch.zeros(3, 2, device="cuda"), (6, 4)),
                  lambda: f(q, None, torch.zeros(2, 1, device="cuda"), (8,)),
