@@ -43,6 +43,7 @@ struct AttentionParams {
   const void* o_rest;
   const void* d_out;
   float* delta;        // [batch][heads][q_tokens]
+  int kv_tiles, q_blocks;  // where one launch has both gradients: that of the queries first
   float* norms;        // fp16: [batch][kv_heads][kNormParts][2], largest |do_i| and |v_j|
   void* dq;
   void* dk;
@@ -77,8 +78,8 @@ struct Where {
   int b, kvh, item;
 };
 template <bool kItemsFirst = false>
-__device__ __forceinline__ Where where(const AttentionParams& p, int items) {
-  const unsigned id = blockIdx.x, step = p.spread ? 8 : 1, j = id / step;
+__device__ __forceinline__ Where where(const AttentionParams& p, unsigned id, int items) {
+  const unsigned step = p.spread ? 8 : 1, j = id / step;
   if (kItemsFirst && p.causal) {
     const unsigned pairs = (unsigned)(p.batch * p.kv_heads) / step, pair = j % pairs * step + id % step;
     return {(int)(pair / p.kv_heads), (int)(pair % p.kv_heads), (int)(j / pairs)};
@@ -258,7 +259,7 @@ attention_forward(const AttentionParams p) {
   __shared__ float joined[2][4][32];
   Lds* lds = (Lds*)lds_;
   const uint32_t lds_at = lds_address(lds);
-  const Where at = where(p, p.tiles * p.splits);
+  const Where at = where(p, blockIdx.x, p.tiles * p.splits);
   if (at.b >= p.batch) return;
   // (the last rows see most: first)
   const int tile = p.tiles - 1 - at.item / p.splits, split = at.item % p.splits;
@@ -519,14 +520,14 @@ struct QueriesShape {
   static constexpr int kLds = kTiles > kJoin ? kTiles : kJoin;
 };
 
-template <class T, int DB, int KW, int NW>
-__global__ void __launch_bounds__(NW* kWave, sizeof(T) == 2 && KW == 1 ? 2 : 1) attention_grad_q(const AttentionParams p) {
+// kDelta: it forms delta and leaves it; else delta is there.
+template <class T, int DB, int KW, int NW, bool kDelta>
+__device__ __forceinline__ void grad_q_tile(const AttentionParams& p, unsigned block, char* lds_) {
   using Shape = QueriesShape<T, DB, KW, NW>;
   using Head = HeadShape<T, DB>;
-  __shared__ __attribute__((aligned(1024))) char lds_[Shape::kLds];
   Lds* lds = (Lds*)lds_;
   const uint32_t lds_at = lds_address(lds);
-  const Where at = where(p, p.tiles);
+  const Where at = where(p, block, p.tiles);
   if (at.b >= p.batch) return;
   const int tile = p.tiles - 1 - at.item;
   const Seen seen = seen_of(p, at.b);
@@ -548,7 +549,9 @@ __global__ void __launch_bounds__(NW* kWave, sizeof(T) == 2 && KW == 1 ? 2 : 1) 
   load_row<T, DB>(p.q.p + at.b * p.q.batch + (int64_t)token * p.q.token + head * p.q.head, live, chunks, q);
   load_row<T, DB>((const char*)p.d_out + dense * (int64_t)sizeof(T), live, chunks, d_out);
   float delta = 0.0f;
-  {
+  if constexpr (!kDelta) {
+    if (there) delta = p.delta[stat];
+  } else {
     constexpr int N = kPerChunk<T>;
     constexpr bool kRest = sizeof(T) == 2;
     Chunk o[Head::kSteps], o_rest[kRest ? Head::kSteps : 1];
@@ -564,7 +567,7 @@ __global__ void __launch_bounds__(NW* kWave, sizeof(T) == 2 && KW == 1 ? 2 : 1) 
     }
     delta = halves_sum(delta);
   }
-  if (there && lane < 32 && (KW == 1 || wave == 0)) p.delta[stat] = delta;
+  if (kDelta && there && lane < 32 && (KW == 1 || wave == 0)) p.delta[stat] = delta;
   const float lse = there ? p.lse[stat] : INFINITY;
   const int range = range_of<T>(p, at);
   const float up = ldexpf(1.0f, range);
@@ -635,6 +638,34 @@ __global__ void __launch_bounds__(NW* kWave, sizeof(T) == 2 && KW == 1 ? 2 : 1) 
   }
 }
 
+template <class T, int DB, int KW, int NW>
+__global__ void __launch_bounds__(NW* kWave, sizeof(T) == 2 && KW == 1 ? 2 : 1) attention_grad_q(const AttentionParams p) {
+  __shared__ __attribute__((aligned(1024))) char lds[QueriesShape<T, DB, KW, NW>::kLds];
+  grad_q_tile<T, DB, KW, NW, true>(p, blockIdx.x, lds);
+}
+
+// delta alone, 16 lanes to a row.
+template <class T>
+__global__ void __launch_bounds__(kAttentionThreads) attention_delta(const AttentionParams p) {
+  const int64_t rows = (int64_t)p.batch * p.q_tokens * p.heads;
+  const int64_t row = (int64_t)blockIdx.x * (kAttentionThreads / 16) + threadIdx.x / 16;  // (b, token, head)
+  if (row >= rows) return;
+  constexpr int N = 128 / 16;  // elements of a lane
+  const int column = (int)(threadIdx.x % 16) * N;
+  const int64_t head = row % p.heads, token = row / p.heads % p.q_tokens, b = row / p.heads / p.q_tokens;
+  float delta = 0.0f;
+  if (column < p.dim && (int)token < seen_of(p, (int)b).q_length) {
+    const int64_t at = row * p.dim + column;
+    const Wide<N> d = widen<T, N>(load<T, N>(static_cast<const T*>(p.d_out) + at));
+    Wide<N> o = widen<T, N>(load<T, N>(static_cast<const T*>(p.o) + at));
+    if constexpr (sizeof(T) == 2) o += widen<T, N>(load<T, N>(static_cast<const T*>(p.o_rest) + at));
+#pragma unroll
+    for (int k = 0; k < N; ++k) delta = fmaf(o[k], d[k], delta);
+  }
+  delta = lanes_sum<16>(delta);
+  if (threadIdx.x % 16 == 0) p.delta[(b * p.heads + head) * p.q_tokens + token] = delta;
+}
+
 // ---------------------------------------------------------------- gradients of the keys and values
 // A wave has 32 keys; the rows of all heads that share them go by, head after
 // head, in one order: no atomics, the same bits every time.
@@ -665,16 +696,15 @@ template <class T>
 constexpr int kLift = kScaled<T> ? 14 : 0;
 
 template <class T, int DB, int KW, int NW>
-__global__ void __launch_bounds__(NW* kWave, sizeof(T) == 2 && KW == 1 ? 2 : 1) attention_grad_kv(const AttentionParams p) {
+__device__ __forceinline__ void grad_kv_tile(const AttentionParams& p, unsigned block, int tiles, char* lds_) {
   using Shape = KeysShape<T, DB, KW, NW>;
   using Head = HeadShape<T, DB>;
-  __shared__ __attribute__((aligned(1024))) char lds_[Shape::kLds];
   __shared__ __attribute__((aligned(16))) float stats[Shape::kBuffers][2][Shape::kStats];  // [lse, delta][row of the tile]
   Lds* lds = (Lds*)lds_;
   __shared__ float nowhere[kWave];
   const uint32_t lds_at = lds_address(lds), stats_at = lds_address((Lds*)&stats[0][0][0]);
   const uint32_t nowhere_at = lds_address((Lds*)nowhere);
-  const Where at = where<true>(p, p.tiles);
+  const Where at = where<true>(p, block, tiles);
   if (at.b >= p.batch) return;
   const Seen seen = seen_of(p, at.b);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
@@ -800,6 +830,23 @@ __global__ void __launch_bounds__(NW* kWave, sizeof(T) == 2 && KW == 1 ? 2 : 1) 
   }
 }
 
+template <class T, int DB, int KW, int NW>
+__global__ void __launch_bounds__(NW* kWave, sizeof(T) == 2 && KW == 1 ? 2 : 1) attention_grad_kv(const AttentionParams p) {
+  __shared__ __attribute__((aligned(1024))) char lds[KeysShape<T, DB, KW, NW>::kLds];
+  grad_kv_tile<T, DB, KW, NW>(p, blockIdx.x, p.tiles, lds);
+}
+
+// Both in one launch, behind attention_delta's, where neither fills the GPU (2 x 257 x
+// 6 x 64 fp32: 19.1 and 20.8 us one after the other, so 22.9 and 3.0 of delta's).
+template <class T, int DB>
+__global__ void __launch_bounds__(kAttentionThreads, 1) attention_grads(const AttentionParams p) {
+  using Q = QueriesShape<T, DB, 4, 4>;
+  using K = KeysShape<T, DB, 4, 4>;
+  __shared__ __attribute__((aligned(1024))) char lds[Q::kLds > K::kLds ? Q::kLds : K::kLds];
+  if ((int)blockIdx.x < p.q_blocks) grad_q_tile<T, DB, 4, 4, false>(p, blockIdx.x, lds);
+  else grad_kv_tile<T, DB, 4, 4>(p, blockIdx.x - p.q_blocks, p.kv_tiles, lds);
+}
+
 // ---------------------------------------------------------------- kernels of a type
 struct AttentionTable {
   // [blocks of 32 elements - 1][0: four waves of 32 rows (or keys) each, 1: eight, 2: four that share 32].  NULL:
@@ -807,6 +854,8 @@ struct AttentionTable {
   const void* forward[4][3];
   const void* grad_q[4][3];
   const void* grad_kv[4][3];
+  const void* grads[4];
+  const void* delta;
   const void* join;
   const void* norms;  // NULL: not needed
 };
@@ -819,6 +868,7 @@ void fill_attention_table(AttentionTable& t) {
   t.grad_q[k][2] = (const void*)attention_grad_q<T, DB, 4, 4>;
   t.grad_kv[k][0] = (const void*)attention_grad_kv<T, DB, 1, 4>;
   t.grad_kv[k][2] = (const void*)attention_grad_kv<T, DB, 4, 4>;
+  t.grads[k] = (const void*)attention_grads<T, DB>;
   t.forward[k][1] = t.grad_q[k][1] = t.grad_kv[k][1] = nullptr;
   if constexpr (sizeof(T) == 2 && DB == 4) {
     t.forward[k][1] = (const void*)attention_forward<T, DB, 1, 8>;
@@ -834,6 +884,7 @@ AttentionTable make_attention_table() {
   fill_attention_table<T, 3>(t);
   fill_attention_table<T, 4>(t);
   t.join = (const void*)attention_join<T>;
+  t.delta = (const void*)attention_delta<T>;
   t.norms = nullptr;
   if constexpr (kScaled<T>) t.norms = (const void*)attention_norms<T>;
   return t;

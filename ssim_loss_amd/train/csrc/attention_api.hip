@@ -231,12 +231,23 @@ int ssim_attention_backward(const ssim_attention_inputs* in, const void* out, co
     rc = launch(t.norms, dim3(pairs * kNormParts), kAttentionThreads, p, stream);
     if (rc != SSIM_OK) return rc;
   }
+  const bool kv = any_k && (dk || dv);
+  if (plan.grad_q.shape == 2 && plan.grad_kv.shape == 2 && pairs * (plan.grad_q.tiles + plan.grad_kv.tiles) <= kCUs) {
+    if (any_q) {
+      rc = launch(t.delta, dim3((unsigned)ceil_div(rows, kAttentionThreads / 16)), kAttentionThreads, p, stream);
+      if (rc != SSIM_OK) return rc;
+    }
+    p.tiles = dq ? plan.grad_q.tiles : 0;
+    p.kv_tiles = kv ? plan.grad_kv.tiles : 0;
+    p.q_blocks = (int)(pairs * p.tiles);
+    return launch(t.grads[blocks], dim3(pairs * (p.tiles + p.kv_tiles)), kAttentionThreads, p, stream);
+  }
   if (any_q) {  // (it forms delta for the other kernel)
     p.tiles = plan.grad_q.tiles;
     rc = launch(t.grad_q[blocks][plan.grad_q.shape], dim3(pairs * plan.grad_q.tiles), plan.grad_q.threads(), p, stream);
     if (rc != SSIM_OK) return rc;
   }
-  if (!any_k || !(dk || dv)) return SSIM_OK;
+  if (!kv) return SSIM_OK;
   p.tiles = plan.grad_kv.tiles;
   return launch(t.grad_kv[blocks][plan.grad_kv.shape], dim3(pairs * plan.grad_kv.tiles), plan.grad_kv.threads(), p, stream);
 }

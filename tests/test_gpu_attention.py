@@ -341,3 +341,14 @@ def test_refusals():
             call()
     with pytest.raises(S.TrainError):
         f(q, k, k, scale=1e300)
+
+
+@pytest.mark.parametrize("n,m", [(45, 60), (300, 280), (700, 900), (0, 30), (30, 0)])
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+def test_any_set_of_leaves_keeps_the_bits(n, m, dtype):
+    """Short sequences' gradients are one launch, longer ones' two."""
+    t, d_out = make(1, n, m, 4, 2, 40, dtype, seed=27)
+    want = run(t, d_out)[1]
+    for leaves in (("q",), ("k",), ("v",), ("q", "v"), ("k", "v")):
+        got = run(t, d_out, leaves=leaves)[1]
+        assert all(torch.equal(got[k], want[k]) for k in leaves), leaves
