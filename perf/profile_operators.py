@@ -144,7 +144,7 @@ def profile(outdir):
 def kernel_of(row):
     if BLOCK:
         name = row["Kernel_Name"]
-        found = re.search(r"attention_(?:forward|join|norms|grad_kv|grad_q)|gated_(?:product|both|finish|slopes|few_rows|copy)|"
+        found = re.search(r"attention_(?:forward|join|norms|delta|grads|grad_kv|grad_q)|gated_(?:product|both|finish|slopes|few_rows|copy)|"
                           r"rotary_kernel", name)
         if not found or found[0] != "gated_product":
             return found and found[0]

@@ -199,6 +199,18 @@ __device__ __forceinline__ Seen seen_of(const AttentionParams& p, int b) {
 __device__ __forceinline__ int last_key(const Seen& s, int i) {
   return i < s.q_length ? min(s.k_length - 1, i + s.shift) : -1;
 }
+// Of the rows from `first` to `end`, all of a group's heads a token: the last key that
+// each of them sees (past it scores are compared), and the last that any does (past it
+// there is nothing to do).
+struct Reach {
+  int open, any;
+};
+__device__ __forceinline__ Reach reach_of(const AttentionParams& p, const Seen& seen, int first, int end) {
+  if (first >= end) return {-1, -1};
+  const int last = (end - 1) / p.group;
+  return {last < seen.q_length ? last_key(seen, first / p.group) : -1,
+          first / p.group < seen.q_length ? last_key(seen, min(last, seen.q_length - 1)) : -1};
+}
 
 // ---- four waves' sums of the same 32 rows together, through the LDS
 template <int DB>
@@ -279,15 +291,12 @@ attention_forward(const AttentionParams p) {
                   there && token < seen.q_length, chunks, q);
 
   // the keys of the workgroup: those that its last row sees, and of them its share
-  const int last_token = min((min(first_row + Shape::kRows, rows) - 1) / p.group, seen.q_length - 1);
-  const int keys = first_row / p.group < seen.q_length ? max(last_key(seen, last_token) + 1, 0) : 0;
+  const int keys = reach_of(p, seen, first_row, min(first_row + Shape::kRows, rows)).any + 1;
   const int key_tiles = (keys + Shape::kKeys - 1) / Shape::kKeys;
   const int each = (key_tiles + p.splits - 1) / p.splits;
   const int begin = min(split * each, key_tiles), end = min(begin + each, key_tiles);
-  // the least that a row of the wave sees, past which scores are compared
-  const int wave_first = (first_row + (KW == 1 ? wave * kRowsOfWave : 0)) / p.group;
-  const int wave_last = min(first_row + (KW == 1 ? wave * kRowsOfWave : 0) + kRowsOfWave, rows) - 1;
-  const int open = wave_last / p.group < seen.q_length && wave_last >= 0 ? last_key(seen, wave_first) : -1;
+  const int wave_row = first_row + (KW == 1 ? wave * kRowsOfWave : 0);
+  const Reach reach = reach_of(p, seen, wave_row, min(wave_row + kRowsOfWave, rows));
 
   const char* k_from = p.k.p + at.b * p.k.batch + at.kvh * p.k.head;
   const char* v_from = p.v.p + at.b * p.v.batch + at.kvh * p.v.head;
@@ -319,45 +328,47 @@ attention_forward(const AttentionParams p) {
     const Lds* v_tile = k_tile + Shape::kTileBytes;
     const int in_tile = KW == 1 ? 0 : wave * 32;
     const int key = t * Shape::kKeys + in_tile;
-    Sums s[Shape::kBlocks];
-    __builtin_amdgcn_s_setprio(1);
+    if (key <= reach.any) {
+      Sums s[Shape::kBlocks];
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int b = 0; b < Shape::kBlocks; ++b) s[b] = along<T, DB>(k_tile, fresh(along_at), in_tile + 32 * b, q);
-    read_ahead<kAhead, kInstructions<T>, Shape::kBlocks * Head::kSteps, 1>();
-    __builtin_amdgcn_s_setprio(0);
-    if (key + 32 * Shape::kBlocks - 1 > open) {
+      for (int b = 0; b < Shape::kBlocks; ++b) s[b] = along<T, DB>(k_tile, fresh(along_at), in_tile + 32 * b, q);
+      read_ahead<kAhead, kInstructions<T>, Shape::kBlocks * Head::kSteps, 1>();
+      __builtin_amdgcn_s_setprio(0);
+      if (key + 32 * Shape::kBlocks - 1 > reach.open) {
+#pragma unroll
+        for (int b = 0; b < Shape::kBlocks; ++b)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            s[b][r] = key + 32 * b + row_of(r) > last ? -INFINITY : s[b][r];
+      }
+      float top = -INFINITY;
 #pragma unroll
       for (int b = 0; b < Shape::kBlocks; ++b)
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          s[b][r] = key + 32 * b + row_of(r) > last ? -INFINITY : s[b][r];
-    }
-    float top = -INFINITY;
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[b][r]);
+      top = halves_max(top);
+      if (__any(top > limit)) {
+        const float before = m == -INFINITY ? -INFINITY : base;
+        m = fmaxf(m, top);
+        base = m == -INFINITY ? 0.0f : m * p.scale2;
+        limit = m + slack;
+        const float less = exp2_fast(before - base);
+        l *= less;
 #pragma unroll
-    for (int b = 0; b < Shape::kBlocks; ++b)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[b][r]);
-    top = halves_max(top);
-    if (__any(top > limit)) {
-      const float before = m == -INFINITY ? -INFINITY : base;
-      m = fmaxf(m, top);
-      base = m == -INFINITY ? 0.0f : m * p.scale2;
-      limit = m + slack;
-      const float less = exp2_fast(before - base);
-      l *= less;
-#pragma unroll
-      for (int d = 0; d < DB; ++d) o[d] *= less;
-    }
-#pragma unroll
-    for (int b = 0; b < Shape::kBlocks; ++b)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        s[b][r] = exp2_fast(fmaf(s[b][r], p.scale2, -base));
-        l += s[b][r];
+        for (int d = 0; d < DB; ++d) o[d] *= less;
       }
 #pragma unroll
-    for (int b = 0; b < Shape::kBlocks; ++b) across<T, DB>(o, v_tile, fresh(across_at), in_tile + 32 * b, s[b]);
-    read_ahead<kAhead, kInstructions<T>, Shape::kBlocks * DB * kAcrossSteps<T>, kAcrossReads<T>>();
+      for (int b = 0; b < Shape::kBlocks; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          s[b][r] = exp2_fast(fmaf(s[b][r], p.scale2, -base));
+          l += s[b][r];
+        }
+#pragma unroll
+      for (int b = 0; b < Shape::kBlocks; ++b) across<T, DB>(o, v_tile, fresh(across_at), in_tile + 32 * b, s[b]);
+      read_ahead<kAhead, kInstructions<T>, Shape::kBlocks * DB * kAcrossSteps<T>, kAcrossReads<T>>();
+    }
     if constexpr (Shape::kBuffers == 1) {
       landed_for_all();
       fetch(t + 1);
@@ -572,12 +583,9 @@ __device__ __forceinline__ void grad_q_tile(const AttentionParams& p, unsigned b
   const int range = range_of<T>(p, at);
   const float up = ldexpf(1.0f, range);
 
-  const int last_token = min((min(first_row + Shape::kRows, rows) - 1) / p.group, seen.q_length - 1);
-  const int keys = first_row / p.group < seen.q_length ? max(last_key(seen, last_token) + 1, 0) : 0;
+  const int keys = reach_of(p, seen, first_row, min(first_row + Shape::kRows, rows)).any + 1;
   const int end = (keys + Shape::kKeys - 1) / Shape::kKeys;
-  const int wave_first = row_of_wave / p.group;
-  const int wave_last = min(row_of_wave + kRowsOfWave, rows) - 1;
-  const int open = wave_last / p.group < seen.q_length ? last_key(seen, wave_first) : -1;
+  const Reach reach = reach_of(p, seen, row_of_wave, min(row_of_wave + kRowsOfWave, rows));
 
   const char* k_from = p.k.p + at.b * p.k.batch + at.kvh * p.k.head;
   const char* v_from = p.v.p + at.b * p.v.batch + at.kvh * p.v.head;
@@ -603,16 +611,17 @@ __device__ __forceinline__ void grad_q_tile(const AttentionParams& p, unsigned b
 #pragma unroll
     for (int b = 0; b < (KW == 1 ? Shape::kKeys / 32 : 1); ++b) {
       const int in_tile = KW == 1 ? 32 * b : 32 * wave;
+      const int key = t * Shape::kKeys + in_tile;
+      if (key > reach.any) continue;
       Sums s = along<T, DB>(k_tile, fresh(along_at), in_tile, q);
       const Sums dp = along<T, DB>(v_tile, fresh(along_at), in_tile, d_out);
       read_ahead<kAhead, kInstructions<T>, 2 * Head::kSteps, 1>();
-      const int key = t * Shape::kKeys + in_tile;
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         s[r] = exp2_fast(fmaf(s[r], p.scale2, -lse)) * (dp[r] - delta);
         if constexpr (kScaled<T>) s[r] *= up;
       }
-      if (key + 31 > open) {
+      if (key + 31 > reach.open) {
 #pragma unroll
         for (int r = 0; r < 16; ++r)
           s[r] = key + row_of(r) > last ? 0.0f : s[r];
@@ -773,6 +782,8 @@ __device__ __forceinline__ void grad_kv_tile(const AttentionParams& p, unsigned 
 #pragma unroll
     for (int b = 0; b < (KW == 1 ? Shape::kRows / 32 : 1); ++b) {
       const int in_tile = KW == 1 ? 32 * b : 32 * wave;
+      // (of rows that see no key of the wave's there is nothing to add)
+      if (last_key(seen, min(token + in_tile + 31, seen.q_length - 1)) < wave_key) continue;
       Sums s = along<T, DB>(q_tile, fresh(along_at), in_tile, k);
       Sums ds;
       if constexpr (Shape::kValuesInLds) ds = along_both<T, DB>(d_tile, v_tile, fresh(along_at), in_tile, wave * 32);
