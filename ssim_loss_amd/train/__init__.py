@@ -322,8 +322,9 @@ def attention(q, k, v, scale=None, causal=False, query_lengths=None, key_lengths
            query sees the last key.
 
     Returns [batch, queries, heads, dim].  A query that sees no key, or is behind
-    its sequence, gives zeros and takes a zero gradient.  A key or value within its
-    sequence's length must be finite also where it is not seen by some queries.
+    its sequence, gives zeros and takes a zero gradient.  Within the sequences' lengths
+    queries, keys, values and the gradient that arrives must be finite: what is not
+    may reach rows that do not see it.  Behind the lengths they may be anything.
     Scores and sums are float32; for half types the probabilities (and in the
     backward, which forms them again, their gradients) are rounded to the type.
     Gradients of q, k and v are available, the same bits every time; gradients of

@@ -314,7 +314,7 @@ attention_forward(const AttentionParams p) {
   // the sums with it, only where scores pass it by 2^8 in p, which both types and the
   // sums hold: in a long row seldom, where a larger maximum comes with every other tile.
   float m = -INFINITY, base = 0.0f, limit = -INFINITY;
-  const float slack = 8.0f / p.scale2;
+  const float slack = 8.0f / fmaxf(p.scale2, 0x1p-100f);  // (finite: of -infinity and it the limit is -infinity)
   float l = 0.0f;  // the sum of this lane's half
   constexpr int kEarly = Shape::kBuffers > 1 ? Shape::kBuffers - 1 : 1;
   if (begin < end) {

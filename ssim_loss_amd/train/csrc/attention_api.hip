@@ -66,6 +66,16 @@ bool stride_ok(const int64_t* s, const ssim_attention_inputs& in, int64_t tokens
   return tokens <= 1 || (s[1] >= in.dim && s[1] * bytes < kMaxStride);
 }
 
+struct Spans {
+  int64_t q, k, v;
+  bool any_bad() const { return q < 0 || k < 0 || v < 0; }
+};
+Spans spans_of(const ssim_attention_inputs& in) {
+  return {span(in.q_stride, in.batch, in.q_tokens, in.heads, in.dim),
+          span(in.k_stride, in.batch, in.k_tokens, in.kv_heads, in.dim),
+          span(in.v_stride, in.batch, in.k_tokens, in.kv_heads, in.dim)};
+}
+
 int check_inputs(const ssim_attention_inputs* in) {
   if (!in) return SSIM_ERR_NULL;
   if (!known_dtype(in->dtype)) return SSIM_ERR_DTYPE;
@@ -80,19 +90,16 @@ int check_inputs(const ssim_attention_inputs* in) {
       !stride_ok(in->v_stride, *in, in->k_tokens))
     return SSIM_ERR_SHAPE;
   if (in->batch > 1 << 24) return SSIM_ERR_OVERFLOW;
-  const Plan p = make_plan(*in);
   const int64_t pairs = in->batch * in->kv_heads, rows = in->q_tokens * (in->heads / in->kv_heads);
-  if (rows >= (int64_t)1 << 31 || pairs > kMaxBlocks / kNormParts || pairs * p.forward.tiles * p.splits > kMaxBlocks ||
-      pairs * p.grad_q.tiles > kMaxBlocks || pairs * p.grad_kv.tiles > kMaxBlocks ||
-      in->batch * in->heads * in->q_tokens > (int64_t)1 << 36)
+  // (a tile's end, too, is counted in 32 bits)
+  if (rows > ((int64_t)1 << 31) - 512 || pairs > kMaxBlocks / kNormParts || pairs * rows > (int64_t)1 << 36 ||
+      spans_of(*in).any_bad())
+    return SSIM_ERR_OVERFLOW;
+  const Plan p = make_plan(*in);
+  if (pairs * p.forward.tiles * p.splits > kMaxBlocks || pairs * p.grad_q.tiles > kMaxBlocks ||
+      pairs * p.grad_kv.tiles > kMaxBlocks)
     return SSIM_ERR_OVERFLOW;
   return SSIM_OK;
-}
-
-// bytes from the first element to the last
-size_t span(const int64_t* s, const ssim_attention_inputs& in, int64_t tokens, int64_t heads) {
-  if (in.batch == 0 || tokens == 0) return 0;
-  return (size_t)((in.batch - 1) * s[0] + (tokens - 1) * s[1] + (heads - 1) * s[2] + in.dim) * elem_bytes(in.dtype);
 }
 
 Strided strided(const void* p, const int64_t* s, int bytes) {
@@ -149,9 +156,10 @@ int ssim_attention_forward(const ssim_attention_inputs* in, void* out, float* ls
   const size_t ws = ssim_attention_workspace_bytes(in), rows = rows_of(*in);
   if (!in->q || (in->k_tokens > 0 && (!in->k || !in->v)) || !out || (ws > 0 && !workspace)) return SSIM_ERR_NULL;
   const int bytes = elem_bytes(in->dtype);
-  const Array ins[] = {{in->q, span(in->q_stride, *in, in->q_tokens, in->heads), 16},
-                       {in->k, span(in->k_stride, *in, in->k_tokens, in->kv_heads), 16},
-                       {in->v, span(in->v_stride, *in, in->k_tokens, in->kv_heads), 16},
+  const Spans spans = spans_of(*in);
+  const Array ins[] = {{in->q, (size_t)spans.q * bytes, 16},
+                       {in->k, (size_t)spans.k * bytes, 16},
+                       {in->v, (size_t)spans.v * bytes, 16},
                        {in->q_lengths, 4 * (size_t)in->batch, 4},
                        {in->k_lengths, 4 * (size_t)in->batch, 4}};
   const Array outs[] = {{out, rows * in->dim * bytes, bytes}, {lse, rows * 4, 4}, {rest, rows * in->dim * bytes, bytes},
@@ -195,11 +203,12 @@ int ssim_attention_backward(const ssim_attention_inputs* in, const void* out, co
       (any_q && (!in->q || !out || !lse || !d_out || (in->dtype != SSIM_DTYPE_F32 && !rest))) || (any_k && (!in->k || !in->v)))
     return SSIM_ERR_NULL;
   const int bytes = elem_bytes(in->dtype);
+  const Spans spans = spans_of(*in);
   const size_t rows = rows_of(*in), keys = (size_t)in->batch * in->k_tokens * in->kv_heads * in->dim * bytes;
   const size_t ws = ssim_attention_backward_workspace_bytes(in);
-  const Array ins[] = {{in->q, span(in->q_stride, *in, in->q_tokens, in->heads), 16},
-                       {in->k, span(in->k_stride, *in, in->k_tokens, in->kv_heads), 16},
-                       {in->v, span(in->v_stride, *in, in->k_tokens, in->kv_heads), 16},
+  const Array ins[] = {{in->q, (size_t)spans.q * bytes, 16},
+                       {in->k, (size_t)spans.k * bytes, 16},
+                       {in->v, (size_t)spans.v * bytes, 16},
                        {in->q_lengths, 4 * (size_t)in->batch, 4},
                        {in->k_lengths, 4 * (size_t)in->batch, 4},
                        {out, rows * in->dim * bytes, 16},

@@ -28,6 +28,9 @@ bool wants_gradient(std::initializer_list<const Tensor*> tensors) {
   return false;
 }
 
+// A gradient may arrive as a view with its sign turned, as from a complex number's conjugate.
+Tensor settled(const Tensor& t) { return t.is_neg() ? t.resolve_neg() : t; }
+
 // GPU tensors of one of the three types, any strides
 int check_strided(const Tensor& t, const char* name) {
   if (!t.device().is_cuda()) throw py::type_error(std::string(name) + " must be a GPU tensor, got device " + t.device().str());
@@ -121,7 +124,8 @@ struct RotaryBackward : torch::autograd::Node {
       if (upstream[k].defined() && task_should_compute_output(k)) which.push_back(k);
     if (which.empty()) return out;
     int rc = SSIM_OK;
-    auto turned = turn(upstream[which[0]], which.size() > 1 ? upstream[which[1]] : Tensor(), at_, plan, true, dev, rc);
+    auto turned = turn(settled(upstream[which[0]]), which.size() > 1 ? settled(upstream[which[1]]) : Tensor(), at_,
+                       plan, true, dev, rc);
     TORCH_CHECK(rc == SSIM_OK, "ssim_rotary: ", text(rc));
     out[which[0]] = turned.first;
     if (which.size() > 1) out[which[1]] = turned.second;
@@ -264,7 +268,7 @@ struct AttentionBackward : torch::autograd::Node {
       grads[k] = out[k].data_ptr();
     }
     const AttentionCall call(t[0], t[1], t[2], t[3], t[4], plan, dev);
-    Tensor d_out = upstream[0].contiguous();
+    Tensor d_out = settled(upstream[0]).contiguous();
     if ((uintptr_t)d_out.const_data_ptr() % 16 != 0) d_out = dense_copy(d_out, dev);
     const c10::DataPtr ws = scratch(ssim_attention_backward_workspace_bytes(&call.in));
     const int rc = ssim_attention_backward(&call.in, t[5].const_data_ptr(), t[6].const_data_ptr<float>(),
@@ -386,7 +390,7 @@ struct GatedLinearBackward : torch::autograd::Node {
     grads.w_up = wanted(2);
     grads.b_gate = wanted(3);
     grads.b_up = wanted(4);
-    const Tensor d_out = upstream[0].contiguous();
+    const Tensor d_out = settled(upstream[0]).contiguous();
     const c10::DataPtr ws = scratch(ssim_gated_linear_backward_workspace_bytes(&in));
     const int rc = ssim_gated_linear_backward(&in, t[5].const_data_ptr<float>(), t[6].const_data_ptr<float>(),
                                               d_out.const_data_ptr(), &grads, ws.get(), stream_of(dev));

@@ -94,6 +94,8 @@ inline const Tensor& unpack(PyObject* o, const char* name, Py_ssize_t k = -1) {
   TORCH_CHECK_NOT_IMPLEMENTED(!t._fw_grad(/*level=*/0).defined(), at_index(name, k),
                               " has a forward-mode tangent: forward-mode derivatives of the "
                               "training operators are not available");
+  // (its memory holds the values with the other sign)
+  TORCH_CHECK_NOT_IMPLEMENTED(!t.is_neg(), at_index(name, k), " is a view with its sign turned: use resolve_neg()");
   return t;
 }
 

@@ -236,11 +236,6 @@ int check_inputs(const ssim_rotary_inputs* in) {
   return SSIM_OK;
 }
 
-// bytes from the first element to the last
-size_t span(const int64_t* stride, int64_t batch, int64_t tokens, int64_t heads, int64_t dim, int bytes) {
-  return (size_t)((batch - 1) * stride[0] + (tokens - 1) * stride[1] + (heads - 1) * stride[2] + dim) * bytes;
-}
-
 }  // namespace
 
 extern "C" int ssim_rotary(const ssim_rotary_inputs* in, void* q_out, void* k_out, void* stream) {
@@ -251,9 +246,13 @@ extern "C" int ssim_rotary(const ssim_rotary_inputs* in, void* q_out, void* k_ou
   const int bytes = elem_bytes(in->dtype), position_bytes = in->position_type == SSIM_POSITION_I64 ? 8 : 4;
   const int64_t n = in->batch * in->tokens;
   const int64_t flat[3] = {in->position_stride[0], in->position_stride[1], 0};
-  const Array ins[] = {{in->q, span(in->q_stride, in->batch, in->tokens, in->q_heads, in->dim, bytes), bytes},
-                       {in->k, in->k ? span(in->k_stride, in->batch, in->tokens, in->k_heads, in->dim, bytes) : 0, bytes},
-                       {in->positions, span(flat, in->batch, in->tokens, 1, in->axes, position_bytes), position_bytes}};
+  const int64_t q_span = span(in->q_stride, in->batch, in->tokens, in->q_heads, in->dim),
+                k_span = in->k ? span(in->k_stride, in->batch, in->tokens, in->k_heads, in->dim) : 0,
+                position_span = span(flat, in->batch, in->tokens, 1, in->axes);
+  if (q_span < 0 || k_span < 0 || position_span < 0) return SSIM_ERR_OVERFLOW;
+  const Array ins[] = {{in->q, (size_t)q_span * bytes, bytes},
+                       {in->k, (size_t)k_span * bytes, bytes},
+                       {in->positions, (size_t)position_span * position_bytes, position_bytes}};
   const Array outs[] = {{q_out, (size_t)(n * in->q_heads * in->dim) * bytes, bytes},
                         {in->k ? k_out : nullptr, in->k ? (size_t)(n * in->k_heads * in->dim) * bytes : 0, bytes}};
   rc = check_arrays(ins, 3, outs, 2);

@@ -158,6 +158,20 @@ inline int check_arrays(const Array* ins, int n_in, const Array* outs, int n_out
   return SSIM_OK;
 }
 
+// Elements from the first of a tensor [batch][tokens][heads][dim] to its last; 0: there
+// are none, -1: 2^58 or more.
+inline int64_t span(const int64_t* stride, int64_t batch, int64_t tokens, int64_t heads, int64_t dim) {
+  constexpr int64_t kMost = (int64_t)1 << 56;
+  const int64_t sizes[3] = {batch, tokens, heads};
+  int64_t sum = dim;
+  for (int k = 0; k < 3; ++k) {
+    if (sizes[k] < 1) return 0;
+    if (sizes[k] > 1 && stride[k] > kMost / (sizes[k] - 1)) return -1;
+    sum += (sizes[k] - 1) * stride[k];
+  }
+  return sum;
+}
+
 template <class Params>
 int launch(const void* kernel, dim3 grid, int threads, Params& params, void* stream) {
   void* args[] = {&params};

@@ -230,8 +230,9 @@ int ssim_rotary(const ssim_rotary_inputs* in, void* q_out, void* k_out, void* st
  * none if i >= ql, else j < kl and, with causal order, j <= i + kl - ql.  A query
  * that sees no key, or whose scores are all minus infinity, gives zeros, and a
  * query or key that takes no part has a gradient of zeros.  Queries past ql and
- * keys and values past kl are not read; the other keys and values of a sequence
- * must be finite also where some queries do not see them.
+ * keys and values past kl are not read.  The others, and the gradient that arrives
+ * at them, must be finite: what is not may reach rows that do not see it (scores of
+ * minus infinity excepted).
  * Scores, sums and statistics are fp32; for half types the probabilities and, in
  * the gradients, their derivatives are rounded to the type before the products.
  */

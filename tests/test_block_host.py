@@ -74,6 +74,9 @@ def test_rotary_argument_errors_return_before_any_hip_call():
     for bad in (dict(pairs=2), dict(inverse=2), dict(base=0.0), dict(base=-1.0), dict(base=math.nan), dict(base=math.inf)):
         assert rot(**bad) == -10, bad
     assert rot(tokens=1 << 45) == -4
+    far = (I64 * 3)(1 << 46, 1 << 46, 1)
+    assert rot(batch=1 << 20, q_stride=far) == -4 and rot(tokens=1 << 20, k_stride=far) == -4  # past 64 bits in bytes
+    assert rot(batch=1 << 20, position_stride=(I64 * 2)(1 << 46, 1)) == -4
     assert rot(q_out=M + 64) == -5 and rot(q_out=5 * M) == -5 and rot(k_out=3 * M) == -5
     assert rot(batch=0, q=None) == 0 and rot(tokens=0, q_out=None) == 0
     assert rot(k=None, k_out=None, q_out=M) == -5  # in place
@@ -108,6 +111,9 @@ def test_attention_input_errors_return_before_any_hip_call(call):
     for bad in (dict(scale=0.0), dict(scale=-1.0), dict(scale=math.nan), dict(scale=1e300), dict(causal=2)):
         assert call(**bad) == -10, bad
     assert call(batch=1 << 30) == -4
+    assert call(batch=1 << 20, kv_heads=1, q_stride=(I64 * 3)(1 << 44, 128, 32)) == -4  # past 64 bits in bytes
+    assert call(batch=1 << 24, q_tokens=(1 << 24) - 1, heads=65536, kv_heads=1) == -4
+    assert call(q_tokens=(1 << 24) - 1, heads=128, kv_heads=1, dim=8, batch=1, q_stride=(I64 * 3)(0, 1024, 8)) == -4  # 2^31 rows
     assert call(batch=0, q=None) == 0
     assert S.train.lib().ssim_attention_forward(None, M, M, M, M, None) == -1
 
@@ -229,6 +235,12 @@ def test_tensors_with_a_forward_mode_tangent_are_refused(which):
             calls(dual)[which]()
         with pytest.raises(TypeError, match="GPU tensor"):
             calls(torch.ones(4, 8))[which]()
+
+
+@pytest.mark.parametrize("which", NAMES)
+def test_views_with_the_sign_turned_are_refused(which):
+    with pytest.raises(NotImplementedError, match="sign"):
+        calls(torch._neg_view(torch.ones(4, 8)))[which]()
 
 
 @pytest.mark.parametrize("which", ["rotary q", "attention q", "gated x"])

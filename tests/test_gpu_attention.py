@@ -171,6 +171,25 @@ def test_large_scores_and_other_scales(dtype):
     verify(t, d_out)
 
 
+@pytest.mark.parametrize("scale", [1e-38, 1e-42])
+def test_scales_next_to_nothing(scale):
+    """Every key that a row sees has the same weight, wherever the row's first one lies."""
+    for n, m in ((40, 200), (300, 200)):
+        t, _ = make(1, n, m, 2, 2, 64, F32, seed=17)
+        out = S.attention(t["q"], t["k"], t["v"], scale=scale, causal=True)
+        want = Attention(t["q"], t["k"], t["v"], scale=scale, causal=True)
+        want.check("out", out)
+
+
+def test_a_gradient_with_its_sign_turned():
+    t, d_out = make(1, 40, 50, 2, 2, 64, F32, seed=18)
+    q = t["q"].requires_grad_()
+    out = S.attention(q, t["k"], t["v"])
+    a, = torch.autograd.grad(out, q, -d_out, retain_graph=True)
+    b, = torch.autograd.grad(out, q, torch._neg_view(d_out))
+    assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("size", [1e-4, 200.0])
 def test_small_and_large_gradients_in_fp16(size):
     t, d_out = make(1, 128, 700, 2, 2, 64, F16, seed=10)
