@@ -267,7 +267,7 @@ __device__ __forceinline__ void product_tile(const GatedParams& p, unsigned bloc
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         fetch_along<kHalfM, Shape::kRow, Shape::kThreads>((const char*)p.w[i] + (m0 * p.w_pitch + k) * kBytes, p.w_pitch * kBytes,
-                                             p.hidden - m0, chunks, a_to + i * (kHalfM * 128));
+                                             p.hidden - m0, chunks, a_to + i * (kHalfM * Shape::kRow));
       fetch_along<Shape::kN, Shape::kRow, Shape::kThreads>((const char*)p.x + (n0 * p.x_pitch + k) * kBytes, p.x_pitch * kBytes,
                                               p.rows - n0, chunks, b_to);
     } else if constexpr (kProduct == kGradX) {

@@ -92,6 +92,15 @@ def test_the_large_tiles(dtype):
     verify(*make((4100, 1032), 2056, dtype, bias=False, seed=7))
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("rows,width,hidden", [(4090, 264, 2040), (4090, 4000, 72), (264, 2040, 4080), (2000, 2040, 4080)])
+def test_the_large_tiles_of_each_product(rows, width, hidden, dtype):
+    """256 tiles of 256 x 256, one to a CU: of the forward, of the gradient of x, of the
+    weights', of both the first and the last."""
+    say("gated large", rows, width, hidden, dtype)
+    verify(*make((rows, width), hidden, dtype, seed=16))
+
+
 @pytest.mark.parametrize("rows", [3, 80])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_tensors_that_start_anywhere(rows, dtype):
