@@ -137,6 +137,32 @@ def test_many_pairs_over_the_xcds():
 
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("dim", [8, 32, 40, 64, 72, 96, 104, 128])
+def test_many_pairs_of_short_sequences(dim, dtype):
+    """Waves with 32 rows (or keys) of their own: 864 blocks of 32 rows and more."""
+    say("attention many", dim, dtype)
+    t, d_out = make(16, 70, 90, 18, 18, dim, dtype, seed=dim + 1)
+    verify(t, d_out)
+    verify(t, d_out, causal=True)
+    t, d_out = make(20, 150, 131, 12, 4, dim, dtype, seed=dim + 2)
+    n = lengths(*(0, 1, 150, 149, 33, 32, 128, 129, 64, 96) * 2)
+    m = lengths(*(5, 131, 131, 0, 131, 64, 1, 33, 32, 96, 131, 20, 128, 130, 129, 3, 131, 90, 31, 0))
+    verify(t, d_out, query_lengths=n, key_lengths=m)
+    verify(t, d_out, causal=True, query_lengths=n, key_lengths=m)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("n,m,batch,dim", [(257, 130, 32, 128), (130, 257, 32, 104), (513, 300, 12, 128)])
+def test_eight_waves(n, m, batch, dim, dtype):
+    """1024 blocks of 256 rows or more: of the queries, of the keys, of both."""
+    say("attention eight", n, m, dtype)
+    t, d_out = make(batch, n, m, 32, 32, dim, dtype, seed=n)
+    verify(t, d_out)
+    some = lengths(*(range(1, 1 + n, n // batch))[:batch])
+    verify(t, d_out, query_lengths=some, key_lengths=lengths(*(range(m, 0, -(m // batch)))[:batch]))
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
 def test_strided_inputs(dtype):
     rng = torch.Generator(device="cuda").manual_seed(8)
     whole = torch.randn(2, 66, 8, 64, generator=rng, device="cuda").to(dtype)
