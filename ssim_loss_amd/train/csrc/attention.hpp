@@ -64,9 +64,7 @@ template <class T>
 constexpr int kAcrossSteps = 32 / kPerStep<T>;
 template <class T>
 constexpr int kAcrossRegs = kPerStep<T> / 2;
-// matrix instructions of a step, and reads of an operand across rows
-template <class T>
-constexpr int kInstructions = sizeof(T) == 4 ? 4 : 1;
+// reads of an operand across rows
 template <class T>
 constexpr int kAcrossReads = sizeof(T) == 4 ? 4 : 2;
 constexpr int kAhead = 4;

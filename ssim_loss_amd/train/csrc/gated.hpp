@@ -176,7 +176,7 @@ __device__ __forceinline__ TileAt tile_at(unsigned block, int m_tiles, int n_til
 // A wave's block of a result, kRows x kColumns, to memory: through its own part of
 // the LDS, so that neighbouring lanes have a row's neighbouring chunks.  Straight
 // from the registers each store would touch 32 rows with 16 bytes of each
-// (16384 x 4096 x 10944 bf16, with g and u: 3419 us, so 2680).
+// (16384 x 4096 x 10944 bf16, with g and u in bf16: 3419 us, so 2680).
 // In: value(i, j, k), the four columns 32 i + 8 k + 4 h of row 32 j + lane % 32.
 template <class T, int MB, int NB, class Value>
 __device__ __forceinline__ void store_block(Lds* region, T* out, int64_t pitch, int64_t row0, int64_t column0,
@@ -294,36 +294,54 @@ __device__ __forceinline__ void product_tile(const GatedParams& p, unsigned bloc
   };
   const int a_at = kProduct == kForward ? along_offset<Shape::kRow>() : across_offset<T, Shape::kM * kBytes, true>();
   const int b_at = kProduct == kGradW ? across_offset<T, Shape::kN * kBytes, true>() : along_offset<Shape::kRow>();
-  if (begin < end) {
-#pragma unroll
-    for (int t = 0; t < kStages - 1; ++t) fetch(begin + t);
-  }
-  for (int t = begin; t < end; ++t) {
-    landed_for_all<(kStages - 2) * Shape::kLoads>();
-    fetch(t + kStages - 1);
+  // A step's operands are read while the one before is multiplied, the next tile's first
+  // with this tile's last: its buffer is free once all waves have read that.
+  // 16384 x 4096 x 10944 bf16, with each step's read before its own products 2815 us
+  // forward, 2550 and 2715 the gradients, so 2580, 2280 and 2590.  (Four waves of twice
+  // the block each read less, but nothing runs beside a wave that waits: 3080, 2430, 2830.
+  // 64 bytes of depth in four buffers: 2830, 2550, 2740.)
+  Chunk a[2][BM], b[2][BN];
+  auto take = [&](int which_, int t, int s) {
     const Lds* a_tile = lds + ((t - begin) % kStages) * Shape::kBytes;
     const Lds* b_tile = a_tile + Shape::kABytes;
 #pragma unroll
+    for (int i = 0; i < BM; ++i) {
+      if constexpr (kProduct == kForward)
+        a[which_][i] = lds_along<Shape::kRow>(a_tile, a_at, 32 * a_block(i), s);
+      else
+        a[which_][i] = lds_across<T, Shape::kM * kBytes, true>(a_tile, a_at, s * kPerStep<T>, a_block(i));
+    }
+#pragma unroll
+    for (int i = 0; i < BN; ++i) {
+      if constexpr (kProduct == kGradW)
+        b[which_][i] = lds_across<T, Shape::kN * kBytes, true>(b_tile, b_at, s * kPerStep<T>, wn * BN + i);
+      else
+        b[which_][i] = lds_along<Shape::kRow>(b_tile, b_at, 32 * (wn * BN + i), s);
+    }
+  };
+  static_assert(Shape::kSteps % 2 == 0, "the next tile's first step goes where this one's did");
+  if (begin < end) {
+#pragma unroll
+    for (int t = 0; t < kStages; ++t) fetch(begin + t);
+    landed_for_all<(kStages - 1) * Shape::kLoads>();
+    take(0, begin, 0);
+  }
+  for (int t = begin; t < end; ++t) {
+#pragma unroll
     for (int s = 0; s < Shape::kSteps; ++s) {
-      Chunk a[BM], b[BN];
-#pragma unroll
-      for (int i = 0; i < BM; ++i) {
-        if constexpr (kProduct == kForward)
-          a[i] = lds_along<Shape::kRow>(a_tile, a_at, 32 * a_block(i), s);
-        else
-          a[i] = lds_across<T, Shape::kM * kBytes, true>(a_tile, a_at, s * kPerStep<T>, a_block(i));
-      }
-#pragma unroll
-      for (int i = 0; i < BN; ++i) {
-        if constexpr (kProduct == kGradW)
-          b[i] = lds_across<T, Shape::kN * kBytes, true>(b_tile, b_at, s * kPerStep<T>, wn * BN + i);
-        else
-          b[i] = lds_along<Shape::kRow>(b_tile, b_at, 32 * (wn * BN + i), s);
+      if (s + 1 < Shape::kSteps) {
+        take((s + 1) % 2, t, s + 1);
+      } else {
+        landed_for_all<(kStages - 2) * Shape::kLoads>();
+        fetch(t + kStages);
+        take(0, t + 1, 0);
       }
 #pragma unroll
       for (int i = 0; i < BM; ++i)
 #pragma unroll
-        for (int j = 0; j < BN; ++j) multiply<T>(c[i][j], a[i], b[j]);
+        for (int j = 0; j < BN; ++j) multiply<T>(c[i][j], a[s % 2][i], b[s % 2][j]);
+      // (2680 without; across rows a read is two, and the gradients were slower with it)
+      if constexpr (kProduct == kForward) read_between<BM + BN, BM * BN * kInstructions<T>>();
     }
   }
 
@@ -636,13 +654,13 @@ GatedTable make_gated_table() {
   GatedTable t;
   t.product[kForward][0] = (const void*)gated_product<T, kForward, 2, 1, 2, 2, 128, 3>;
   t.product[kForward][1] = (const void*)gated_product<T, kForward, 2, 2, 2, 2, 128, 2>;
-  t.product[kForward][2] = (const void*)gated_product<T, kForward, 4, 2, 2, 4, 64, 4>;
+  t.product[kForward][2] = (const void*)gated_product<T, kForward, 4, 2, 2, 4, 128, 2>;
   t.product[kGradX][0] = (const void*)gated_product<T, kGradX, 1, 1, 2, 2, 128, 3>;
   t.product[kGradX][1] = (const void*)gated_product<T, kGradX, 2, 2, 2, 2, 128, 2>;
-  t.product[kGradX][2] = (const void*)gated_product<T, kGradX, 4, 2, 2, 4, 64, 4>;
+  t.product[kGradX][2] = (const void*)gated_product<T, kGradX, 4, 2, 2, 4, 128, 2>;
   t.product[kGradW][0] = (const void*)gated_product<T, kGradW, 1, 1, 2, 2, 128, 3>;
   t.product[kGradW][1] = (const void*)gated_product<T, kGradW, 2, 2, 2, 2, 128, 2>;
-  t.product[kGradW][2] = (const void*)gated_product<T, kGradW, 4, 2, 2, 4, 64, 4>;
+  t.product[kGradW][2] = (const void*)gated_product<T, kGradW, 4, 2, 2, 4, 128, 2>;
   t.few[0] = (const void*)gated_few_rows<T, 1>;
   t.few[1] = (const void*)gated_few_rows<T, 2>;
   t.few[2] = (const void*)gated_few_rows<T, 4>;

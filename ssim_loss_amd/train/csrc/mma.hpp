@@ -141,6 +141,10 @@ __device__ __forceinline__ Chunk lds_across(const Lds* tile, int offset, int row
   }
 }
 
+// matrix instructions of a product of two operands
+template <class T>
+constexpr int kInstructions = sizeof(T) == 4 ? 4 : 1;
+
 // ---- order of instructions.  Left alone the compiler reads an operand from LDS just
 // before the instruction that needs it and waits.  These lines, behind a sequence of
 // products in the same basic block, ask for kAhead products' reads before the first
@@ -157,6 +161,17 @@ __device__ __forceinline__ void read_ahead() {
     } else if (i + kAhead < N0 + N1) {
       if constexpr (R1 > 0) __builtin_amdgcn_sched_group_barrier(kLdsRead, R1, 0);
     }
+  }
+}
+
+// ... and here, for R reads spread between N instructions that do not need them.
+template <int R, int N>
+__device__ __forceinline__ void read_between() {
+  constexpr int kLdsRead = 0x100, kMatrix = 0x8, kEach = (R + N - 1) / N;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(kMatrix, 1, 0);
+    if (i * kEach < R) __builtin_amdgcn_sched_group_barrier(kLdsRead, kEach, 0);
   }
 }
 
