@@ -41,6 +41,11 @@ The rest of a training step (the ``train`` subpackage, with a C ABI of its own):
   clip_grads_(grads, max_norm, out=None), grad_norm(grads)
   AdamW(params, lr, ..., max_norm=None).step(grads)
   block_norm(x, branch, gate, scale, post_weight, pre_weight) -> (residual, normed)
+Inside a block of an image network (the same subpackage), with autograd:
+  rotary(q, k, positions, axes, base=10000.0, pairs="adjacent") -> (q, k) turned
+  attention(q, k, v, scale, causal, query_lengths, key_lengths) -> the attended values
+  gated_linear(x, w_gate, w_up, b_gate, b_up, act="silu")
+      -> act(x w_gate^T + b_gate) * (x w_up^T + b_up)
 """
 from __future__ import annotations
 

@@ -8,7 +8,9 @@
 // are the left operand.  Both operands go from memory straight to LDS, two tiles
 // in turn, 128 bytes of the axis that is summed over in each.  The forward's left
 // tile is half Wg's and half Wu's rows, so a wave has g and u of the same elements
-// in its registers and neither has to be written for the product.
+// in its registers and neither has to be written for the product.  The bound is the matrix
+// instructions and the clock under them (1.75 to 1.8 GHz): 16384 x 4096 x 10944 bf16, dx
+// 1.27 PFLOP/s, dW 1.13, forward 1.11 with g and u written (a library product 1.32).
 
 #pragma once
 
@@ -541,7 +543,8 @@ __global__ void __launch_bounds__(256) gated_copy(const GatedParams p) {
 }
 
 // ---- few rows: the weights go by once, from memory straight to the matrix
-// instruction (16 rows of weights, 16 of x); four waves share the summed axis.
+// instruction (16 rows of weights, 16 of x); four waves share the summed axis.  The bound
+// is the memory: 1 x 4096 x 10944 bf16, 179 MB in 37.8 us, 4.8 TB/s.
 typedef float Sums4 __attribute__((ext_vector_type(4)));
 template <class T>
 __device__ __forceinline__ void multiply16(Sums4& c, Chunk a, Chunk b) {
