@@ -101,6 +101,15 @@ def test_the_large_tiles_of_each_product(rows, width, hidden, dtype):
     verify(*make((rows, width), hidden, dtype, seed=16))
 
 
+@pytest.mark.parametrize("rows,width,hidden,dtype", [
+    (145, 34, 438, BF16), (132, 35, 115, F32), (730, 36, 34, F16), (233, 35, 32, F32), (3270, 67, 2248, F32),
+    (8651, 785, 66, F32), (36639, 2095, 69, BF16), (135, 4249, 6778, F32), (5774, 145, 4180, F32)])
+def test_the_summed_axis_in_parts(rows, width, hidden, dtype):
+    """Of the gradient of x or the weights', with each size of tile."""
+    say("gated parts", rows, width, hidden, dtype)
+    verify(*make((rows, width), hidden, dtype, seed=17))
+
+
 @pytest.mark.parametrize("rows", [3, 80])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_tensors_that_start_anywhere(rows, dtype):
