@@ -197,6 +197,13 @@ __device__ __forceinline__ Seen seen_of(const AttentionParams& p, int b) {
 __device__ __forceinline__ int last_key(const Seen& s, int i) {
   return i < s.q_length ? min(s.k_length - 1, i + s.shift) : -1;
 }
+// ... and the last whose score matters: a row that sees one key gives it all, whatever its
+// score, and has no gradient, where do . v - do . o would leave its roundings.  (Such rows
+// come first of those that see any: the comparisons are made wherever they are.)
+__device__ __forceinline__ int last_with_slope(const Seen& s, int i) {
+  const int last = last_key(s, i);
+  return last == 0 ? -1 : last;
+}
 // Of the rows from `first` to `end`, all of a group's heads a token: the last key that
 // each of them sees (past it scores are compared), and the last that any does (past it
 // there is nothing to do).
@@ -556,7 +563,7 @@ __device__ __forceinline__ void grad_q_tile(const AttentionParams& p, unsigned b
   const int row = there ? row_ : 0;
   const int token = row / p.group, head = at.kvh * p.group + row % p.group;
   const bool live = there && token < seen.q_length;
-  const int last = there ? last_key(seen, token) : -1;
+  const int last = there ? last_with_slope(seen, token) : -1;
   const int64_t dense = (((int64_t)at.b * p.q_tokens + token) * p.heads + head) * p.dim;
   const int64_t stat = ((int64_t)at.b * p.heads + head) * p.q_tokens + token;
 
@@ -810,9 +817,8 @@ __device__ __forceinline__ void grad_kv_tile(const AttentionParams& p, unsigned 
       if (last_key(seen, token + in_tile) < wave_key + 31 || token + in_tile + 31 >= seen.q_length) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          const bool hidden = key > last_key(seen, token + in_tile + row_of(r));
-          s[r] = hidden ? 0.0f : s[r];
-          ds[r] = hidden ? 0.0f : ds[r];
+          s[r] = key > last_key(seen, token + in_tile + row_of(r)) ? 0.0f : s[r];
+          ds[r] = key > last_with_slope(seen, token + in_tile + row_of(r)) ? 0.0f : ds[r];
         }
       }
       across<T, DB>(dv, d_tile, fresh(across_at), in_tile, s);

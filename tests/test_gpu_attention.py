@@ -250,6 +250,18 @@ def test_no_tokens(n, m):
     assert out.shape == t["q"].shape
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("batch,n", [(2, 1), (2, 40), (30, 300)])
+def test_a_row_of_one_key_has_no_gradient(batch, n, dtype):
+    """It gives that key all, whatever their product is."""
+    t, d_out = make(batch, n, n, 4, 2, 64, dtype, seed=19)
+    _, grads = verify(t, d_out, causal=True)
+    assert not grads["q"][:, 0].any()
+    m = lengths(*(1 for _ in range(batch)))
+    _, grads = verify(t, d_out, key_lengths=m)
+    assert not grads["q"].any() and not grads["k"].any() and grads["v"][:, 0].any()
+
+
 def test_the_same_bits_again():
     t, d_out = make(2, 500, 700, 6, 2, 72, F16, seed=14)
     a, b = run(t, d_out, causal=True), run(t, d_out, causal=True)
