@@ -344,7 +344,8 @@ def gated_linear(x, w_gate, w_up, b_gate=None, b_up=None, act="silu"):
 
     Returns [..., hidden].  Sums are float32, and where gradients are wanted the two
     projections are kept in float32 for the backward, whose gradients of them are
-    rounded to the type before the products.  Gradients of all inputs are
+    rounded to the type before the products (float16: times a power of two that brings the
+    largest into its range).  Gradients of all inputs are
     available, gradients of gradients are not."""
     kind = GATED_ACT.get(act)
     if kind is None:

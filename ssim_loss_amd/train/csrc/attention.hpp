@@ -467,8 +467,6 @@ __global__ void __launch_bounds__(kAttentionThreads) attention_join(const Attent
 // 2^e, with |ds_ij| <= 2 max |do_i| max |v_j| kept below 2^15; the products are
 // divided again in fp32.
 constexpr int kNormParts = 16;
-template <class T>
-constexpr bool kScaled = __is_same(T, F16);
 
 // Each of kNormParts workgroups of a (batch, key head) takes a part of its rows and
 // keys, 16 lanes to one.

@@ -32,6 +32,9 @@ struct GatedParams {
   const void* d_out;    // [rows][hidden]
   void* d[2];           // dg, du: [rows][h_pitch], zeros behind hidden
   float* part_bias;     // [blocks of rows][2][hidden] or NULL
+  float* tops;          // fp16: of each workgroup of gated_tops, the largest finite |dg| and |du|; NULL: not wanted
+  int* range;           // ... and the power of two that dg and du are kept times.  NULL: 0
+  int top_count;
   int row_blocks;
   int rows_of_block;
   void* dx;             // [rows][width]
@@ -384,12 +387,14 @@ __device__ __forceinline__ void product_tile(const GatedParams& p, unsigned bloc
   } else {
     const int64_t rows = kProduct == kGradX ? p.rows : p.hidden;
     constexpr int MB = BM < 2 ? 1 : 2;  // at once
+    const float down = kScaled<T> && p.range ? ldexpf(1.0f, -*p.range) : 1.0f;
 #pragma unroll
     for (int i0 = 0; i0 < BM; i0 += MB) {
       const int64_t column0 = m0 + 32 * (wm * BM + i0);
       auto value = [&](int i, int j, int k) {
         const Sums& s = c[i0 + i][j];
-        return Wide<4>{s[4 * k], s[4 * k + 1], s[4 * k + 2], s[4 * k + 3]};
+        const Wide<4> v = {s[4 * k], s[4 * k + 1], s[4 * k + 2], s[4 * k + 3]};
+        return kScaled<T> ? v * down : v;
       };
       if (splits > 1) {
         float* to = p.part[kProduct] + ((int64_t)split * (kProduct == kGradW ? 2 : 1) + which) * rows * p.width;
@@ -470,43 +475,98 @@ __global__ void __launch_bounds__(256) gated_finish(const GatedParams p) {
   }
 }
 
-// dg and du, and what they add up to over a block of rows.  A thread has a vector
+// dg and du of a workgroup's rows and columns: take(place, dg, du).  A thread has a vector
 // of columns; 64 of them beside each other, four rows at a time.
+template <class T, class Take>
+__device__ __forceinline__ void each_slope(const GatedParams& p, int64_t column, Take take) {
+  constexpr int V = kPerChunk<T>;
+  const int64_t first = (int64_t)blockIdx.y * p.rows_of_block;
+  const int64_t end = first + p.rows_of_block < p.rows ? first + p.rows_of_block : p.rows;
+  if (column >= p.h_pitch) return;
+  for (int64_t row = first + threadIdx.x / kWave; row < end; row += 4) {
+    const int64_t at = row * p.h_pitch + column;
+    const Wide<V> g = load_once<float, V>(p.saved[0] + at), u = load_once<float, V>(p.saved[1] + at);
+    const T* d_row = static_cast<const T*>(p.d_out) + row * p.hidden;
+    Wide<V> d = {};
+    if (column + V <= p.hidden) d = widen<T, V>(load<T, V>(d_row + column));
+    else
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (column + k < p.hidden) d[k] = (float)d_row[column + k];
+    Wide<V> dg, du;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      float a, slope;
+      act_slope<T>(g[k], p.act, a, slope);
+      const bool in = column + k < p.hidden;
+      dg[k] = in ? d[k] * u[k] * slope : 0.0f;
+      du[k] = in ? d[k] * a : 0.0f;
+    }
+    take(at, dg, du);
+  }
+}
+
+// The largest number of a workgroup's threads, none of them below 0, for all of them.
+__device__ __forceinline__ float largest_of(float v) {
+  __shared__ float most[4];
+  for (int step = 1; step < kWave; step *= 2) v = fmaxf(v, __shfl_xor(v, step));
+  if ((threadIdx.x & (kWave - 1)) == 0) most[threadIdx.x / kWave] = v;
+  __syncthreads();
+  return fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+}
+
+// The largest |dg| and |du| of a workgroup's share, by which fp16's are brought into its range: left
+// as they are, gradients scaled by 2^16 overflow, and of those of 10^-6 dw is 2% off.  What is not finite is
+// left out.  A read of g, u and d_out more, the memory's bound: forward and gradients of 16384 x 4096 x 10944
+// fp16 8340, so 8720 us, 4100 x 1153 x 2997 322, so 348.  (A bound by the norms of rows would need x and the
+// weights alone, but may be far too large.)
+template <class T>
+__global__ void __launch_bounds__(256) gated_tops(const GatedParams p) {
+  constexpr int V = kPerChunk<T>;
+  const int64_t column = ((int64_t)blockIdx.x * kWave + (threadIdx.x & (kWave - 1))) * V;
+  float top = 0.0f;
+  each_slope<T>(p, column, [&](int64_t, Wide<V> dg, Wide<V> du) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const float a = fabsf(dg[k]), b = fabsf(du[k]);
+      if (a < INFINITY) top = fmaxf(top, a);
+      if (b < INFINITY) top = fmaxf(top, b);
+    }
+  });
+  top = largest_of(top);
+  if (threadIdx.x == 0) p.tops[blockIdx.y * gridDim.x + blockIdx.x] = top;
+}
+
+// dg and du, and what they add up to over a block of rows.
 template <class T>
 __global__ void __launch_bounds__(256) gated_slopes(const GatedParams p) {
   constexpr int V = kPerChunk<T>;
   __shared__ float sums[3][2][kWave * V];
   const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
   const int64_t column = ((int64_t)blockIdx.x * kWave + lane) * V;
-  const int64_t first = (int64_t)blockIdx.y * p.rows_of_block;
-  const int64_t end = first + p.rows_of_block < p.rows ? first + p.rows_of_block : p.rows;
-  Wide<V> total[2] = {};
-  if (column < p.h_pitch) {
-    for (int64_t row = first + wave; row < end; row += 4) {
-      const int64_t at = row * p.h_pitch + column;
-      const Wide<V> g = load_once<float, V>(p.saved[0] + at), u = load_once<float, V>(p.saved[1] + at);
-      const T* d_row = static_cast<const T*>(p.d_out) + row * p.hidden;
-      Wide<V> d = {};
-      if (column + V <= p.hidden) d = widen<T, V>(load<T, V>(d_row + column));
-      else
-#pragma unroll
-        for (int k = 0; k < V; ++k)
-          if (column + k < p.hidden) d[k] = (float)d_row[column + k];
-      Wide<V> dg, du;
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        float a, slope;
-        act_slope<T>(g[k], p.act, a, slope);
-        const bool in = column + k < p.hidden;
-        dg[k] = in ? d[k] * u[k] * slope : 0.0f;
-        du[k] = in ? d[k] * a : 0.0f;
-      }
-      store<T, V>(static_cast<T*>(p.d[0]) + at, narrow<T, V>(dg));
-      store<T, V>(static_cast<T*>(p.d[1]) + at, narrow<T, V>(du));
-      total[0] += dg;
-      total[1] += du;
+  float up = 1.0f;
+  if constexpr (kScaled<T>) {
+    if (p.tops) {
+      float top = 0.0f;
+      for (int k = threadIdx.x; k < p.top_count; k += 256) top = fmaxf(top, p.tops[k]);
+      top = largest_of(top);
+      // (top < 2^exponent: the largest is kept below 2^15)
+      const int range = top > 0.0f ? min(15 - __builtin_amdgcn_frexp_expf(top), 100) : 0;
+      up = ldexpf(1.0f, range);
+      if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.range = range;
     }
   }
+  Wide<V> total[2] = {};
+  each_slope<T>(p, column, [&](int64_t at, Wide<V> dg, Wide<V> du) {
+    total[0] += dg;
+    total[1] += du;
+    if constexpr (kScaled<T>) {
+      dg *= up;
+      du *= up;
+    }
+    store<T, V>(static_cast<T*>(p.d[0]) + at, narrow<T, V>(dg));
+    store<T, V>(static_cast<T*>(p.d[1]) + at, narrow<T, V>(du));
+  });
   if (!p.part_bias) return;
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -647,6 +707,7 @@ __global__ void __launch_bounds__(256) gated_few_rows(const GatedParams p) {
 struct GatedTable {
   const void* product[3][3];  // [Product][tiles of 64, 128, 256 rows]
   const void* few[3];         // 16, 32, 64 rows
+  const void* tops;           // NULL: not needed
   const void* slopes;
   const void* both;
   const void* finish;
@@ -667,6 +728,8 @@ GatedTable make_gated_table() {
   t.few[0] = (const void*)gated_few_rows<T, 1>;
   t.few[1] = (const void*)gated_few_rows<T, 2>;
   t.few[2] = (const void*)gated_few_rows<T, 4>;
+  t.tops = nullptr;
+  if constexpr (kScaled<T>) t.tops = (const void*)gated_tops<T>;
   t.slopes = (const void*)gated_slopes<T>;
   t.both = (const void*)gated_both<T>;
   t.finish = (const void*)gated_finish<T>;

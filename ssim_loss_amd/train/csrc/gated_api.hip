@@ -179,19 +179,22 @@ Slopes slopes_of(const ssim_gated_linear_inputs& in) {
   return s;
 }
 
+size_t top_count(const Slopes& s) { return (size_t)s.column_blocks * s.row_blocks; }
+
 struct BackwardSpace {
   Copies copies;
-  size_t d, bias, part[3], total;
+  size_t d, bias, tops, part[3], total;
 };
 BackwardSpace space_of(const ssim_gated_linear_inputs& in) {
   BackwardSpace s;
   s.copies = copies_of(in);
   s.d = (size_t)in.rows * padded(in, in.hidden) * elem_bytes(in.dtype);
   s.bias = to_16((size_t)slopes_of(in).row_blocks * 2 * in.hidden * 4);
+  s.tops = table_of(in.dtype).tops ? to_16(4 * top_count(slopes_of(in))) + 16 : 0;  // (the range behind them)
   s.part[kForward] = 0;
   s.part[kGradX] = part_bytes(in, kGradX);
   s.part[kGradW] = part_bytes(in, kGradW);
-  s.total = s.copies.x + 2 * s.copies.w + 2 * s.d + s.bias + s.part[kGradX] + s.part[kGradW];
+  s.total = s.copies.x + 2 * s.copies.w + 2 * s.d + s.bias + s.tops + s.part[kGradX] + s.part[kGradW];
   return s;
 }
 
@@ -306,10 +309,18 @@ int ssim_gated_linear_backward(const ssim_gated_linear_inputs* in, const float* 
     p.d[0] = at;
     p.d[1] = at + space.d;
     p.part_bias = biases ? reinterpret_cast<float*>(at + 2 * space.d) : nullptr;
+    if (t.tops && (weights || grads->x)) {
+      char* tops = at + 2 * space.d + space.bias;
+      p.tops = reinterpret_cast<float*>(tops);
+      p.range = reinterpret_cast<int*>(tops + space.tops - 16);
+      p.top_count = (int)top_count(s);
+      rc = launch(t.tops, dim3(s.column_blocks, s.row_blocks), 256, p, stream);
+      if (rc != SSIM_OK) return rc;
+    }
     rc = launch(t.slopes, dim3(s.column_blocks, s.row_blocks), 256, p, stream);
     if (rc != SSIM_OK) return rc;
   }
-  char* part = at + 2 * space.d + space.bias;
+  char* part = at + 2 * space.d + space.bias + space.tops;
   const Choice x = choose(*in, kGradX), w = choose(*in, kGradW);
   set_product(p, x, kGradX, part);
   set_product(p, w, kGradW, part + space.part[kGradX]);

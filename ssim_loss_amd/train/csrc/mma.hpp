@@ -26,6 +26,11 @@ constexpr int kPerChunk = 16 / (int)sizeof(T);
 template <class T>
 constexpr int kPerStep = 2 * kPerChunk<T>;
 
+// fp16 ends at 65504 and loses bits below 2^-14, so what is rounded to it between two
+// products is taken times a power of two, which the second's sums are divided by.
+template <class T>
+constexpr bool kScaled = __is_same(T, F16);
+
 // c += a b over one step
 template <class T>
 __device__ __forceinline__ void multiply(Sums& c, Chunk a, Chunk b) {

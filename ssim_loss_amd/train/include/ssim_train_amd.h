@@ -315,7 +315,9 @@ int ssim_gated_linear_forward(const ssim_gated_linear_inputs* in, void* out, flo
                               void* workspace, void* stream);
 
 /* The gradients for d_out ([rows, hidden]), each of its input's shape; NULL: not
- * wanted.  Those of g and u are rounded to dtype before the products. */
+ * wanted.  Those of g and u are rounded to dtype before the products (fp16: times a
+ * power of two, by which the products' sums are divided, that brings the largest of
+ * them that is finite into its range). */
 typedef struct {
   void* x;
   void* w_gate;
