@@ -32,7 +32,9 @@ struct AttentionParams {
   int q_tokens, k_tokens, heads, kv_heads, group, dim, batch;
   int causal, spread;  // spread: (batch, key head) pairs are dealt out over the XCDs
   int tiles, splits;   // of rows (or keys); parts of the keys that workgroups of their own take
-  float scale, scale2; // scale2 = scale log2(e)
+  float scale2;        // scale log2(e), not 0: of a masked score it is a factor
+  float scale;         // scale 2^scale_power is the scale, of which fp32 would hold few bits below 2^-126
+  int scale_power;
   void* out;           // [batch][q_tokens][heads][dim]
   void* rest;          // as out: what out's rounding left, rounded itself; NULL: not wanted, or fp32
   float* lse;          // [batch][heads][q_tokens], log2 of the row's sum; +inf: no keys.  NULL: not wanted
@@ -163,9 +165,18 @@ __device__ __forceinline__ void store_with_rest(T* to, T* rest, Wide<4> v) {
   if constexpr (sizeof(T) == 2)
     if (rest) store<T, 4>(rest, narrow<T, 4>(v - widen<T, 4>(n)));
 }
-// A lane's row of the result, of which it holds the columns row_of() of each block.
+// v times factor 2^power
+template <int N>
+__device__ __forceinline__ Wide<N> times(Wide<N> v, float factor, int power) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = __builtin_amdgcn_ldexpf(v[k] * factor, power);
+  return v;
+}
+// A lane's row of the result, of which it holds the columns row_of() of each block,
+// times factor 2^power.
 template <class T, int DB>
-__device__ __forceinline__ void store_row(T* row, const Sums (&v)[DB], float factor, int dim, T* rest = nullptr) {
+__device__ __forceinline__ void store_row(T* row, const Sums (&v)[DB], float factor, int dim, T* rest = nullptr,
+                                          int power = 0) {
   const int h = threadIdx.x >> 5 & 1;
 #pragma unroll
   for (int d = 0; d < DB; ++d)
@@ -174,8 +185,8 @@ __device__ __forceinline__ void store_row(T* row, const Sums (&v)[DB], float fac
       const int column = 32 * d + 8 * k + 4 * h;
       Wide<4> w;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = v[d][4 * k + e] * factor;
-      if (column < dim) store_with_rest<T>(row + column, rest ? rest + column : nullptr, w);
+      for (int e = 0; e < 4; ++e) w[e] = v[d][4 * k + e];
+      if (column < dim) store_with_rest<T>(row + column, rest ? rest + column : nullptr, times<4>(w, factor, power));
     }
 }
 
@@ -645,14 +656,14 @@ __device__ __forceinline__ void grad_q_tile(const AttentionParams& p, unsigned b
   }
   landed_for_all();  // what was fetched past the end, too
   T* to = static_cast<T*>(p.dq) + dense;
-  const float factor = ldexpf(p.scale, -range);
+  const int power = p.scale_power - range;
   if constexpr (KW == 1) {
-    if (there && p.dq) store_row<T, DB>(to, dq, factor, p.dim);
+    if (there && p.dq) store_row<T, DB>(to, dq, p.scale, p.dim, nullptr, power);
   } else {
     give_to_join<DB>(lds_, dq);
     landed_for_all();
     if (there && p.dq)
-      take_joined<DB>(lds_, p.dim, [&](int c, Wide<4> sum) { store<T, 4>(to + c, narrow<T, 4>(sum * factor)); });
+      take_joined<DB>(lds_, p.dim, [&](int c, Wide<4> sum) { store<T, 4>(to + c, narrow<T, 4>(times<4>(sum, p.scale, power))); });
   }
 }
 
@@ -831,16 +842,17 @@ __device__ __forceinline__ void grad_kv_tile(const AttentionParams& p, unsigned 
   landed_for_all();  // what was fetched past the end, too
   const int64_t dense = (((int64_t)at.b * p.k_tokens + key_read) * p.kv_heads + at.kvh) * p.dim;
   T *to_k = p.dk ? static_cast<T*>(p.dk) + dense : nullptr, *to_v = p.dv ? static_cast<T*>(p.dv) + dense : nullptr;
-  const float k_factor = ldexpf(p.scale, -range), v_factor = ldexpf(1.0f, -kLift<T>);
+  const int power = p.scale_power - range;
+  const float v_factor = ldexpf(1.0f, -kLift<T>);
   const bool there = key < p.k_tokens;
   if constexpr (KW == 1) {
-    if (there && to_k) store_row<T, DB>(to_k, dk, k_factor, p.dim);
+    if (there && to_k) store_row<T, DB>(to_k, dk, p.scale, p.dim, nullptr, power);
     if (there && to_v) store_row<T, DB>(to_v, dv, v_factor, p.dim);
   } else {
     give_to_join<DB>(lds_, dk);
     landed_for_all();
     if (there && to_k)
-      take_joined<DB>(lds_, p.dim, [&](int c, Wide<4> sum) { store<T, 4>(to_k + c, narrow<T, 4>(sum * k_factor)); });
+      take_joined<DB>(lds_, p.dim, [&](int c, Wide<4> sum) { store<T, 4>(to_k + c, narrow<T, 4>(times<4>(sum, p.scale, power))); });
     landed_for_all();
     give_to_join<DB>(lds_, dv);
     landed_for_all();

@@ -124,8 +124,9 @@ AttentionParams params_of(const ssim_attention_inputs& in, const Plan& plan) {
   p.batch = (int)in.batch;
   p.causal = in.causal;
   p.spread = in.batch * in.kv_heads % 8 == 0;
-  p.scale = (float)in.scale;
+  p.scale = (float)frexp(in.scale, &p.scale_power);
   p.scale2 = (float)(in.scale * 1.4426950408889634);
+  if (p.scale2 == 0.0f) p.scale2 = 0x1p-149f;  // (times any score it is next to nothing, and times minus infinity that)
   p.splits = plan.splits;
   p.tiles = plan.forward.tiles;
   return p;

@@ -253,7 +253,7 @@ typedef struct {
   int32_t causal;
   int32_t dtype;
   int32_t reserved;    /* 0 */
-  double scale;        /* > 0 */
+  double scale;        /* > 0; at most 3.4e37 */
 } ssim_attention_inputs;
 
 /* Bytes of the workspace (16-byte aligned) of the forward; 0 also where it needs
