@@ -192,6 +192,17 @@ __device__ __forceinline__ void store_row(T* row, const Sums (&v)[DB], float fac
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 
+// What is subtracted from the scaled scores of a row whose largest score is `top`.  It is rounded, by up
+// to 2^-24 of itself, and 2 to that is in all of the row's probabilities, which hold it while it is below
+// 2^7 (fp16: 2^4).  A row past that is NaN, not one that has lost its keys; one as far below 0 gives zeros,
+// as one of minus infinity does.
+template <class T>
+__device__ __forceinline__ float base_of(const AttentionParams& p, float top) {
+  constexpr float kMost = kScaled<T> ? 0x1p27f : 0x1p31f;
+  const float base = top * p.scale2;
+  return top == -INFINITY ? 0.0f : base < kMost ? fmaxf(base, -kMost) : NAN;
+}
+
 // What rows see: of sequence b the first q_length queries, the first k_length
 // keys; with causal order the last query sees the last key.
 struct Seen {
@@ -371,7 +382,7 @@ attention_forward(const AttentionParams p) {
       if (__any(top > limit)) {
         const float before = m == -INFINITY ? -INFINITY : base;
         m = fmaxf(m, top);
-        base = m == -INFINITY ? 0.0f : m * p.scale2;
+        base = base_of<T>(p, m);
         limit = m + slack;
         const float less = exp2_fast(before - base);
         l *= less;
@@ -404,7 +415,7 @@ attention_forward(const AttentionParams p) {
 #pragma unroll
     for (int w = 1; w < 4; ++w) top = fmaxf(top, joined[0][w][lane & 31]);
     const float before = m == -INFINITY ? -INFINITY : base;
-    base = top == -INFINITY ? 0.0f : top * p.scale2;
+    base = base_of<T>(p, top);
     const float less = exp2_fast(before - base);
     l *= less;
     if (lane < 32) joined[1][wave][lane] = l;

@@ -1,8 +1,9 @@
-"""Attention at the ends of its range: scales that fp32 does not hold."""
+"""Attention at the ends of its range: scales that fp32 does not hold, scores past fp32."""
 
 import pytest
 import torch
 
+import ssim_loss_amd as S
 from block_oracle import Attention
 from test_gpu_attention import lengths, make, run
 
@@ -34,3 +35,39 @@ def test_gradients_with_a_scale_that_fp32_holds_in_few_bits(n, scale):
     want = Attention(t["q"], t["k"], t["v"], scale=scale, d_out=d_out)
     assert want.value["q"].abs().max() > 1e-20
     want.check("q", grads["q"])
+
+
+SHAPES = [(40, 200), (300, 200), (1, 3000), (9000, 130)]  # rows shared by waves, keys in parts, rows of a wave's own
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("n,m", SHAPES)
+def test_scores_past_fp32_are_not_taken_for_rows_without_keys(n, m, dtype):
+    t, _ = make(1, n, m, 2, 2, 64, dtype, seed=53)
+    t["q"][:] = t["q"][:, :1].clone()
+    t["k"][:, 5] = 8 * t["q"][:, 0].sign()  # the largest score by far
+    for scale in (3e37, 1e30, 1e8):
+        assert torch.isnan(S.attention(t["q"], t["k"], t["v"], scale=scale)).all(), scale
+    for scale in (1e5, 1e3):
+        # that key has it all: its weight is rounded to a half type, the product with 1 / sum three
+        # times, the result once
+        out, want = S.attention(t["q"], t["k"], t["v"], scale=scale).double(), t["v"][:, 5:6].double()
+        step = 0.0 if dtype == F32 else torch.finfo(dtype).eps / 2
+        assert ((out - want).abs() <= want.abs() * (2.01 * step + 4 * 2.0 ** -24) + 2.0 ** -25).all(), scale
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n,m", SHAPES)
+@pytest.mark.parametrize("low", [-1e8, -1e12, -1e30, -3e38])
+def test_keys_far_below_the_others(low, n, m, dtype):
+    """They come first, and with the others they have no weight; rows that see no others give zeros."""
+    t, _ = make(1, n, m, 2, 2, 64, dtype, seed=54)
+    t["q"][..., 0] = 1.0
+    t["k"][..., 0] = 0.0
+    t["k"][:, :100, :, 1:] = 0.0
+    t["k"][:, :100, :, 0] = low
+    out = S.attention(t["q"], t["k"], t["v"])
+    want = Attention(t["q"], t["k"][:, 100:], t["v"][:, 100:])
+    want.check("out", out)
+    if low < -1e11:
+        assert not S.attention(t["q"], t["k"], t["v"], key_lengths=lengths(100)).any()
