@@ -196,11 +196,15 @@ __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_ex
 // to 2^-24 of itself, and 2 to that is in all of the row's probabilities, which hold it while it is below
 // 2^7 (fp16: 2^4).  A row past that is NaN, not one that has lost its keys; one as far below 0 gives zeros,
 // as one of minus infinity does.
+// fp16's probabilities are kept times 2^7, the most that its largest number leaves where they may be 2^8:
+// of 2^17 keys with 2^-26 of the largest weight each, 2^-9 of the result, nothing was left without.
 template <class T>
 __device__ __forceinline__ float base_of(const AttentionParams& p, float top) {
   constexpr float kMost = kScaled<T> ? 0x1p27f : 0x1p31f;
   const float base = top * p.scale2;
-  return top == -INFINITY ? 0.0f : base < kMost ? fmaxf(base, -kMost) : NAN;
+  if (top == -INFINITY) return 0.0f;
+  if (kScaled<T> && fabsf(base) < 0x1p23f) return base - 7.0f;
+  return base < kMost ? fmaxf(base, -kMost) : NAN;
 }
 
 // What rows see: of sequence b the first q_length queries, the first k_length

@@ -1,10 +1,13 @@
-"""Attention at the ends of its range: scales that fp32 does not hold, scores past fp32."""
+"""Attention at the ends of its range: scales that fp32 does not hold, scores past
+fp32, weights far below a row's largest in fp16."""
+import math
 
 import pytest
 import torch
 
 import ssim_loss_amd as S
 from block_oracle import Attention
+from gpu_util import say
 from test_gpu_attention import lengths, make, run
 
 pytestmark = pytest.mark.gpu
@@ -71,3 +74,23 @@ def test_keys_far_below_the_others(low, n, m, dtype):
     want.check("out", out)
     if low < -1e11:
         assert not S.attention(t["q"], t["k"], t["v"], key_lengths=lengths(100)).any()
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_weights_far_below_a_rows_largest_in_fp16(n):
+    """2^17 keys of 2^-26 of the largest weight each are 2^-9 of the result.  A weight,
+    rounded times 2^7 at least, is off by 2^-25 2^-7 = 2^-32 at most; a result by half a
+    step; the sums of positive terms by 2 m U of themselves."""
+    m, heads, dim = 1 << 17, 520, 32  # (heads enough that no keys are in parts, whose largest weights would differ)
+    k = torch.zeros(1, m, 1, dim, dtype=F16, device="cuda")
+    k[:, 0, :, 0] = 18.0
+    v = torch.ones(1, m, 1, dim, dtype=F16, device="cuda")
+    v[:, 0] = 0.0
+    q = torch.zeros(1, n, heads, dim, dtype=F16, device="cuda")
+    q[..., 0] = 1.0
+    say("attention", n, m)
+    out = S.attention(q, k.expand(1, m, heads, dim), v.expand(1, m, heads, dim), scale=1.0)
+    w = (m - 1) * math.exp(-18.0)
+    want = w / (1 + w)
+    off = float((out.double() - want).abs().max())
+    assert off <= m * 2.0 ** -32 + want * (2.0 ** -11 + 1e-5), (off, want)
