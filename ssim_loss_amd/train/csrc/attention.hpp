@@ -193,14 +193,14 @@ __device__ __forceinline__ void store_row(T* row, const Sums (&v)[DB], float fac
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 
 // What is subtracted from the scaled scores of a row whose largest score is `top`.  It is rounded, by up
-// to 2^-24 of itself, and 2 to that is in all of the row's probabilities, which hold it while it is below
-// 2^7 (fp16: 2^4).  A row past that is NaN, not one that has lost its keys; one as far below 0 gives zeros,
-// as one of minus infinity does.
+// to 2^-24 of itself, as is the limit from which scores raise it, and 2 to both is in the row's
+// probabilities beside the 2^8 that they may reach: 2^72 below 2^30, 2^12 below 2^26 (fp16).  A row past that
+// is NaN, not one that has lost its keys; one as far below 0 gives zeros, as one of minus infinity does.
 // fp16's probabilities are kept times 2^7, the most that its largest number leaves where they may be 2^8:
 // of 2^17 keys with 2^-26 of the largest weight each, 2^-9 of the result, nothing was left without.
 template <class T>
 __device__ __forceinline__ float base_of(const AttentionParams& p, float top) {
-  constexpr float kMost = kScaled<T> ? 0x1p27f : 0x1p31f;
+  constexpr float kMost = kScaled<T> ? 0x1p26f : 0x1p30f;
   const float base = top * p.scale2;
   if (top == -INFINITY) return 0.0f;
   if (kScaled<T> && fabsf(base) < 0x1p23f) return base - 7.0f;

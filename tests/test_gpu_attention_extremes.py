@@ -51,7 +51,7 @@ def test_scores_past_fp32_are_not_taken_for_rows_without_keys(n, m, dtype):
     t["k"][:, 5] = 8 * t["q"][:, 0].sign()  # the largest score by far
     for scale in (3e37, 1e30, 1e8):
         assert torch.isnan(S.attention(t["q"], t["k"], t["v"], scale=scale)).all(), scale
-    for scale in (1e5, 1e3):
+    for scale in (4e4, 1e3):
         # that key has it all: its weight is rounded to a half type, the product with 1 / sum three
         # times, the result once
         out, want = S.attention(t["q"], t["k"], t["v"], scale=scale).double(), t["v"][:, 5:6].double()
@@ -94,3 +94,20 @@ def test_weights_far_below_a_rows_largest_in_fp16(n):
     want = w / (1 + w)
     off = float((out.double() - want).abs().max())
     assert off <= m * 2.0 ** -32 + want * (2.0 ** -11 + 1e-5), (off, want)
+
+
+@pytest.mark.parametrize("dtype,most", [(F32, 2.0 ** 30), (F16, 2.0 ** 26), (BF16, 2.0 ** 30)])
+@pytest.mark.parametrize("n,m", SHAPES)
+def test_scores_up_to_the_bound_stay_numbers(n, m, dtype, most):
+    """Keys one after the other a little above those before, up to the largest score that is
+    taken: no probability passes the type, none of the row's keys is lost.  The largest differ
+    by less than fp32 tells apart, so the weights between them are free."""
+    dim = 8
+    steps = torch.linspace(0.97, 0.999, m, device="cuda", dtype=torch.float64)
+    for way in (steps, steps.flip(0), steps[torch.randperm(m, generator=torch.Generator().manual_seed(1)).cuda()]):
+        q, k = torch.zeros(1, n, 2, dim, device="cuda", dtype=dtype), torch.zeros(1, m, 2, dim, device="cuda", dtype=dtype)
+        q[..., 0], q[..., 1] = 1.0, 1.0
+        k[..., 0] = (way * 1024).to(dtype)[None, :, None]  # (a score is a sum of two, to tell more apart in a half type)
+        k[..., 1] = (way * 1024 - k[0, :, 0, 0].double()).to(dtype)[None, :, None]
+        out = S.attention(q, k, torch.ones_like(k), scale=most / 1.4427 / 1024)
+        assert ((out.double() - 1).abs() < 0.02).all()
