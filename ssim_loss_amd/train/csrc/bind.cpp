@@ -15,9 +15,10 @@ namespace {
 // ---- clipping
 Tensor clip(const py::object& grads_, double max_norm, const py::object& out_, bool scales) {
   check_tracing(scales ? "clip_grads_" : "grad_norm");
-  const List grads(grads_, "grads");
+  // (a norm and a scaling do not see the sign, as long as gradient and output have the same)
+  const List grads(grads_, "grads", true);
   const bool in_place = out_.is_none();
-  const List out(in_place ? grads_ : out_, "out");
+  const List out(in_place ? grads_ : out_, "out", true);
   if (out.size != grads.size) throw py::value_error("out must have as many tensors as grads");
   if (grads.size == 0) throw py::value_error("grads must hold at least one tensor");
   if (scales && !(max_norm >= 0.0 && max_norm <= 1.7976931348623157e308))
@@ -42,6 +43,10 @@ Tensor clip(const py::object& grads_, double max_norm, const py::object& out_, b
       if (o.sizes() != g.sizes())
         throw py::value_error(at_index("out", k) + " must have its gradient's shape");
       check_order(o, g, "out", k);
+      if (o.is_neg() != g.is_neg()) {
+        check_sign(o, "out", k);
+        check_sign(g, "grads", k);
+      }
     }
     it.out = o.data_ptr();
   }

@@ -87,15 +87,20 @@ inline void check_device(const Tensor& t, const c10::Device& dev, const char* na
                          t.device().str());
 }
 
-inline const Tensor& unpack(PyObject* o, const char* name, Py_ssize_t k = -1) {
+inline void check_sign(const Tensor& t, const char* name, Py_ssize_t k = -1) {
+  // (its memory holds the values with the other sign)
+  TORCH_CHECK_NOT_IMPLEMENTED(!t.is_neg(), at_index(name, k), " is a view with its sign turned: use resolve_neg()");
+}
+
+// any_sign: a view with its sign turned will do
+inline const Tensor& unpack(PyObject* o, const char* name, Py_ssize_t k = -1, bool any_sign = false) {
   if (!THPVariable_Check(o)) throw py::type_error(at_index(name, k) + " must be a torch.Tensor");
   const Tensor& t = THPVariable_Unpack(o);
   // (it would be left out of the results: these calls do not pass torch's dispatcher)
   TORCH_CHECK_NOT_IMPLEMENTED(!t._fw_grad(/*level=*/0).defined(), at_index(name, k),
                               " has a forward-mode tangent: forward-mode derivatives of the "
                               "training operators are not available");
-  // (its memory holds the values with the other sign)
-  TORCH_CHECK_NOT_IMPLEMENTED(!t.is_neg(), at_index(name, k), " is a view with its sign turned: use resolve_neg()");
+  if (!any_sign) check_sign(t, name, k);
   return t;
 }
 
@@ -114,15 +119,16 @@ inline void check_tracing(const char* what) {
 struct List {
   py::object fast;
   const char* name;
+  bool any_sign;
   Py_ssize_t size = 0;
-  List(const py::object& o, const char* name_) : name(name_) {
+  List(const py::object& o, const char* name_, bool any_sign_ = false) : name(name_), any_sign(any_sign_) {
     if (THPVariable_Check(o.ptr()) || !(PyList_Check(o.ptr()) || PyTuple_Check(o.ptr())))
       throw py::type_error(std::string(name) + " must be a list or tuple of tensors");
     fast = o;
     size = PySequence_Fast_GET_SIZE(o.ptr());
   }
   const Tensor& operator[](Py_ssize_t k) const {
-    return unpack(PySequence_Fast_GET_ITEM(fast.ptr(), k), name, k);
+    return unpack(PySequence_Fast_GET_ITEM(fast.ptr(), k), name, k, any_sign);
   }
   bool none(Py_ssize_t k) const { return PySequence_Fast_GET_ITEM(fast.ptr(), k) == Py_None; }
 };
