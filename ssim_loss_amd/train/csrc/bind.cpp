@@ -241,8 +241,8 @@ struct BlockNormBackward : torch::autograd::Node {
     grads.post_weight = (float*)wanted(4);
     grads.pre_weight = (float*)wanted(5);
     if (in.rows == 0) return out;
-    if (dr.defined()) dr = dr.contiguous();
-    if (dh.defined()) dh = dh.contiguous();
+    if (dr.defined()) dr = settled(dr).contiguous();
+    if (dh.defined()) dh = settled(dh).contiguous();
     const c10::DataPtr ws = scratch(ssim_block_norm_workspace_bytes(&in));
     const int rc = ssim_block_norm_backward(
         &in, stats.const_data_ptr<float>(), dr.defined() ? dr.const_data_ptr() : nullptr,

@@ -28,9 +28,6 @@ bool wants_gradient(std::initializer_list<const Tensor*> tensors) {
   return false;
 }
 
-// A gradient may arrive as a view with its sign turned, as from a complex number's conjugate.
-Tensor settled(const Tensor& t) { return t.is_neg() ? t.resolve_neg() : t; }
-
 // GPU tensors of one of the three types, any strides
 int check_strided(const Tensor& t, const char* name) {
   if (!t.device().is_cuda()) throw py::type_error(std::string(name) + " must be a GPU tensor, got device " + t.device().str());

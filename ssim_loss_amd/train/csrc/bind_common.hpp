@@ -92,6 +92,9 @@ inline void check_sign(const Tensor& t, const char* name, Py_ssize_t k = -1) {
   TORCH_CHECK_NOT_IMPLEMENTED(!t.is_neg(), at_index(name, k), " is a view with its sign turned: use resolve_neg()");
 }
 
+// A gradient may arrive as a view with its sign turned, as from a complex number's conjugate.
+inline Tensor settled(const Tensor& t) { return t.is_neg() ? t.resolve_neg() : t; }
+
 // any_sign: a view with its sign turned will do
 inline const Tensor& unpack(PyObject* o, const char* name, Py_ssize_t k = -1, bool any_sign = false) {
   if (!THPVariable_Check(o)) throw py::type_error(at_index(name, k) + " must be a torch.Tensor");

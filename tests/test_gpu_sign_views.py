@@ -35,3 +35,16 @@ def test_clipping_between_signs_is_refused():
     for grad, out in ((torch._neg_view(a), torch.zeros_like(a)), (a, torch._neg_view(torch.zeros_like(a)))):
         with pytest.raises(NotImplementedError, match="sign"):
             S.clip_grads_([grad], 1.0, out=[out])
+
+
+@pytest.mark.parametrize("which", ["residual", "normed", "both"])
+def test_a_gradient_that_arrives_at_the_joint_with_its_sign_turned(which):
+    x, branch = numbers(20, 64, seed=4).requires_grad_(True), numbers(20, 64, seed=5).requires_grad_(True)
+    post = (1 + 0.1 * numbers(64, seed=6)).requires_grad_(True)
+    outs = S.block_norm(x, branch, post_weight=post)
+    ups = [numbers(20, 64, seed=7), numbers(20, 64, seed=8)]
+    some = {"residual": [0], "normed": [1], "both": [0, 1]}[which]
+    leaves = (x, branch, post)
+    want = torch.autograd.grad([outs[k] for k in some], leaves, [-ups[k] for k in some], retain_graph=True)
+    got = torch.autograd.grad([outs[k] for k in some], leaves, [torch._neg_view(ups[k]) for k in some])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
