@@ -39,6 +39,10 @@ int check_strided(const Tensor& t, const char* name) {
   return code;
 }
 
+// (an expanded tensor has more heads than memory, and than the ABI's ints count)
+constexpr int64_t kMostHeads = 65536;
+[[noreturn]] void refuse_heads() { throw py::value_error("there must be at most " + std::to_string(kMostHeads) + " heads"); }
+
 Tensor dense_copy(const Tensor& t, const c10::Device& dev) {
   const at::NoGradGuard no_grad;
   Tensor c = fresh(t.sizes(), t.scalar_type(), dev);
@@ -145,6 +149,7 @@ py::tuple rotary(const py::object& q_, const py::object& k_, const py::object& p
   }
   if (q.size(2) < 1 || q.size(3) < 1 || (k.defined() && k.size(2) < 1))
     throw py::value_error("q and k must have at least one head of one element");
+  if (q.size(2) > kMostHeads || (k.defined() && k.size(2) > kMostHeads)) refuse_heads();
   RotaryPlan plan;
   plan.base = base;
   plan.pairs = pairs;
@@ -298,6 +303,7 @@ Tensor attention(const py::object& q_, const py::object& k_, const py::object& v
   if (k.size(0) != q.size(0) || k.size(3) != q.size(3)) throw py::value_error("k and v must have q's batch and dim");
   if (q.size(2) < 1 || k.size(2) < 1 || q.size(2) % k.size(2) != 0)
     throw py::value_error("q's heads must be a multiple of k's");
+  if (q.size(2) > kMostHeads) refuse_heads();
   if (q.size(3) < 8 || q.size(3) > SSIM_ATTENTION_MAX_DIM || q.size(3) % 8 != 0)
     throw py::value_error("dim must be a multiple of 8, to " + std::to_string(SSIM_ATTENTION_MAX_DIM));
   AttentionPlan plan;

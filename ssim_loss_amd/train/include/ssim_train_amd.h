@@ -250,7 +250,7 @@ typedef struct {
   int64_t k_stride[3]; /* each a multiple of 16 bytes, a token's at least dim and less */
   int64_t v_stride[3]; /* than 2^24 bytes, and q, k, v aligned to 16 bytes */
   int64_t batch, q_tokens, k_tokens; /* >= 0, tokens < 2^24 */
-  int32_t heads, kv_heads; /* kv_heads divides heads */
+  int32_t heads, kv_heads; /* 1 .. 65536; kv_heads divides heads */
   int32_t dim;         /* a multiple of 8, to SSIM_ATTENTION_MAX_DIM */
   int32_t causal;
   int32_t dtype;

@@ -1,5 +1,5 @@
 """Attention at the ends of its range: scales that fp32 does not hold, scores past
-fp32, weights far below a row's largest in fp16."""
+fp32, weights far below a row's largest in fp16, more heads than an int counts."""
 import math
 
 import pytest
@@ -94,6 +94,16 @@ def test_weights_far_below_a_rows_largest_in_fp16(n):
     want = w / (1 + w)
     off = float((out.double() - want).abs().max())
     assert off <= m * 2.0 ** -32 + want * (2.0 ** -11 + 1e-5), (off, want)
+
+
+def test_more_heads_than_an_int_counts():
+    one = torch.zeros(1, 1, 1, 8, dtype=F16, device="cuda")
+    many = one.expand(1, 1, (1 << 32) + 1, 8)
+    position = torch.zeros(1, 1, device="cuda")
+    for call in (lambda: S.attention(many, one, one), lambda: S.attention(many, many, many),
+                 lambda: S.rotary(many, None, position, (8,)), lambda: S.rotary(one, many, position, (8,))):
+        with pytest.raises(ValueError, match="heads"):
+            call()
 
 
 @pytest.mark.parametrize("dtype,most", [(F32, 2.0 ** 30), (F16, 2.0 ** 26), (BF16, 2.0 ** 30)])
