@@ -29,6 +29,8 @@ COUNTERS = {"fetch": ["FETCH_SIZE"], "write": ["WRITE_SIZE"], "sq": ["SQ_INSTS_V
 BLOCK = False  # the operators inside a block
 MATRIX, ACTIVE = "SQ_VALU_MFMA_BUSY_CYCLES", "GRBM_GUI_ACTIVE"
 SIMDS, XCDS = 1024, 8
+CYCLES_FROM = 100.0  # microseconds: of shorter kernels the counter's cycles are largely launch and drain
+REGISTER_UNIT = 2  # the tool halves what is allocated (a kernel of 184 registers reads 92)
 FETCH_UNIT = 2.0  # a large copy reads this many bytes for each that the counter names
 CUS = 256
 
@@ -144,7 +146,7 @@ def profile(outdir):
 def kernel_of(row):
     if BLOCK:
         name = row["Kernel_Name"]
-        found = re.search(r"attention_(?:forward|join|norms|delta|grads|grad_kv|grad_q)|gated_(?:product|both|finish|slopes|few_rows|copy)|"
+        found = re.search(r"attention_(?:forward|join|norms|delta|grads|grad_kv|grad_q)|gated_(?:product|both|finish|slopes|tops|few_rows|copy)|"
                           r"rotary_kernel", name)
         if not found or found[0] != "gated_product":
             return found and found[0]
@@ -192,16 +194,17 @@ def summarize(outdir):
             threads = int(r["Workgroup_Size_X"])
             lines.append("| %s | %s | %d | %.2f | %.2f | %d x %s, %d | %s | %s |" % (
                 case, kernel, len(us), times[case, kernel], min(us), int(r["Grid_Size_X"]) // threads,
-                r["Grid_Size_Y"], threads, r["VGPR_Count"], r["Scratch_Size"]))
+                r["Grid_Size_Y"], threads, REGISTER_UNIT * int(r["VGPR_Count"]), r["Scratch_Size"]))
     what, file = ("operators inside a block", "block") if BLOCK else ("training operators", "train")
     with open(os.path.join(PROFILES, file + "_operators_kernel_trace.md"), "w") as f:
         f.write(f"""# Kernel times of the {what} (rocprofv3 --kernel-trace), MI355X
 
 By `perf/profile_operators.py`: one process, each case of `perf/{module().__name__[5:]}.py` {TRACED} times over {SEEDS} sets
 of inputs in turn. Times in microseconds. Profiled kernels of a few microseconds read 0.3 to 1 us
-longer than unprofiled ones.
+longer than unprofiled ones. Registers are those allocated to a thread, vector and accumulation registers
+together ({REGISTER_UNIT} times the tool's number), of 512 that the waves of a SIMD share.
 
-| case | kernel | calls | median us | least us | workgroups, threads | VGPRs | scratch B |
+| case | kernel | calls | median us | least us | workgroups, threads | registers | scratch B |
 |---|---|---|---|---|---|---|---|
 """ + "\n".join(lines) + "\n")
 
@@ -228,11 +231,13 @@ longer than unprofiled ones.
                 counts[case, kernel, "SQ_INSTS_VALU"] / CUS / (us * 1e3)))
             if BLOCK:
                 busy, active = (counts[case, kernel, c] for c in (MATRIX, ACTIVE))
-                lines[-1] += " %.0f%% | %.2f |" % (100 * busy / SIMDS / (active / XCDS), active / XCDS / us / 1e3)
+                lines[-1] += " %.0f%% | %.2f |" % (100 * busy / SIMDS / (active / XCDS), active / XCDS / us / 1e3) \
+                    if us >= CYCLES_FROM else " | |"
         lines.append("| %s | all; the case needs %.1f | %.1f | | | |" % (case, need[case], total) + " | |" * BLOCK)
-    matrix = """ The share of the kernel's
+    matrix = f""" The share of the kernel's
 cycles in which a matrix instruction runs, over all SIMDs, and the cycles in GHz of its time in the trace (the
-counter run's own is a little longer).""" if BLOCK else ""
+counter run's own is a little longer); left out below {CYCLES_FROM:.0f} us, where launch and drain, which the
+cycles include, are a large part of them.""" if BLOCK else ""
     more = (" matrix | GHz |", "---|---|") if BLOCK else ("", "")
     with open(os.path.join(PROFILES, file + "_operators_counters.md"), "w") as f:
         f.write(f"""# Traffic and vector instructions of the {what} (rocprofv3 --pmc), MI355X
