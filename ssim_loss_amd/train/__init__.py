@@ -289,7 +289,8 @@ def rotary(q, k, positions, axes, base=10000.0, pairs="adjacent"):
                be fewer) of one type, float32, float16 or bfloat16; any strides,
                such as views of one projection's output.
     positions: [tokens, axes] or [batch, tokens, axes], float32, int32 or int64;
-               fractions and far positions keep their angle (it is reduced in fp64).
+               fractions and far positions keep their angle, which is reduced in
+               fp64 and off by at most 2^-50 of the position.
     axes:      for each of 1 to 4 axes the number of elements of a head that turn
                by it, one part after the other: even, together at most dim (which
                is at most 512).  The elements behind them pass as they are.

@@ -273,9 +273,9 @@ __device__ __forceinline__ void take_joined(const char* lds, int dim, Take take)
 // ---------------------------------------------------------------- forward
 // NW waves.  KW of them share rows and take keys in turn: 1, a wave has 32 rows of
 // its own; 4, all have the same 32 (few rows, many keys).
-// The bound is the matrix instructions, and the exponentials where they run beside
-// none: 1 x 16384 x 16 x 128 bf16 1900 to 1980 us, 1.11 to 1.16 PFLOP/s at 1.9 GHz (1650
-// without the softmax).  One token against 8 x 8193 keys, 32 (8) heads of 128: the
+// The bound is the matrix instructions (56% of the cycles), and the exponentials where they
+// run beside none: 1 x 16384 x 16 x 128 bf16 1870 to 2000 us, 1.10 to 1.18 PFLOP/s at 1.9 to
+// 2.0 GHz (1650 without the softmax).  One token against 8 x 8193 keys, 32 (8) heads of 128: the
 // memory, 44 to 48 us, 3.9 to 4.2 TB/s, and 4 for the join.
 //
 // Tiles of keys are loaded kBuffers - 1 ahead.  Eight waves with four buffers, one
@@ -346,7 +346,7 @@ attention_forward(const AttentionParams p) {
   const int along_at = along_offset<Head::kRow>(), across_at = across_offset<T, Head::kRow>();
   Sums o[DB] = {};
   // The row's reference, a maximum so far: p = exp2(scale2 s - base).  It is raised, and
-  // the sums with it, only where scores pass it by 2^8 in p, which both types and the
+  // the sums with it, only where scores pass it by 2^8 in p, which the types and the
   // sums hold: in a long row seldom, where a larger maximum comes with every other tile.
   float m = -INFINITY, base = 0.0f, limit = -INFINITY;
   const float slack = 8.0f / fmaxf(p.scale2, 0x1p-100f);  // (finite: of -infinity and it the limit is -infinity)
@@ -549,9 +549,11 @@ __device__ __forceinline__ int range_of(const AttentionParams& p, const Where& a
 
 // ---------------------------------------------------------------- gradient of the queries
 // As the forward: a wave has 32 rows, the keys go by.  It forms delta_i = do_i . o_i
-// and leaves it for the other kernel.  Three products, so the matrix instructions are the
-// bound: 4 x 4096 x 16 (8) x 128 bf16, causal, sequences of different lengths: 258 us,
-// the forward 193, the keys' and values' gradients (four products) 370.
+// and leaves it for the other kernel.  Three products; the bound is the chain of scores,
+// exponentials and products in each wave, beside which only the SIMD's other wave runs: matrix
+// instructions take 35% of the cycles (the forward's 30, the keys' and values' gradients', of four
+// products, 31).  4 x 4096 x 16 (8) x 128 bf16, causal, sequences of different lengths: 251 us, the
+// forward 190, the keys' and values' gradients 371.
 template <class T, int DB, int KW, int NW>
 struct QueriesShape {
   static constexpr int kThreads = NW * kWave;

@@ -6,10 +6,10 @@
 // Three products of one kernel's kind.  A workgroup forms a tile of the result,
 // of which a lane has four neighbouring elements of a row at a time: the weights
 // are the left operand.  Both operands go from memory straight to LDS, two tiles
-// in turn, 128 bytes of the axis that is summed over in each.  The forward's left
-// tile is half Wg's and half Wu's rows, so a wave has g and u of the same elements
-// in its registers and neither has to be written for the product.  The bound is the matrix
-// instructions and the clock under them (1.75 to 1.8 GHz): 16384 x 4096 x 10944 bf16, dx
+// (of the smallest size three) in turn, 128 bytes of the axis that is summed over in
+// each.  The forward's left tile is half Wg's and half Wu's rows, so a wave has g and u
+// of the same elements in its registers and neither has to be written for the product.
+// The bound is the matrix instructions and the clock under them (1.75 to 1.8 GHz): 16384 x 4096 x 10944 bf16, dx
 // 1.27 PFLOP/s, dW 1.13, forward 1.11 with g and u written (a library product 1.32).
 
 #pragma once
@@ -302,7 +302,7 @@ __device__ __forceinline__ void product_tile(const GatedParams& p, unsigned bloc
   // A step's operands are read while the one before is multiplied, the next tile's first
   // with this tile's last: its buffer is free once all waves have read that.
   // 16384 x 4096 x 10944 bf16, with each step's read before its own products 2815 us
-  // forward, 2550 and 2715 the gradients, so 2580, 2280 and 2590.  (Four waves of twice
+  // forward, 2550 and 2715 the gradients, so 2580, 2290 and 2590.  (Four waves of twice
   // the block each read less, but nothing runs beside a wave that waits: 3080, 2430, 2830.
   // 64 bytes of depth in four buffers: 2830, 2550, 2740.)
   Chunk a[2][BM], b[2][BN];

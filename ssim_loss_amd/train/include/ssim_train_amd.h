@@ -189,7 +189,7 @@ int ssim_block_norm_backward(const ssim_block_norm_inputs* in, const float* stat
  * positions[.., a] base^(-2 i / axis_size[a]):
  *   y0 = x0 cos - x1 sin,  y1 = x1 cos + x0 sin
  * The angle is reduced in fp64, so positions may lie far out and between whole
- * numbers.
+ * numbers: it is off by at most 2^-50 of the position.
  */
 enum {
   SSIM_PAIRS_ADJACENT = 0, /* elements 2 i and 2 i + 1 of the part */
@@ -234,9 +234,10 @@ int ssim_rotary(const ssim_rotary_inputs* in, void* q_out, void* k_out, void* st
  * at them, must be finite: what is not may reach rows that do not see it (scores of
  * minus infinity excepted).  A query whose largest s_ij is above 7 10^8 (fp16: 4 10^7)
  * gives NaN, and one whose all are as far below 0 zeros: fp32 does not tell them apart.
- * Scores, sums and statistics are fp32: a probability that the gradients form again is off
- * by some 2^-23 of its score, by a hundredth where scores are 10^5.  For half types the probabilities and, in
- * the gradients, their derivatives are rounded to the type before the products.
+ * Scores, sums and statistics are fp32: a probability that the gradients form again
+ * is off by some 2^-23 of its score, by a hundredth where scores are 10^5.  For half
+ * types the probabilities and, in the gradients, their derivatives are rounded to the
+ * type before the products.
  */
 #define SSIM_ATTENTION_MAX_DIM 128
 
