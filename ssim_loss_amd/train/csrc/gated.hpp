@@ -537,7 +537,9 @@ __global__ void __launch_bounds__(256) gated_tops(const GatedParams p) {
   if (threadIdx.x == 0) p.tops[blockIdx.y * gridDim.x + blockIdx.x] = top;
 }
 
-// dg and du, and what they add up to over a block of rows.
+// dg and du, rounded to the type as the products' operands (bf16: gradients 2.3e-3 of the
+// norm, with fp32 operands, whose instructions take 16 times as long, 1.7e-3), and what they
+// add up to over a block of rows, unrounded.
 template <class T>
 __global__ void __launch_bounds__(256) gated_slopes(const GatedParams p) {
   constexpr int V = kPerChunk<T>;
