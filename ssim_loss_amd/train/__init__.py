@@ -326,7 +326,7 @@ def attention(q, k, v, scale=None, causal=False, query_lengths=None, key_lengths
     its sequence, gives zeros and takes a zero gradient.  Within the sequences' lengths
     queries, keys, values and the gradient that arrives must be finite: what is not
     may reach rows that do not see it.  Behind the lengths they may be anything.
-    A query whose largest scaled score is above 7 10^8 (float16: 4 10^7) gives NaN, and one
+    A query whose largest scaled score is above 10^9 (float16: 10^8) gives NaN, and one
     whose all are as far below 0 zeros: float32 does not tell them apart.
     Scores and sums are float32 (a probability that the backward forms again is off by some
     2^-23 of its score); for half types the probabilities (and in the

@@ -193,17 +193,18 @@ __device__ __forceinline__ void store_row(T* row, const Sums (&v)[DB], float fac
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 
 // What is subtracted from the scaled scores of a row whose largest score is `top`.  It is rounded, by up
-// to 2^-24 of itself, as is the limit from which scores raise it, and 2 to both is in the row's
-// probabilities beside the 2^8 that they may reach: 2^72 below 2^30, 2^12 below 2^26 (fp16).  A row past that
-// is NaN, not one that has lost its keys; one as far below 0 gives zeros, as one of minus infinity does.
+// to 2^-24 of itself, and 2 to that is in all of the row's probabilities: 2^64 below 2^31, 2^8 below 2^28
+// (fp16).  A row past that is NaN, not one that has lost its keys; one as far below 0 gives zeros, as one of
+// minus infinity does.
 // fp16's probabilities are kept times 2^7, the most that its largest number leaves where they may be 2^8:
 // of 2^17 keys with 2^-26 of the largest weight each, 2^-9 of the result, nothing was left without.
+constexpr float kSlackBelow = 0x1p23f;  // further out a score's own step is 1 and more
 template <class T>
 __device__ __forceinline__ float base_of(const AttentionParams& p, float top) {
-  constexpr float kMost = kScaled<T> ? 0x1p26f : 0x1p30f;
+  constexpr float kMost = kScaled<T> ? 0x1p28f : 0x1p31f;
   const float base = top * p.scale2;
   if (top == -INFINITY) return 0.0f;
-  if (kScaled<T> && fabsf(base) < 0x1p23f) return base - 7.0f;
+  if (kScaled<T> && fabsf(base) < kSlackBelow) return base - 7.0f;
   return base < kMost ? fmaxf(base, -kMost) : NAN;
 }
 
@@ -387,7 +388,7 @@ attention_forward(const AttentionParams p) {
         const float before = m == -INFINITY ? -INFINITY : base;
         m = fmaxf(m, top);
         base = base_of<T>(p, m);
-        limit = m + slack;
+        limit = m + (fabsf(base) < kSlackBelow ? slack : 0.0f);
         const float less = exp2_fast(before - base);
         l *= less;
 #pragma unroll

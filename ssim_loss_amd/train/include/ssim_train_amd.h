@@ -232,7 +232,7 @@ int ssim_rotary(const ssim_rotary_inputs* in, void* q_out, void* k_out, void* st
  * query or key that takes no part has a gradient of zeros.  Queries past ql and
  * keys and values past kl are not read.  The others, and the gradient that arrives
  * at them, must be finite: what is not may reach rows that do not see it (scores of
- * minus infinity excepted).  A query whose largest s_ij is above 7 10^8 (fp16: 4 10^7)
+ * minus infinity excepted).  A query whose largest s_ij is above 10^9 (fp16: 10^8)
  * gives NaN, and one whose all are as far below 0 zeros: fp32 does not tell them apart.
  * Scores, sums and statistics are fp32: a probability that the gradients form again
  * is off by some 2^-23 of its score, by a hundredth where scores are 10^5.  For half
